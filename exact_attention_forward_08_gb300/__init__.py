@@ -8,11 +8,14 @@ library is missing or a call fails, an exception is raised.
     from exact_attention_forward_08_gb300 import attention_forward
     o, lse = attention_forward(q, k, v, causal=True)   # q [B,Sq,Hq,d] bf16 on cuda
     o, lse = attention_forward_varlen(q, k, v, cu_q, cu_k)  # q [total_q,Hq,d], cu_q int32 [B+1]
+    kv_append(k, v, k_cache, v_cache, k_scale, v_scale, table, lens, cu_q)  # paged 8-bit cache
+    o, lse = attention_forward_paged(q, k_cache, v_cache, k_scale, v_scale, table, lens, cu_q, max_seqlen_q)
 
 Raw entry points with the C names: ``fa_fwd``, ``fa_fwd_ex``, ``fa_fwd_varlen``,
 ``fa_fwd_varlen_ex``, ``fa_varlen_workspace_size``, ``fa_varlen_plan_host``,
 ``fa_device_status``, ``fa_status_string``, ``fa_make_plan``, ``fa_plan_task``, ``fa_plan_set_grid``,
-``fa_plan_block_masked``, ``fa_plan_first_masked_block``, ``fa_version``.
+``fa_plan_block_masked``, ``fa_plan_first_masked_block``, ``fa_version``, ``fa_kv_append``, ``fa_fwd_paged``,
+``fa_fwd_paged_workspace_size``.
 """
 from __future__ import annotations
 
@@ -29,7 +32,8 @@ __all__ = ["fa_fwd", "fa_fwd_ex", "fa_fwd_varlen", "fa_fwd_varlen_ex", "fa_varle
            "fa_fwd_varlen_noalloc", "fa_noalloc_scratch_bytes", "fa_device_status", "fa_device_status_code", "fa_status_string", "fa_selftest_exp2", "fa_make_plan",
            "fa_plan_task", "fa_plan_set_grid", "fa_plan_block_masked", "fa_plan_first_masked_block", "fa_version", "FaOptions", "FaPlan",
            "FaTask", "FaVarlenTask", "attention_forward", "attention_forward_varlen", "FaError", "load_library",
-           "LIB_PATH", "STATUS", "VARLEN_HEADER_BYTES"]
+           "LIB_PATH", "STATUS", "VARLEN_HEADER_BYTES", "FaKvCache", "fa_kv_append", "fa_fwd_paged",
+           "fa_fwd_paged_workspace_size", "kv_append", "attention_forward_paged"]
 
 LIB_PATH = _build.LIB
 STATUS = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED", 3: "FA_ERR_CUDA",
@@ -71,6 +75,13 @@ class FaTask(ctypes.Structure):
 class FaVarlenTask(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("b", "g", "mblock", "reserved", "q_row0", "seqlen_q", "k_row0",
                                             "seqlen_k")]
+
+
+class FaKvCache(ctypes.Structure):
+    """``fa_kv_cache`` of include/fa.h: pointers as integers, strides in bytes."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "block_table", "seqlens_k")] + \
+               [("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3), ("table_stride", ctypes.c_int64)] + \
+               [(n, ctypes.c_int) for n in ("num_pages", "page_size", "heads_kv", "d_qk", "d_v", "max_pages")]
 
 
 # a varlen workspace holds the task count at byte 0 and the task records from this offset
@@ -157,6 +168,15 @@ def load_library(path: str | None = None):
     lib.fa_varlen_plan_host.argtypes = [_P, _P] + [_I] * 6 + [ctypes.c_int64, _I, ctypes.POINTER(FaVarlenTask),
                                                              ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)]
     lib.fa_varlen_plan_host.restype = _I
+    i64 = ctypes.c_int64
+    lib.fa_kv_append.argtypes = [ctypes.POINTER(FaKvCache), _P, _P, _P, i64, i64, i64, _P, _P, _I, i64, _I, _P, _I, _I,
+                                 _I, _P]
+    lib.fa_kv_append.restype = _I
+    lib.fa_fwd_paged.argtypes = [_P, ctypes.POINTER(FaKvCache), _P, _P, _P, _I, i64, _I, i64, _I, _I, ctypes.c_float, _P,
+                                 ctypes.c_size_t, _P]
+    lib.fa_fwd_paged.restype = _I
+    lib.fa_fwd_paged_workspace_size.argtypes = [_I, _I, _I, i64, _I, i64, _I, _I]
+    lib.fa_fwd_paged_workspace_size.restype = ctypes.c_size_t
     if path is None:
         _lib = lib
     return lib
@@ -570,3 +590,207 @@ def attention_backward_varlen(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k,
     if rc != FA_OK:
         raise FaError(rc, "fa_bwd_varlen")
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------------------
+# the paged 8-bit key/value cache
+# ---------------------------------------------------------------------------
+
+def fa_kv_append(cache: FaKvCache, q, k, v, q_stride, k_stride, v_stride, q_out, cu_seqlens, batch, total, heads_q,
+                 cos_sin, max_positions, rot_dim, interleaved, stream) -> int:
+    """``fa_kv_append`` of include/fa.h; pointer arguments are integers (device addresses)."""
+    return load_library().fa_kv_append(ctypes.byref(cache) if cache is not None else None, q, k, v, q_stride, k_stride,
+                                       v_stride, q_out, cu_seqlens, batch, total, heads_q, cos_sin, max_positions,
+                                       rot_dim, int(interleaved), stream)
+
+
+def fa_fwd_paged_workspace_size(batch, heads_q, heads_kv, total_q, max_seqlen_q, total_k, d_qk, d_v) -> int:
+    return load_library().fa_fwd_paged_workspace_size(batch, heads_q, heads_kv, total_q, max_seqlen_q, total_k, d_qk,
+                                                      d_v)
+
+
+def fa_fwd_paged(q, cache: FaKvCache, o, lse, cu_seqlens_q, batch, total_q, max_seqlen_q, total_k, heads_q, causal,
+                 scale, workspace, workspace_bytes, stream) -> int:
+    """``fa_fwd_paged`` of include/fa.h; pointer arguments are integers (device addresses)."""
+    return load_library().fa_fwd_paged(q, ctypes.byref(cache) if cache is not None else None, o, lse, cu_seqlens_q,
+                                       batch, total_q, max_seqlen_q, total_k, heads_q, int(causal), float(scale),
+                                       workspace, workspace_bytes, stream)
+
+
+def _bad(what: str):
+    raise FaError(FA_ERR_INVALID_ARG, what)
+
+
+def _paged_cache(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, cu_seqlens, device) -> FaKvCache:
+    """The cache's tensors, checked, as an ``FaKvCache``."""
+    import torch
+
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype != torch.float8_e4m3fn or t.dim() != 4 or t.device != device or (t.numel() and t.stride(3) != 1):
+            _bad(f"{name} must be a 4-D float8_e4m3fn tensor [num_pages, heads_kv, page_size, d] on {device}, its last "
+                 "dimension contiguous")
+    pages, heads, page, d_qk = k_cache.shape
+    if v_cache.shape[:3] != k_cache.shape[:3]:
+        _bad("k_cache and v_cache must have the same pages, heads and page size")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t.dtype != torch.float8_e8m0fnu or t.shape != (pages, heads) or t.device != device or not t.is_contiguous():
+            _bad(f"{name} must be a contiguous float8_e8m0fnu tensor [num_pages, heads_kv] on {device}")
+    for name, t, dim in (("block_table", block_table, 2), ("seqlens_k", seqlens_k, 1), ("cu_seqlens", cu_seqlens, 1)):
+        if t.dtype != torch.int32 or t.dim() != dim or t.device != device or (t.numel() and t.stride(-1) != 1):
+            _bad(f"{name} must be a {dim}-D int32 tensor on {device}, its last dimension contiguous")
+    batch, width = block_table.shape
+    if seqlens_k.shape[0] != batch or cu_seqlens.shape[0] != batch + 1:
+        _bad("block_table, seqlens_k and cu_seqlens must hold batch rows, batch lengths and batch + 1 offsets")
+    return FaKvCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                     block_table.data_ptr(), seqlens_k.data_ptr(), k_cache.stride()[:3], v_cache.stride()[:3],
+                     block_table.stride(0) if batch > 1 else width, pages, page, heads, d_qk, v_cache.shape[3], width)
+
+
+class _OnDevice:
+    """Makes `device` the current one for a call when it is not."""
+
+    def __init__(self, device):
+        self.device, self.guard = device, None
+
+    def __enter__(self):
+        import torch
+
+        if torch.cuda.current_device() != self.device.index:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _token_stride(name, t, heads, d, device):
+    """Elements from token to token of a bf16 tensor [total, heads, d] whose heads lie side by side."""
+    import torch
+
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.device != device:
+        _bad(f"{name} must be a 3-D bf16 tensor on {device}")
+    if t.shape[1] != heads or t.shape[2] != d:
+        _bad(f"{name} must be [total, {heads}, {d}]")
+    if t.numel() == 0 or (t.stride(2) == 1 and (heads == 1 or t.stride(1) == d)):
+        return t.stride(0) if t.shape[0] > 1 else heads * d
+    _bad(f"{name}: a token's heads must be contiguous")
+
+
+def kv_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, cu_seqlens, q=None, cos_sin=None,
+              interleaved: bool = False, q_out=None, stream=None):
+    """Append the new tokens' keys and values to a paged 8-bit cache (``fa_kv_append`` of include/fa.h).
+
+    k [total,Hkv,dqk], v [total,Hkv,dv] and, to be rotated along with the keys, q [total,Hq,dqk] are bf16 CUDA tensors
+    whose tokens may lie apart (views of one projection's output); k_cache, v_cache float8_e4m3fn
+    [num_pages,Hkv,page_size,d] of any strides with contiguous codes, k_scale, v_scale float8_e8m0fnu [num_pages,Hkv];
+    block_table int32 [B,max_pages], seqlens_k int32 [B] (lengths with the new tokens), cu_seqlens int32 [B+1];
+    cos_sin fp32 [positions, rot_dim] or None (no rotation).  The cache is updated in place; returns q_out (allocated
+    when not given; may be q), None without q.  Launches on ``stream`` (default: torch's current stream).  Offsets,
+    lengths and pages out of range are detected on the device and reported by ``fa_device_status``.
+    """
+    import torch
+
+    device = k.device
+    if device.type != "cuda":
+        _bad("k must be a CUDA tensor")
+    cache = _paged_cache(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, cu_seqlens, device)
+    total = k.shape[0]
+    ks = _token_stride("k", k, cache.heads_kv, cache.d_qk, device)
+    vs = _token_stride("v", v, cache.heads_kv, cache.d_v, device)
+    if v.shape[0] != total:
+        _bad("k and v must hold the same tokens")
+    rot = positions = 0
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.device != device or not cos_sin.is_contiguous():
+            _bad(f"cos_sin must be a contiguous 2-D fp32 tensor on {device}")
+        positions, rot = cos_sin.shape
+    with _OnDevice(device):
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        sptr = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+        heads_q = qs = 0
+        if q is not None:
+            heads_q = q.shape[1] if q.dim() == 3 else 0
+            qs = _token_stride("q", q, heads_q, cache.d_qk, device)
+            if q.shape[0] != total:
+                _bad("q must hold the same tokens as k")
+            if q_out is None:
+                q_out = _empty((total, heads_q, cache.d_qk), torch.bfloat16, device, stream)
+            elif q_out.dtype != torch.bfloat16 or q_out.shape != q.shape or q_out.device != device or \
+                    not q_out.is_contiguous():
+                _bad(f"q_out must be a contiguous bf16 tensor of q's shape on {device}")
+        elif q_out is not None:
+            _bad("q_out without q")
+        rc = fa_kv_append(cache, q.data_ptr() if q is not None else None, k.data_ptr(), v.data_ptr(), qs, ks, vs,
+                          q_out.data_ptr() if q is not None else None, cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1,
+                          total, heads_q, cos_sin.data_ptr() if cos_sin is not None else None, positions, rot,
+                          interleaved, sptr)
+    if rc != FA_OK:
+        raise FaError(rc, "fa_kv_append")
+    return q_out
+
+
+def _empty(shape, dtype, device, stream):
+    """torch.empty whose memory is not reused before the work on `stream` that it is for has run."""
+    import torch
+
+    current = torch.cuda.current_stream(device)
+    ptr = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+    if (ptr or 0) == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(ptr or 0, device=device)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def attention_forward_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, cu_seqlens_q,
+                            max_seqlen_q: int, causal: bool = True, scale: float | None = None,
+                            total_k: int | None = None, out=None, lse=None, return_lse: bool = True, workspace=None,
+                            stream=None):
+    """O (and LSE) of new tokens over a paged 8-bit cache (``fa_fwd_paged`` of include/fa.h).
+
+    q [total_q,Hq,dqk] bf16 (packed, cu_seqlens_q int32 [B+1], at most ``max_seqlen_q`` tokens a sequence); the cache
+    as ``kv_append`` fills it, seqlens_k the lengths with the new tokens.  ``total_k``: an upper limit of their sum,
+    which bounds the workspace of calls with long sequences of new tokens (default: what the block table can hold).
+    Allocates ``out`` [total_q,Hq,dv] bf16, ``lse`` [Hq,total_q] fp32 and the workspace (uint8) when not given.
+    Offsets, lengths and pages out of range are detected on the device and reported by ``fa_device_status``.
+    """
+    import torch
+
+    device = q.device
+    if device.type != "cuda" or q.dtype != torch.bfloat16 or q.dim() != 3 or not q.is_contiguous():
+        _bad("q must be a contiguous 3-D bf16 CUDA tensor")
+    cache = _paged_cache(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, cu_seqlens_q, device)
+    total_q, heads_q, d_qk = q.shape
+    if d_qk != cache.d_qk:
+        _bad(f"q must be [total_q, heads_q, {cache.d_qk}]")
+    batch = cu_seqlens_q.shape[0] - 1
+    if total_k is None:
+        total_k = batch * cache.max_pages * cache.page_size
+    with _OnDevice(device):
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        sptr = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+        if out is None:
+            out = _empty((total_q, heads_q, cache.d_v), torch.bfloat16, device, stream)
+        elif out.dtype != torch.bfloat16 or out.shape != (total_q, heads_q, cache.d_v) or out.device != device or \
+                not out.is_contiguous():
+            _bad(f"out must be a contiguous bf16 tensor [total_q, heads_q, {cache.d_v}] on {device}")
+        if lse is None and return_lse:
+            lse = _empty((heads_q, total_q), torch.float32, device, stream)
+        elif lse is not None and (lse.dtype != torch.float32 or lse.shape != (heads_q, total_q) or
+                                  lse.device != device or not lse.is_contiguous()):
+            _bad(f"lse must be a contiguous fp32 tensor [heads_q, total_q] on {device}")
+        if workspace is None:
+            need = fa_fwd_paged_workspace_size(batch, heads_q, cache.heads_kv, total_q, max_seqlen_q, total_k, d_qk,
+                                               cache.d_v)
+            workspace = _empty((max(need, 16),), torch.uint8, device, stream)
+        elif workspace.device != device or not workspace.is_contiguous():
+            _bad(f"workspace must be a contiguous tensor on {device}")
+        rc = fa_fwd_paged(q.data_ptr(), cache, out.data_ptr(), lse.data_ptr() if lse is not None else None,
+                          cu_seqlens_q.data_ptr(), batch, total_q, max_seqlen_q, total_k, heads_q, causal,
+                          0.0 if scale is None else scale, workspace.data_ptr(),
+                          workspace.numel() * workspace.element_size(), sptr)
+    if rc != FA_OK:
+        raise FaError(rc, "fa_fwd_paged")
+    return (out, lse) if return_lse else out

@@ -16,6 +16,7 @@
 #include "fa.h"
 #include "fa_bwd_dispatch.h"
 #include "fa_dispatch.h"
+#include "fa_host.h"
 #include "fa_schedule.h"
 
 // {code, wait site, block} of the first device-side failure since the last read
@@ -475,6 +476,41 @@ int validate(const void* q, const void* k, const void* v, void* o, const float* 
 }
 
 }  // namespace
+
+namespace fa {
+
+int host_device(HostDevice* out) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
+  DeviceState* st = nullptr;
+  const int rc = init_device(dev, &st);
+  if (rc != FA_OK) return rc;
+  out->dev = dev;
+  out->sms = st->sms;
+  out->status = st->status;
+  return FA_OK;
+}
+
+bool host_is_device_ptr(const void* p, int dev) { return is_device_ptr(p, dev); }
+
+int host_encode_bytes(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                      const uint32_t* box, int swizzle) {
+  const cuuint32_t elem_strides[5] = {1, 1, 1, 1, 1};
+  cuuint64_t d[5], s[4];
+  cuuint32_t b[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    if (i + 1 < rank) s[i] = strides[i];
+  }
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, s,
+                        b, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        swizzle == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // namespace fa
 
 extern "C" {
 

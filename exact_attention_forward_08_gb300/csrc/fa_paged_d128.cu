@@ -1,0 +1,12 @@
+// paged attention kernels, d_qk = 128
+#include "fa_paged_launch.cuh"
+
+namespace fa {
+
+int paged_launch_d128(const PagedParams& p, int d_v, int rows, int grid, cudaStream_t stream) {
+  if (d_v == 64) return paged_launch_rows<128, 64>(p, rows, grid, stream);
+  if (d_v == 128) return paged_launch_rows<128, 128>(p, rows, grid, stream);
+  return FA_ERR_UNSUPPORTED;
+}
+
+}  // namespace fa

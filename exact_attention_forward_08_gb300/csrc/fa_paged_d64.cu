@@ -1,0 +1,11 @@
+// paged attention kernels, d_qk = 64
+#include "fa_paged_launch.cuh"
+
+namespace fa {
+
+int paged_launch_d64(const PagedParams& p, int d_v, int rows, int grid, cudaStream_t stream) {
+  if (d_v == 64) return paged_launch_rows<64, 64>(p, rows, grid, stream);
+  return FA_ERR_UNSUPPORTED;
+}
+
+}  // namespace fa

@@ -408,6 +408,118 @@ int fa_fwd_varlen_noalloc(const void* q, const void* k, const void* v, void* o, 
 size_t fa_noalloc_scratch_bytes(void);
 
 /*
+ * A paged key/value cache in 8 bits.  Keys and values are e4m3 codes in pages
+ * of page_size tokens; each page and key/value head has one power-of-two scale
+ * for its keys and one for its values, and a code stands for code * scale.
+ *
+ *   k  [num_pages, heads_kv, page_size, d_qk] e4m3     k_scale [num_pages, heads_kv] e8m0
+ *   v  [num_pages, heads_kv, page_size, d_v ] e4m3     v_scale [num_pages, heads_kv] e8m0
+ *   block_table [batch, max_pages] int32, row stride table_stride: the page
+ *               that holds tokens j * page_size .. of sequence b is
+ *               block_table[b * table_stride + j]; entries behind a sequence's
+ *               last page are not read
+ *   seqlens_k   [batch] int32: tokens of each sequence, for a call that brings
+ *               new tokens the new ones among them
+ *
+ * k_stride and v_stride hold the bytes between pages, heads and tokens
+ * (multiples of 16; a token's codes are contiguous), so other orders of the
+ * first three dimensions, and a cache that is part of a larger allocation,
+ * are fine.  k and v are 16-byte aligned device memory.  page_size is 16, 32,
+ * 64 or 128, (d_qk, d_v) one of fa_fwd's pairs.  An e8m0 byte e stands for
+ * 2^(e - 127), 255 for NaN; the append writes 64 to 247.
+ *
+ * block_table, seqlens_k and the offsets live on the device and are checked
+ * there: a sequence whose offsets, length or positions are out of range is
+ * left out (site 511 and its index in the status word), a page index outside
+ * [0, num_pages) is never followed (site 512); fa_device_status then reports
+ * FA_ERR_INVALID_ARG, and outputs of the sequences concerned are not valid.
+ */
+typedef struct fa_kv_cache {
+  void* k;
+  void* v;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  const int* block_table;
+  const int* seqlens_k;
+  int64_t k_stride[3]; /* bytes between pages, heads, tokens */
+  int64_t v_stride[3];
+  int64_t table_stride;
+  int num_pages, page_size, heads_kv, d_qk, d_v;
+  int max_pages;       /* entries of a row of block_table */
+} fa_kv_cache;
+
+/*
+ * Append new tokens to the cache, with the position rotation on the way.
+ *
+ *   k  [total, heads_kv, d_qk], v [total, heads_kv, d_v] bf16, k_stride and
+ *      v_stride elements from token to token (multiples of 8; a token's heads
+ *      are contiguous): the new tokens of all sequences, packed
+ *   cu_seqlens [batch + 1] int32: new tokens of sequence b are rows
+ *      cu_seqlens[b] .. cu_seqlens[b+1]-1; the last of them is its token
+ *      seqlens_k[b] - 1
+ *   q, q_out   NULL, or the new tokens' queries [total, heads_q, d_qk] bf16
+ *      (q with q_stride, q_out contiguous; q_out may be q if q is contiguous):
+ *      rotated as the keys are and rounded to bf16
+ *   cos_sin    [max_positions, rot_dim] fp32: for each position rot_dim / 2
+ *      cosines, then as many sines.  rot_dim is a multiple of 16 up to d_qk;
+ *      0: no rotation, cos_sin not read.  Columns 0 .. rot_dim - 1 are rotated:
+ *      pairs (i, i + rot_dim / 2), or (2 i, 2 i + 1) if interleaved:
+ *      (a, b) -> (a cos - b sin, b cos + a sin), in fp32
+ *
+ * The scale of a page and head becomes the smallest power of two (2^-63 at
+ * least) with max|x| <= 448 * scale over the tokens it holds, as far as those
+ * that were there before had not made it larger; where it grows, the older
+ * codes are rounded again under the new scale.  A page whose first token is
+ * among the new ones ignores the scale that was there.  Values that are not
+ * finite are stored as NaN and do not count for the scale.  Bytes behind a
+ * sequence's last token are left as they were.
+ *
+ * A page that receives tokens may belong to one sequence of the call only
+ * (full pages may be shared).  One launch; no workspace.  A sequence with
+ * positions beyond max_positions (rot_dim > 0) or beyond its row of the block
+ * table is left out and reported as above.
+ */
+int fa_kv_append(const fa_kv_cache* cache, const void* q, const void* k, const void* v, int64_t q_stride,
+                 int64_t k_stride, int64_t v_stride, void* q_out, const int* cu_seqlens, int batch, int64_t total,
+                 int heads_q, const float* cos_sin, int max_positions, int rot_dim, int interleaved,
+                 fa_stream_t stream);
+
+/*
+ * Attention of new tokens over a paged cache that holds their keys and values
+ * already (fa_kv_append).
+ *
+ *   q [total_q, heads_q, d_qk] bf16, o [total_q, heads_q, d_v] bf16 (rows of
+ *   the sequences are written, others left), lse [heads_q, total_q] fp32 or
+ *   NULL, cu_seqlens_q [batch + 1] int32: as fa_fwd_varlen's.  causal is
+ *   bottom-right inside each sequence: new token i of n sees token j iff
+ *   j <= i + seqlens_k[b] - n.  A row without a key gets O = 0, lse = -inf.
+ *   max_seqlen_q: an upper limit of the new tokens of a sequence (a longer one
+ *   is left out: site 511).  total_k: an upper limit of the sum of seqlens_k;
+ *   it bounds the workspace where max_seqlen_q * heads_q / heads_kv > 64 and
+ *   is not used below (a larger sum: nothing of the longer sequences is
+ *   computed, site 513).
+ *
+ * Sequences of up to 64 rows (new tokens x query heads a key/value head) are
+ * computed straight from the pages, their keys split over the whole GPU;
+ * longer ones are unpacked to bf16 (exactly) in the workspace and run through
+ * fa_fwd_varlen's kernel.  Both kinds may be in one batch.
+ *
+ * A token whose keys or values hold a NaN (or whose scale is NaN) makes NaN
+ * of the rows that see it, and of no others.
+ *
+ * workspace: device memory of fa_fwd_paged_workspace_size(...) bytes, 16-byte
+ * aligned; it needs no initialisation, and calls that may overlap (captured
+ * graphs that run at the same time among them) need different ones.
+ * Deterministic: no atomics on results.
+ */
+size_t fa_fwd_paged_workspace_size(int batch, int heads_q, int heads_kv, int64_t total_q, int max_seqlen_q,
+                                   int64_t total_k, int d_qk, int d_v);
+
+int fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse, const int* cu_seqlens_q, int batch,
+                 int64_t total_q, int max_seqlen_q, int64_t total_k, int heads_q, int causal, float scale,
+                 void* workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/*
  * Host-only copy of the planning kernel's task list (no CUDA call): the same
  * records in the same order, for host cu_seqlens arrays.  l2_bytes is the L2
  * budget of the causal sections (0 selects 64 MiB; the kernel uses half the
