@@ -22,6 +22,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 from . import _build
 
@@ -169,10 +170,10 @@ def load_library(path: str | None = None):
                                                              ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)]
     lib.fa_varlen_plan_host.restype = _I
     i64 = ctypes.c_int64
-    lib.fa_kv_append.argtypes = [ctypes.POINTER(FaKvCache), _P, _P, _P, i64, i64, i64, _P, _P, _I, i64, _I, _P, _I, _I,
+    lib.fa_kv_append.argtypes = [_P, _P, _P, _P, i64, i64, i64, _P, _P, _I, i64, _I, _P, _I, _I,
                                  _I, _P]
     lib.fa_kv_append.restype = _I
-    lib.fa_fwd_paged.argtypes = [_P, ctypes.POINTER(FaKvCache), _P, _P, _P, _I, i64, _I, i64, _I, _I, ctypes.c_float, _P,
+    lib.fa_fwd_paged.argtypes = [_P, _P, _P, _P, _P, _I, i64, _I, i64, _I, _I, ctypes.c_float, _P,
                                  ctypes.c_size_t, _P]
     lib.fa_fwd_paged.restype = _I
     lib.fa_fwd_paged_workspace_size.argtypes = [_I, _I, _I, i64, _I, i64, _I, _I]
@@ -621,59 +622,98 @@ def _bad(what: str):
     raise FaError(FA_ERR_INVALID_ARG, what)
 
 
-def _paged_cache(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, cu_seqlens, device) -> FaKvCache:
-    """The cache's tensors, checked, as an ``FaKvCache``."""
+# an fa_kv_cache as bytes: what FaKvCache lays out, built in one step
+_KV_CACHE = struct.Struct("6P7q6i")
+
+
+def _paged_cache(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, cu_seqlens, index):
+    """(fa_kv_cache as bytes, heads_kv, d_qk, d_v, batch, capacity) of the cache's tensors, which are checked."""
     import torch
 
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype != torch.float8_e4m3fn or t.dim() != 4 or t.device != device or (t.numel() and t.stride(3) != 1):
-            _bad(f"{name} must be a 4-D float8_e4m3fn tensor [num_pages, heads_kv, page_size, d] on {device}, its last "
-                 "dimension contiguous")
-    pages, heads, page, d_qk = k_cache.shape
+    f8, e8, i32 = torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.int32
+    kd, vd, td = k_cache.shape, v_cache.shape, block_table.shape
+    if not (len(kd) == 4 and kd[:3] == vd[:3] and k_cache.dtype is f8 and v_cache.dtype is f8 and
+            k_scale.dtype is e8 and v_scale.dtype is e8 and k_scale.shape == kd[:2] and v_scale.shape == kd[:2] and
+            k_scale.is_contiguous() and v_scale.is_contiguous() and len(td) == 2 and block_table.dtype is i32 and
+            seqlens_k.dtype is i32 and cu_seqlens.dtype is i32 and seqlens_k.shape == td[:1] and
+            cu_seqlens.dim() == 1 and cu_seqlens.shape[0] == td[0] + 1 and seqlens_k.is_contiguous() and
+            cu_seqlens.is_contiguous() and k_cache.get_device() == index and v_cache.get_device() == index and
+            k_scale.get_device() == index and v_scale.get_device() == index and block_table.get_device() == index and
+            seqlens_k.get_device() == index and cu_seqlens.get_device() == index):
+        _paged_cache_error(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, cu_seqlens, index)
+    ks, vs, ts = k_cache.stride(), v_cache.stride(), block_table.stride()
+    if (ks[3] != 1 and kd[3] > 1) or (vs[3] != 1 and vd[3] > 1) or (ts[1] != 1 and td[1] > 1):
+        _bad("the codes of a token and the entries of a row of block_table must be contiguous")
+    pages, heads, page, d_qk = kd
+    batch, width = td
+    packed = _KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                            block_table.data_ptr(), seqlens_k.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
+                            ts[0] if batch > 1 else width, pages, page, heads, d_qk, vd[3], width)
+    return packed, heads, d_qk, vd[3], batch, width * page
+
+
+def _paged_cache_error(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, cu_seqlens, index):
+    """Says which tensor is wrong."""
+    import torch
+
+    for name, t, dtype, dim in (("k_cache", k_cache, torch.float8_e4m3fn, 4), ("v_cache", v_cache, torch.float8_e4m3fn, 4),
+                                ("k_scale", k_scale, torch.float8_e8m0fnu, 2), ("v_scale", v_scale, torch.float8_e8m0fnu, 2),
+                                ("block_table", block_table, torch.int32, 2), ("seqlens_k", seqlens_k, torch.int32, 1),
+                                ("cu_seqlens", cu_seqlens, torch.int32, 1)):
+        if t.dtype != dtype or t.dim() != dim or t.get_device() != index:
+            _bad(f"{name} must be a {dim}-D {str(dtype).removeprefix('torch.')} tensor on cuda:{index}")
+        if dim < 4 and name != "block_table" and not t.is_contiguous():
+            _bad(f"{name} must be contiguous")
     if v_cache.shape[:3] != k_cache.shape[:3]:
-        _bad("k_cache and v_cache must have the same pages, heads and page size")
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t.dtype != torch.float8_e8m0fnu or t.shape != (pages, heads) or t.device != device or not t.is_contiguous():
-            _bad(f"{name} must be a contiguous float8_e8m0fnu tensor [num_pages, heads_kv] on {device}")
-    for name, t, dim in (("block_table", block_table, 2), ("seqlens_k", seqlens_k, 1), ("cu_seqlens", cu_seqlens, 1)):
-        if t.dtype != torch.int32 or t.dim() != dim or t.device != device or (t.numel() and t.stride(-1) != 1):
-            _bad(f"{name} must be a {dim}-D int32 tensor on {device}, its last dimension contiguous")
-    batch, width = block_table.shape
-    if seqlens_k.shape[0] != batch or cu_seqlens.shape[0] != batch + 1:
-        _bad("block_table, seqlens_k and cu_seqlens must hold batch rows, batch lengths and batch + 1 offsets")
-    return FaKvCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                     block_table.data_ptr(), seqlens_k.data_ptr(), k_cache.stride()[:3], v_cache.stride()[:3],
-                     block_table.stride(0) if batch > 1 else width, pages, page, heads, d_qk, v_cache.shape[3], width)
+        _bad("k_cache and v_cache must be [num_pages, heads_kv, page_size, d]")
+    if k_scale.shape != k_cache.shape[:2] or v_scale.shape != k_cache.shape[:2]:
+        _bad("k_scale and v_scale must be [num_pages, heads_kv]")
+    _bad("block_table, seqlens_k and cu_seqlens must hold batch rows, batch lengths and batch + 1 offsets")
 
 
 class _OnDevice:
-    """Makes `device` the current one for a call when it is not."""
+    """Makes device `index` the current one for a call when it is not, and finds the call's stream."""
 
-    def __init__(self, device):
-        self.device, self.guard = device, None
-
-    def __enter__(self):
+    def __init__(self, index, stream):
         import torch
 
-        if torch.cuda.current_device() != self.device.index:
-            self.guard = torch.cuda.device(self.device)
+        self.guard = None
+        if torch.cuda.current_device() != index:
+            self.guard = torch.cuda.device(index)
             self.guard.__enter__()
+        self.index = index
+        self.current = torch._C._cuda_getCurrentRawStream(index)
+        if stream is None:
+            self.ptr = self.current
+        else:
+            self.ptr = (stream.cuda_stream if hasattr(stream, "cuda_stream") else stream) or 0
+
+    def empty(self, shape, dtype):
+        """torch.empty whose memory is not reused before the work on the call's stream has run."""
+        import torch
+
+        if self.ptr == self.current:
+            return torch.empty(shape, dtype=dtype, device=self.index)
+        with torch.cuda.stream(torch.cuda.ExternalStream(self.ptr, device=self.index)):
+            return torch.empty(shape, dtype=dtype, device=self.index)
+
+    def __enter__(self):
+        return self
 
     def __exit__(self, *exc):
         if self.guard is not None:
             self.guard.__exit__(*exc)
 
 
-def _token_stride(name, t, heads, d, device):
+def _token_stride(name, t, total, heads, d, index):
     """Elements from token to token of a bf16 tensor [total, heads, d] whose heads lie side by side."""
     import torch
 
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.device != device:
-        _bad(f"{name} must be a 3-D bf16 tensor on {device}")
-    if t.shape[1] != heads or t.shape[2] != d:
-        _bad(f"{name} must be [total, {heads}, {d}]")
-    if t.numel() == 0 or (t.stride(2) == 1 and (heads == 1 or t.stride(1) == d)):
-        return t.stride(0) if t.shape[0] > 1 else heads * d
+    if t.dtype is not torch.bfloat16 or t.shape != (total, heads, d) or t.get_device() != index:
+        _bad(f"{name} must be a bf16 tensor [{total}, {heads}, {d}] on cuda:{index}")
+    st = t.stride()
+    if total == 0 or (st[2] == 1 and (heads == 1 or st[1] == d)):
+        return st[0] if total > 1 else heads * d
     _bad(f"{name}: a token's heads must be contiguous")
 
 
@@ -691,56 +731,41 @@ def kv_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, 
     """
     import torch
 
-    device = k.device
-    if device.type != "cuda":
+    index = k.get_device()
+    if index < 0:
         _bad("k must be a CUDA tensor")
-    cache = _paged_cache(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, cu_seqlens, device)
+    cache, heads, d_qk, d_v, batch, _ = _paged_cache(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k,
+                                                     cu_seqlens, index)
     total = k.shape[0]
-    ks = _token_stride("k", k, cache.heads_kv, cache.d_qk, device)
-    vs = _token_stride("v", v, cache.heads_kv, cache.d_v, device)
-    if v.shape[0] != total:
-        _bad("k and v must hold the same tokens")
+    ks = _token_stride("k", k, total, heads, d_qk, index)
+    vs = _token_stride("v", v, total, heads, d_v, index)
     rot = positions = 0
+    cs = qp = qo = None
     if cos_sin is not None:
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.device != device or not cos_sin.is_contiguous():
-            _bad(f"cos_sin must be a contiguous 2-D fp32 tensor on {device}")
+        if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or cos_sin.get_device() != index or \
+                not cos_sin.is_contiguous():
+            _bad(f"cos_sin must be a contiguous 2-D fp32 tensor on cuda:{index}")
         positions, rot = cos_sin.shape
-    with _OnDevice(device):
-        if stream is None:
-            stream = torch.cuda.current_stream(device)
-        sptr = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+        cs = cos_sin.data_ptr()
+    with _OnDevice(index, stream) as on:
         heads_q = qs = 0
         if q is not None:
-            heads_q = q.shape[1] if q.dim() == 3 else 0
-            qs = _token_stride("q", q, heads_q, cache.d_qk, device)
-            if q.shape[0] != total:
-                _bad("q must hold the same tokens as k")
+            shape = q.shape
+            heads_q = shape[1] if len(shape) == 3 else 0
+            qs = _token_stride("q", q, total, heads_q, d_qk, index)
             if q_out is None:
-                q_out = _empty((total, heads_q, cache.d_qk), torch.bfloat16, device, stream)
-            elif q_out.dtype != torch.bfloat16 or q_out.shape != q.shape or q_out.device != device or \
+                q_out = on.empty(shape, torch.bfloat16)
+            elif q_out.dtype is not torch.bfloat16 or q_out.shape != shape or q_out.get_device() != index or \
                     not q_out.is_contiguous():
-                _bad(f"q_out must be a contiguous bf16 tensor of q's shape on {device}")
+                _bad(f"q_out must be a contiguous bf16 tensor of q's shape on cuda:{index}")
+            qp, qo = q.data_ptr(), q_out.data_ptr()
         elif q_out is not None:
             _bad("q_out without q")
-        rc = fa_kv_append(cache, q.data_ptr() if q is not None else None, k.data_ptr(), v.data_ptr(), qs, ks, vs,
-                          q_out.data_ptr() if q is not None else None, cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1,
-                          total, heads_q, cos_sin.data_ptr() if cos_sin is not None else None, positions, rot,
-                          interleaved, sptr)
+        rc = load_library().fa_kv_append(cache, qp, k.data_ptr(), v.data_ptr(), qs, ks, vs, qo, cu_seqlens.data_ptr(),
+                                         batch, total, heads_q, cs, positions, rot, interleaved, on.ptr)
     if rc != FA_OK:
         raise FaError(rc, "fa_kv_append")
     return q_out
-
-
-def _empty(shape, dtype, device, stream):
-    """torch.empty whose memory is not reused before the work on `stream` that it is for has run."""
-    import torch
-
-    current = torch.cuda.current_stream(device)
-    ptr = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
-    if (ptr or 0) == current.cuda_stream:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(ptr or 0, device=device)):
-        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def attention_forward_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, cu_seqlens_q,
@@ -757,40 +782,39 @@ def attention_forward_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, 
     """
     import torch
 
-    device = q.device
-    if device.type != "cuda" or q.dtype != torch.bfloat16 or q.dim() != 3 or not q.is_contiguous():
+    index = q.get_device()
+    qd = q.shape
+    if index < 0 or q.dtype is not torch.bfloat16 or len(qd) != 3 or not q.is_contiguous():
         _bad("q must be a contiguous 3-D bf16 CUDA tensor")
-    cache = _paged_cache(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, cu_seqlens_q, device)
-    total_q, heads_q, d_qk = q.shape
-    if d_qk != cache.d_qk:
-        _bad(f"q must be [total_q, heads_q, {cache.d_qk}]")
-    batch = cu_seqlens_q.shape[0] - 1
+    cache, heads, d_qk, d_v, batch, capacity = _paged_cache(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k,
+                                                            cu_seqlens_q, index)
+    total_q, heads_q, d = qd
+    if d != d_qk:
+        _bad(f"q must be [total_q, heads_q, {d_qk}]")
     if total_k is None:
-        total_k = batch * cache.max_pages * cache.page_size
-    with _OnDevice(device):
-        if stream is None:
-            stream = torch.cuda.current_stream(device)
-        sptr = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+        total_k = batch * capacity
+    with _OnDevice(index, stream) as on:
         if out is None:
-            out = _empty((total_q, heads_q, cache.d_v), torch.bfloat16, device, stream)
-        elif out.dtype != torch.bfloat16 or out.shape != (total_q, heads_q, cache.d_v) or out.device != device or \
+            out = on.empty((total_q, heads_q, d_v), torch.bfloat16)
+        elif out.dtype is not torch.bfloat16 or out.shape != (total_q, heads_q, d_v) or out.get_device() != index or \
                 not out.is_contiguous():
-            _bad(f"out must be a contiguous bf16 tensor [total_q, heads_q, {cache.d_v}] on {device}")
-        if lse is None and return_lse:
-            lse = _empty((heads_q, total_q), torch.float32, device, stream)
-        elif lse is not None and (lse.dtype != torch.float32 or lse.shape != (heads_q, total_q) or
-                                  lse.device != device or not lse.is_contiguous()):
-            _bad(f"lse must be a contiguous fp32 tensor [heads_q, total_q] on {device}")
+            _bad(f"out must be a contiguous bf16 tensor [total_q, heads_q, {d_v}] on cuda:{index}")
+        if lse is None:
+            if return_lse:
+                lse = on.empty((heads_q, total_q), torch.float32)
+        elif lse.dtype is not torch.float32 or lse.shape != (heads_q, total_q) or lse.get_device() != index or \
+                not lse.is_contiguous():
+            _bad(f"lse must be a contiguous fp32 tensor [heads_q, total_q] on cuda:{index}")
+        lib = load_library()
         if workspace is None:
-            need = fa_fwd_paged_workspace_size(batch, heads_q, cache.heads_kv, total_q, max_seqlen_q, total_k, d_qk,
-                                               cache.d_v)
-            workspace = _empty((max(need, 16),), torch.uint8, device, stream)
-        elif workspace.device != device or not workspace.is_contiguous():
-            _bad(f"workspace must be a contiguous tensor on {device}")
-        rc = fa_fwd_paged(q.data_ptr(), cache, out.data_ptr(), lse.data_ptr() if lse is not None else None,
-                          cu_seqlens_q.data_ptr(), batch, total_q, max_seqlen_q, total_k, heads_q, causal,
-                          0.0 if scale is None else scale, workspace.data_ptr(),
-                          workspace.numel() * workspace.element_size(), sptr)
+            need = lib.fa_fwd_paged_workspace_size(batch, heads_q, heads, total_q, max_seqlen_q, total_k, d_qk, d_v)
+            workspace = on.empty((need or 16,), torch.uint8)
+        elif workspace.get_device() != index or not workspace.is_contiguous():
+            _bad(f"workspace must be a contiguous tensor on cuda:{index}")
+        rc = lib.fa_fwd_paged(q.data_ptr(), cache, out.data_ptr(), lse.data_ptr() if lse is not None else None,
+                              cu_seqlens_q.data_ptr(), batch, total_q, max_seqlen_q, total_k, heads_q,
+                              1 if causal else 0, 0.0 if scale is None else scale, workspace.data_ptr(),
+                              workspace.numel() * workspace.element_size(), on.ptr)
     if rc != FA_OK:
         raise FaError(rc, "fa_fwd_paged")
     return (out, lse) if return_lse else out
