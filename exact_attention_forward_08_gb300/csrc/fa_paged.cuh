@@ -13,7 +13,6 @@ namespace fa {
 constexpr unsigned int kSitePagedSeq = 511;   // a sequence's offsets, length or position out of range (index: sequence)
 constexpr unsigned int kSitePagedPage = 512;  // a block-table entry out of range (index: sequence)
 constexpr unsigned int kSitePagedTotal = 513; // the lengths sum to more than total_k (index: 0)
-constexpr unsigned int kSitePagedWait = 520;  // a bounded wait of the paged attention kernel expired
 
 // the smallest scale that the append writes: 2^-63
 constexpr int kMinScale = 64;

@@ -10,6 +10,7 @@ namespace fa {
 
 struct PagedParams;
 
+constexpr int kPagedMaxTeams = 8;     // most teams of a block
 constexpr int kPagedMaxBlocks = 160;  // most blocks of the attention kernel (one an SM)
 // Sequences with at most this many rows (new tokens x query heads a key head)
 // are read straight from the pages; longer ones are unpacked first.

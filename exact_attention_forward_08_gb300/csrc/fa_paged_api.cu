@@ -1,6 +1,5 @@
 // C ABI of the paged 8-bit key/value cache: argument checks, tensor maps,
 // workspace layout and launches.  See include/fa.h for the contract.
-#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -23,10 +22,10 @@ bool dims_supported(int d_qk, int d_v) {
 
 // strides in bytes {page, head, token} of a cache of rows of d codes
 bool strides_ok(const int64_t* s, int pages, int heads, int d) {
-  const int64_t most = int64_t(1) << 40;  // the tensor map's limit
+  const int64_t most = int64_t(1) << 40;
   for (int i = 0; i < 3; ++i)
     if (s[i] < 0 || s[i] % 16 != 0 || s[i] >= most) return false;
-  if (s[2] < d) return false;
+  if (s[2] < d || s[2] >= int64_t(1) << 24) return false;  // offsets inside a page are counted in 32 bits
   return (heads == 1 || s[1] >= d) && (pages == 1 || s[0] >= d);
 }
 
@@ -59,18 +58,6 @@ bool cache_on_device(const fa_kv_cache* c, int dev) {
 
 int page_shift(int page_size) { return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7; }
 
-// codes viewed as (d, token, head, page); one box is the tokens of a page that fit one tile, of one head
-int encode_pages(CUtensorMap* m, const void* base, const int64_t* s, const fa_kv_cache* c, int d, int columns) {
-  const uint64_t dims[4] = {static_cast<uint64_t>(d), static_cast<uint64_t>(c->page_size),
-                            static_cast<uint64_t>(c->heads_kv), static_cast<uint64_t>(c->num_pages)};
-  // the stride of a dimension of extent 1 is never used, but has to be one
-  const uint64_t token = s[2], head = c->heads_kv > 1 ? s[1] : token, page = c->num_pages > 1 ? s[0] : token;
-  const uint64_t strides[3] = {token, head, page};
-  const int rows = c->page_size < fa::kTileTokens ? c->page_size : fa::kTileTokens;
-  const uint32_t box[4] = {static_cast<uint32_t>(columns), static_cast<uint32_t>(rows), 1, 1};
-  return fa::host_encode_bytes(m, base, 4, dims, strides, box, columns);
-}
-
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 // The workspace: parts, references and sums, and joins of the cut units, then
@@ -88,8 +75,7 @@ Workspace workspace_of(int batch, int heads_q, int heads_kv, int64_t total_q, in
   Workspace w;
   std::memset(&w, 0, sizeof(w));
   const int tr = team_rows(rows);
-  const size_t teams = tr <= 16 ? 8 : tr == 32 ? 4 : 2;
-  const size_t pieces = static_cast<size_t>(fa::kPagedMaxBlocks) * teams;
+  const size_t pieces = static_cast<size_t>(fa::kPagedMaxBlocks) * fa::kPagedMaxTeams;
   size_t at = up256(2 * pieces * tr * d_v * sizeof(float));
   w.part_ml = at;
   at += up256(2 * pieces * tr * sizeof(float2));
@@ -241,9 +227,15 @@ int fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse, c
 
   fa::PagedParams p;
   std::memset(&p, 0, sizeof(p));
-  if (encode_pages(&p.tm_k, c.k, c.k_stride, cache, c.d_qk, c.d_qk == 128 ? 128 : 64) != FA_OK ||
-      encode_pages(&p.tm_v, c.v, c.v_stride, cache, c.d_v, c.d_v) != FA_OK)
-    return FA_ERR_CUDA;
+  const int most = rows < fa::kPagedRowLimit ? static_cast<int>(rows) : fa::kPagedRowLimit;
+  p.k = static_cast<const uint8_t*>(c.k);
+  p.v = static_cast<const uint8_t*>(c.v);
+  p.k_page = c.k_stride[0];
+  p.k_head = c.k_stride[1];
+  p.k_token = static_cast<uint32_t>(c.k_stride[2]);
+  p.v_page = c.v_stride[0];
+  p.v_head = c.v_stride[1];
+  p.v_token = static_cast<uint32_t>(c.v_stride[2]);
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
@@ -258,7 +250,6 @@ int fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse, c
   p.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
   p.joins = reinterpret_cast<fa::PagedJoin*>(ws + w.joins);
   p.total_q = total_q;
-  p.timeout_ns = 1000000000ull;
   p.batch = batch;
   p.heads_q = heads_q;
   p.heads_kv = c.heads_kv;
@@ -271,7 +262,6 @@ int fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse, c
   p.row_limit = fa::kPagedRowLimit;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   const int grid = host.sms < fa::kPagedMaxBlocks ? host.sms : fa::kPagedMaxBlocks;
-  const int most = rows < fa::kPagedRowLimit ? static_cast<int>(rows) : fa::kPagedRowLimit;
   if (c.d_qk == 64) return fa::paged_launch_d64(p, c.d_v, most, grid, stream);
   if (c.d_qk == 128) return fa::paged_launch_d128(p, c.d_v, most, grid, stream);
   return fa::paged_launch_d192(p, c.d_v, most, grid, stream);

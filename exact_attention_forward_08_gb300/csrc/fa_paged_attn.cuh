@@ -13,18 +13,19 @@
 // P is rounded to f16 scaled by 2^7, 11 bits where bf16 would keep 8.
 // Scores, maxima, sums and O stay in fp32.
 //
-// Work: a tile is 32 tokens of one key/value head; the tiles of all sequences,
-// heads and row groups form one line that is cut into equal pieces, one for
-// each team of warps (a team is 1 to 4 warps with 8 or 16 rows each that read
-// the same tiles).  A team streams its piece through its own ring of stages
-// (TMA, one mbarrier a stage), independently of the others.  A (sequence, head)
-// that lies in one piece is written out at once, one that is cut leaves
-// unnormalised parts that paged_merge_kernel joins.
+// Work: a tile is 32 or 64 tokens of one key/value head; the tiles of all
+// sequences and heads form one line that is cut into equal pieces, one for
+// each team (1 to 4 warps of 8 or 16 rows each that read the same tiles).  A
+// team streams its piece through its own ring of slots, K and V tiles by turns,
+// filled by asynchronous 16-byte copies kSlots - 1 slots ahead, independently
+// of the other teams.  A (sequence, head) that lies in one piece is written out
+// at once, one that is cut leaves unnormalised parts that paged_merge_kernel
+// joins.
 #pragma once
-#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "fa_paged.cuh"
 #include "ptx.cuh"
@@ -32,10 +33,13 @@
 namespace fa {
 
 struct PagedParams {
-  CUtensorMap tm_k, tm_v;  // (d, token, head, page) of codes
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
   float* lse;
+  const uint8_t* k;  // codes
+  const uint8_t* v;
+  int64_t k_page, k_head, v_page, v_head;  // bytes between pages and heads
+  uint32_t k_token, v_token;               // and tokens
   const uint8_t* k_scale;
   const uint8_t* v_scale;
   const int* table;
@@ -47,36 +51,37 @@ struct PagedParams {
   float2* part_ml;  // [2 * pieces][rows] {reference, sum}
   struct PagedJoin* joins;  // [pieces]
   int64_t total_q;
-  unsigned long long timeout_ns;
   int batch, heads_q, heads_kv, ratio, num_pages, max_pages, page_shift, causal;
   int max_n;      // longest sequence of new tokens allowed
   int row_limit;  // sequences with more rows (new tokens x ratio) are not this kernel's
   float scale_log2;
 };
 
-// A cut (sequence, head, row group) that starts in a piece and ends in piece `last`.
+// A cut (sequence, head) that starts in a piece and ends in piece `last`.
 struct PagedJoin {
   int last;  // -1: none
-  int cu0, head, row0, rows, pad;
+  int cu0, head, rows;
 };
 
-constexpr int kPagedWarps = 8;
-constexpr int kPagedThreads = kPagedWarps * 32;
-constexpr int kTileTokens = 32;
-constexpr int kMinTiles = 2;          // a piece is not cut smaller
+constexpr int kMinTokens = 64;        // a piece is not cut smaller
 constexpr float kPShift = 7.f;        // P is scaled by 2^7: f16 then holds weights down to 2^-31
 constexpr float kRefLag = 8.f;        // the reference follows the maximum when it lags by more (log2 units)
 
+// NT groups of 8 rows a warp, TW warps a team.  64 tokens a tile halve what a
+// tile costs beside its products (B8 x 32768, 32/8 heads of 128: 93 us against
+// 97 with 32; 16 heads of 64 in pages of 16: 123 against 150); more rows or
+// wider keys leave registers for 32.  Two warps a scheduler: with three, 168
+// registers a thread spill (116 us for the first of these).
 template <int DQK, int DV, int NT, int TW>
 struct PagedShape {
   static constexpr int kRows = 8 * NT * TW;  // rows of a team
-  static constexpr int kTeams = kPagedWarps / TW;
-  static constexpr int kTileK = kTileTokens * DQK, kTileV = kTileTokens * DV;
-  static constexpr int kTileBytes = kTileK + kTileV;
-  static constexpr int kSmemTiles = (200 * 1024) / kTileBytes / kPagedWarps * kPagedWarps;
-  static constexpr int kStages = kSmemTiles / kTeams;
-  static constexpr int kLag = TW > 1 ? 1 : 0;  // tiles between reading a stage and refilling it
-  static constexpr int kBytes = kSmemTiles * kTileBytes + 1024;
+  static constexpr int kTile = NT == 1 && DQK <= 128 ? 64 : 32;  // tokens
+  static constexpr int kWarps = 8, kThreads = 32 * kWarps;
+  static constexpr int kTeams = kWarps / TW;
+  static constexpr int kSlotBytes = kTile * (DQK > DV ? DQK : DV);
+  static constexpr int kSlots = 206 * 1024 / kSlotBytes / kTeams;  // of a team's ring
+  static constexpr int kBytes = kTeams * kSlots * kSlotBytes + 128;
+  static_assert(kSlots >= 3, "a tile in use and one under way");
 };
 
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -85,6 +90,14 @@ __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// the same from a sum of 0
+__device__ __forceinline__ void mma_f16_zero(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
@@ -110,31 +123,44 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   return v;
 }
 
-// shared-memory offset of 16-byte chunk `chunk` of row `row`: the layouts that
-// TMA writes with 128-byte rows (128-byte swizzle) and 64-byte rows (64-byte)
-__device__ __forceinline__ uint32_t sw128(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
-__device__ __forceinline__ uint32_t sw64(int row, int chunk) { return row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4); }
-
-// K chunk (16 codes) number `step` (0 .. DQK/64 - 1) of lane column c: 128-byte rows hold chunk 2 c + step,
-// 64-byte sub-tiles chunk c of sub-tile `step`.  The same rule gives the query columns below.
-template <int DQK>
-__device__ __forceinline__ uint32_t k_offset(int row, int c, int step) {
-  if constexpr (DQK == 128) return sw128(row, 2 * c + step);
-  return step * (kTileTokens * 64) + sw64(row, c);
+// Where a tile's 16-byte chunk `chunk` of token `row` lies in its slot, so that
+// the reads below meet no bank twice.  K is read as chunks of eight tokens
+// (two a quarter warp), V as chunks of the even or the odd of eight tokens.
+template <int D>
+__device__ __forceinline__ uint32_t k_place(int row, int chunk) {
+  if constexpr (D == 128) return row * 128 + ((chunk ^ (row & 7)) << 4);
+  return row * D + (chunk << 4);  // rows of 64 and 192 bytes: neighbours fall on different halves of the banks
 }
+template <int D>
+__device__ __forceinline__ uint32_t v_place(int row, int chunk) {
+  if constexpr (D == 128) return row * 128 + ((chunk ^ (row & 7)) << 4);
+  const int at = (row & ~7) | ((row >> 1) & 3) | ((row & 1) << 2);  // even tokens first
+  return at * 64 + ((chunk ^ (at & 2)) << 4);
+}
+// K chunk number `step` of lane column c: all chunks of a row once, and query columns by the same rule
 template <int DQK>
-__device__ __forceinline__ int k_column(int c, int step) {
-  return DQK == 128 ? 16 * (2 * c + step) : 64 * step + 16 * c;
+__device__ __forceinline__ int k_chunk(int c, int step) {
+  return DQK == 128 ? 2 * c + step : 4 * step + c;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// waits until at most N of this thread's groups of copies are under way
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // One sequence as the kernel sees it.
 struct PagedSeq {
   int cu0, n, len;
-  int rows, groups, tiles;  // new tokens x ratio, row groups, tiles of 32 tokens
+  int rows, tiles;  // new tokens x ratio (0: not this kernel's), tiles
   bool bad;
 };
 
-template <int ROWS>
+template <int TILE>
 __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
   PagedSeq s;
   s.cu0 = p.cu[b];
@@ -145,75 +171,62 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
           s.len > (static_cast<int64_t>(p.max_pages) << p.page_shift);
   const int64_t rows = s.bad ? 0 : static_cast<int64_t>(s.n) * p.ratio;
   s.rows = rows > p.row_limit ? 0 : static_cast<int>(rows);
-  s.groups = (s.rows + ROWS - 1) / ROWS;
-  s.tiles = s.len > 0 ? (s.len + kTileTokens - 1) / kTileTokens : 1;  // without a key: one tile that is masked
+  s.tiles = s.len > 0 ? (s.len + TILE - 1) / TILE : 1;  // without a key: one tile that is masked
   return s;
 }
 
 // A place on the line of tiles.
 struct PagedCursor {
   PagedSeq s;
-  int b, head, group, tile;
+  int b, head, tile;
 };
 
-template <int ROWS>
-__device__ __forceinline__ void paged_next_unit(const PagedParams& p, PagedCursor& c) {
+// To the next tile (the caller knows that there is one).
+template <int TILE>
+__device__ __forceinline__ void paged_next(const PagedParams& p, PagedCursor& c) {
+  if (++c.tile < c.s.tiles) return;
   c.tile = 0;
-  if (++c.group < c.s.groups) return;
-  c.group = 0;
   if (++c.head < p.heads_kv) return;
   c.head = 0;
   do {
     if (c.b + 1 >= p.batch) return;
-    c.s = paged_seq<ROWS>(p, ++c.b);
-  } while (c.s.groups == 0);
+    c.s = paged_seq<TILE>(p, ++c.b);
+  } while (c.s.rows == 0);
 }
 
-template <int DQK, int DV, int NT, int TW>
-__global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __grid_constant__ PagedParams p) {
+// G16: pages of 16 tokens, each with its own scale; else a scale holds for 32 tokens at least.
+template <int DQK, int DV, int NT, int TW, bool G16>
+__global__ void __launch_bounds__(PagedShape<DQK, DV, NT, TW>::kThreads, 1)
+    paged_attn_kernel(const __grid_constant__ PagedParams p) {
   using Shape = PagedShape<DQK, DV, NT, TW>;
+  constexpr int kTile = Shape::kTile;
   constexpr int kSteps = DQK / 64;       // 64-column groups of K
   constexpr int kVWords = DV / 32;       // 32-bit words of V codes a lane reads per token
   constexpr int kVTiles = DV / 16;       // m16 tiles of O^T
-  constexpr int kTeams = Shape::kTeams, kStages = Shape::kStages, kRows = Shape::kRows;
+  constexpr int kMT = kTile / 16;        // m16 tiles of S^T
+  constexpr int kTeams = Shape::kTeams, kSlots = Shape::kSlots, kRows = Shape::kRows, kThreads = Shape::kThreads;
+  constexpr int kWarps = Shape::kWarps;
 
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kTeams * kStages];
-  __shared__ float4 meta[kTeams * kStages];  // {K scale of tokens 0-15, 16-31, V scale of the same}
-  __shared__ long long scan[kPagedThreads];
-  __shared__ long long warp_sum[kPagedWarps];
-  __shared__ int abort_flag;
+  __shared__ __align__(16) float slot_scale[kTeams * kSlots][4];  // of 16 tokens each
+  __shared__ PagedCursor begin_at[kTeams];
+  __shared__ long long scan[kThreads];
+  __shared__ long long warp_sum[kWarps];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int team = warp / TW, sub = warp % TW;
-  const int g = lane >> 2, c = lane & 3;
-  const uint32_t ring = ((smem_u32(smem_raw) + 1023u) & ~1023u) + team * kStages * Shape::kTileBytes;
-  const uint32_t full0 = smem_u32(&bars[team * 2 * kStages]), empty0 = full0 + 8 * kStages;
-  WaitCtx wc{&abort_flag, p.status, p.timeout_ns};
+  const uint32_t smem0 = (smem_u32(smem_raw) + 127u) & ~127u;
 
   // let the merge kernel's blocks take their places early: they wait for this grid's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  if (tid == 0) {
-    abort_flag = 0;
-    for (int i = 0; i < kTeams; ++i)
-      for (int s = 0; s < kStages; ++s) {
-        mbar_init(smem_u32(&bars[i * 2 * kStages + s]), 1);
-        mbar_init(smem_u32(&bars[i * 2 * kStages + kStages + s]), TW);
-      }
-    fence_mbar_init();
-    tma_prefetch_desc(&p.tm_k);
-    tma_prefetch_desc(&p.tm_v);
-  }
-
   // ---- the line of tiles: its length, and where this team's piece begins ----
-  auto scan_block = [&](int base) -> long long {  // inclusive scan of 256 sequences' tiles into scan[]
+  auto scan_block = [&](int base) -> long long {  // inclusive scan of kThreads sequences' tiles into scan[]
     const int b = base + tid;
     long long v = 0;
     if (b < p.batch) {
-      const PagedSeq s = paged_seq<kRows>(p, b);
+      const PagedSeq s = paged_seq<kTile>(p, b);
       if (s.bad && blockIdx.x == 0) paged_error(p.status, kSitePagedSeq, b);
-      v = static_cast<long long>(s.groups) * s.tiles * p.heads_kv;
+      v = s.rows > 0 ? static_cast<long long>(s.tiles) * p.heads_kv : 0;
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -226,137 +239,179 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
     for (int w = 0; w < warp; ++w) before += warp_sum[w];
     scan[tid] = before + v;
     __syncthreads();
-    return scan[kPagedThreads - 1];
+    return scan[kThreads - 1];
   };
   long long total = 0;
-  for (int base = 0; base < p.batch; base += kPagedThreads) total += scan_block(base);
+  for (int base = 0; base < p.batch; base += kThreads) total += scan_block(base);
   const long long pieces = static_cast<long long>(gridDim.x) * kTeams;
   long long per = (total + pieces - 1) / pieces;
-  if (per < kMinTiles) per = kMinTiles;
+  if (per < kMinTokens / kTile) per = kMinTokens / kTile;
   const long long used = (total + per - 1) / per;  // pieces that hold tiles
   const int teams_used = static_cast<int>((used + gridDim.x - 1) / gridDim.x);  // of a block
-  const long long piece = static_cast<long long>(blockIdx.x) * teams_used + team;
-  const bool active = team < teams_used && piece < used;
-  const long long begin = piece * per;
-  const int count = !active ? 0 : static_cast<int>(total - begin < per ? total - begin : per);
+  // tiles of a team of this block
+  auto piece_of = [&](int team) { return static_cast<long long>(blockIdx.x) * teams_used + team; };
+  auto count_of = [&](int team) -> int {
+    const long long piece = piece_of(team), left = total - piece * per;
+    return team >= teams_used || left <= 0 ? 0 : static_cast<int>(left < per ? left : per);
+  };
 
-  PagedCursor cur;
-  cur.b = -1;
   long long offset = 0;
-  for (int base = 0; base < p.batch; base += kPagedThreads) {
-    if (p.batch > kPagedThreads) scan_block(base);
-    const long long sum = scan[kPagedThreads - 1];
-    if (active && begin >= offset && begin < offset + sum) {
-      const long long x = begin - offset;  // the first sequence whose inclusive sum exceeds x
-      int lo = 0, hi = kPagedThreads - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (scan[mid] > x) hi = mid;
-        else lo = mid + 1;
+  for (int base = 0; base < p.batch; base += kThreads) {
+    if (p.batch > kThreads) scan_block(base);
+    const long long sum = scan[kThreads - 1];
+    if (tid < kTeams && count_of(tid) > 0) {
+      const long long x = piece_of(tid) * per - offset;
+      if (x >= 0 && x < sum) {  // the first sequence whose inclusive sum exceeds x
+        int lo = 0, hi = kThreads - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (scan[mid] > x) hi = mid;
+          else lo = mid + 1;
+        }
+        PagedCursor c;
+        c.b = base + lo;
+        c.s = paged_seq<kTile>(p, c.b);
+        const long long in = x - (lo > 0 ? scan[lo - 1] : 0);
+        c.head = static_cast<int>(in / c.s.tiles);
+        c.tile = static_cast<int>(in - static_cast<long long>(c.head) * c.s.tiles);
+        begin_at[tid] = c;
       }
-      cur.b = base + lo;
-      cur.s = paged_seq<kRows>(p, cur.b);
-      const long long in = x - (lo > 0 ? scan[lo - 1] : 0);
-      const int unit = static_cast<int>(in / cur.s.tiles);
-      cur.tile = static_cast<int>(in - static_cast<long long>(unit) * cur.s.tiles);
-      cur.head = unit / cur.s.groups;
-      cur.group = unit - cur.head * cur.s.groups;
     }
     offset += sum;
-    if (p.batch > kPagedThreads) __syncthreads();
+    if (p.batch > kThreads) __syncthreads();
   }
-  __syncthreads();  // barriers are initialised
-
-  // every piece that could hold something says first that it leaves nothing to join
-  if (sub == 0 && lane == 0) {
-    // the pieces of this launch are numbered 0 .. gridDim.x * kTeams - 1; those that no team of the
-    // assignment above owns are cleared by the team with the same place in plain order
-    const int64_t own = active ? piece : -1;
-    const int64_t plain = static_cast<int64_t>(blockIdx.x) * kTeams + team;
-    if (own >= 0) p.joins[own].last = -1;
+  // every piece says first that it leaves nothing to join; pieces beyond the used ones are cleared in plain order
+  if (tid < kTeams) {
+    if (count_of(tid) > 0) p.joins[piece_of(tid)].last = -1;
+    const long long plain = static_cast<long long>(blockIdx.x) * kTeams + tid;
     if (plain >= used) p.joins[plain].last = -1;
   }
-  if (!active || count == 0) return;
+  __syncthreads();  // starting places written
 
-  // ---- producer: the warp walks the line `kStages` tiles ahead ----
-  PagedCursor pc = cur;
-  int page_base = -1, page_entry = 0, page_b = -1, page_head = -1;
-  float page_ks = 0.f, page_vs = 0.f;
-  int issued = 0;
-  const int page_tokens = 1 << p.page_shift;
-  const int box_rows = page_tokens < kTileTokens ? page_tokens : kTileTokens;
+  const int team = warp / TW, sub = warp % TW;
+  const int g = lane >> 2, c = lane & 3;
+  const int count = count_of(team);
+  if (count == 0) return;
+  const long long piece = piece_of(team), begin = piece * per;
+  PagedCursor cur = begin_at[team];
+  const uint32_t ring = smem0 + team * kSlots * Shape::kSlotBytes;
 
-  auto issue = [&]() {  // the next tile into its stage (warp-uniform; the team's first warp only)
-    const int stage = issued % kStages;
-    const uint32_t full = full0 + 8 * stage;
-    const uint32_t at = ring + stage * Shape::kTileBytes;
-    const int token = pc.tile * kTileTokens;
-    const int pages = (pc.s.len + page_tokens - 1) >> p.page_shift;
-    const int first = token >> p.page_shift;
-    if (pc.b != page_b || pc.head != page_head || first < page_base || first >= page_base + 31) {
-      // 32 entries of the block table and their scales, one a lane
-      page_b = pc.b;
-      page_head = pc.head;
-      page_base = first;
-      const int idx = first + lane;
-      page_entry = 0;
-      page_ks = page_vs = 1.f;
-      if (idx < pages) {
-        page_entry = p.table[pc.b * p.table_stride + idx];
-        if (page_entry < 0 || page_entry >= p.num_pages) {
-          paged_error(p.status, kSitePagedPage, pc.b);
-          page_entry = 0;
-        }
-        const int64_t at_scale = static_cast<int64_t>(page_entry) * p.heads_kv + pc.head;
-        const int ek = p.k_scale[at_scale], ev = p.v_scale[at_scale];
-        page_ks = ev == 255 ? scale_of(255) : scale_of(ek);  // no number in either: rows that see it are NaN
-        page_vs = ev == 255 ? 1.f : scale_of(ev);
+  // ---- the team fills its ring: tile after tile, K and V by turns, each warp its share of the tokens ----
+  constexpr int kShare = kTile / TW;
+  constexpr int kRun = kShare < (G16 ? 16 : 32) ? kShare : (G16 ? 16 : 32);  // tokens that surely lie in one page
+  PagedCursor ahead = cur;  // the tile that is filled in next
+  int filled = 0;           // slots filled so far
+  int fill_slot = 0;
+  // lane l holds page page0 + l of the cursor's sequence: its index, the scales of the cursor's head, and (as
+  // loaded) those of the next head
+  int page0 = 0, entry = 0, ks_next = 127, vs_next = 127;
+  float ks = 1.f, vs = 1.f;
+  bool fresh = true;  // the pages' scales are still to be taken over
+  auto load_scales = [&](int head) {
+    ks_next = vs_next = 127;
+    if (((page0 + lane) << p.page_shift) < ahead.s.len) {
+      const int64_t at = static_cast<int64_t>(entry) * p.heads_kv + head;
+      ks_next = p.k_scale[at];
+      vs_next = p.v_scale[at];
+    }
+  };
+  auto take_scales = [&]() {
+    ks = vs_next == 255 ? scale_of(255) : scale_of(ks_next);  // NaN in either: NaN scores
+    vs = vs_next == 255 ? 1.f : scale_of(vs_next);
+    if (ahead.head + 1 < p.heads_kv) load_scales(ahead.head + 1);
+  };
+  auto load_pages = [&](int first) {
+    page0 = first;
+    entry = 0;
+    if (((first + lane) << p.page_shift) < ahead.s.len) {
+      entry = p.table[ahead.b * p.table_stride + first + lane];
+      if (entry < 0 || entry >= p.num_pages) {
+        paged_error(p.status, kSitePagedPage, ahead.b);
+        entry = 0;
       }
     }
-    const int i0 = first - page_base;
-    const int e0 = __shfl_sync(0xffffffffu, page_entry, i0), e1 = __shfl_sync(0xffffffffu, page_entry, i0 + 1);
-    const float k0 = __shfl_sync(0xffffffffu, page_ks, i0), k1 = __shfl_sync(0xffffffffu, page_ks, i0 + 1);
-    const float v0 = __shfl_sync(0xffffffffu, page_vs, i0), v1 = __shfl_sync(0xffffffffu, page_vs, i0 + 1);
-    if (lane == 0) {
-      const bool split = page_tokens < kTileTokens;  // two pages of 16 tokens
-      meta[team * kStages + stage] = split ? make_float4(k0, k1, v0, v1) : make_float4(k0, k0, v0, v0);
-      const int boxes = pc.s.len == 0 ? 0 : (split && first + 1 < pages) ? 2 : 1;
-      if (boxes == 0) {
-        mbar_arrive(full);
-      } else {
-        mbar_arrive_expect_tx(full, boxes * box_rows * (DQK + DV));
-        for (int i = 0; i < boxes; ++i) {
-          const int e = i == 0 ? e0 : e1;
-          const int row = split ? 0 : token & (page_tokens - 1);
-          if constexpr (DQK == 128) {
-            tma_load_4d(at + i * 16 * 128, &p.tm_k, full, 0, row, pc.head, e);
-          } else {
+    load_scales(ahead.head);
+    fresh = true;
+  };
+  // scale k of a slot belongs to 16 tokens: their page's lane, counted from the tile's first
+  const int scale_lane = G16 ? lane : lane >> (p.page_shift - 4);
+  // This warp's tokens of a tile, 16 bytes a lane; pages behind the last are left out.  Lane l's chunks in a run
+  // of tokens are l, l + 32, ..: with rows of 4 or 8 chunks they are one column, with 12 the rows repeat by 8.
+  auto lane_offset = [&](int d, uint32_t token_stride, int i) -> uint32_t {
+    const int at = i * 32 + lane, chunks = d / 16;
+    return static_cast<uint32_t>(at / chunks) * token_stride + (at % chunks) * 16;
+  };
+  constexpr int kOffsets = DQK == 192 ? 3 : 1;
+  uint32_t k_off[kOffsets];
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s)
-              tma_load_4d(at + s * kTileTokens * 64 + i * 16 * 64, &p.tm_k, full, 64 * s, row, pc.head, e);
-          }
-          tma_load_4d(at + Shape::kTileK + i * 16 * DV, &p.tm_v, full, 0, row, pc.head, e);
+  for (int i = 0; i < kOffsets; ++i) k_off[i] = lane_offset(DQK, p.k_token, i);
+  const uint32_t v_off = lane_offset(DV, p.v_token, 0);
+  const uint8_t *k_at, *v_at;  // of the cursor's head
+  auto set_head = [&]() {
+    k_at = p.k + ahead.head * p.k_head;
+    v_at = p.v + ahead.head * p.v_head;
+  };
+  auto copy = [&](auto is_k, uint32_t dst, int token) {
+    constexpr bool kK = decltype(is_k)::value;
+    constexpr int D = kK ? DQK : DV, kChunks = D / 16;
+    static_assert(kRun * kChunks % 32 == 0, "whole warps of chunks");
+    const uint32_t ts = kK ? p.k_token : p.v_token;
+#pragma unroll
+    for (int r0 = 0; r0 < kShare; r0 += kRun) {
+      const int row0 = sub * kShare + r0, t = token + row0;
+      const int e = __shfl_sync(0xffffffffu, entry, (t >> p.page_shift) - page0);
+      if (t < ahead.s.len) {
+        const uint8_t* src = (kK ? k_at : v_at) + e * (kK ? p.k_page : p.v_page) +
+                             static_cast<uint64_t>(static_cast<uint32_t>(t & ((1 << p.page_shift) - 1)) * ts);
+        if constexpr (D != 192) src += kK ? k_off[0] : v_off;
+#pragma unroll
+        for (int i = 0; i < kRun * kChunks / 32; ++i) {
+          const int at = i * 32 + lane, row = at / kChunks, chunk = at % kChunks;
+          const uint8_t* from = D == 192 ? src + k_off[i % kOffsets] + (i / 3) * 8 * ts : src + i * (32 / kChunks) * ts;
+          cp_async16(dst + (kK ? k_place<D>(row0 + row, chunk) : v_place<D>(row0 + row, chunk)), from);
         }
       }
     }
-    __syncwarp();
-    ++issued;
-    if (++pc.tile == pc.s.tiles && issued < count) paged_next_unit<kRows>(p, pc);
+  };
+  auto fill = [&]() {  // the next slot, which has been read
+    if (filled < 2 * count) {
+      const bool is_k = (filled & 1) == 0;
+      const int token = ahead.tile * kTile;
+      const uint32_t dst = ring + fill_slot * Shape::kSlotBytes;
+      if (is_k) copy(std::true_type{}, dst, token);
+      else copy(std::false_type{}, dst, token);
+      if (fresh) {
+        take_scales();
+        fresh = false;
+      }
+      const float scale = __shfl_sync(0xffffffffu, is_k ? ks : vs, (token >> p.page_shift) - page0 + scale_lane);
+      if (sub == 0 && lane < kTile / 16) slot_scale[team * kSlots + fill_slot][lane] = scale;
+      ++filled;
+      if (++fill_slot == kSlots) fill_slot = 0;
+      if (!is_k && filled < 2 * count) {  // on to the next tile
+        const int b = ahead.b, head = ahead.head;
+        paged_next<kTile>(p, ahead);
+        if (ahead.head != head) set_head();
+        const int next = (ahead.tile * kTile) >> p.page_shift;
+        if (ahead.b == b && ahead.head == head + 1 && page0 == 0) take_scales();  // the same pages, the next head
+        else if (ahead.b != b || ahead.head != head || next + kTile / 16 > page0 + 32) load_pages(next);
+      }
+    }
+    cp_async_commit();  // a group for each slot, empty ones at the end
+  };
+  set_head();
+  load_pages((ahead.tile * kTile) >> p.page_shift);
+  for (int e = 0; e < kSlots - 1; ++e) fill();
+  int slot = -1;
+  // The next slot's tokens are there for the whole team, which has read the slot before: that one is refilled.
+  auto advance = [&]() {
+    cp_async_wait<kSlots - 2>();
+    if constexpr (TW == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(32 * TW) : "memory");
+    if (++slot == kSlots) slot = 0;
+    fill();
   };
 
-  // after a failed wait: the copies in flight land before the block's memory is given up
-  auto drain = [&](int from) {
-    if (sub != 0) return;
-    const uint64_t t0 = globaltimer_ns();
-    for (int i = from; i < issued; ++i)
-      while (!mbar_try_wait(full0 + 8 * (i % kStages), (i / kStages) & 1))
-        if (globaltimer_ns() - t0 > 1000000000ull) return;
-  };
-
-  if (sub == 0)
-    for (int i = 0; i < kStages && i < count; ++i) issue();
-
-  // ---- consumer ----
   uint32_t qf[NT][kSteps * 4][2];
   float qfac[NT][2], ref[NT][2], sum[NT][2];
   int limit[NT][2];
@@ -366,9 +421,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
 
   for (int i = 0; i < count; ++i) {
     if (i == 0 || cur.tile == 0) {
-      // ---- a new (sequence, head, row group): the query rows as B fragments ----
+      // ---- a new (sequence, head): the query rows as B fragments ----
       started_here = cur.tile == 0;
-      const int row0 = cur.group * kRows + sub * 8 * NT;
+      const int row0 = sub * 8 * NT;
       min_limit = cur.s.len;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -382,7 +437,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
           for (int s = 0; s < kSteps; ++s)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              raw[s * 2 + h] = __ldg(reinterpret_cast<const uint4*>(src + k_column<DQK>(c, s) + 8 * h));
+              raw[s * 2 + h] = __ldg(reinterpret_cast<const uint4*>(src + 16 * k_chunk<DQK>(c, s) + 8 * h));
         } else {
 #pragma unroll
           for (int s = 0; s < kSteps * 2; ++s) raw[s] = make_uint4(0, 0, 0, 0);
@@ -393,8 +448,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
         for (int s = 0; s < kSteps * 2; ++s) {
           const uint32_t w[4] = {raw[s].x, raw[s].y, raw[s].z, raw[s].w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t a = w[j] & 0x7f80u, b = (w[j] >> 16) & 0x7f80u;
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t a = w[k] & 0x7f80u, b = (w[k] >> 16) & 0x7f80u;
             top = top > a ? top : a;
             top = top > b ? top : b;
           }
@@ -407,16 +462,21 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
         ex = ex == 0 || ex == 255 ? 127 : ex;  // a row of zeros, or one that holds no numbers
         const float down = scale_of(254 - ex);
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s)
+        for (int s = 0; s < kSteps; ++s) {
+          uint32_t f[8];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint4 v = raw[s * 2 + h];
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)  // word j holds columns 8 h + 2 j, + 1: step (8 h + 2 j) / 4, half j & 1
-              qf[nt][s * 4 + h * 2 + (j >> 1)][j & 1] =
-                  pack_f16x2(__uint_as_float(w[j] << 16) * down, __uint_as_float(w[j] & 0xffff0000u) * down);
+            for (int k = 0; k < 4; ++k)  // word k holds columns 8 h + 2 k, + 1: step (8 h + 2 k) / 4, half k & 1
+              f[4 * h + k] = pack_f16x2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
           }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            qf[nt][s * 4 + k][0] = f[2 * k], qf[nt][s * 4 + k][1] = f[2 * k + 1];
+          }
+        }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {  // this lane's columns of S^T are rows 2 c and 2 c + 1
           const int e = __shfl_sync(0xffffffffu, ex, (2 * c + k) * 4);
@@ -441,109 +501,95 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
       min_limit = min(min_limit, __shfl_xor_sync(0xffffffffu, min_limit, 2));
     }
 
-    const int stage = i % kStages;
-    if (!mbar_wait(full0 + 8 * stage, (i / kStages) & 1, wc, kSitePagedWait)) {
-      drain(i);
-      return;
-    }
-    const uint32_t tk = ring + stage * Shape::kTileBytes, tv = tk + Shape::kTileK;
-    const float4 m = meta[team * kStages + stage];
-    const int token0 = cur.tile * kTileTokens;
-    const bool masked = token0 + kTileTokens > min_limit;
+    const int token0 = cur.tile * kTile;
+    const bool masked = token0 + kTile > min_limit;
 
-    // S^T of 2 x 16 tokens
-    float s[2][NT][4];
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s[mt][nt][k] = 0.f;
+    // ---- S^T: kMT x 16 tokens ----
+    advance();
+    float s[kMT][NT][4];
+    {
+      const uint32_t tk = ring + slot * Shape::kSlotBytes;
 #pragma unroll
       for (int st = 0; st < kSteps; ++st) {
-        const uint4 ra = lds128(tk + k_offset<DQK>(16 * mt + g, c, st));
-        const uint4 rb = lds128(tk + k_offset<DQK>(16 * mt + 8 + g, c, st));
-        const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+        uint32_t wa[kMT][4], wb[kMT][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t a0 = e4m3x2_f16x2(wa[j]), a1 = e4m3x2_f16x2(wb[j]);
-          const uint32_t a2 = e4m3x2_hi_f16x2(wa[j]), a3 = e4m3x2_hi_f16x2(wb[j]);
+        for (int mt = 0; mt < kMT; ++mt) {
+          const uint4 ra = lds128(tk + k_place<DQK>(16 * mt + g, k_chunk<DQK>(c, st)));
+          const uint4 rb = lds128(tk + k_place<DQK>(16 * mt + 8 + g, k_chunk<DQK>(c, st)));
+          wa[mt][0] = ra.x, wa[mt][1] = ra.y, wa[mt][2] = ra.z, wa[mt][3] = ra.w;
+          wb[mt][0] = rb.x, wb[mt][1] = rb.y, wb[mt][2] = rb.z, wb[mt][3] = rb.w;
+        }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma_f16(s[mt][nt], a0, a1, a2, a3, qf[nt][st * 4 + j][0], qf[nt][st * 4 + j][1]);
+        for (int k = 0; k < 4; ++k) {
+#pragma unroll
+          for (int mt = 0; mt < kMT; ++mt) {
+            const uint32_t a0 = e4m3x2_f16x2(wa[mt][k]), a1 = e4m3x2_f16x2(wb[mt][k]);
+            const uint32_t a2 = e4m3x2_hi_f16x2(wa[mt][k]), a3 = e4m3x2_hi_f16x2(wb[mt][k]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if (st == 0 && k == 0) mma_f16_zero(s[mt][nt], a0, a1, a2, a3, qf[nt][st * 4 + k][0], qf[nt][st * 4 + k][1]);
+              else mma_f16(s[mt][nt], a0, a1, a2, a3, qf[nt][st * 4 + k][0], qf[nt][st * 4 + k][1]);
+            }
+          }
         }
       }
+      // scores in log2 units
+      const float4 m = *reinterpret_cast<const float4*>(slot_scale[team * kSlots + slot]);
+      const float ms[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+      for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[mt][nt][k] *= qfac[nt][k & 1] * ms[G16 ? mt : mt & ~1];
     }
-
-    // V codes of this lane: tokens 16 mt + {2 c, 2 c + 1, 2 c + 8, 2 c + 9}, columns DV / 8 * g ..
-    uint32_t vw[2][4][kVWords];
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int row = 16 * mt + 2 * c + (t & 1) + (t >> 1) * 8;
-        if constexpr (DV == 128) {
-          const uint4 v = lds128(tv + sw128(row, g));
-          vw[mt][t][0] = v.x, vw[mt][t][1] = v.y, vw[mt][t][2] = v.z, vw[mt][t][3] = v.w;
-        } else {
-          const uint2 v = lds64(tv + sw64(row, g >> 1) + (g & 1) * 8);
-          vw[mt][t][0] = v.x, vw[mt][t][1] = v.y;
-        }
-      }
-
-    // scores in log2 units
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s[mt][nt][k] *= qfac[nt][k & 1] * (mt == 0 ? m.x : m.y);
-
+    advance();
+    const uint32_t tv = ring + slot * Shape::kSlotBytes;
+    uint32_t keep[kTile / 32];
     if (masked) {
       // A hidden token has weight 0, but 0 times a value that is no number is none: tokens behind the
       // sequence's end count as 0, and a token whose values hold a NaN code counts as 0 with a NaN score,
       // which only the rows that see it take in.
-      const int mine = token0 + lane;
-      uint32_t nan = 0;
-      if (mine < cur.s.len) {
 #pragma unroll
-        for (int j = 0; j < DV / 16; ++j) {
-          const uint4 v = lds128(tv + (DV == 128 ? sw128(lane, j) : sw64(lane, j)));
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int h = 0; h < kTile / 32; ++h) {
+        const int row = 32 * h + lane;
+        const bool inside = token0 + row < cur.s.len;
+        uint32_t nan = 0;
+        if (inside) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) nan |= ((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-        }
-      }
-      const uint32_t poison = __ballot_sync(0xffffffffu, nan != 0);
-      const uint32_t inside = __ballot_sync(0xffffffffu, mine < cur.s.len);
-      const uint32_t keep = inside & ~poison;
+          for (int k = 0; k < DV / 16; ++k) {
+            const uint4 v = lds128(tv + v_place<DV>(row, k));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int row = 16 * mt + 2 * c + (t & 1) + (t >> 1) * 8;
-#pragma unroll
-          for (int j = 0; j < kVWords; ++j) vw[mt][t][j] = (keep >> row) & 1 ? vw[mt][t][j] : 0u;
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int row = 16 * mt + g + (k >> 1) * 8;
-            float x = (poison >> row) & 1 ? __uint_as_float(0x7fc00000u) : s[mt][nt][k];
-            s[mt][nt][k] = token0 + row < limit[nt][k & 1] ? x : -INFINITY;
+            for (int x = 0; x < 4; ++x) nan |= ((w[x] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
           }
+        }
+        const uint32_t poison = __ballot_sync(0xffffffffu, nan != 0);
+        keep[h] = __ballot_sync(0xffffffffu, inside) & ~poison;
+#pragma unroll
+        for (int mt = 2 * h; mt < 2 * h + 2; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int at = 16 * (mt & 1) + g + (k >> 1) * 8;
+              const float x = (poison >> at) & 1 ? __uint_as_float(0x7fc00000u) : s[mt][nt][k];
+              s[mt][nt][k] = token0 + 32 * h + at < limit[nt][k & 1] ? x : -INFINITY;
+            }
       }
     }
 
-    // online softmax: the reference moves only when it lags the maximum by more than 2^8
-    uint32_t pf[2][NT][2];
+    // ---- online softmax: the reference moves only when it lags the maximum by more than 2^8 ----
+    uint32_t pf[kMT][NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float alpha[2];
+      bool moved = false;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        float mx = fmaxf(fmaxf(s[0][nt][k], s[0][nt][k + 2]), fmaxf(s[1][nt][k], s[1][nt][k + 2]));
+        float mx = fmaxf(s[0][nt][k], s[0][nt][k + 2]);
+#pragma unroll
+        for (int mt = 1; mt < kMT; ++mt) mx = fmax3(mx, s[mt][nt][k], s[mt][nt][k + 2]);
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -551,9 +597,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
         if (mx > ref[nt][k] + kRefLag) {  // also from -inf
           alpha[k] = ex2_approx(ref[nt][k] - mx);
           ref[nt][k] = mx;
+          moved = true;
         }
       }
-      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+      if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
         for (int v = 0; v < kVTiles; ++v) {
           o[nt][v][0] *= alpha[0], o[nt][v][1] *= alpha[1];
@@ -561,12 +608,13 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
         }
         sum[nt][0] *= alpha[0], sum[nt][1] *= alpha[1];
       }
-      const float r0 = ref[nt][0] == -INFINITY ? 0.f : ref[nt][0], r1 = ref[nt][1] == -INFINITY ? 0.f : ref[nt][1];
+      const float r0 = ref[nt][0] == -INFINITY ? 0.f : kPShift - ref[nt][0];
+      const float r1 = ref[nt][1] == -INFINITY ? 0.f : kPShift - ref[nt][1];
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
+      for (int mt = 0; mt < kMT; ++mt) {
         float e[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) e[k] = ex2_approx(s[mt][nt][k] - ((k & 1) ? r1 : r0) + kPShift);
+        for (int k = 0; k < 4; ++k) e[k] = ex2_approx(s[mt][nt][k] + ((k & 1) ? r1 : r0));
         sum[nt][0] += e[0] + e[2];
         sum[nt][1] += e[1] + e[3];
         // accumulator layout (token g, rows 2 c ..) to operand layout (tokens 2 c .., row g)
@@ -575,77 +623,87 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
       }
     }
 
-    // O^T += V^T P^T, the page's scale applied to each 16 or 32 tokens' product
-    const bool two_scales = m.z != m.w;
+    // ---- O^T += V^T P^T, the page's scale applied to each 16 or 32 tokens' product ----
+    const float4 m = *reinterpret_cast<const float4*>(slot_scale[team * kSlots + slot]);
+    const float ms[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
-    for (int w = 0; w < kVWords; ++w) {
-      uint32_t lo[2][2], hi[2][2];  // tokens (0, 1) and (2, 3) of columns 4 w, 4 w + 1 and 4 w + 2, 4 w + 3
+    for (int h = 0; h < kTile / 32; ++h) {
+      // codes of this lane: tokens 16 t + {2 c, 2 c + 1, 2 c + 8, 2 c + 9} of the half, columns DV / 8 * g ..
+      uint32_t vw[2][4][kVWords];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          lo[mt][t] = __byte_perm(vw[mt][2 * t][w], vw[mt][2 * t + 1][w], 0x5140);
-          hi[mt][t] = __byte_perm(vw[mt][2 * t][w], vw[mt][2 * t + 1][w], 0x7362);
+        for (int t = 0; t < 4; ++t) {
+          const int row = 32 * h + 16 * mt + 2 * c + (t & 1) + (t >> 1) * 8;
+          if constexpr (DV == 128) {
+            const uint4 v = lds128(tv + v_place<DV>(row, g));
+            vw[mt][t][0] = v.x, vw[mt][t][1] = v.y, vw[mt][t][2] = v.z, vw[mt][t][3] = v.w;
+          } else {
+            const uint2 v = lds64(tv + v_place<DV>(row, g >> 1) + (g & 1) * 8);
+            vw[mt][t][0] = v.x, vw[mt][t][1] = v.y;
+          }
         }
+      if (masked) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        uint32_t a[2][4];
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const int row = 16 * mt + 2 * c + (t & 1) + (t >> 1) * 8;
+#pragma unroll
+            for (int k = 0; k < kVWords; ++k) vw[mt][t][k] = (keep[h] >> row) & 1 ? vw[mt][t][k] : 0u;
+          }
+      }
+#pragma unroll
+      for (int w = 0; w < kVWords; ++w) {
+        uint32_t pair[2][2][2];  // [16 tokens][columns 4 w + 0, 1 or 2, 3][tokens (0, 1) or (2, 3)]
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            const uint32_t pair = x == 0 ? lo[mt][t] : hi[mt][t];
-            a[mt][2 * t] = e4m3x2_f16x2(pair);
-            a[mt][2 * t + 1] = e4m3x2_hi_f16x2(pair);
+            pair[mt][0][t] = __byte_perm(vw[mt][2 * t][w], vw[mt][2 * t + 1][w], 0x5140);
+            pair[mt][1][t] = __byte_perm(vw[mt][2 * t][w], vw[mt][2 * t + 1][w], 0x7362);
           }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_f16(acc, a[0][0], a[0][1], a[0][2], a[0][3], pf[0][nt][0], pf[0][nt][1]);
-          if (two_scales) {
+        for (int x = 0; x < 2; ++x) {
+          uint32_t a[2][4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              o[nt][2 * w + x][k] = fmaf(acc[k], m.z, o[nt][2 * w + x][k]);
-              acc[k] = 0.f;
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              a[mt][2 * t] = e4m3x2_f16x2(pair[mt][x][t]);
+              a[mt][2 * t + 1] = e4m3x2_hi_f16x2(pair[mt][x][t]);
+            }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float* const out = o[nt][2 * w + x];
+            float acc[4];
+            mma_f16_zero(acc, a[0][0], a[0][1], a[0][2], a[0][3], pf[2 * h][nt][0], pf[2 * h][nt][1]);
+            if constexpr (G16) {
+              float acc1[4];
+              mma_f16_zero(acc1, a[1][0], a[1][1], a[1][2], a[1][3], pf[2 * h + 1][nt][0], pf[2 * h + 1][nt][1]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) out[k] = fmaf(acc1[k], ms[2 * h + 1], fmaf(acc[k], ms[2 * h], out[k]));
+            } else {
+              mma_f16(acc, a[1][0], a[1][1], a[1][2], a[1][3], pf[2 * h + 1][nt][0], pf[2 * h + 1][nt][1]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) out[k] = fmaf(acc[k], ms[2 * h], out[k]);
             }
           }
-          mma_f16(acc, a[1][0], a[1][1], a[1][2], a[1][3], pf[1][nt][0], pf[1][nt][1]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) o[nt][2 * w + x][k] = fmaf(acc[k], m.w, o[nt][2 * w + x][k]);
         }
       }
     }
-
-    // the stage is read: refill
-    __syncwarp();
-    if constexpr (TW == 1) {
-      if (issued < count) issue();
-    } else {
-      if (lane == 0) mbar_arrive(empty0 + 8 * stage);
-      if (sub == 0 && issued < count && i >= Shape::kLag) {
-        const int k = issued / kStages;  // times the stage was used before
-        if (k > 0 && !mbar_wait(empty0 + 8 * (issued % kStages), (k - 1) & 1, wc, kSitePagedWait)) {
-          drain(i + 1);
-          return;
-        }
-        issue();
-      }
-    }
-
     // ---- the end of the unit or of the piece: write out ----
     const bool unit_end = cur.tile + 1 == cur.s.tiles;
     if (unit_end || i + 1 == count) {
       const bool whole = started_here && unit_end;
-      const int64_t slot = 2 * piece + (started_here ? 1 : 0);
+      const int64_t part = 2 * piece + (started_here ? 1 : 0);
       if (!whole && started_here && sub == 0 && lane == 0) {
         // the rest of the unit lies in the pieces that follow
         PagedJoin j;
         j.last = static_cast<int>((begin + i + (cur.s.tiles - 1 - cur.tile)) / per);
         j.cu0 = cur.s.cu0;
         j.head = cur.head;
-        j.row0 = cur.group * kRows;
         j.rows = cur.s.rows;
-        j.pad = 0;
         p.joins[piece] = j;
       }
 #pragma unroll
@@ -656,9 +714,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
           l += __shfl_xor_sync(0xffffffffu, l, 4);
           l += __shfl_xor_sync(0xffffffffu, l, 8);
           l += __shfl_xor_sync(0xffffffffu, l, 16);
-          const int local = sub * 8 * NT + nt * 8 + 2 * c + k;
-          const int r = cur.group * kRows + local;
-          const float rf = l != 0.f && ref[nt][k] == -INFINITY ? 0.f : ref[nt][k];
+          const int r = sub * 8 * NT + nt * 8 + 2 * c + k;
+          const float rf = l != 0.f && ref[nt][k] == -INFINITY ? kPShift : ref[nt][k];
           if (r < cur.s.rows) {
             if (whole) {
               const int pos = r / p.ratio, hq = cur.head * p.ratio + (r - pos * p.ratio);
@@ -675,16 +732,16 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                 p.lse[hq * p.total_q + token] =
                     l == 0.f ? -INFINITY : (rf - kPShift + log2f(l)) * 0.6931471805599453f;
             } else {
-              float4* dst = reinterpret_cast<float4*>(p.part_o + (slot * kRows + local) * DV + g * (DV / 8));
+              float4* dst = reinterpret_cast<float4*>(p.part_o + (part * kRows + r) * DV + g * (DV / 8));
 #pragma unroll
               for (int v = 0; v < kVTiles / 2; ++v)
                 dst[v] = make_float4(o[nt][2 * v][k], o[nt][2 * v][k + 2], o[nt][2 * v + 1][k], o[nt][2 * v + 1][k + 2]);
-              if (g == 0) p.part_ml[slot * kRows + local] = make_float2(rf, l);
+              if (g == 0) p.part_ml[part * kRows + r] = make_float2(rf, l);
             }
           }
         }
     }
-    if (++cur.tile == cur.s.tiles && i + 1 < count) paged_next_unit<kRows>(p, cur);
+    if (i + 1 < count) paged_next<kTile>(p, cur);
   }
 }
 
@@ -702,8 +759,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
   if (j.last < 0) return;
   const int lane = threadIdx.x & 31;
   const int local = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const int r = j.row0 + local;
-  if (r >= j.rows) return;
+  if (local >= j.rows) return;
   const int parts = j.last - piece + 1;
   auto slot = [&](int i) { return 2 * static_cast<int64_t>(piece + i) + (i == 0 ? 1 : 0); };
   float top = -INFINITY;
@@ -739,7 +795,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  const int pos = r / p.ratio, hq = j.head * p.ratio + (r - pos * p.ratio);
+  const int pos = local / p.ratio, hq = j.head * p.ratio + (local - pos * p.ratio);
   const int64_t token = j.cu0 + pos;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (token * p.heads_q + hq) * DV + lane * kPer);

@@ -4,8 +4,8 @@
 namespace fa {
 
 int paged_launch_d128(const PagedParams& p, int d_v, int rows, int grid, cudaStream_t stream) {
-  if (d_v == 64) return paged_launch_rows<128, 64>(p, rows, grid, stream);
-  if (d_v == 128) return paged_launch_rows<128, 128>(p, rows, grid, stream);
+  if (d_v == 64) return paged_launch_pages<128, 64>(p, rows, grid, stream);
+  if (d_v == 128) return paged_launch_pages<128, 128>(p, rows, grid, stream);
   return FA_ERR_UNSUPPORTED;
 }
 

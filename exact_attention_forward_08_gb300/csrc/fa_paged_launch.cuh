@@ -7,7 +7,7 @@
 
 namespace fa {
 
-template <int DQK, int DV, int NT, int TW>
+template <int DQK, int DV, int NT, int TW, bool G16>
 int paged_launch(const PagedParams& p, int grid, cudaStream_t stream) {
   using Shape = PagedShape<DQK, DV, NT, TW>;
   static std::mutex mutex;
@@ -17,13 +17,13 @@ int paged_launch(const PagedParams& p, int grid, cudaStream_t stream) {
   {
     std::lock_guard<std::mutex> lock(mutex);
     if (!ready[dev]) {
-      if (cudaFuncSetAttribute(paged_attn_kernel<DQK, DV, NT, TW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      if (cudaFuncSetAttribute(paged_attn_kernel<DQK, DV, NT, TW, G16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                Shape::kBytes) != cudaSuccess)
         return FA_ERR_CUDA;
       ready[dev] = true;
     }
   }
-  paged_attn_kernel<DQK, DV, NT, TW><<<grid, kPagedThreads, Shape::kBytes, stream>>>(p);
+  paged_attn_kernel<DQK, DV, NT, TW, G16><<<grid, Shape::kThreads, Shape::kBytes, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   // the merge's blocks may be placed while the attention kernel still runs; they wait for its end
   cudaLaunchConfig_t cfg = {};
@@ -39,13 +39,19 @@ int paged_launch(const PagedParams& p, int grid, cudaStream_t stream) {
   return FA_OK;
 }
 
-// rows of a team: the smallest build that holds a sequence's rows, at most 64
-template <int DQK, int DV>
+// rows of a team: the smallest build that holds a sequence's rows, at most 64.
+template <int DQK, int DV, bool G16>
 int paged_launch_rows(const PagedParams& p, int rows, int grid, cudaStream_t stream) {
-  if (rows <= 8) return paged_launch<DQK, DV, 1, 1>(p, grid, stream);
-  if (rows <= 16) return paged_launch<DQK, DV, 2, 1>(p, grid, stream);
-  if (rows <= 32) return paged_launch<DQK, DV, 2, 2>(p, grid, stream);
-  return paged_launch<DQK, DV, 2, 4>(p, grid, stream);
+  if (rows <= 8) return paged_launch<DQK, DV, 1, 1, G16>(p, grid, stream);
+  if (rows <= 16) return paged_launch<DQK, DV, 2, 1, G16>(p, grid, stream);
+  if (rows <= 32) return paged_launch<DQK, DV, 2, 2, G16>(p, grid, stream);
+  return paged_launch<DQK, DV, 2, 4, G16>(p, grid, stream);
+}
+
+template <int DQK, int DV>
+int paged_launch_pages(const PagedParams& p, int rows, int grid, cudaStream_t stream) {
+  return p.page_shift == 4 ? paged_launch_rows<DQK, DV, true>(p, rows, grid, stream)
+                           : paged_launch_rows<DQK, DV, false>(p, rows, grid, stream);
 }
 
 }  // namespace fa
