@@ -19,7 +19,7 @@ constexpr int kPagedRowLimit = 64;
 // fa_paged_append.cu
 int append_launch(const fa_kv_cache& c, const void* q, const void* k, const void* v, int64_t q_stride,
                   int64_t k_stride, int64_t v_stride, void* q_out, const int* cu, int batch, int64_t total,
-                  int heads_q, const float* cos_sin, int max_pos, int rot, int interleaved, unsigned int* status,
+                  int heads_q, const float* cos_sin, int max_pos, int rot, int interleaved, unsigned int* status, int sms,
                   cudaStream_t stream);
 
 // fa_paged_d{64,128,192}.cu: the attention kernel and the merge for rows of a

@@ -139,7 +139,7 @@ int fa_kv_append(const fa_kv_cache* cache, const void* q, const void* k, const v
       (rot_dim > 0 && !fa::host_is_device_ptr(cos_sin, host.dev)))
     return FA_ERR_INVALID_ARG;
   return fa::append_launch(*cache, q, k, v, q_stride, k_stride, v_stride, q_out, cu_seqlens, batch, total, heads_q,
-                           cos_sin, max_positions, rot_dim, interleaved, host.status,
+                           cos_sin, max_positions, rot_dim, interleaved, host.status, host.sms,
                            reinterpret_cast<cudaStream_t>(stream));
 }
 
