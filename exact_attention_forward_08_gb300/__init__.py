@@ -20,6 +20,7 @@ Raw entry points with the C names: ``fa_fwd``, ``fa_fwd_ex``, ``fa_fwd_varlen``,
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import struct
@@ -637,9 +638,7 @@ def _paged_cache(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, cu_
             k_scale.is_contiguous() and v_scale.is_contiguous() and len(td) == 2 and block_table.dtype is i32 and
             seqlens_k.dtype is i32 and cu_seqlens.dtype is i32 and seqlens_k.shape == td[:1] and
             cu_seqlens.dim() == 1 and cu_seqlens.shape[0] == td[0] + 1 and seqlens_k.is_contiguous() and
-            cu_seqlens.is_contiguous() and k_cache.get_device() == index and v_cache.get_device() == index and
-            k_scale.get_device() == index and v_scale.get_device() == index and block_table.get_device() == index and
-            seqlens_k.get_device() == index and cu_seqlens.get_device() == index):
+            cu_seqlens.is_contiguous()):  # where they lie, the library checks
         _paged_cache_error(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, cu_seqlens, index)
     ks, vs, ts = k_cache.stride(), v_cache.stride(), block_table.stride()
     if (ks[3] != 1 and kd[3] > 1) or (vs[3] != 1 and vd[3] > 1) or (ts[1] != 1 and td[1] > 1):
@@ -671,46 +670,37 @@ def _paged_cache_error(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_
     _bad("block_table, seqlens_k and cu_seqlens must hold batch rows, batch lengths and batch + 1 offsets")
 
 
-class _OnDevice:
-    """Makes device `index` the current one for a call when it is not, and finds the call's stream."""
+def _call_stream(index, stream):
+    """(pointer of the call's stream, pointer of the current one) on device `index`."""
+    import torch
 
-    def __init__(self, index, stream):
-        import torch
-
-        self.guard = None
-        if torch.cuda.current_device() != index:
-            self.guard = torch.cuda.device(index)
-            self.guard.__enter__()
-        self.index = index
-        self.current = torch._C._cuda_getCurrentRawStream(index)
-        if stream is None:
-            self.ptr = self.current
-        else:
-            self.ptr = (stream.cuda_stream if hasattr(stream, "cuda_stream") else stream) or 0
-
-    def empty(self, shape, dtype):
-        """torch.empty whose memory is not reused before the work on the call's stream has run."""
-        import torch
-
-        if self.ptr == self.current:
-            return torch.empty(shape, dtype=dtype, device=self.index)
-        with torch.cuda.stream(torch.cuda.ExternalStream(self.ptr, device=self.index)):
-            return torch.empty(shape, dtype=dtype, device=self.index)
-
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+    current = torch._C._cuda_getCurrentRawStream(index)
+    if stream is None:
+        return current, current
+    return (stream.cuda_stream if hasattr(stream, "cuda_stream") else stream) or 0, current
 
 
-def _token_stride(name, t, total, heads, d, index):
+def _empty(shape, dtype, index, ptr, current):
+    """torch.empty whose memory is not reused before the work on the stream `ptr` has run."""
+    import torch
+
+    if ptr == current:
+        return torch.empty(shape, dtype=dtype, device=index)
+    with torch.cuda.stream(torch.cuda.ExternalStream(ptr, device=index)):
+        return torch.empty(shape, dtype=dtype, device=index)
+
+
+@functools.lru_cache(maxsize=256)
+def _paged_workspace_bytes(*sizes):
+    return load_library().fa_fwd_paged_workspace_size(*sizes)
+
+
+def _token_stride(name, t, total, heads, d):
     """Elements from token to token of a bf16 tensor [total, heads, d] whose heads lie side by side."""
     import torch
 
-    if t.dtype is not torch.bfloat16 or t.shape != (total, heads, d) or t.get_device() != index:
-        _bad(f"{name} must be a bf16 tensor [{total}, {heads}, {d}] on cuda:{index}")
+    if t.dtype is not torch.bfloat16 or t.shape != (total, heads, d):
+        _bad(f"{name} must be a bf16 tensor [{total}, {heads}, {d}]")
     st = t.stride()
     if total == 0 or (st[2] == 1 and (heads == 1 or st[1] == d)):
         return st[0] if total > 1 else heads * d
@@ -734,35 +724,37 @@ def kv_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, 
     index = k.get_device()
     if index < 0:
         _bad("k must be a CUDA tensor")
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return kv_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, cu_seqlens, q, cos_sin,
+                             interleaved, q_out, stream)
     cache, heads, d_qk, d_v, batch, _ = _paged_cache(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k,
                                                      cu_seqlens, index)
     total = k.shape[0]
-    ks = _token_stride("k", k, total, heads, d_qk, index)
-    vs = _token_stride("v", v, total, heads, d_v, index)
+    ks = _token_stride("k", k, total, heads, d_qk)
+    vs = _token_stride("v", v, total, heads, d_v)
     rot = positions = 0
     cs = qp = qo = None
     if cos_sin is not None:
-        if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or cos_sin.get_device() != index or \
-                not cos_sin.is_contiguous():
-            _bad(f"cos_sin must be a contiguous 2-D fp32 tensor on cuda:{index}")
+        if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            _bad("cos_sin must be a contiguous 2-D fp32 tensor")
         positions, rot = cos_sin.shape
         cs = cos_sin.data_ptr()
-    with _OnDevice(index, stream) as on:
-        heads_q = qs = 0
-        if q is not None:
-            shape = q.shape
-            heads_q = shape[1] if len(shape) == 3 else 0
-            qs = _token_stride("q", q, total, heads_q, d_qk, index)
-            if q_out is None:
-                q_out = on.empty(shape, torch.bfloat16)
-            elif q_out.dtype is not torch.bfloat16 or q_out.shape != shape or q_out.get_device() != index or \
-                    not q_out.is_contiguous():
-                _bad(f"q_out must be a contiguous bf16 tensor of q's shape on cuda:{index}")
-            qp, qo = q.data_ptr(), q_out.data_ptr()
-        elif q_out is not None:
-            _bad("q_out without q")
-        rc = load_library().fa_kv_append(cache, qp, k.data_ptr(), v.data_ptr(), qs, ks, vs, qo, cu_seqlens.data_ptr(),
-                                         batch, total, heads_q, cs, positions, rot, interleaved, on.ptr)
+    ptr, current = _call_stream(index, stream)
+    heads_q = qs = 0
+    if q is not None:
+        shape = q.shape
+        heads_q = shape[1] if len(shape) == 3 else 0
+        qs = _token_stride("q", q, total, heads_q, d_qk)
+        if q_out is None:
+            q_out = _empty(shape, torch.bfloat16, index, ptr, current)
+        elif q_out.dtype is not torch.bfloat16 or q_out.shape != shape or not q_out.is_contiguous():
+            _bad("q_out must be a contiguous bf16 tensor of q's shape")
+        qp, qo = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        _bad("q_out without q")
+    rc = load_library().fa_kv_append(cache, qp, k.data_ptr(), v.data_ptr(), qs, ks, vs, qo, cu_seqlens.data_ptr(), batch,
+                                     total, heads_q, cs, positions, rot, interleaved, ptr)
     if rc != FA_OK:
         raise FaError(rc, "fa_kv_append")
     return q_out
@@ -786,6 +778,10 @@ def attention_forward_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, 
     qd = q.shape
     if index < 0 or q.dtype is not torch.bfloat16 or len(qd) != 3 or not q.is_contiguous():
         _bad("q must be a contiguous 3-D bf16 CUDA tensor")
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return attention_forward_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, cu_seqlens_q,
+                                           max_seqlen_q, causal, scale, total_k, out, lse, return_lse, workspace, stream)
     cache, heads, d_qk, d_v, batch, capacity = _paged_cache(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k,
                                                             cu_seqlens_q, index)
     total_q, heads_q, d = qd
@@ -793,28 +789,26 @@ def attention_forward_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, 
         _bad(f"q must be [total_q, heads_q, {d_qk}]")
     if total_k is None:
         total_k = batch * capacity
-    with _OnDevice(index, stream) as on:
-        if out is None:
-            out = on.empty((total_q, heads_q, d_v), torch.bfloat16)
-        elif out.dtype is not torch.bfloat16 or out.shape != (total_q, heads_q, d_v) or out.get_device() != index or \
-                not out.is_contiguous():
-            _bad(f"out must be a contiguous bf16 tensor [total_q, heads_q, {d_v}] on cuda:{index}")
-        if lse is None:
-            if return_lse:
-                lse = on.empty((heads_q, total_q), torch.float32)
-        elif lse.dtype is not torch.float32 or lse.shape != (heads_q, total_q) or lse.get_device() != index or \
-                not lse.is_contiguous():
-            _bad(f"lse must be a contiguous fp32 tensor [heads_q, total_q] on cuda:{index}")
-        lib = load_library()
-        if workspace is None:
-            need = lib.fa_fwd_paged_workspace_size(batch, heads_q, heads, total_q, max_seqlen_q, total_k, d_qk, d_v)
-            workspace = on.empty((need or 16,), torch.uint8)
-        elif workspace.get_device() != index or not workspace.is_contiguous():
-            _bad(f"workspace must be a contiguous tensor on cuda:{index}")
-        rc = lib.fa_fwd_paged(q.data_ptr(), cache, out.data_ptr(), lse.data_ptr() if lse is not None else None,
-                              cu_seqlens_q.data_ptr(), batch, total_q, max_seqlen_q, total_k, heads_q,
-                              1 if causal else 0, 0.0 if scale is None else scale, workspace.data_ptr(),
-                              workspace.numel() * workspace.element_size(), on.ptr)
+    ptr, current = _call_stream(index, stream)
+    if out is None:
+        out = _empty((total_q, heads_q, d_v), torch.bfloat16, index, ptr, current)
+    elif out.dtype is not torch.bfloat16 or out.shape != (total_q, heads_q, d_v) or not out.is_contiguous():
+        _bad(f"out must be a contiguous bf16 tensor [total_q, heads_q, {d_v}]")
+    if lse is None:
+        if return_lse:
+            lse = _empty((heads_q, total_q), torch.float32, index, ptr, current)
+    elif lse.dtype is not torch.float32 or lse.shape != (heads_q, total_q) or not lse.is_contiguous():
+        _bad("lse must be a contiguous fp32 tensor [heads_q, total_q]")
+    if workspace is None:
+        size = _paged_workspace_bytes(batch, heads_q, heads, total_q, max_seqlen_q, total_k, d_qk, d_v)
+        workspace = _empty((size or 16,), torch.uint8, index, ptr, current)
+    else:
+        if not workspace.is_contiguous():
+            _bad("workspace must be contiguous")
+        size = workspace.numel() * workspace.element_size()
+    rc = load_library().fa_fwd_paged(q.data_ptr(), cache, out.data_ptr(), lse.data_ptr() if lse is not None else None,
+                                     cu_seqlens_q.data_ptr(), batch, total_q, max_seqlen_q, total_k, heads_q,
+                                     1 if causal else 0, 0.0 if scale is None else scale, workspace.data_ptr(), size, ptr)
     if rc != FA_OK:
         raise FaError(rc, "fa_fwd_paged")
     return (out, lse) if return_lse else out
