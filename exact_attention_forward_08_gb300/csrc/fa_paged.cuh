@@ -12,6 +12,7 @@ namespace fa {
 // sites of the status word (fa_device_status_detail)
 constexpr unsigned int kSitePagedSeq = 511;   // a sequence's offsets, length or position out of range (index: sequence)
 constexpr unsigned int kSitePagedPage = 512;  // a block-table entry out of range (index: sequence)
+constexpr unsigned int kSitePagedWait = 520;  // a bounded wait of paged_tc_kernel expired
 constexpr unsigned int kSitePagedTotal = 513; // the lengths sum to more than total_k (index: 0)
 
 // the smallest scale that the append writes: 2^-63

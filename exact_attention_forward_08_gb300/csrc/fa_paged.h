@@ -14,7 +14,7 @@ constexpr int kPagedMaxTeams = 8;     // most teams of a block
 constexpr int kPagedMaxBlocks = 160;  // most blocks of the attention kernel (one an SM)
 // Sequences with at most this many rows (new tokens x query heads a key head)
 // are read straight from the pages; longer ones are unpacked first.
-constexpr int kPagedRowLimit = 64;
+constexpr int kPagedRowLimit = 128;
 
 // fa_paged_append.cu
 int append_launch(const fa_kv_cache& c, const void* q, const void* k, const void* v, int64_t q_stride,

@@ -68,14 +68,14 @@ struct Workspace {
 };
 
 // rows of a team of the attention kernel's build for sequences of `rows` rows
-int team_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+int team_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 128; }
 
 Workspace workspace_of(int batch, int heads_q, int heads_kv, int64_t total_q, int64_t rows, int64_t total_k, int d_qk,
                        int d_v) {
   Workspace w;
   std::memset(&w, 0, sizeof(w));
   const int tr = team_rows(rows);
-  const size_t pieces = static_cast<size_t>(fa::kPagedMaxBlocks) * fa::kPagedMaxTeams;
+  const size_t pieces = static_cast<size_t>(fa::kPagedMaxBlocks) * (tr <= 16 ? fa::kPagedMaxTeams : 1);
   size_t at = up256(2 * pieces * tr * d_v * sizeof(float));
   w.part_ml = at;
   at += up256(2 * pieces * tr * sizeof(float2));
@@ -258,6 +258,7 @@ int fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse, c
   p.max_pages = c.max_pages;
   p.page_shift = page_shift(c.page_size);
   p.causal = causal ? 1 : 0;
+  p.timeout_ns = 1000000000ull;
   p.max_n = max_seqlen_q;
   p.row_limit = fa::kPagedRowLimit;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);

@@ -52,6 +52,7 @@ struct PagedParams {
   struct PagedJoin* joins;  // [pieces]
   int64_t total_q;
   int batch, heads_q, heads_kv, ratio, num_pages, max_pages, page_shift, causal;
+  unsigned long long timeout_ns;  // of a wait (paged_tc_kernel)
   int max_n;      // longest sequence of new tokens allowed
   int row_limit;  // sequences with more rows (new tokens x ratio) are not this kernel's
   float scale_log2;
@@ -83,6 +84,24 @@ struct PagedShape {
   static constexpr int kBytes = kTeams * kSlots * kSlotBytes + 128;
   static_assert(kSlots >= 3, "a tile in use and one under way");
 };
+
+// Bounded wait for an mbarrier phase; false after the time limit or an abort.
+// The clock is read only now and then: that takes longer than most waits here.
+__device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, const WaitCtx& w) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 0u) {
+      if (*w.abort_flag) return false;
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > w.timeout_ns) {
+        raise_abort(w, kStatusTimeout, kSitePagedWait);
+        return false;
+      }
+    }
+  }
+}
 
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -194,6 +213,90 @@ __device__ __forceinline__ void paged_next(const PagedParams& p, PagedCursor& c)
   } while (c.s.rows == 0);
 }
 
+// The line of tiles of all sequences and heads, and its equal pieces.
+struct PagedLine {
+  long long total, per, used;  // tiles, tiles of a piece, pieces that hold tiles
+  int teams_used;              // of a block
+  __device__ __forceinline__ long long piece(int team) const {
+    return static_cast<long long>(blockIdx.x) * teams_used + team;
+  }
+  __device__ __forceinline__ int count(int team) const {  // tiles of a team of this block
+    const long long left = total - piece(team) * per;
+    return team >= teams_used || left <= 0 ? 0 : static_cast<int>(left < per ? left : per);
+  }
+};
+
+// By all threads of the block: cuts the line, finds the places where this
+// block's pieces begin, and says that no piece leaves anything to join yet.
+// Ends with a barrier.
+template <int TILE, int THREADS, int TEAMS>
+__device__ __forceinline__ void paged_line(const PagedParams& p, long long* scan, long long* warp_sum,
+                                           PagedCursor* begin_at, PagedLine& line) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto scan_block = [&](int base) -> long long {  // inclusive scan of THREADS sequences' tiles into scan[]
+    const int b = base + tid;
+    long long v = 0;
+    if (b < p.batch) {
+      const PagedSeq s = paged_seq<TILE>(p, b);
+      if (s.bad && blockIdx.x == 0) paged_error(p.status, kSitePagedSeq, b);
+      v = s.rows > 0 ? static_cast<long long>(s.tiles) * p.heads_kv : 0;
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    if (lane == 31) warp_sum[warp] = v;
+    __syncthreads();
+    long long before = 0;
+    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    scan[tid] = before + v;
+    __syncthreads();
+    return scan[THREADS - 1];
+  };
+  line.total = 0;
+  for (int base = 0; base < p.batch; base += THREADS) line.total += scan_block(base);
+  const long long pieces = static_cast<long long>(gridDim.x) * TEAMS;
+  line.per = (line.total + pieces - 1) / pieces;
+  if (line.per < kMinTokens / TILE) line.per = kMinTokens / TILE;
+  if (line.per < 1) line.per = 1;
+  line.used = (line.total + line.per - 1) / line.per;
+  line.teams_used = static_cast<int>((line.used + gridDim.x - 1) / gridDim.x);
+
+  long long offset = 0;
+  for (int base = 0; base < p.batch; base += THREADS) {
+    if (p.batch > THREADS) scan_block(base);
+    const long long sum = scan[THREADS - 1];
+    if (tid < TEAMS && line.count(tid) > 0) {
+      const long long x = line.piece(tid) * line.per - offset;
+      if (x >= 0 && x < sum) {  // the first sequence whose inclusive sum exceeds x
+        int lo = 0, hi = THREADS - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (scan[mid] > x) hi = mid;
+          else lo = mid + 1;
+        }
+        PagedCursor c;
+        c.b = base + lo;
+        c.s = paged_seq<TILE>(p, c.b);
+        const long long in = x - (lo > 0 ? scan[lo - 1] : 0);
+        c.head = static_cast<int>(in / c.s.tiles);
+        c.tile = static_cast<int>(in - static_cast<long long>(c.head) * c.s.tiles);
+        begin_at[tid] = c;
+      }
+    }
+    offset += sum;
+    if (p.batch > THREADS) __syncthreads();
+  }
+  // pieces beyond the used ones are cleared in plain order
+  if (tid < TEAMS) {
+    if (line.count(tid) > 0) p.joins[line.piece(tid)].last = -1;
+    const long long plain = static_cast<long long>(blockIdx.x) * TEAMS + tid;
+    if (plain >= line.used) p.joins[plain].last = -1;
+  }
+  __syncthreads();
+}
+
 // G16: pages of 16 tokens, each with its own scale; else a scale holds for 32 tokens at least.
 template <int DQK, int DV, int NT, int TW, bool G16>
 __global__ void __launch_bounds__(PagedShape<DQK, DV, NT, TW>::kThreads, 1)
@@ -219,80 +322,14 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT, TW>::kThreads, 1)
   // let the merge kernel's blocks take their places early: they wait for this grid's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- the line of tiles: its length, and where this team's piece begins ----
-  auto scan_block = [&](int base) -> long long {  // inclusive scan of kThreads sequences' tiles into scan[]
-    const int b = base + tid;
-    long long v = 0;
-    if (b < p.batch) {
-      const PagedSeq s = paged_seq<kTile>(p, b);
-      if (s.bad && blockIdx.x == 0) paged_error(p.status, kSitePagedSeq, b);
-      v = s.rows > 0 ? static_cast<long long>(s.tiles) * p.heads_kv : 0;
-    }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += y;
-    }
-    if (lane == 31) warp_sum[warp] = v;
-    __syncthreads();
-    long long before = 0;
-    for (int w = 0; w < warp; ++w) before += warp_sum[w];
-    scan[tid] = before + v;
-    __syncthreads();
-    return scan[kThreads - 1];
-  };
-  long long total = 0;
-  for (int base = 0; base < p.batch; base += kThreads) total += scan_block(base);
-  const long long pieces = static_cast<long long>(gridDim.x) * kTeams;
-  long long per = (total + pieces - 1) / pieces;
-  if (per < kMinTokens / kTile) per = kMinTokens / kTile;
-  const long long used = (total + per - 1) / per;  // pieces that hold tiles
-  const int teams_used = static_cast<int>((used + gridDim.x - 1) / gridDim.x);  // of a block
-  // tiles of a team of this block
-  auto piece_of = [&](int team) { return static_cast<long long>(blockIdx.x) * teams_used + team; };
-  auto count_of = [&](int team) -> int {
-    const long long piece = piece_of(team), left = total - piece * per;
-    return team >= teams_used || left <= 0 ? 0 : static_cast<int>(left < per ? left : per);
-  };
-
-  long long offset = 0;
-  for (int base = 0; base < p.batch; base += kThreads) {
-    if (p.batch > kThreads) scan_block(base);
-    const long long sum = scan[kThreads - 1];
-    if (tid < kTeams && count_of(tid) > 0) {
-      const long long x = piece_of(tid) * per - offset;
-      if (x >= 0 && x < sum) {  // the first sequence whose inclusive sum exceeds x
-        int lo = 0, hi = kThreads - 1;
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (scan[mid] > x) hi = mid;
-          else lo = mid + 1;
-        }
-        PagedCursor c;
-        c.b = base + lo;
-        c.s = paged_seq<kTile>(p, c.b);
-        const long long in = x - (lo > 0 ? scan[lo - 1] : 0);
-        c.head = static_cast<int>(in / c.s.tiles);
-        c.tile = static_cast<int>(in - static_cast<long long>(c.head) * c.s.tiles);
-        begin_at[tid] = c;
-      }
-    }
-    offset += sum;
-    if (p.batch > kThreads) __syncthreads();
-  }
-  // every piece says first that it leaves nothing to join; pieces beyond the used ones are cleared in plain order
-  if (tid < kTeams) {
-    if (count_of(tid) > 0) p.joins[piece_of(tid)].last = -1;
-    const long long plain = static_cast<long long>(blockIdx.x) * kTeams + tid;
-    if (plain >= used) p.joins[plain].last = -1;
-  }
-  __syncthreads();  // starting places written
+  PagedLine line;
+  paged_line<kTile, kThreads, kTeams>(p, scan, warp_sum, begin_at, line);
 
   const int team = warp / TW, sub = warp % TW;
   const int g = lane >> 2, c = lane & 3;
-  const int count = count_of(team);
+  const int count = line.count(team);
   if (count == 0) return;
-  const long long piece = piece_of(team), begin = piece * per;
+  const long long piece = line.piece(team), begin = piece * line.per;
   PagedCursor cur = begin_at[team];
   const uint32_t ring = smem0 + team * kSlots * Shape::kSlotBytes;
 
@@ -700,7 +737,7 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT, TW>::kThreads, 1)
       if (!whole && started_here && sub == 0 && lane == 0) {
         // the rest of the unit lies in the pieces that follow
         PagedJoin j;
-        j.last = static_cast<int>((begin + i + (cur.s.tiles - 1 - cur.tile)) / per);
+        j.last = static_cast<int>((begin + i + (cur.s.tiles - 1 - cur.tile)) / line.per);
         j.cu0 = cur.s.cu0;
         j.head = cur.head;
         j.rows = cur.s.rows;

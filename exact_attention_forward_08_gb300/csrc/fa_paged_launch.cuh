@@ -4,30 +4,29 @@
 
 #include "fa_paged.h"
 #include "fa_paged_attn.cuh"
+#include "fa_paged_tc.cuh"
 
 namespace fa {
 
-template <int DQK, int DV, int NT, int TW, bool G16>
-int paged_launch(const PagedParams& p, int grid, cudaStream_t stream) {
-  using Shape = PagedShape<DQK, DV, NT, TW>;
+// Lets `kernel` use `smem` bytes of dynamic shared memory, once a device.
+inline int paged_allow_smem(const void* kernel, int smem, bool (&ready)[64]) {
   static std::mutex mutex;
-  static bool ready[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FA_ERR_CUDA;
-  {
-    std::lock_guard<std::mutex> lock(mutex);
-    if (!ready[dev]) {
-      if (cudaFuncSetAttribute(paged_attn_kernel<DQK, DV, NT, TW, G16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               Shape::kBytes) != cudaSuccess)
-        return FA_ERR_CUDA;
-      ready[dev] = true;
-    }
+  std::lock_guard<std::mutex> lock(mutex);
+  if (!ready[dev]) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      return FA_ERR_CUDA;
+    ready[dev] = true;
   }
-  paged_attn_kernel<DQK, DV, NT, TW, G16><<<grid, Shape::kThreads, Shape::kBytes, stream>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  // the merge's blocks may be placed while the attention kernel still runs; they wait for its end
+  return FA_OK;
+}
+
+// The merge's blocks may be placed while the attention kernel still runs; they wait for its end.
+template <int DV, int ROWS>
+int paged_merge_launch(const PagedParams& p, int pieces, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid * Shape::kTeams, Shape::kRows / 8, 1);
+  cfg.gridDim = dim3(pieces, ROWS / 8, 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -35,17 +34,39 @@ int paged_launch(const PagedParams& p, int grid, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, paged_merge_kernel<DV, Shape::kRows>, p) != cudaSuccess) return FA_ERR_CUDA;
-  return FA_OK;
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<DV, ROWS>, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-// rows of a team: the smallest build that holds a sequence's rows, at most 64.
+template <int DQK, int DV, int NT, int TW, bool G16>
+int paged_launch(const PagedParams& p, int grid, cudaStream_t stream) {
+  using Shape = PagedShape<DQK, DV, NT, TW>;
+  static bool ready[64] = {};
+  auto* kernel = paged_attn_kernel<DQK, DV, NT, TW, G16>;
+  const int rc = paged_allow_smem(reinterpret_cast<const void*>(kernel), Shape::kBytes, ready);
+  if (rc != FA_OK) return rc;
+  kernel<<<grid, Shape::kThreads, Shape::kBytes, stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  return paged_merge_launch<DV, Shape::kRows>(p, grid * Shape::kTeams, stream);
+}
+
+template <int DQK, int DV>
+int paged_tc_launch(const PagedParams& p, int grid, cudaStream_t stream) {
+  using Shape = TcShape<DQK, DV>;
+  static bool ready[64] = {};
+  auto* kernel = paged_tc_kernel<DQK, DV>;
+  const int rc = paged_allow_smem(reinterpret_cast<const void*>(kernel), Shape::kBytes, ready);
+  if (rc != FA_OK) return rc;
+  kernel<<<grid, Shape::kThreads, Shape::kBytes, stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  return paged_merge_launch<DV, Shape::kRows>(p, grid, stream);
+}
+
+// rows: the most that a sequence has
 template <int DQK, int DV, bool G16>
 int paged_launch_rows(const PagedParams& p, int rows, int grid, cudaStream_t stream) {
   if (rows <= 8) return paged_launch<DQK, DV, 1, 1, G16>(p, grid, stream);
   if (rows <= 16) return paged_launch<DQK, DV, 2, 1, G16>(p, grid, stream);
-  if (rows <= 32) return paged_launch<DQK, DV, 2, 2, G16>(p, grid, stream);
-  return paged_launch<DQK, DV, 2, 4, G16>(p, grid, stream);
+  return paged_tc_launch<DQK, DV>(p, grid, stream);
 }
 
 template <int DQK, int DV>

@@ -495,11 +495,11 @@ int fa_kv_append(const fa_kv_cache* cache, const void* q, const void* k, const v
  *   j <= i + seqlens_k[b] - n.  A row without a key gets O = 0, lse = -inf.
  *   max_seqlen_q: an upper limit of the new tokens of a sequence (a longer one
  *   is left out: site 511).  total_k: an upper limit of the sum of seqlens_k;
- *   it bounds the workspace where max_seqlen_q * heads_q / heads_kv > 64 and
+ *   it bounds the workspace where max_seqlen_q * heads_q / heads_kv > 128 and
  *   is not used below (a larger sum: nothing of the longer sequences is
  *   computed, site 513).
  *
- * Sequences of up to 64 rows (new tokens x query heads a key/value head) are
+ * Sequences of up to 128 rows (new tokens x query heads a key/value head) are
  * computed straight from the pages, their keys split over the whole GPU;
  * longer ones are unpacked to bf16 (exactly) in the workspace and run through
  * fa_fwd_varlen's kernel.  Both kinds may be in one batch.

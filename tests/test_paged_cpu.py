@@ -106,10 +106,10 @@ def test_workspace_size(fa):
     one = size(1, 8, 2, 1, 1, 1, 128, 128)
     # single tokens: independent of the batch and of the keys
     assert one == size(500, 8, 2, 500, 1, 1 << 30, 128, 128) and 0 < one < 64 << 20
-    # 16 tokens x 4 heads are read from the pages, 17 are unpacked: room for the keys and values in bf16
-    few, many = size(2, 8, 2, 32, 16, 5000, 128, 128), size(2, 8, 2, 34, 17, 5000, 128, 128)
-    assert many >= few + 5000 * 2 * (128 + 128) * 2 + fa.fa_varlen_workspace_size(2, 8, 34)
-    assert many == size(2, 8, 2, 34, 1000, 5000, 128, 128)
+    # 32 tokens x 4 heads are read from the pages, 33 are unpacked: room for the keys and values in bf16
+    few, many = size(2, 8, 2, 64, 32, 5000, 128, 128), size(2, 8, 2, 66, 33, 5000, 128, 128)
+    assert many >= few + 5000 * 2 * (128 + 128) * 2 + fa.fa_varlen_workspace_size(2, 8, 66)
+    assert many == size(2, 8, 2, 66, 1000, 5000, 128, 128)
 
 
 def test_python_checks_want_cuda_tensors(fa):
