@@ -12,16 +12,19 @@
 // is cut into equal pieces, one for each block; cut (sequence, head)s are
 // joined by paged_merge_kernel.  Roles of a block (one per SM):
 //   warps 0-3   softmax: thread = row = TMEM lane.  The reference of a row
-//               follows its maximum when it lags by more than 2^8; O is then
-//               rescaled in place by the same threads.
-//   warps 4-11  codes to operands: each thread copies its 16-byte chunks to
-//               shared memory some tiles ahead, converts them and writes them
+//               follows its maximum when it lags by more than 2^8; so a tile's
+//               weights are formed with the reference there is, in one pass
+//               over S, and once more in the rare case that it has to move (O
+//               is then rescaled in place by the same threads).
+//   warp 4      issues the MMAs, S of the next tile before P V of this one.
+//   warps 5-20  codes to operands: each thread copies its 16-byte chunks to
+//               shared memory two tiles ahead, converts them and writes them
 //               in the tensor cores' swizzled layout.
-//   warp 12     issues the MMAs, S of the next tile before P V of this one.
-// TMEM: S of even and odd tiles (P over their first half), O.  What bounds it:
+// TMEM: S of even and odd tiles, O, P of even and odd tiles.  What bounds it:
 // per 128 tokens and head 32 KB of codes come in (about 1400 cycles at this
 // GPU's bandwidth), the two products take about 1000 cycles, the exponentials
-// of a warp of rows 1024, the shared memory carries 230 KB (1800 cycles).
+// of a warp of rows 1024, the shared memory carries 230 KB (1800 cycles), and
+// the conversion issues about 1200 instructions a scheduler.
 #pragma once
 #include "fa_paged_attn.cuh"
 
@@ -30,17 +33,22 @@ namespace fa {
 template <int DQK, int DV>
 struct TcShape {
   static constexpr int kTile = 128, kRows = 128;
-  static constexpr int kFillWarps = 8, kFillThreads = 32 * kFillWarps;
-  static constexpr int kThreads = 128 + kFillThreads + 32;
-  static constexpr int kChunk = 128 * 128;               // 128 rows of 64 operands, swizzled
+  static constexpr int kFillWarps = 16, kFillThreads = 32 * kFillWarps;
+  static constexpr int kMmaWarp = 4, kFillWarp0 = 5;
+  static constexpr int kThreads = 32 * (kFillWarp0 + kFillWarps);
+  static constexpr int kChunk = 128 * 128;  // 128 rows of 64 operands, swizzled
   static constexpr int kQBytes = DQK / 64 * kChunk;
-  static constexpr int kSlotBytes = DQK / 64 * kChunk;   // a K tile or a V tile
+  // operand slots, K and V tiles by turns: three, or with wide keys one of each kind
   static constexpr int kSlots = DQK == 192 ? 2 : 3;
-  static constexpr int kCodeBytes = kTile * DQK;         // codes of a K tile or a V tile
-  static constexpr int kCodes = DQK == 192 ? 3 : DQK == 128 ? 4 : 8;  // of them under way
-  static constexpr int oRing = kQBytes, oCodes = oRing + kSlots * kSlotBytes;
+  static constexpr int kKBytes = DQK / 64 * kChunk, kVBytes = DV / 64 * kChunk;
+  static constexpr int kRingBytes = kSlots == 3 ? 3 * kKBytes : kKBytes + kVBytes;
+  static __device__ __forceinline__ int slot_offset(int slot) { return slot * kKBytes; }
+  static constexpr int kCodeBytes = kTile * (DQK + DV);  // codes of a tile
+  static constexpr int kCodes = 2;                       // tiles under way
+  static constexpr int oRing = kQBytes, oCodes = oRing + kRingBytes;
   static constexpr int kBytes = oCodes + kCodes * kCodeBytes + 1024;
-  static_assert(kBytes <= 227 * 1024 - 2048, "shared memory");
+  static_assert(kBytes <= 227 * 1024 - 10 * 1024, "shared memory");
+  static constexpr uint32_t kColO = 256, kColP = 384;  // TMEM columns (S: 0 and 128)
 };
 
 // two e4m3 codes as f16, times a scale, as bf16 (exact)
@@ -79,7 +87,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
   if (tid == 0) {
     abort_flag = 0;
     for (int i = 0; i < L::kSlots; ++i) {
-      mbar_init(kv_full(i), L::kFillThreads);
+      mbar_init(kv_full(i), L::kFillWarps);
       mbar_init(kv_empty(i), 1);
     }
     mbar_init(bar_q, 128);
@@ -91,7 +99,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
     }
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == L::kMmaWarp) {
     tmem_alloc(smem_u32(&tmem_base), 512);
     tmem_relinquish();
   }
@@ -118,7 +126,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
       PagedCursor cur = begin_at;
       const long long piece = line.piece(0);
       const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-      const uint32_t t_o = t_lane + 256;
+      const uint32_t t_o = t_lane + L::kColO;
       const int r = tid;
       float fac = 0.f, ref = -INFINITY, sum = 0.f;
       int limit = 0, min_limit = 0;
@@ -189,80 +197,83 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (active) {
-          const uint32_t t_s = t_lane + 128 * buf;
-          float f[8];
-#pragma unroll
-          for (int g = 0; g < 8; ++g) f[g] = fac * k_scales[i & 3][g];
-          uint32_t bad[4] = {0, 0, 0, 0};
-          if (masked) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) bad[w] = poison[i & 7][w];
-          }
-          // maximum
-          float mx = -INFINITY;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t s[64];
-            tmem_ld64_wait(t_s + 64 * h, s);
-            if (masked) {
-#pragma unroll
-              for (int c = 0; c < 64; ++c)
-                if (token0 + 64 * h + c >= limit) s[c] = 0xff800000u;
-            }
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              float m = __uint_as_float(s[16 * g]);
-#pragma unroll
-              for (int c = 1; c < 15; c += 2) m = fmax3(m, __uint_as_float(s[16 * g + c]), __uint_as_float(s[16 * g + c + 1]));
-              m = fmaxf(m, __uint_as_float(s[16 * g + 15]));
-              if (m != -INFINITY) mx = fmaxf(mx, m * f[4 * h + g]);
-            }
-          }
-          float alpha = 1.f;
-          if (mx > ref + kRefLag) {  // also from -inf
-            alpha = ex2_approx(ref - mx);
-            ref = mx;
-          }
-          if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
-            // P V of the tile before has to be in O
-            ok = __all_sync(0xffffffffu, tc_wait(bar_o, (i - 1) & 1, wc));
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < DV; c += 32) {
-              uint32_t v[32];
-              tmem_ld32_wait(t_o + c, v);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
-              tmem_st32(t_o + c, v);
-            }
-            tmem_wait_st();
-          }
-          sum *= alpha;
-          const float back = ref == -INFINITY ? 0.f : -ref;
-          // weights
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t s[64];
-            tmem_ld64_wait(t_s + 64 * h, s);
+          const uint32_t t_s = t_lane + 128 * buf, t_p = t_lane + L::kColP + 64 * buf;
+          float mx = -INFINITY, part = 0.f;
+          // weights of the tile with the present reference, their sum, and the scores' maximum
+          auto weights = [&](auto with_mask) {
+            constexpr bool kMask = decltype(with_mask)::value;
+            const float back = ref == -INFINITY ? 0.f : -ref;
             float e0 = 0.f, e1 = 0.f;
+            mx = -INFINITY;
+#pragma unroll 1
+            for (int g = 0; g < 4; ++g) {
+              uint32_t s[32];
+              tmem_ld32_wait(t_s + 32 * g, s);
+              const float2 ks = *reinterpret_cast<const float2*>(&k_scales[i & 3][2 * g]);
+              const float f0 = fac * ks.x, f1 = fac * ks.y;
+              const uint32_t bad = kMask ? poison[i & 7][g] : 0u;
+              const int left = kMask ? limit - token0 - 32 * g : 32;  // columns that the row sees
+              float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 64; ++c) {
-              float e = ex2_approx(fmaf(__uint_as_float(s[c]), f[4 * h + c / 16], back));
-              if (masked) {
-                if ((bad[2 * h + c / 32] >> (c % 32)) & 1) e = __uint_as_float(0x7fc00000u);
-                if (token0 + 64 * h + c >= limit) e = 0.f;
+              for (int c = 0; c < 16; c += 2) {
+                if (kMask) {
+                  if (c < left) m0 = fmaxf(m0, __uint_as_float(s[c]));
+                  if (c + 1 < left) m0 = fmaxf(m0, __uint_as_float(s[c + 1]));
+                  if (c + 16 < left) m1 = fmaxf(m1, __uint_as_float(s[c + 16]));
+                  if (c + 17 < left) m1 = fmaxf(m1, __uint_as_float(s[c + 17]));
+                } else {
+                  m0 = fmax3(m0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+                  m1 = fmax3(m1, __uint_as_float(s[c + 16]), __uint_as_float(s[c + 17]));
+                }
               }
-              if (c & 1) e1 += e;
-              else e0 += e;
-              s[c] = __float_as_uint(e);
-            }
-            sum += e0 + e1;
-            uint32_t pk[32];
+              if (m0 != -INFINITY) mx = fmaxf(mx, m0 * f0);
+              if (m1 != -INFINITY) mx = fmaxf(mx, m1 * f1);
+              uint32_t pk[16];
 #pragma unroll
-            for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
-            tmem_st32(t_s + 32 * h, pk);
+              for (int c = 0; c < 32; c += 2) {
+                const float f = c < 16 ? f0 : f1;
+                float a = ex2_approx(fmaf(__uint_as_float(s[c]), f, back));
+                float b = ex2_approx(fmaf(__uint_as_float(s[c + 1]), f, back));
+                if (kMask) {
+                  if ((bad >> c) & 1) a = __uint_as_float(0x7fc00000u);
+                  if ((bad >> (c + 1)) & 1) b = __uint_as_float(0x7fc00000u);
+                  if (c >= left) a = 0.f;
+                  if (c + 1 >= left) b = 0.f;
+                }
+                e0 += a;
+                e1 += b;
+                pk[c / 2] = pack_bf16x2(a, b);
+              }
+              tmem_st16(t_p + 16 * g, pk);
+            }
+            part = e0 + e1;
+          };
+          if (masked) weights(std::true_type{});
+          else weights(std::false_type{});
+          const bool move = mx > ref + kRefLag;  // also from -inf
+          if (__any_sync(0xffffffffu, move)) {
+            const float alpha = move ? ex2_approx(ref - mx) : 1.f;
+            if (move) ref = mx;
+            sum *= alpha;
+            if (!first) {
+              // P V of the tile before has to be in O
+              ok = __all_sync(0xffffffffu, tc_wait(bar_o, (i - 1) & 1, wc));
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < DV; c += 32) {
+                uint32_t v[32];
+                tmem_ld32_wait(t_o + c, v);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+                tmem_st32(t_o + c, v);
+              }
+            }
+            tmem_wait_st();  // also of the first weights, which are written again
+            if (masked) weights(std::true_type{});
+            else weights(std::false_type{});
           }
+          sum += part;
           tmem_wait_st();
         }
         tc_fence_before();
@@ -288,7 +299,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
             const int64_t token = cur.s.cu0 + pos;
             const float rf = sum != 0.f && ref == -INFINITY ? 0.f : ref;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < DV; c += 32) {
               uint32_t v[32];
               tmem_ld32_wait(t_o + c, v);
@@ -320,11 +331,11 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
         }
         if (i + 1 < count) paged_next<kTile>(p, cur);
       }
-    } else if (warp < 12) {
+    } else if (warp >= L::kFillWarp0) {
       // ======== codes to operands ========
-      const int ft = tid - 128;
+      const int ft = tid - 32 * L::kFillWarp0;
       PagedCursor ahead = begin_at, cur = begin_at;  // the tiles that are copied and converted next
-      int copied = 0;                                // entries (K, V by turns) under way or done
+      int copied = 0;                                // tiles under way or done
       int page0 = 0, entry = 0;
       auto load_pages = [&](int first_page) {
         page0 = first_page;
@@ -338,85 +349,68 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
         }
       };
       load_pages((ahead.tile * kTile) >> p.page_shift);
-      // a thread's chunk number i of an entry: row and 16-code column
-      auto copy = [&](auto is_k) {
+      // this thread's chunks of a tile's K or V: row and 16-code column of chunk number k
+      auto copy = [&](auto is_k, uint32_t dst) {
         constexpr bool kK = decltype(is_k)::value;
         constexpr int D = kK ? DQK : DV, kChunks = D / 16, kPer = kTile * kChunks / L::kFillThreads;
         const uint8_t* base = kK ? p.k + ahead.head * p.k_head : p.v + ahead.head * p.v_head;
         const int64_t page_stride = kK ? p.k_page : p.v_page;
         const uint32_t ts = kK ? p.k_token : p.v_token;
-        const uint32_t dst = smem0 + L::oCodes + (copied % L::kCodes) * L::kCodeBytes + ft * 16;
         const int token0 = ahead.tile * kTile;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int at = i * L::kFillThreads + ft, row = at / kChunks, chunk = at % kChunks;
+        for (int k = 0; k < kPer; ++k) {
+          const int at = k * L::kFillThreads + ft, row = at / kChunks, chunk = at % kChunks;
           const int t = token0 + row;
-          const int src_lane = (t >> p.page_shift) - page0;
-          const int e = __shfl_sync(0xffffffffu, entry, src_lane & 31);
+          const int e = __shfl_sync(0xffffffffu, entry, ((t >> p.page_shift) - page0) & 31);
           if (t < ahead.s.len)
-            cp_async16(dst + i * L::kFillThreads * 16,
+            cp_async16(dst + k * L::kFillThreads * 16,
                        base + e * page_stride + static_cast<uint32_t>(t & ((1 << p.page_shift) - 1)) * ts + chunk * 16);
         }
       };
-      auto fetch = [&]() {  // the next entry
-        if (copied < 2 * count) {
-          if ((copied & 1) == 0) {
-            copy(std::true_type{});
-          } else {
-            copy(std::false_type{});
-            if (copied + 1 < 2 * count) {
-              const int b = ahead.b, head = ahead.head;
-              paged_next<kTile>(p, ahead);
-              const int next = (ahead.tile * kTile) >> p.page_shift;
-              if (ahead.b != b || (ahead.head != head && page0 != 0) || next < page0 || next + kTile / 16 > page0 + 32)
-                load_pages(next);
-            }
+      // The next tile's codes, and in lanes 0 .. 7 its scales, one for 16 tokens.
+      int ek = 127, ev = 127, ek_next = 127, ev_next = 127;
+      auto fetch = [&]() {
+        ek_next = ev_next = 127;
+        if (copied < count) {
+          const uint32_t dst = smem0 + L::oCodes + (copied & 1) * L::kCodeBytes + ft * 16;
+          copy(std::true_type{}, dst);
+          copy(std::false_type{}, dst + kTile * DQK);
+          const int token = ahead.tile * kTile + 16 * (lane & 7);
+          const int e = __shfl_sync(0xffffffffu, entry, ((token >> p.page_shift) - page0) & 31);
+          if (lane < 8 && token < ahead.s.len) {
+            const int64_t at = static_cast<int64_t>(e) * p.heads_kv + ahead.head;
+            ek_next = p.k_scale[at];
+            ev_next = p.v_scale[at];
+          }
+          if (copied + 1 < count) {
+            const int b = ahead.b, head = ahead.head;
+            paged_next<kTile>(p, ahead);
+            const int next = (ahead.tile * kTile) >> p.page_shift;
+            if (ahead.b != b || (ahead.head != head && page0 != 0) || next + kTile / 16 > page0 + 32) load_pages(next);
           }
         }
         ++copied;
-        cp_async_commit();  // a group for each entry, empty ones at the end
+        cp_async_commit();  // a group for each tile, empty ones at the end
       };
-      // lanes 0 .. 7: the scales of the tile that is converted next, one for 16 tokens
-      int ek = 127, ev = 127;
-      auto load_scales = [&]() {
-        const int token = cur.tile * kTile + 16 * lane;
-        ek = ev = 127;
-        if (lane < 8 && token < cur.s.len) {
-          int page = p.table[cur.b * p.table_stride + (token >> p.page_shift)];
-          if (page < 0 || page >= p.num_pages) page = 0;
-          const int64_t at = static_cast<int64_t>(page) * p.heads_kv + cur.head;
-          ek = p.k_scale[at];
-          ev = p.v_scale[at];
-        }
-      };
-      for (int e = 0; e < L::kCodes - 1; ++e) fetch();
-      load_scales();
+      fetch();
+      ek = ek_next, ev = ev_next;
+      fetch();
       bool ok = true;
-      for (int e = 0; e < 2 * count && ok; ++e) {
-        const bool is_k = (e & 1) == 0;
-        const int i = e >> 1, slot = e % L::kSlots, use = e / L::kSlots;
+      for (int i = 0; i < count && ok; ++i) {
         const int token0 = cur.tile * kTile;
         const bool masked = token0 + kTile > least_limit(cur.s);
-        fetch();
-        cp_async_wait<L::kCodes - 1>();
-        if (use > 0) ok = __all_sync(0xffffffffu, tc_wait(kv_empty(slot), (use - 1) & 1, wc));
-        if (!ok) break;
-        const float scale = is_k ? (ev == 255 ? scale_of(255) : scale_of(ek))  // NaN in either: NaN scores
-                                 : (ev == 255 ? 1.f : scale_of(ev));
-        if (is_k && ft < 8) k_scales[i & 3][ft] = scale;
-        // cleared for a tile far enough ahead that neither its conversion has begun nor the softmax of the last
-        // tile that used these words is still under way
-        if (!is_k && ft < 4) poison[(i + 4) & 7][ft] = 0;
-        const uint32_t tile = smem0 + L::oRing + slot * L::kSlotBytes;
-        const uint32_t codes = smem0 + L::oCodes + (e % L::kCodes) * L::kCodeBytes + ft * 16;
-        auto convert = [&](auto kind) {
+        cp_async_wait<1>();
+        const uint32_t codes = smem0 + L::oCodes + (i & 1) * L::kCodeBytes + ft * 16;
+        const float ks = ev == 255 ? scale_of(255) : scale_of(ek);  // NaN in either: NaN scores
+        const float vs = ev == 255 ? 1.f : scale_of(ev);
+        auto convert = [&](auto kind, uint32_t from, uint32_t tile) {
           constexpr bool kK = decltype(kind)::value;
           constexpr int D = kK ? DQK : DV, kChunks = D / 16, kPer = kTile * kChunks / L::kFillThreads;
 #pragma unroll
           for (int k = 0; k < kPer; ++k) {
             const int at = k * L::kFillThreads + ft, row = at / kChunks, chunk = at % kChunks;
-            const float vs = kK ? 1.f : __shfl_sync(0xffffffffu, scale, row >> 4);
-            const uint4 v = lds128(codes + k * L::kFillThreads * 16);
+            const float scale = kK ? 1.f : __shfl_sync(0xffffffffu, vs, row >> 4);
+            const uint4 v = lds128(from + k * L::kFillThreads * 16);
             uint32_t w[4] = {v.x, v.y, v.z, v.w};
             if (!kK && masked) {  // hidden from some row: no value may be NaN
               const bool inside = token0 + row < cur.s.len;
@@ -435,8 +429,8 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
               f[2 * x] = e4m3x2_f16x2(w[x]);
               f[2 * x + 1] = e4m3x2_hi_f16x2(w[x]);
               if constexpr (!kK) {
-                f[2 * x] = scaled_bf16x2(f[2 * x], vs);
-                f[2 * x + 1] = scaled_bf16x2(f[2 * x + 1], vs);
+                f[2 * x] = scaled_bf16x2(f[2 * x], scale);
+                f[2 * x + 1] = scaled_bf16x2(f[2 * x + 1], scale);
               }
             }
             // two groups of 8 operands; lanes of the right half write their second first (banks)
@@ -454,14 +448,28 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
             }
           }
         };
-        if (is_k) convert(std::true_type{});
-        else convert(std::false_type{});
-        fence_proxy_async_smem();
-        mbar_arrive(kv_full(slot));
-        if (!is_k && i + 1 < count) {
-          paged_next<kTile>(p, cur);
-          load_scales();
-        }
+        // entry 2 i (K) and 2 i + 1 (V) of the ring: free once the MMA on its last use is done
+        auto put = [&](auto kind, int e, uint32_t from) -> bool {
+          const int slot = e % L::kSlots, use = e / L::kSlots;
+          if (use > 0 && !__all_sync(0xffffffffu, tc_wait(kv_empty(slot), (use - 1) & 1, wc))) return false;
+          if (decltype(kind)::value) {
+            if (ft < 8) k_scales[i & 3][ft] = ks;
+          } else if (ft < 4) {
+            // cleared for a tile far enough ahead that neither its conversion has begun nor the softmax of the
+            // last tile that used these words is still under way
+            poison[(i + 4) & 7][ft] = 0;
+          }
+          convert(kind, from, smem0 + L::oRing + L::slot_offset(slot));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(kv_full(slot));
+          return true;
+        };
+        ok = put(std::true_type{}, 2 * i, codes) && put(std::false_type{}, 2 * i + 1, codes + kTile * DQK);
+        if (!ok) break;
+        ek = ek_next, ev = ev_next;
+        fetch();
+        if (i + 1 < count) paged_next<kTile>(p, cur);
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
@@ -473,7 +481,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
       auto wait_entry = [&](int e) { return wait(kv_full(e % L::kSlots), (e / L::kSlots) & 1); };
       auto issue_s = [&](int i) {  // S of tile i; its K slot is free after it
         const int slot = (2 * i) % L::kSlots;
-        const uint32_t k_at = smem0 + L::oRing + slot * L::kSlotBytes;
+        const uint32_t k_at = smem0 + L::oRing + L::slot_offset(slot);
 #pragma unroll
         for (int c = 0; c < DQK / 64; ++c) {
           const uint32_t co = opaque_u32(static_cast<uint32_t>(c * L::kChunk));
@@ -505,12 +513,12 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const int slot = (2 * i + 1) % L::kSlots;
-        const uint32_t v_at = smem0 + L::oRing + slot * L::kSlotBytes;
+        const uint32_t v_at = smem0 + L::oRing + L::slot_offset(slot);
         const bool begun = i != 0 && cur.tile != 0;  // O holds tiles of this unit
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t va = opaque_u32(v_at + static_cast<uint32_t>(h * 64 * 128));
-          mma_ts_x4<(16 * 128 >> 4)>(tmem + 256, tmem + 128 * (i & 1) + 32 * h, smem_desc_sw128(va, L::kChunk, 1024),
+          mma_ts_x4<(16 * 128 >> 4)>(tmem + L::kColO, tmem + L::kColP + 64 * (i & 1) + 32 * h, smem_desc_sw128(va, L::kChunk, 1024),
                                      kIdescO, h != 0 || begun ? 1u : 0u, leader);
         }
         mma_commit(bar_o, leader);
@@ -530,7 +538,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == L::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
