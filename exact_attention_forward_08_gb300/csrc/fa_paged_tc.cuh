@@ -3,10 +3,15 @@
 // tiles, which cost the same for any number of rows and read each key once.
 //
 //     S[128 rows x 128 tokens] = Q K^T,   O[128 rows x DV] += P V
-// K codes become f16 exactly; a query row is divided by a power of two first
-// (f16 then holds its bf16 values), and the keys' scales, one for 16 tokens,
-// multiply the scores.  V codes times their scales are bf16 numbers exactly;
-// P is rounded to bf16 for that product.  S, maxima, sums and O are fp32.
+// Codes become f16 exactly; a query row is divided by a power of two first (f16
+// then holds its bf16 values), and the keys' scales, one for 16 tokens,
+// multiply the scores.  The values' scales are powers of two too: they go into
+// the exponents of the weights, P' = 2^(x - m + k - k0) with k the scale's
+// exponent and 2^k0 the unit that O is kept in, rounded to f16.  That holds for
+// scales between 2^(k0-3) and 2^(k0+6) (weights then lose bits only below
+// 2^-11 of the largest, vanish below 2^-21); a tile with others ("wide") takes its
+// V as code * 2^(k-k0) and its P in bf16, which has the exponents for them.
+// S, maxima, sums and O are fp32.
 //
 // Work: the tiles of 128 tokens of all sequences and heads form one line that
 // is cut into equal pieces, one for each block; cut (sequence, head)s are
@@ -17,14 +22,14 @@
 //               over S, and once more in the rare case that it has to move (O
 //               is then rescaled in place by the same threads).
 //   warp 4      issues the MMAs, S of the next tile before P V of this one.
-//   warps 5-20  codes to operands: each thread copies its 16-byte chunks to
+//   warps 5-12  codes to operands: each thread copies its 16-byte chunks to
 //               shared memory two tiles ahead, converts them and writes them
 //               in the tensor cores' swizzled layout.
 // TMEM: S of even and odd tiles, O, P of even and odd tiles.  What bounds it:
 // per 128 tokens and head 32 KB of codes come in (about 1400 cycles at this
 // GPU's bandwidth), the two products take about 1000 cycles, the exponentials
 // of a warp of rows 1024, the shared memory carries 230 KB (1800 cycles), and
-// the conversion issues about 1200 instructions a scheduler.
+// the conversion issues about 600 instructions a scheduler.
 #pragma once
 #include "fa_paged_attn.cuh"
 
@@ -33,7 +38,7 @@ namespace fa {
 template <int DQK, int DV>
 struct TcShape {
   static constexpr int kTile = 128, kRows = 128;
-  static constexpr int kFillWarps = 16, kFillThreads = 32 * kFillWarps;
+  static constexpr int kFillWarps = 8, kFillThreads = 32 * kFillWarps;
   static constexpr int kMmaWarp = 4, kFillWarp0 = 5;
   static constexpr int kThreads = 32 * (kFillWarp0 + kFillWarps);
   static constexpr int kChunk = 128 * 128;  // 128 rows of 64 operands, swizzled
@@ -57,6 +62,19 @@ __device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t f16x2, float scale) {
   return pack_bf16x2(x.x * scale, x.y * scale);
 }
 
+// 2^k for any k, 0 or infinity beyond fp32
+__device__ __forceinline__ float pow2(int k) {
+  const float a = __uint_as_float(static_cast<uint32_t>((k >> 1) + 127) << 23);
+  return a * __uint_as_float(static_cast<uint32_t>(k - (k >> 1) + 127) << 23);
+}
+
+// What the roles know of a tile's scales, one for 16 tokens.
+struct TcTile {
+  float ks[8];   // of the keys
+  int vk[8];     // of the values: k - k0
+  int wide, k0;
+};
+
 template <int DQK, int DV>
 __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
     paged_tc_kernel(const __grid_constant__ PagedParams p) {
@@ -64,7 +82,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
   constexpr int kTile = L::kTile;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * L::kSlots + 7];
-  __shared__ float k_scales[4][8];        // of a tile's 16-token groups, for four tiles
+  __shared__ __align__(16) TcTile tiles[4];  // of four tiles
   __shared__ uint32_t poison[8][4];       // tokens of a masked tile whose values hold a NaN, for eight tiles
   __shared__ PagedCursor begin_at;
   __shared__ long long scan[L::kThreads];
@@ -129,7 +147,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
       const uint32_t t_o = t_lane + L::kColO;
       const int r = tid;
       float fac = 0.f, ref = -INFINITY, sum = 0.f;
-      int limit = 0, min_limit = 0;
+      int limit = 0, min_limit = 0, unit_k0 = 0;
       bool started_here = false;
       bool ok = true;
       for (int i = 0; i < count && ok; ++i) {
@@ -198,19 +216,25 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
         tc_fence_after();
         if (active) {
           const uint32_t t_s = t_lane + 128 * buf, t_p = t_lane + L::kColP + 64 * buf;
+          const bool wide = tiles[i & 3].wide != 0;
+          if (first) unit_k0 = tiles[i & 3].k0;
           float mx = -INFINITY, part = 0.f;
           // weights of the tile with the present reference, their sum, and the scores' maximum
           auto weights = [&](auto with_mask) {
             constexpr bool kMask = decltype(with_mask)::value;
             const float back = ref == -INFINITY ? 0.f : -ref;
-            float e0 = 0.f, e1 = 0.f;
             mx = -INFINITY;
+            part = 0.f;
 #pragma unroll 1
             for (int g = 0; g < 4; ++g) {
               uint32_t s[32];
               tmem_ld32_wait(t_s + 32 * g, s);
-              const float2 ks = *reinterpret_cast<const float2*>(&k_scales[i & 3][2 * g]);
+              const float2 ks = *reinterpret_cast<const float2*>(&tiles[i & 3].ks[2 * g]);
+              const int2 vk = *reinterpret_cast<const int2*>(&tiles[i & 3].vk[2 * g]);
               const float f0 = fac * ks.x, f1 = fac * ks.y;
+              const float back0 = wide ? back : back + static_cast<float>(vk.x);
+              const float back1 = wide ? back : back + static_cast<float>(vk.y);
+              float e0 = 0.f, e1 = 0.f;
               const uint32_t bad = kMask ? poison[i & 7][g] : 0u;
               const int left = kMask ? limit - token0 - 32 * g : 32;  // columns that the row sees
               float m0 = -INFINITY, m1 = -INFINITY;
@@ -228,25 +252,28 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
               }
               if (m0 != -INFINITY) mx = fmaxf(mx, m0 * f0);
               if (m1 != -INFINITY) mx = fmaxf(mx, m1 * f1);
-              uint32_t pk[16];
 #pragma unroll
-              for (int c = 0; c < 32; c += 2) {
-                const float f = c < 16 ? f0 : f1;
-                float a = ex2_approx(fmaf(__uint_as_float(s[c]), f, back));
-                float b = ex2_approx(fmaf(__uint_as_float(s[c + 1]), f, back));
+              for (int c = 0; c < 32; ++c) {
+                float e = ex2_approx(fmaf(__uint_as_float(s[c]), c < 16 ? f0 : f1, c < 16 ? back0 : back1));
                 if (kMask) {
-                  if ((bad >> c) & 1) a = __uint_as_float(0x7fc00000u);
-                  if ((bad >> (c + 1)) & 1) b = __uint_as_float(0x7fc00000u);
-                  if (c >= left) a = 0.f;
-                  if (c + 1 >= left) b = 0.f;
+                  if ((bad >> c) & 1) e = __uint_as_float(0x7fc00000u);
+                  if (c >= left) e = 0.f;
                 }
-                e0 += a;
-                e1 += b;
-                pk[c / 2] = pack_bf16x2(a, b);
+                if (c < 16) e0 += e;
+                else e1 += e;
+                s[c] = __float_as_uint(e);
+              }
+              part += wide ? e0 + e1 : fmaf(e0, pow2(-vk.x), e1 * pow2(-vk.y));
+              uint32_t pk[16];
+              if (wide) {
+#pragma unroll
+                for (int c = 0; c < 16; ++c) pk[c] = pack_bf16x2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
+              } else {
+#pragma unroll
+                for (int c = 0; c < 16; ++c) pk[c] = pack_f16x2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
               }
               tmem_st16(t_p + 16 * g, pk);
             }
-            part = e0 + e1;
           };
           if (masked) weights(std::true_type{});
           else weights(std::false_type{});
@@ -298,7 +325,8 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
             const int pos = r / p.ratio, hq = cur.head * p.ratio + (r - pos * p.ratio);
             const int64_t token = cur.s.cu0 + pos;
             const float rf = sum != 0.f && ref == -INFINITY ? 0.f : ref;
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const float unit = pow2(unit_k0);
+            const float inv = sum == 0.f ? 0.f : unit / sum;
 #pragma unroll 1
             for (int c = 0; c < DV; c += 32) {
               uint32_t v[32];
@@ -317,6 +345,8 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
                   }
                 } else {
                   uint4* dst = reinterpret_cast<uint4*>(p.part_o + (part * L::kRows + r) * DV + c);
+#pragma unroll
+                  for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * unit);
 #pragma unroll
                   for (int k = 0; k < 8; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                 }
@@ -349,38 +379,45 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
         }
       };
       load_pages((ahead.tile * kTile) >> p.page_shift);
-      // this thread's chunks of a tile's K or V: row and 16-code column of chunk number k
-      auto copy = [&](auto is_k, uint32_t dst) {
-        constexpr bool kK = decltype(is_k)::value;
-        constexpr int D = kK ? DQK : DV, kChunks = D / 16, kPer = kTile * kChunks / L::kFillThreads;
-        const uint8_t* base = kK ? p.k + ahead.head * p.k_head : p.v + ahead.head * p.v_head;
-        const int64_t page_stride = kK ? p.k_page : p.v_page;
-        const uint32_t ts = kK ? p.k_token : p.v_token;
-        const int token0 = ahead.tile * kTile;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          const int at = k * L::kFillThreads + ft, row = at / kChunks, chunk = at % kChunks;
-          const int t = token0 + row;
-          const int e = __shfl_sync(0xffffffffu, entry, ((t >> p.page_shift) - page0) & 31);
-          if (t < ahead.s.len)
-            cp_async16(dst + k * L::kFillThreads * 16,
-                       base + e * page_stride + static_cast<uint32_t>(t & ((1 << p.page_shift) - 1)) * ts + chunk * 16);
-        }
-      };
+      // Eight lanes take 4 neighbouring chunks of 16 codes of two neighbouring rows (so that they write to
+      // different banks); pass k of a thread is column group k % (D / 64) of row my_row or my_row + 64.
+      const int my_row = 2 * (ft >> 3) + ((ft >> 2) & 1), my_chunk = ft & 3;
+      // where the two halves of a chunk's operands go in a column group's 128 rows
+      const uint32_t out0 = my_row * 128 + (((2 * my_chunk) ^ (my_row & 7)) << 4);
+      const uint32_t out1 = my_row * 128 + (((2 * my_chunk + 1) ^ (my_row & 7)) << 4);
+      constexpr int kPassK = 2 * (DQK / 64), kPassV = 2 * (DV / 64);
+      constexpr uint32_t kPassBytes = L::kFillThreads * 16;  // of codes
       // The next tile's codes, and in lanes 0 .. 7 its scales, one for 16 tokens.
       int ek = 127, ev = 127, ek_next = 127, ev_next = 127;
       auto fetch = [&]() {
         ek_next = ev_next = 127;
         if (copied < count) {
           const uint32_t dst = smem0 + L::oCodes + (copied & 1) * L::kCodeBytes + ft * 16;
-          copy(std::true_type{}, dst);
-          copy(std::false_type{}, dst + kTile * DQK);
-          const int token = ahead.tile * kTile + 16 * (lane & 7);
+          const int token0 = ahead.tile * kTile, mask = (1 << p.page_shift) - 1;
+          const uint8_t* kh = p.k + ahead.head * p.k_head + my_chunk * 16;
+          const uint8_t* vh = p.v + ahead.head * p.v_head + my_chunk * 16;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int t = token0 + my_row + 64 * h;
+            const int e = __shfl_sync(0xffffffffu, entry, ((t >> p.page_shift) - page0) & 31);
+            if (t < ahead.s.len) {
+              const uint32_t in_page = t & mask;
+              const uint8_t* ks = kh + e * p.k_page + static_cast<uint64_t>(in_page * p.k_token);
+              const uint8_t* vs = vh + e * p.v_page + static_cast<uint64_t>(in_page * p.v_token);
+#pragma unroll
+              for (int k = 0; k < DQK / 64; ++k) cp_async16(dst + (h * (DQK / 64) + k) * kPassBytes, ks + 64 * k);
+#pragma unroll
+              for (int k = 0; k < DV / 64; ++k) cp_async16(dst + (kPassK + h * (DV / 64) + k) * kPassBytes, vs + 64 * k);
+            }
+          }
+          const int token = token0 + 16 * (lane & 7);
           const int e = __shfl_sync(0xffffffffu, entry, ((token >> p.page_shift) - page0) & 31);
-          if (lane < 8 && token < ahead.s.len) {
+          if (token < ahead.s.len) {
             const int64_t at = static_cast<int64_t>(e) * p.heads_kv + ahead.head;
             ek_next = p.k_scale[at];
             ev_next = p.v_scale[at];
+          } else {
+            ev_next = -1;  // no tokens: does not count
           }
           if (copied + 1 < count) {
             const int b = ahead.b, head = ahead.head;
@@ -396,77 +433,116 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
       ek = ek_next, ev = ev_next;
       fetch();
       bool ok = true;
+      int k0 = 0;
       for (int i = 0; i < count && ok; ++i) {
         const int token0 = cur.tile * kTile;
         const bool masked = token0 + kTile > least_limit(cur.s);
+        // the unit of O: 2^-3 of the largest of the values' scales in the piece's first tile of the sequence, kept
+        // moderate; a scale that is NaN makes the keys' NaN
+        const bool none = ev < 0, nan = ev == 255;
+        int vk = none || nan ? -1000 : ev - 127;
+        if (i == 0 || cur.tile == 0) {
+          k0 = __reduce_max_sync(0xffffffffu, vk);
+          k0 = k0 == -1000 ? 0 : k0 - 3;
+          k0 = k0 < -20 ? -20 : k0 > 30 ? 30 : k0;
+        }
+        vk = none || nan ? 0 : vk - k0;
+        const bool wide = __any_sync(0xffffffffu, vk < -3 || vk > 6);
+        const float ks = nan ? scale_of(255) : scale_of(ek);
         cp_async_wait<1>();
         const uint32_t codes = smem0 + L::oCodes + (i & 1) * L::kCodeBytes + ft * 16;
-        const float ks = ev == 255 ? scale_of(255) : scale_of(ek);  // NaN in either: NaN scores
-        const float vs = ev == 255 ? 1.f : scale_of(ev);
-        auto convert = [&](auto kind, uint32_t from, uint32_t tile) {
-          constexpr bool kK = decltype(kind)::value;
-          constexpr int D = kK ? DQK : DV, kChunks = D / 16, kPer = kTile * kChunks / L::kFillThreads;
-#pragma unroll
-          for (int k = 0; k < kPer; ++k) {
-            const int at = k * L::kFillThreads + ft, row = at / kChunks, chunk = at % kChunks;
-            const float scale = kK ? 1.f : __shfl_sync(0xffffffffu, vs, row >> 4);
-            const uint4 v = lds128(from + k * L::kFillThreads * 16);
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            if (!kK && masked) {  // hidden from some row: no value may be NaN
-              const bool inside = token0 + row < cur.s.len;
-              uint32_t any = 0;
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const uint32_t nan = ((w[x] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                any |= nan;
-                w[x] = inside ? w[x] & ~((nan >> 7) * 0xffu) : 0u;
-              }
-              if (any != 0 && inside) atomicOr(&poison[i & 7][row >> 5], 1u << (row & 31));
-            }
-            uint32_t f[8];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              f[2 * x] = e4m3x2_f16x2(w[x]);
-              f[2 * x + 1] = e4m3x2_hi_f16x2(w[x]);
-              if constexpr (!kK) {
-                f[2 * x] = scaled_bf16x2(f[2 * x], scale);
-                f[2 * x + 1] = scaled_bf16x2(f[2 * x + 1], scale);
-              }
-            }
-            // two groups of 8 operands; lanes of the right half write their second first (banks)
-            const uint32_t line_at = tile + (chunk >> 2) * L::kChunk + row * 128;
-            const int c0 = (2 * chunk) & 7;
-            const bool swap = kChunks == 8 && (chunk & 4) != 0;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const bool second = (h == 1) != swap;
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                               line_at + (((c0 + (second ? 1 : 0)) ^ (row & 7)) << 4)),
-                           "r"(second ? f[4] : f[0]), "r"(second ? f[5] : f[1]), "r"(second ? f[6] : f[2]),
-                           "r"(second ? f[7] : f[3])
-                           : "memory");
-            }
-          }
-        };
-        // entry 2 i (K) and 2 i + 1 (V) of the ring: free once the MMA on its last use is done
-        auto put = [&](auto kind, int e, uint32_t from) -> bool {
+        // an entry's slot of the ring is free once the MMA on its last use is done
+        auto slot_free = [&](int e) {
           const int slot = e % L::kSlots, use = e / L::kSlots;
-          if (use > 0 && !__all_sync(0xffffffffu, tc_wait(kv_empty(slot), (use - 1) & 1, wc))) return false;
-          if (decltype(kind)::value) {
-            if (ft < 8) k_scales[i & 3][ft] = ks;
-          } else if (ft < 4) {
-            // cleared for a tile far enough ahead that neither its conversion has begun nor the softmax of the
-            // last tile that used these words is still under way
-            poison[(i + 4) & 7][ft] = 0;
-          }
-          convert(kind, from, smem0 + L::oRing + L::slot_offset(slot));
+          return use == 0 || __all_sync(0xffffffffu, tc_wait(kv_empty(slot), (use - 1) & 1, wc));
+        };
+        auto slot_done = [&](int e) {
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(kv_full(slot));
-          return true;
+          if (lane == 0) mbar_arrive(kv_full(e % L::kSlots));
         };
-        ok = put(std::true_type{}, 2 * i, codes) && put(std::false_type{}, 2 * i + 1, codes + kTile * DQK);
-        if (!ok) break;
+        auto put = [&](uint32_t at, const uint32_t (&f)[8]) {
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + out0), "r"(f[0]), "r"(f[1]), "r"(f[2]),
+                       "r"(f[3])
+                       : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + out1), "r"(f[4]), "r"(f[5]), "r"(f[6]),
+                       "r"(f[7])
+                       : "memory");
+        };
+        auto to_f16 = [&](const uint4& v, uint32_t (&f)[8]) {
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            f[2 * x] = e4m3x2_f16x2(w[x]);
+            f[2 * x + 1] = e4m3x2_hi_f16x2(w[x]);
+          }
+        };
+
+        if (!slot_free(2 * i)) break;
+        if (ft < 8) {
+          tiles[i & 3].ks[ft] = ks;
+          tiles[i & 3].vk[ft] = vk;
+          if (ft == 0) tiles[i & 3].wide = wide, tiles[i & 3].k0 = k0;
+        }
+        {
+          const uint32_t tile = smem0 + L::oRing + L::slot_offset((2 * i) % L::kSlots);
+#pragma unroll
+          for (int k = 0; k < kPassK; ++k) {
+            uint32_t f[8];
+            to_f16(lds128(codes + k * kPassBytes), f);
+            put(tile + (k % (DQK / 64)) * L::kChunk + (k / (DQK / 64)) * 64 * 128, f);
+          }
+        }
+        slot_done(2 * i);
+
+        const uint32_t v_codes = codes + kPassK * kPassBytes;
+        if (masked) {  // hidden from some row: no value may be NaN
+#pragma unroll 1
+          for (int k = 0; k < kPassV; ++k) {
+            const int row = my_row + 64 * (k / (DV / 64));
+            uint4 v = lds128(v_codes + k * kPassBytes);
+            uint32_t* w = &v.x;
+            const bool inside = token0 + row < cur.s.len;
+            uint32_t any = 0;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t bad = ((w[x] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+              any |= bad;
+              w[x] = inside ? w[x] & ~((bad >> 7) * 0xffu) : 0u;
+            }
+            if (any != 0 && inside) atomicOr(&poison[i & 7][row >> 5], 1u << (row & 31));
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(v_codes + k * kPassBytes), "r"(v.x), "r"(v.y),
+                         "r"(v.z), "r"(v.w)
+                         : "memory");
+          }
+        }
+        if (!slot_free(2 * i + 1)) break;
+        // cleared for a tile far enough ahead that neither its conversion has begun nor the softmax of the
+        // last tile that used these words is still under way
+        if (ft < 4) poison[(i + 4) & 7][ft] = 0;
+        {
+          const uint32_t tile = smem0 + L::oRing + L::slot_offset((2 * i + 1) % L::kSlots);
+          if (!wide) {
+#pragma unroll
+            for (int k = 0; k < kPassV; ++k) {
+              uint32_t f[8];
+              to_f16(lds128(v_codes + k * kPassBytes), f);
+              put(tile + (k % (DV / 64)) * L::kChunk + (k / (DV / 64)) * 64 * 128, f);
+            }
+          } else {
+#pragma unroll 1
+            for (int k = 0; k < kPassV; ++k) {
+              const int row = my_row + 64 * (k / (DV / 64));
+              const float scale = pow2(__shfl_sync(0xffffffffu, vk, row >> 4));
+              uint32_t f[8];
+              to_f16(lds128(v_codes + k * kPassBytes), f);
+#pragma unroll
+              for (int x = 0; x < 8; ++x) f[x] = scaled_bf16x2(f[x], scale);
+              put(tile + (k % (DV / 64)) * L::kChunk + (k / (DV / 64)) * 64 * 128, f);
+            }
+          }
+        }
+        slot_done(2 * i + 1);
         ek = ek_next, ev = ev_next;
         fetch();
         if (i + 1 < count) paged_next<kTile>(p, cur);
@@ -475,7 +551,8 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
     } else {
       // ======== MMA ========
       constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false) & ~((1u << 7) | (1u << 10));  // f16 operands
-      constexpr uint32_t kIdescO = idesc_bf16_f32(128, DV, false, true);
+      constexpr uint32_t kIdescWide = idesc_bf16_f32(128, DV, false, true);  // bf16 operands
+      constexpr uint32_t kIdescO = kIdescWide & ~((1u << 7) | (1u << 10));
       const uint32_t leader = lane == 0 ? 1u : 0u;
       auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, tc_wait(bar, parity, wc)); };
       auto wait_entry = [&](int e) { return wait(kv_full(e % L::kSlots), (e / L::kSlots) & 1); };
@@ -515,11 +592,12 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
         const int slot = (2 * i + 1) % L::kSlots;
         const uint32_t v_at = smem0 + L::oRing + L::slot_offset(slot);
         const bool begun = i != 0 && cur.tile != 0;  // O holds tiles of this unit
+        const uint32_t idesc = tiles[i & 3].wide != 0 ? kIdescWide : kIdescO;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t va = opaque_u32(v_at + static_cast<uint32_t>(h * 64 * 128));
           mma_ts_x4<(16 * 128 >> 4)>(tmem + L::kColO, tmem + L::kColP + 64 * (i & 1) + 32 * h, smem_desc_sw128(va, L::kChunk, 1024),
-                                     kIdescO, h != 0 || begun ? 1u : 0u, leader);
+                                     idesc, h != 0 || begun ? 1u : 0u, leader);
         }
         mma_commit(bar_o, leader);
         mma_commit(kv_empty(slot), leader);
