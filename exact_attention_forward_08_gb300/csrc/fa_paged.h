@@ -24,9 +24,9 @@ int append_launch(const fa_kv_cache& c, const void* q, const void* k, const void
 
 // fa_paged_d{64,128,192}.cu: the attention kernel and the merge for rows of a
 // team 8, 16, 32 or 64; `smem_ready` remembers the shared-memory attribute
-int paged_launch_d64(const PagedParams& p, int d_v, int rows, int grid, cudaStream_t stream);
-int paged_launch_d128(const PagedParams& p, int d_v, int rows, int grid, cudaStream_t stream);
-int paged_launch_d192(const PagedParams& p, int d_v, int rows, int grid, cudaStream_t stream);
+int paged_launch_d64(const PagedParams& p, const fa_kv_cache& c, int d_v, int rows, int grid, cudaStream_t stream);
+int paged_launch_d128(const PagedParams& p, const fa_kv_cache& c, int d_v, int rows, int grid, cudaStream_t stream);
+int paged_launch_d192(const PagedParams& p, const fa_kv_cache& c, int d_v, int rows, int grid, cudaStream_t stream);
 
 // fa_paged_unpack.cu: the codes of the long sequences as bf16 rows, packed, and their offsets
 struct UnpackParams {

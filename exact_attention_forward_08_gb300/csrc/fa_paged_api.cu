@@ -259,13 +259,14 @@ int fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse, c
   p.page_shift = page_shift(c.page_size);
   p.causal = causal ? 1 : 0;
   p.timeout_ns = 1000000000ull;
+  p.copies = 1;
   p.max_n = max_seqlen_q;
   p.row_limit = fa::kPagedRowLimit;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   const int grid = host.sms < fa::kPagedMaxBlocks ? host.sms : fa::kPagedMaxBlocks;
-  if (c.d_qk == 64) return fa::paged_launch_d64(p, c.d_v, most, grid, stream);
-  if (c.d_qk == 128) return fa::paged_launch_d128(p, c.d_v, most, grid, stream);
-  return fa::paged_launch_d192(p, c.d_v, most, grid, stream);
+  if (c.d_qk == 64) return fa::paged_launch_d64(p, c, c.d_v, most, grid, stream);
+  if (c.d_qk == 128) return fa::paged_launch_d128(p, c, c.d_v, most, grid, stream);
+  return fa::paged_launch_d192(p, c, c.d_v, most, grid, stream);
 }
 
 }  // extern "C"

@@ -53,6 +53,7 @@ struct PagedParams {
   int64_t total_q;
   int batch, heads_q, heads_kv, ratio, num_pages, max_pages, page_shift, causal;
   unsigned long long timeout_ns;  // of a wait (paged_tc_kernel)
+  int copies;     // of the rows in the 128 lanes (paged_tc_kernel), each with its share of the tokens
   int max_n;      // longest sequence of new tokens allowed
   int row_limit;  // sequences with more rows (new tokens x ratio) are not this kernel's
   float scale_log2;
@@ -798,9 +799,9 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
   const int local = blockIdx.y * 8 + (threadIdx.x >> 5);
   if (local >= j.rows) return;
   const int parts = j.last - piece + 1;
-  auto slot = [&](int i) { return 2 * static_cast<int64_t>(piece + i) + (i == 0 ? 1 : 0); };
+  auto row = [&](int i) { return (2 * static_cast<int64_t>(piece + i) + (i == 0 ? 1 : 0)) * ROWS + local; };
   float top = -INFINITY;
-  for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.part_ml[slot(i) * ROWS + local].x);
+  for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.part_ml[row(i)].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const float base = top == -INFINITY ? 0.f : top;
@@ -811,7 +812,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
   for (int i0 = 0; i0 < parts; i0 += 32) {
     float w = 0.f;
     if (i0 + lane < parts) {
-      const float2 ml = p.part_ml[slot(i0 + lane) * ROWS + local];
+      const float2 ml = p.part_ml[row(i0 + lane)];
       w = ex2_approx(ml.x - base);
       l += w * ml.y;
     }
@@ -819,7 +820,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
 #pragma unroll 8
     for (int i = 0; i < n; ++i) {
       const float wi = __shfl_sync(0xffffffffu, w, i);
-      const float* src = p.part_o + (slot(i0 + i) * ROWS + local) * DV + lane * kPer;
+      const float* src = p.part_o + row(i0 + i) * DV + lane * kPer;
       if constexpr (kPer == 4) {
         const float4 x = *reinterpret_cast<const float4*>(src);
         acc[0] = fmaf(wi, x.x, acc[0]), acc[1] = fmaf(wi, x.y, acc[1]);

@@ -20,16 +20,18 @@
 //               follows its maximum when it lags by more than 2^8; so a tile's
 //               weights are formed with the reference there is, in one pass
 //               over S, and once more in the rare case that it has to move (O
-//               is then rescaled in place by the same threads).
+//               is then rescaled in place by the same threads).  Up to 64 or
+//               32 rows stand in the 128 lanes twice or four times: each copy
+//               takes a half or a quarter of every tile's tokens, with weights
+//               of 0 for the others, and the copies are added up at the end.
 //   warp 4      issues the MMAs, S of the next tile before P V of this one.
-//   warps 5-12  codes to operands: each thread copies its 16-byte chunks to
-//               shared memory two tiles ahead, converts them and writes them
-//               in the tensor cores' swizzled layout.
+//   warp 5      loads: block table, scales, and the codes by TMA two tiles ahead.
+//   warps 6-13  codes to operands, in the tensor cores' swizzled layout.
 // TMEM: S of even and odd tiles, O, P of even and odd tiles.  What bounds it:
 // per 128 tokens and head 32 KB of codes come in (about 1400 cycles at this
-// GPU's bandwidth), the two products take about 1000 cycles, the exponentials
-// of a warp of rows 1024, the shared memory carries 230 KB (1800 cycles), and
-// the conversion issues about 600 instructions a scheduler.
+// GPU's bandwidth), the two products take about 1000 cycles, the shared memory
+// carries 230 KB (1800 cycles), and the conversion issues about 400
+// instructions a scheduler.
 #pragma once
 #include "fa_paged_attn.cuh"
 
@@ -39,7 +41,7 @@ template <int DQK, int DV>
 struct TcShape {
   static constexpr int kTile = 128, kRows = 128;
   static constexpr int kFillWarps = 8, kFillThreads = 32 * kFillWarps;
-  static constexpr int kMmaWarp = 4, kFillWarp0 = 5;
+  static constexpr int kMmaWarp = 4, kLoadWarp = 5, kFillWarp0 = 6;
   static constexpr int kThreads = 32 * (kFillWarp0 + kFillWarps);
   static constexpr int kChunk = 128 * 128;  // 128 rows of 64 operands, swizzled
   static constexpr int kQBytes = DQK / 64 * kChunk;
@@ -68,21 +70,27 @@ __device__ __forceinline__ float pow2(int k) {
   return a * __uint_as_float(static_cast<uint32_t>(k - (k >> 1) + 127) << 23);
 }
 
-// What the roles know of a tile's scales, one for 16 tokens.
+// What the loading warp tells of a tile: its scales, one for 16 tokens, and more.
 struct TcTile {
-  float ks[8];   // of the keys
-  int vk[8];     // of the values: k - k0
-  int wide, k0;
+  float ks[8];  // of the keys
+  int vk[8];    // of the values: k - k0
+  int k0;
+  int wide, masked;  // V in bf16; some row does not see all of it
+  int left;          // tokens from the tile's first to the sequence's end
+};
+
+struct TcParams : PagedParams {
+  CUtensorMap tm_k, tm_v;  // (d, token, head, page) of codes; a box is what a tile and a page share
 };
 
 template <int DQK, int DV>
 __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
-    paged_tc_kernel(const __grid_constant__ PagedParams p) {
+    paged_tc_kernel(const __grid_constant__ TcParams p) {
   using L = TcShape<DQK, DV>;
   constexpr int kTile = L::kTile;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * L::kSlots + 7];
-  __shared__ __align__(16) TcTile tiles[4];  // of four tiles
+  __shared__ __align__(8) uint64_t bars[2 * L::kSlots + 9 + 2 * L::kCodes];
+  __shared__ __align__(16) TcTile tiles[8];  // of eight tiles
   __shared__ uint32_t poison[8][4];       // tokens of a masked tile whose values hold a NaN, for eight tiles
   __shared__ PagedCursor begin_at;
   __shared__ long long scan[L::kThreads];
@@ -95,9 +103,15 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
   const uint32_t bar0 = smem_u32(bars);
   auto kv_full = [&](int slot) { return bar0 + 8 * slot; };
   auto kv_empty = [&](int slot) { return bar0 + 8 * (L::kSlots + slot); };
-  const uint32_t bar_q = bar0 + 16 * L::kSlots, bar_o = bar_q + 8, bar_drain = bar_q + 16;
+  const uint32_t bar_q = bar0 + 16 * L::kSlots, bar_drain = bar_q + 8, bar_x = bar_q + 16;
   auto s_full = [&](int buf) { return bar_q + 24 + 8 * buf; };
   auto p_full = [&](int buf) { return bar_q + 40 + 8 * buf; };
+  // P V of even and odd tiles: with one barrier, whose last phase may still be open when a tile's is waited for, that
+  // wait would take the phase before the last for its own
+  auto o_full = [&](int buf) { return bar_q + 56 + 8 * buf; };
+  auto code_full = [&](int c) { return bar_q + 72 + 8 * c; };
+  auto code_empty = [&](int c) { return bar_q + 72 + 8 * (L::kCodes + c); };
+  __shared__ float2 copy_ml[128];  // a copy's reference and sum
   const WaitCtx wc{&abort_flag, p.status, p.timeout_ns};
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -109,13 +123,20 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
       mbar_init(kv_empty(i), 1);
     }
     mbar_init(bar_q, 128);
-    mbar_init(bar_o, 1);
     mbar_init(bar_drain, 1);
+    mbar_init(bar_x, 128);
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full(i), 1);
       mbar_init(p_full(i), 128);
+      mbar_init(o_full(i), 1);
+    }
+    for (int i = 0; i < L::kCodes; ++i) {
+      mbar_init(code_full(i), 1);
+      mbar_init(code_empty(i), L::kFillWarps);
     }
     fence_mbar_init();
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
   }
   if (warp == L::kMmaWarp) {
     tmem_alloc(smem_u32(&tmem_base), 512);
@@ -145,14 +166,24 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
       const long long piece = line.piece(0);
       const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
       const uint32_t t_o = t_lane + L::kColO;
-      const int r = tid;
+      // lanes' copies of the rows: this thread's row, and the tokens of a tile that its copy takes
+      const int copies = p.copies, copy_rows = 128 / copies, copy = tid / copy_rows, r = tid - copy * copy_rows;
+      const int groups = 4 / copies, group0 = copy * groups;  // of 32 tokens
+      if (copies > 1) {  // weights of other copies' tokens are 0 for good
+        uint32_t zero[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) zero[k] = 0;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) tmem_st32(t_lane + L::kColP + c, zero);
+        tmem_wait_st();
+      }
       float fac = 0.f, ref = -INFINITY, sum = 0.f;
-      int limit = 0, min_limit = 0, unit_k0 = 0;
+      int limit = 0, min_limit = 0, unit_k0 = 0, x_phase = 0;
       bool started_here = false;
       bool ok = true;
       for (int i = 0; i < count && ok; ++i) {
         const bool first = i == 0 || cur.tile == 0;
-        const bool active = warp * 32 < cur.s.rows;  // some row of this warp is one of the sequence's
+        const bool active = warp * 32 - copy * copy_rows < cur.s.rows;  // some row of this warp is one of the sequence's
         if (first) {
           started_here = cur.tile == 0;
           // this thread's query row as f16, divided by the power of two of its largest value
@@ -198,7 +229,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
             for (int k = 0; k < 4; ++k)
               f[k] = pack_f16x2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             smem0 + (c >> 3) * L::kChunk + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
+                             smem0 + (c >> 3) * L::kChunk + tid * 128 + (((c & 7) ^ (tid & 7)) << 4)),
                          "r"(f[0]), "r"(f[1]), "r"(f[2]), "r"(f[3])
                          : "memory");
           }
@@ -216,8 +247,8 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
         tc_fence_after();
         if (active) {
           const uint32_t t_s = t_lane + 128 * buf, t_p = t_lane + L::kColP + 64 * buf;
-          const bool wide = tiles[i & 3].wide != 0;
-          if (first) unit_k0 = tiles[i & 3].k0;
+          const bool wide = tiles[i & 7].wide != 0;
+          if (first) unit_k0 = tiles[i & 7].k0;
           float mx = -INFINITY, part = 0.f;
           // weights of the tile with the present reference, their sum, and the scores' maximum
           auto weights = [&](auto with_mask) {
@@ -226,11 +257,11 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
             mx = -INFINITY;
             part = 0.f;
 #pragma unroll 1
-            for (int g = 0; g < 4; ++g) {
+            for (int g = group0; g < group0 + groups; ++g) {
               uint32_t s[32];
               tmem_ld32_wait(t_s + 32 * g, s);
-              const float2 ks = *reinterpret_cast<const float2*>(&tiles[i & 3].ks[2 * g]);
-              const int2 vk = *reinterpret_cast<const int2*>(&tiles[i & 3].vk[2 * g]);
+              const float2 ks = *reinterpret_cast<const float2*>(&tiles[i & 7].ks[2 * g]);
+              const int2 vk = *reinterpret_cast<const int2*>(&tiles[i & 7].vk[2 * g]);
               const float f0 = fac * ks.x, f1 = fac * ks.y;
               const float back0 = wide ? back : back + static_cast<float>(vk.x);
               const float back1 = wide ? back : back + static_cast<float>(vk.y);
@@ -284,7 +315,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
             sum *= alpha;
             if (!first) {
               // P V of the tile before has to be in O
-              ok = __all_sync(0xffffffffu, tc_wait(bar_o, (i - 1) & 1, wc));
+              ok = __all_sync(0xffffffffu, tc_wait(o_full(buf ^ 1), ((i - 1) >> 1) & 1, wc));
               if (!ok) break;
               tc_fence_after();
 #pragma unroll 1
@@ -317,10 +348,60 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
             j.rows = cur.s.rows;
             p.joins[piece] = j;
           }
-          ok = __all_sync(0xffffffffu, tc_wait(bar_o, i & 1, wc));
+          ok = __all_sync(0xffffffffu, tc_wait(o_full(buf), (i >> 1) & 1, wc));
           if (!ok) break;
           tc_fence_after();
-          if (active) {
+          // Copies are added up in halves, upper ones into lower ones, through the queries' place in shared memory,
+          // which the MMAs are done with: row `place` of it, in 16-byte steps that spread over the banks.
+          auto meet = [&]() {  // all softmax threads
+            mbar_arrive(bar_x);
+            return __all_sync(0xffffffffu, tc_wait(bar_x, x_phase++ & 1, wc));
+          };
+          for (int half = copies >> 1; half > 0 && ok; half >>= 1) {
+            const bool gives = copy >= half && copy < 2 * half, takes = copy < half;
+            // a step's upper copies write where they read before, so that nobody else can still be reading there
+            const int place = (half == 1 ? copies / 2 - 1 : gives ? copy - half : copy) * copy_rows + r;
+            const uint32_t at = smem0 + place * (DV * 4);
+            if (gives) {
+              copy_ml[place] = make_float2(ref, sum);
+#pragma unroll 1
+              for (int c = 0; c < DV; c += 32) {
+                uint32_t v[32];
+                tmem_ld32_wait(t_o + c, v);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((c / 4 + k) ^ (r & 7)) << 4)),
+                               "r"(v[4 * k]), "r"(v[4 * k + 1]), "r"(v[4 * k + 2]), "r"(v[4 * k + 3])
+                               : "memory");
+              }
+            }
+            ok = meet();
+            if (ok && takes) {
+              const float2 other = copy_ml[place];
+              const float m = fmaxf(ref, other.x);
+              const float a = m == -INFINITY ? 1.f : ex2_approx(ref - m), b = m == -INFINITY ? 1.f : ex2_approx(other.x - m);
+              ref = m;
+              sum = a * sum + b * other.y;
+#pragma unroll 1
+              for (int c = 0; c < DV; c += 32) {
+                uint32_t v[32];
+                tmem_ld32_wait(t_o + c, v);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const uint4 w = lds128(at + (((c / 4 + k) ^ (r & 7)) << 4));
+                  v[4 * k] = __float_as_uint(fmaf(b, __uint_as_float(w.x), a * __uint_as_float(v[4 * k])));
+                  v[4 * k + 1] = __float_as_uint(fmaf(b, __uint_as_float(w.y), a * __uint_as_float(v[4 * k + 1])));
+                  v[4 * k + 2] = __float_as_uint(fmaf(b, __uint_as_float(w.z), a * __uint_as_float(v[4 * k + 2])));
+                  v[4 * k + 3] = __float_as_uint(fmaf(b, __uint_as_float(w.w), a * __uint_as_float(v[4 * k + 3])));
+                }
+                tmem_st32(t_o + c, v);
+              }
+              tmem_wait_st();
+            }
+          }
+          if (copies > 1 && ok) ok = meet();  // read before the next queries come there
+          if (!ok) break;
+          if (active && copy == 0) {
             const int64_t part = 2 * piece + (started_here ? 1 : 0);
             const int pos = r / p.ratio, hq = cur.head * p.ratio + (r - pos * p.ratio);
             const int64_t token = cur.s.cu0 + pos;
@@ -361,85 +442,61 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
         }
         if (i + 1 < count) paged_next<kTile>(p, cur);
       }
-    } else if (warp >= L::kFillWarp0) {
-      // ======== codes to operands ========
-      const int ft = tid - 32 * L::kFillWarp0;
-      PagedCursor ahead = begin_at, cur = begin_at;  // the tiles that are copied and converted next
-      int copied = 0;                                // tiles under way or done
-      int page0 = 0, entry = 0;
+    } else if (warp == L::kLoadWarp) {
+      // ======== loads ========
+      PagedCursor cur = begin_at;
+      int page0 = 0, entry = 0, k0 = 0;
       auto load_pages = [&](int first_page) {
         page0 = first_page;
         entry = 0;
-        if (((first_page + lane) << p.page_shift) < ahead.s.len) {
-          entry = p.table[ahead.b * p.table_stride + first_page + lane];
+        if (((first_page + lane) << p.page_shift) < cur.s.len) {
+          entry = p.table[cur.b * p.table_stride + first_page + lane];
           if (entry < 0 || entry >= p.num_pages) {
-            paged_error(p.status, kSitePagedPage, ahead.b);
+            paged_error(p.status, kSitePagedPage, cur.b);
             entry = 0;
           }
         }
       };
-      load_pages((ahead.tile * kTile) >> p.page_shift);
-      // Eight lanes take 4 neighbouring chunks of 16 codes of two neighbouring rows (so that they write to
-      // different banks); pass k of a thread is column group k % (D / 64) of row my_row or my_row + 64.
-      const int my_row = 2 * (ft >> 3) + ((ft >> 2) & 1), my_chunk = ft & 3;
-      // where the two halves of a chunk's operands go in a column group's 128 rows
-      const uint32_t out0 = my_row * 128 + (((2 * my_chunk) ^ (my_row & 7)) << 4);
-      const uint32_t out1 = my_row * 128 + (((2 * my_chunk + 1) ^ (my_row & 7)) << 4);
-      constexpr int kPassK = 2 * (DQK / 64), kPassV = 2 * (DV / 64);
-      constexpr uint32_t kPassBytes = L::kFillThreads * 16;  // of codes
-      // The next tile's codes, and in lanes 0 .. 7 its scales, one for 16 tokens.
-      int ek = 127, ev = 127, ek_next = 127, ev_next = 127;
-      auto fetch = [&]() {
-        ek_next = ev_next = 127;
-        if (copied < count) {
-          const uint32_t dst = smem0 + L::oCodes + (copied & 1) * L::kCodeBytes + ft * 16;
-          const int token0 = ahead.tile * kTile, mask = (1 << p.page_shift) - 1;
-          const uint8_t* kh = p.k + ahead.head * p.k_head + my_chunk * 16;
-          const uint8_t* vh = p.v + ahead.head * p.v_head + my_chunk * 16;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int t = token0 + my_row + 64 * h;
-            const int e = __shfl_sync(0xffffffffu, entry, ((t >> p.page_shift) - page0) & 31);
-            if (t < ahead.s.len) {
-              const uint32_t in_page = t & mask;
-              const uint8_t* ks = kh + e * p.k_page + static_cast<uint64_t>(in_page * p.k_token);
-              const uint8_t* vs = vh + e * p.v_page + static_cast<uint64_t>(in_page * p.v_token);
-#pragma unroll
-              for (int k = 0; k < DQK / 64; ++k) cp_async16(dst + (h * (DQK / 64) + k) * kPassBytes, ks + 64 * k);
-#pragma unroll
-              for (int k = 0; k < DV / 64; ++k) cp_async16(dst + (kPassK + h * (DV / 64) + k) * kPassBytes, vs + 64 * k);
-            }
-          }
-          const int token = token0 + 16 * (lane & 7);
-          const int e = __shfl_sync(0xffffffffu, entry, ((token >> p.page_shift) - page0) & 31);
-          if (token < ahead.s.len) {
-            const int64_t at = static_cast<int64_t>(e) * p.heads_kv + ahead.head;
-            ek_next = p.k_scale[at];
-            ev_next = p.v_scale[at];
+      load_pages((cur.tile * kTile) >> p.page_shift);
+      int issued = 0;
+      const int box_shift = p.page_shift;  // tokens of one copy: a page, of at most a tile
+      for (int i = 0; i < count; ++i) {
+        const int stage = i % L::kCodes, use = i / L::kCodes;
+        if (use > 0 && !__all_sync(0xffffffffu, tc_wait(code_empty(stage), (use - 1) & 1, wc))) break;
+        const int token0 = cur.tile * kTile, left = cur.s.len - token0;
+        int boxes = (left + (1 << box_shift) - 1) >> box_shift;
+        if (boxes > (kTile >> box_shift)) boxes = kTile >> box_shift;
+        const uint32_t full = code_full(stage);
+        const uint32_t dst = smem0 + L::oCodes + stage * L::kCodeBytes;
+        const int first = (token0 >> p.page_shift) - page0, mine = lane - first;
+        if (mine >= 0 && mine < boxes) {
+          // each copy announces its own bytes; the barrier's one arrival comes below
+          asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(full),
+                       "r"((DQK + DV) << box_shift)
+                       : "memory");
+          const uint32_t row = mine << box_shift;
+          if constexpr (DQK == 128) {
+            tma_load_4d(dst + row * 128, &p.tm_k, full, 0, 0, cur.head, entry);
           } else {
-            ev_next = -1;  // no tokens: does not count
+#pragma unroll
+            for (int c = 0; c < DQK / 64; ++c)
+              tma_load_4d(dst + c * kTile * 64 + row * 64, &p.tm_k, full, 64 * c, 0, cur.head, entry);
           }
-          if (copied + 1 < count) {
-            const int b = ahead.b, head = ahead.head;
-            paged_next<kTile>(p, ahead);
-            const int next = (ahead.tile * kTile) >> p.page_shift;
-            if (ahead.b != b || (ahead.head != head && page0 != 0) || next + kTile / 16 > page0 + 32) load_pages(next);
-          }
+          tma_load_4d(dst + kTile * DQK + row * DV, &p.tm_v, full, 0, 0, cur.head, entry);
         }
-        ++copied;
-        cp_async_commit();  // a group for each tile, empty ones at the end
-      };
-      fetch();
-      ek = ek_next, ev = ev_next;
-      fetch();
-      bool ok = true;
-      int k0 = 0;
-      for (int i = 0; i < count && ok; ++i) {
-        const int token0 = cur.tile * kTile;
-        const bool masked = token0 + kTile > least_limit(cur.s);
+        // lanes 0 .. 7 (and again in the others): the scales of 16 tokens each
+        const int group = lane & 7;
+        const int e = __shfl_sync(0xffffffffu, entry, (first + ((16 * group) >> p.page_shift)) & 31);
+        const bool none = 16 * group >= left;
+        int ek = 127, ev = 127;
+        if (!none) {
+          const int64_t at = static_cast<int64_t>(e) * p.heads_kv + cur.head;
+          ek = p.k_scale[at];
+          ev = p.v_scale[at];
+        }
         // the unit of O: 2^-3 of the largest of the values' scales in the piece's first tile of the sequence, kept
         // moderate; a scale that is NaN makes the keys' NaN
-        const bool none = ev < 0, nan = ev == 255;
+        const bool nan = ev == 255;
         int vk = none || nan ? -1000 : ev - 127;
         if (i == 0 || cur.tile == 0) {
           k0 = __reduce_max_sync(0xffffffffu, vk);
@@ -448,61 +505,101 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
         }
         vk = none || nan ? 0 : vk - k0;
         const bool wide = __any_sync(0xffffffffu, vk < -3 || vk > 6);
-        const float ks = nan ? scale_of(255) : scale_of(ek);
-        cp_async_wait<1>();
-        const uint32_t codes = smem0 + L::oCodes + (i & 1) * L::kCodeBytes + ft * 16;
-        // an entry's slot of the ring is free once the MMA on its last use is done
-        auto slot_free = [&](int e) {
-          const int slot = e % L::kSlots, use = e / L::kSlots;
-          return use == 0 || __all_sync(0xffffffffu, tc_wait(kv_empty(slot), (use - 1) & 1, wc));
-        };
-        auto slot_done = [&](int e) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(kv_full(e % L::kSlots));
-        };
-        auto put = [&](uint32_t at, const uint32_t (&f)[8]) {
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + out0), "r"(f[0]), "r"(f[1]), "r"(f[2]),
-                       "r"(f[3])
-                       : "memory");
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + out1), "r"(f[4]), "r"(f[5]), "r"(f[6]),
-                       "r"(f[7])
-                       : "memory");
-        };
-        auto to_f16 = [&](const uint4& v, uint32_t (&f)[8]) {
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            f[2 * x] = e4m3x2_f16x2(w[x]);
-            f[2 * x + 1] = e4m3x2_hi_f16x2(w[x]);
+        if (lane < 8) {
+          tiles[i & 7].ks[lane] = nan ? scale_of(255) : scale_of(ek);
+          tiles[i & 7].vk[lane] = vk;
+          if (lane == 0) {
+            tiles[i & 7].k0 = k0;
+            tiles[i & 7].wide = wide;
+            tiles[i & 7].masked = token0 + kTile > least_limit(cur.s);
+            tiles[i & 7].left = left;
           }
-        };
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full);
+        ++issued;
+        if (i + 1 < count) {
+          const int b = cur.b, head = cur.head;
+          paged_next<kTile>(p, cur);
+          const int next = (cur.tile * kTile) >> p.page_shift;
+          if (cur.b != b || (cur.head != head && page0 != 0) || next + kTile / 16 > page0 + 32) load_pages(next);
+        }
+      }
+      // the copies under way land before the block's memory is given up, also after a failure
+      const uint64_t t0 = globaltimer_ns();
+      for (int i = issued > L::kCodes ? issued - L::kCodes : 0; i < issued; ++i)
+        while (!mbar_try_wait(code_full(i % L::kCodes), (i / L::kCodes) & 1) && globaltimer_ns() - t0 < 1000000000ull) {
+        }
+    } else if (warp >= L::kFillWarp0) {
+      // ======== codes to operands ========
+      const int ft = tid - 32 * L::kFillWarp0;
+      // Eight lanes take 4 neighbouring chunks of 16 codes of the rows r and r ^ 5 (so that they read and write
+      // different banks); pass k of a thread is column group k % (D / 64) of row my_row or my_row + 64.
+      const int pair = (ft >> 3) & 3, low = (ft >> 2) & 1;
+      const int my_row = ((ft >> 5) << 3) + (low ? pair ^ 5 : pair), my_chunk = ft & 3;
+      // where a chunk's codes lie (128-byte rows: column groups side by side; 64-byte rows: one after the other),
+      // and where the two halves of its operands go in a column group's 128 rows
+      auto code_at = [&](int d, int group, int row) -> uint32_t {
+        if (d == 128) return row * 128 + (((4 * group + my_chunk) ^ (row & 7)) << 4);
+        return group * (kTile * 64) + row * 64 + ((my_chunk ^ ((row >> 1) & 3)) << 4);
+      };
+      const uint32_t out0 = my_row * 128 + (((2 * my_chunk) ^ (my_row & 7)) << 4);
+      const uint32_t out1 = my_row * 128 + (((2 * my_chunk + 1) ^ (my_row & 7)) << 4);
+      constexpr int kGroupsK = DQK / 64, kGroupsV = DV / 64;
+      auto to_f16 = [&](uint32_t from, uint32_t (&f)[8]) {
+        const uint4 v = lds128(from);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          f[2 * x] = e4m3x2_f16x2(w[x]);
+          f[2 * x + 1] = e4m3x2_hi_f16x2(w[x]);
+        }
+      };
+      auto put = [&](uint32_t at, const uint32_t (&f)[8]) {
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + out0), "r"(f[0]), "r"(f[1]), "r"(f[2]),
+                     "r"(f[3])
+                     : "memory");
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + out1), "r"(f[4]), "r"(f[5]), "r"(f[6]),
+                     "r"(f[7])
+                     : "memory");
+      };
+      // an entry's slot of the ring is free once the MMA on its last use is done
+      auto slot_free = [&](int e) {
+        const int slot = e % L::kSlots, use = e / L::kSlots;
+        return use == 0 || __all_sync(0xffffffffu, tc_wait(kv_empty(slot), (use - 1) & 1, wc));
+      };
+      auto slot_done = [&](int e) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(kv_full(e % L::kSlots));
+      };
+      for (int i = 0; i < count; ++i) {
+        const int stage = i % L::kCodes;
+        if (!__all_sync(0xffffffffu, tc_wait(code_full(stage), (i / L::kCodes) & 1, wc))) break;
+        const uint32_t k_codes = smem0 + L::oCodes + stage * L::kCodeBytes, v_codes = k_codes + kTile * DQK;
+        const bool wide = tiles[i & 7].wide != 0, masked = tiles[i & 7].masked != 0;
 
         if (!slot_free(2 * i)) break;
-        if (ft < 8) {
-          tiles[i & 3].ks[ft] = ks;
-          tiles[i & 3].vk[ft] = vk;
-          if (ft == 0) tiles[i & 3].wide = wide, tiles[i & 3].k0 = k0;
-        }
-        {
-          const uint32_t tile = smem0 + L::oRing + L::slot_offset((2 * i) % L::kSlots);
+        const uint32_t k_tile = smem0 + L::oRing + L::slot_offset((2 * i) % L::kSlots);
 #pragma unroll
-          for (int k = 0; k < kPassK; ++k) {
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int c = 0; c < kGroupsK; ++c) {
             uint32_t f[8];
-            to_f16(lds128(codes + k * kPassBytes), f);
-            put(tile + (k % (DQK / 64)) * L::kChunk + (k / (DQK / 64)) * 64 * 128, f);
+            to_f16(k_codes + code_at(DQK, c, my_row + 64 * h), f);
+            put(k_tile + c * L::kChunk + h * 64 * 128, f);
           }
-        }
         slot_done(2 * i);
 
-        const uint32_t v_codes = codes + kPassK * kPassBytes;
-        if (masked) {  // hidden from some row: no value may be NaN
+        if (masked) {  // hidden from some row: no value may be NaN (a thread's own chunks, in place)
+          const int left = tiles[i & 7].left;
 #pragma unroll 1
-          for (int k = 0; k < kPassV; ++k) {
-            const int row = my_row + 64 * (k / (DV / 64));
-            uint4 v = lds128(v_codes + k * kPassBytes);
+          for (int k = 0; k < 2 * kGroupsV; ++k) {
+            const int row = my_row + 64 * (k / kGroupsV);
+            const uint32_t at = v_codes + code_at(DV, k % kGroupsV, row);
+            uint4 v = lds128(at);
             uint32_t* w = &v.x;
-            const bool inside = token0 + row < cur.s.len;
+            const bool inside = row < left;
             uint32_t any = 0;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -511,76 +608,76 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
               w[x] = inside ? w[x] & ~((bad >> 7) * 0xffu) : 0u;
             }
             if (any != 0 && inside) atomicOr(&poison[i & 7][row >> 5], 1u << (row & 31));
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(v_codes + k * kPassBytes), "r"(v.x), "r"(v.y),
-                         "r"(v.z), "r"(v.w)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                          : "memory");
           }
+          fence_proxy_async_smem();  // the next copy into the same place comes by TMA
         }
         if (!slot_free(2 * i + 1)) break;
         // cleared for a tile far enough ahead that neither its conversion has begun nor the softmax of the
         // last tile that used these words is still under way
         if (ft < 4) poison[(i + 4) & 7][ft] = 0;
-        {
-          const uint32_t tile = smem0 + L::oRing + L::slot_offset((2 * i + 1) % L::kSlots);
-          if (!wide) {
+        const uint32_t v_tile = smem0 + L::oRing + L::slot_offset((2 * i + 1) % L::kSlots);
+        if (!wide) {
 #pragma unroll
-            for (int k = 0; k < kPassV; ++k) {
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int c = 0; c < kGroupsV; ++c) {
               uint32_t f[8];
-              to_f16(lds128(v_codes + k * kPassBytes), f);
-              put(tile + (k % (DV / 64)) * L::kChunk + (k / (DV / 64)) * 64 * 128, f);
+              to_f16(v_codes + code_at(DV, c, my_row + 64 * h), f);
+              put(v_tile + c * L::kChunk + h * 64 * 128, f);
             }
-          } else {
+        } else {
 #pragma unroll 1
-            for (int k = 0; k < kPassV; ++k) {
-              const int row = my_row + 64 * (k / (DV / 64));
-              const float scale = pow2(__shfl_sync(0xffffffffu, vk, row >> 4));
-              uint32_t f[8];
-              to_f16(lds128(v_codes + k * kPassBytes), f);
+          for (int k = 0; k < 2 * kGroupsV; ++k) {
+            const int row = my_row + 64 * (k / kGroupsV);
+            const float scale = pow2(tiles[i & 7].vk[row >> 4]);
+            uint32_t f[8];
+            to_f16(v_codes + code_at(DV, k % kGroupsV, row), f);
 #pragma unroll
-              for (int x = 0; x < 8; ++x) f[x] = scaled_bf16x2(f[x], scale);
-              put(tile + (k % (DV / 64)) * L::kChunk + (k / (DV / 64)) * 64 * 128, f);
-            }
+            for (int x = 0; x < 8; ++x) f[x] = scaled_bf16x2(f[x], scale);
+            put(v_tile + (k % kGroupsV) * L::kChunk + (k / kGroupsV) * 64 * 128, f);
           }
         }
         slot_done(2 * i + 1);
-        ek = ek_next, ev = ev_next;
-        fetch();
-        if (i + 1 < count) paged_next<kTile>(p, cur);
+        if (lane == 0) mbar_arrive(code_empty(stage));  // behind slot_done's __syncwarp: the warp has read it
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
       // ======== MMA ========
       constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false) & ~((1u << 7) | (1u << 10));  // f16 operands
       constexpr uint32_t kIdescWide = idesc_bf16_f32(128, DV, false, true);  // bf16 operands
       constexpr uint32_t kIdescO = kIdescWide & ~((1u << 7) | (1u << 10));
       const uint32_t leader = lane == 0 ? 1u : 0u;
+      // what the instructions take comes by a shuffle, which tells the compiler that it is the same in all lanes
+      auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+      const uint32_t t0_mem = uniform(tmem), base = uniform(smem0);
+      const int n = uniform(count);
       auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, tc_wait(bar, parity, wc)); };
       auto wait_entry = [&](int e) { return wait(kv_full(e % L::kSlots), (e / L::kSlots) & 1); };
       auto issue_s = [&](int i) {  // S of tile i; its K slot is free after it
         const int slot = (2 * i) % L::kSlots;
-        const uint32_t k_at = smem0 + L::oRing + L::slot_offset(slot);
+        const uint32_t k_at = base + L::oRing + L::slot_offset(slot);
 #pragma unroll
         for (int c = 0; c < DQK / 64; ++c) {
           const uint32_t co = opaque_u32(static_cast<uint32_t>(c * L::kChunk));
-          mma_ss_x4<2, 2>(tmem + 128 * (i & 1), smem_desc_sw128(smem0 + co, 16, 1024), smem_desc_sw128(k_at + co, 16, 1024),
+          mma_ss_x4<2, 2>(t0_mem + 128 * (i & 1), smem_desc_sw128(base + co, 16, 1024), smem_desc_sw128(k_at + co, 16, 1024),
                           kIdescS, c != 0 ? 1u : 0u, leader);
         }
         mma_commit(s_full(i & 1), leader);
         mma_commit(kv_empty(slot), leader);
       };
       PagedCursor cur = begin_at;
-      int units = 0;
+      int tile = uniform(cur.tile), unit_tiles = uniform(cur.s.tiles), units = 0;
       bool ok = true;
-      for (int i = 0; i < count && ok; ++i) {
-        if (i == 0 || cur.tile == 0) {
+      for (int i = 0; i < n && ok; ++i) {
+        if (i == 0 || tile == 0) {
           ok = wait(bar_q, units & 1) && wait_entry(2 * i);
           if (!ok) break;
           ++units;
           tc_fence_after();
           issue_s(i);
         }
-        const bool more = cur.tile + 1 < cur.s.tiles && i + 1 < count;  // the unit goes on
-        if (more) {
+        if (tile + 1 < unit_tiles && i + 1 < n) {  // the unit goes on
           ok = wait_entry(2 * i + 2);
           if (!ok) break;
           tc_fence_after();
@@ -590,18 +687,30 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const int slot = (2 * i + 1) % L::kSlots;
-        const uint32_t v_at = smem0 + L::oRing + L::slot_offset(slot);
-        const bool begun = i != 0 && cur.tile != 0;  // O holds tiles of this unit
-        const uint32_t idesc = tiles[i & 3].wide != 0 ? kIdescWide : kIdescO;
+        const uint32_t v_at = base + L::oRing + L::slot_offset(slot);
+        const uint32_t begun = i != 0 && tile != 0 ? 1u : 0u;  // O holds tiles of this unit
+        const uint32_t p_at = t0_mem + L::kColP + 64 * (i & 1);
+        if (uniform(tiles[i & 7].wide) == 0) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t va = opaque_u32(v_at + static_cast<uint32_t>(h * 64 * 128));
-          mma_ts_x4<(16 * 128 >> 4)>(tmem + L::kColO, tmem + L::kColP + 64 * (i & 1) + 32 * h, smem_desc_sw128(va, L::kChunk, 1024),
-                                     idesc, h != 0 || begun ? 1u : 0u, leader);
+          for (int h = 0; h < 2; ++h)
+            mma_ts_x4<(16 * 128 >> 4)>(t0_mem + L::kColO, p_at + 32 * h,
+                                       smem_desc_sw128(opaque_u32(v_at + static_cast<uint32_t>(h * 64 * 128)), L::kChunk, 1024),
+                                       kIdescO, h != 0 ? 1u : begun, leader);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            mma_ts_x4<(16 * 128 >> 4)>(t0_mem + L::kColO, p_at + 32 * h,
+                                       smem_desc_sw128(opaque_u32(v_at + static_cast<uint32_t>(h * 64 * 128)), L::kChunk, 1024),
+                                       kIdescWide, h != 0 ? 1u : begun, leader);
         }
-        mma_commit(bar_o, leader);
+        mma_commit(o_full(i & 1), leader);
         mma_commit(kv_empty(slot), leader);
-        if (i + 1 < count) paged_next<kTile>(p, cur);
+        if (++tile == unit_tiles && i + 1 < n) {
+          cur.tile = cur.s.tiles - 1;
+          paged_next<kTile>(p, cur);
+          tile = 0;
+          unit_tiles = uniform(cur.s.tiles);
+        }
       }
       // every MMA issued so far has completed once this fires
       mma_commit(bar_drain, leader);
