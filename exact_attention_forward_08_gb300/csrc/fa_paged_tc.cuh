@@ -25,7 +25,7 @@
 //               takes a half or a quarter of every tile's tokens, with weights
 //               of 0 for the others, and the copies are added up at the end.
 //   warp 4      issues the MMAs, S of the next tile before P V of this one.
-//   warp 5      loads: block table, scales, and the codes by TMA two tiles ahead.
+//   warp 5      loads: block table, scales, and the codes by TMA ahead of their use.
 //   warps 6-13  codes to operands, in the tensor cores' swizzled layout.
 // TMEM: S of even and odd tiles, O, P of even and odd tiles.  What bounds it:
 // per 128 tokens and head 32 KB of codes come in (about 1400 cycles at this
@@ -45,13 +45,16 @@ struct TcShape {
   static constexpr int kThreads = 32 * (kFillWarp0 + kFillWarps);
   static constexpr int kChunk = 128 * 128;  // 128 rows of 64 operands, swizzled
   static constexpr int kQBytes = DQK / 64 * kChunk;
-  // operand slots, K and V tiles by turns: three, or with wide keys one of each kind
-  static constexpr int kSlots = DQK == 192 ? 2 : 3;
+  // operand slots, K and V tiles by turns: two of each kind, or one where keys are wide.  With three that take turns K
+  // of the next tile waits for P V of the one before, and everything behind it too.
+  static constexpr int kSlots = DQK == 192 ? 2 : 4;
   static constexpr int kKBytes = DQK / 64 * kChunk, kVBytes = DV / 64 * kChunk;
-  static constexpr int kRingBytes = kSlots == 3 ? 3 * kKBytes : kKBytes + kVBytes;
-  static __device__ __forceinline__ int slot_offset(int slot) { return slot * kKBytes; }
-  static constexpr int kCodeBytes = kTile * (DQK + DV);  // codes of a tile
-  static constexpr int kCodes = 2;                       // tiles under way
+  static constexpr int kRingBytes = kSlots / 2 * (kKBytes + kVBytes);
+  static __device__ __forceinline__ int slot_offset(int slot) {
+    return (slot >> 1) * (kKBytes + kVBytes) + (slot & 1) * kKBytes;
+  }
+  static constexpr int kCodeBytes = kTile * (DQK > DV ? DQK : DV);  // codes of K or V of a tile
+  static constexpr int kCodes = 3;                                  // of them under way, K and V by turns
   static constexpr int oRing = kQBytes, oCodes = oRing + kRingBytes;
   static constexpr int kBytes = oCodes + kCodes * kCodeBytes + 1024;
   static_assert(kBytes <= 227 * 1024 - 10 * 1024, "shared memory");
@@ -168,15 +171,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
       const uint32_t t_o = t_lane + L::kColO;
       // lanes' copies of the rows: this thread's row, and the tokens of a tile that its copy takes
       const int copies = p.copies, copy_rows = 128 / copies, copy = tid / copy_rows, r = tid - copy * copy_rows;
-      const int groups = 4 / copies, group0 = copy * groups;  // of 32 tokens
-      if (copies > 1) {  // weights of other copies' tokens are 0 for good
-        uint32_t zero[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) zero[k] = 0;
-#pragma unroll 1
-        for (int c = 0; c < 128; c += 32) tmem_st32(t_lane + L::kColP + c, zero);
-        tmem_wait_st();
-      }
+      const int groups = 8 / copies, group0 = copy * groups;  // of 16 tokens
       float fac = 0.f, ref = -INFINITY, sum = 0.f;
       int limit = 0, min_limit = 0, unit_k0 = 0, x_phase = 0;
       bool started_here = false;
@@ -235,6 +230,14 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
           }
           fence_proxy_async_smem();
           mbar_arrive(bar_q);
+          if (i == 0 && copies > 1) {  // weights of other copies' tokens are 0 for good
+            uint32_t zero[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) zero[k] = 0;
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) tmem_st32(t_lane + L::kColP + c, zero);
+            tmem_wait_st();
+          }
         }
         const int buf = i & 1, token0 = cur.tile * kTile;
         const bool masked = token0 + kTile > min_limit;
@@ -258,58 +261,52 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
             part = 0.f;
 #pragma unroll 1
             for (int g = group0; g < group0 + groups; ++g) {
-              uint32_t s[32];
-              tmem_ld32_wait(t_s + 32 * g, s);
-              const float2 ks = *reinterpret_cast<const float2*>(&tiles[i & 7].ks[2 * g]);
-              const int2 vk = *reinterpret_cast<const int2*>(&tiles[i & 7].vk[2 * g]);
-              const float f0 = fac * ks.x, f1 = fac * ks.y;
-              const float back0 = wide ? back : back + static_cast<float>(vk.x);
-              const float back1 = wide ? back : back + static_cast<float>(vk.y);
-              float e0 = 0.f, e1 = 0.f;
-              const uint32_t bad = kMask ? poison[i & 7][g] : 0u;
-              const int left = kMask ? limit - token0 - 32 * g : 32;  // columns that the row sees
-              float m0 = -INFINITY, m1 = -INFINITY;
+              uint32_t s[16];
+              tmem_ld16_wait(t_s + 16 * g, s);
+              const int vk = tiles[i & 7].vk[g];
+              const float f = fac * tiles[i & 7].ks[g];
+              const float from = wide ? back : back + static_cast<float>(vk);
+              const uint32_t bad = kMask ? poison[i & 7][g >> 1] >> (16 * (g & 1)) : 0u;
+              const int left = kMask ? limit - token0 - 16 * g : 16;  // columns that the row sees
+              float m = -INFINITY, e0 = 0.f, e1 = 0.f;
 #pragma unroll
               for (int c = 0; c < 16; c += 2) {
                 if (kMask) {
-                  if (c < left) m0 = fmaxf(m0, __uint_as_float(s[c]));
-                  if (c + 1 < left) m0 = fmaxf(m0, __uint_as_float(s[c + 1]));
-                  if (c + 16 < left) m1 = fmaxf(m1, __uint_as_float(s[c + 16]));
-                  if (c + 17 < left) m1 = fmaxf(m1, __uint_as_float(s[c + 17]));
+                  if (c < left) m = fmaxf(m, __uint_as_float(s[c]));
+                  if (c + 1 < left) m = fmaxf(m, __uint_as_float(s[c + 1]));
                 } else {
-                  m0 = fmax3(m0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-                  m1 = fmax3(m1, __uint_as_float(s[c + 16]), __uint_as_float(s[c + 17]));
+                  m = fmax3(m, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
                 }
               }
-              if (m0 != -INFINITY) mx = fmaxf(mx, m0 * f0);
-              if (m1 != -INFINITY) mx = fmaxf(mx, m1 * f1);
+              if (m != -INFINITY) mx = fmaxf(mx, m * f);
 #pragma unroll
-              for (int c = 0; c < 32; ++c) {
-                float e = ex2_approx(fmaf(__uint_as_float(s[c]), c < 16 ? f0 : f1, c < 16 ? back0 : back1));
+              for (int c = 0; c < 16; ++c) {
+                float e = ex2_approx(fmaf(__uint_as_float(s[c]), f, from));
                 if (kMask) {
                   if ((bad >> c) & 1) e = __uint_as_float(0x7fc00000u);
                   if (c >= left) e = 0.f;
                 }
-                if (c < 16) e0 += e;
-                else e1 += e;
+                if (c & 1) e1 += e;
+                else e0 += e;
                 s[c] = __float_as_uint(e);
               }
-              part += wide ? e0 + e1 : fmaf(e0, pow2(-vk.x), e1 * pow2(-vk.y));
-              uint32_t pk[16];
+              part = wide ? part + (e0 + e1) : fmaf(e0 + e1, pow2(-vk), part);
+              uint32_t pk[8];
               if (wide) {
 #pragma unroll
-                for (int c = 0; c < 16; ++c) pk[c] = pack_bf16x2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
+                for (int c = 0; c < 8; ++c) pk[c] = pack_bf16x2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
               } else {
 #pragma unroll
-                for (int c = 0; c < 16; ++c) pk[c] = pack_f16x2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
+                for (int c = 0; c < 8; ++c) pk[c] = pack_f16x2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
               }
-              tmem_st16(t_p + 16 * g, pk);
+              tmem_st8(t_p + 8 * g, pk);
             }
           };
-          if (masked) weights(std::true_type{});
-          else weights(std::false_type{});
-          const bool move = mx > ref + kRefLag;  // also from -inf
-          if (__any_sync(0xffffffffu, move)) {
+          for (;;) {
+            if (masked) weights(std::true_type{});
+            else weights(std::false_type{});
+            const bool move = mx > ref + kRefLag;  // also from -inf
+            if (!__any_sync(0xffffffffu, move)) break;
             const float alpha = move ? ex2_approx(ref - mx) : 1.f;
             if (move) ref = mx;
             sum *= alpha;
@@ -328,9 +325,8 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
               }
             }
             tmem_wait_st();  // also of the first weights, which are written again
-            if (masked) weights(std::true_type{});
-            else weights(std::false_type{});
           }
+          if (!ok) break;
           sum += part;
           tmem_wait_st();
         }
@@ -445,7 +441,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
     } else if (warp == L::kLoadWarp) {
       // ======== loads ========
       PagedCursor cur = begin_at;
-      int page0 = 0, entry = 0, k0 = 0;
+      int page0 = 0, entry = 0, k0 = 0;  // lane l holds the table's entry of page page0 + l
       auto load_pages = [&](int first_page) {
         page0 = first_page;
         entry = 0;
@@ -457,48 +453,76 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
           }
         }
       };
+      // what is known of a tile before its copies are due: each lane's page, and the scales, lane l's of the tokens
+      // 16 (l % 8) ..
+      struct Ahead {
+        int entry, head, left, ek, ev;
+        int box;  // this lane's copy in the tile, or -1
+        bool first, masked;
+      };
+      auto look_ahead = [&](bool first_of_piece) {
+        Ahead a;
+        const int token0 = cur.tile * kTile;
+        a.left = cur.s.len - token0;
+        a.head = cur.head;
+        a.first = first_of_piece || cur.tile == 0;
+        a.masked = token0 + kTile > least_limit(cur.s);
+        int boxes = (a.left + (1 << p.page_shift) - 1) >> p.page_shift;
+        if (boxes > (kTile >> p.page_shift)) boxes = kTile >> p.page_shift;
+        const int first = (token0 >> p.page_shift) - page0;
+        a.box = lane >= first && lane - first < boxes ? lane - first : -1;
+        a.entry = entry;
+        const int group = lane & 7;
+        const int e = __shfl_sync(0xffffffffu, entry, (first + ((16 * group) >> p.page_shift)) & 31);
+        a.ek = a.ev = 0;
+        if (16 * group < a.left) {
+          const int64_t at = static_cast<int64_t>(e) * p.heads_kv + cur.head;
+          a.ek = p.k_scale[at];
+          a.ev = p.v_scale[at];
+        }
+        return a;
+      };
       load_pages((cur.tile * kTile) >> p.page_shift);
+      Ahead now = look_ahead(true);
+      // an entry's codes: even ones K, odd ones V; each copy announces its own bytes
+      auto place_free = [&](int e) {
+        const int place = e % L::kCodes, use = e / L::kCodes;
+        return use == 0 || __all_sync(0xffffffffu, tc_wait(code_empty(place), (use - 1) & 1, wc));
+      };
+      auto announce = [&](int e, int d) {
+        asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(code_full(e % L::kCodes)),
+                     "r"(d << p.page_shift)
+                     : "memory");
+        return smem0 + L::oCodes + (e % L::kCodes) * L::kCodeBytes;
+      };
       int issued = 0;
-      const int box_shift = p.page_shift;  // tokens of one copy: a page, of at most a tile
       for (int i = 0; i < count; ++i) {
-        const int stage = i % L::kCodes, use = i / L::kCodes;
-        if (use > 0 && !__all_sync(0xffffffffu, tc_wait(code_empty(stage), (use - 1) & 1, wc))) break;
-        const int token0 = cur.tile * kTile, left = cur.s.len - token0;
-        int boxes = (left + (1 << box_shift) - 1) >> box_shift;
-        if (boxes > (kTile >> box_shift)) boxes = kTile >> box_shift;
-        const uint32_t full = code_full(stage);
-        const uint32_t dst = smem0 + L::oCodes + stage * L::kCodeBytes;
-        const int first = (token0 >> p.page_shift) - page0, mine = lane - first;
-        if (mine >= 0 && mine < boxes) {
-          // each copy announces its own bytes; the barrier's one arrival comes below
-          asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(full),
-                       "r"((DQK + DV) << box_shift)
-                       : "memory");
-          const uint32_t row = mine << box_shift;
+        if (!place_free(2 * i)) break;
+        const uint32_t row = now.box << p.page_shift;
+        if (now.box >= 0) {
+          const uint32_t dst = announce(2 * i, DQK), full = code_full((2 * i) % L::kCodes);
           if constexpr (DQK == 128) {
-            tma_load_4d(dst + row * 128, &p.tm_k, full, 0, 0, cur.head, entry);
+            tma_load_4d(dst + row * 128, &p.tm_k, full, 0, 0, now.head, now.entry);
           } else {
 #pragma unroll
             for (int c = 0; c < DQK / 64; ++c)
-              tma_load_4d(dst + c * kTile * 64 + row * 64, &p.tm_k, full, 64 * c, 0, cur.head, entry);
+              tma_load_4d(dst + c * kTile * 64 + row * 64, &p.tm_k, full, 64 * c, 0, now.head, now.entry);
           }
-          tma_load_4d(dst + kTile * DQK + row * DV, &p.tm_v, full, 0, 0, cur.head, entry);
         }
-        // lanes 0 .. 7 (and again in the others): the scales of 16 tokens each
-        const int group = lane & 7;
-        const int e = __shfl_sync(0xffffffffu, entry, (first + ((16 * group) >> p.page_shift)) & 31);
-        const bool none = 16 * group >= left;
-        int ek = 127, ev = 127;
-        if (!none) {
-          const int64_t at = static_cast<int64_t>(e) * p.heads_kv + cur.head;
-          ek = p.k_scale[at];
-          ev = p.v_scale[at];
+        // the next tile's pages and scales are asked for before this one's are used
+        Ahead next = now;
+        if (i + 1 < count) {
+          const int b = cur.b, head = cur.head;
+          paged_next<kTile>(p, cur);
+          const int page = (cur.tile * kTile) >> p.page_shift;
+          if (cur.b != b || (cur.head != head && page0 != 0) || page + kTile / 16 > page0 + 32) load_pages(page);
+          next = look_ahead(false);
         }
         // the unit of O: 2^-3 of the largest of the values' scales in the piece's first tile of the sequence, kept
         // moderate; a scale that is NaN makes the keys' NaN
-        const bool nan = ev == 255;
-        int vk = none || nan ? -1000 : ev - 127;
-        if (i == 0 || cur.tile == 0) {
+        const bool none = 16 * (lane & 7) >= now.left, nan = !none && now.ev == 255;
+        int vk = none || nan ? -1000 : now.ev - 127;
+        if (now.first) {
           k0 = __reduce_max_sync(0xffffffffu, vk);
           k0 = k0 == -1000 ? 0 : k0 - 3;
           k0 = k0 < -20 ? -20 : k0 > 30 ? 30 : k0;
@@ -506,46 +530,48 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
         vk = none || nan ? 0 : vk - k0;
         const bool wide = __any_sync(0xffffffffu, vk < -3 || vk > 6);
         if (lane < 8) {
-          tiles[i & 7].ks[lane] = nan ? scale_of(255) : scale_of(ek);
+          tiles[i & 7].ks[lane] = none ? 1.f : scale_of(nan ? 255 : now.ek);
           tiles[i & 7].vk[lane] = vk;
           if (lane == 0) {
             tiles[i & 7].k0 = k0;
             tiles[i & 7].wide = wide;
-            tiles[i & 7].masked = token0 + kTile > least_limit(cur.s);
-            tiles[i & 7].left = left;
+            tiles[i & 7].masked = now.masked;
+            tiles[i & 7].left = now.left;
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(full);
+        if (lane == 0) mbar_arrive(code_full((2 * i) % L::kCodes));
         ++issued;
-        if (i + 1 < count) {
-          const int b = cur.b, head = cur.head;
-          paged_next<kTile>(p, cur);
-          const int next = (cur.tile * kTile) >> p.page_shift;
-          if (cur.b != b || (cur.head != head && page0 != 0) || next + kTile / 16 > page0 + 32) load_pages(next);
-        }
+        if (!place_free(2 * i + 1)) break;
+        if (now.box >= 0)
+          tma_load_4d(announce(2 * i + 1, DV) + row * DV, &p.tm_v, code_full((2 * i + 1) % L::kCodes), 0, 0, now.head,
+                      now.entry);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(code_full((2 * i + 1) % L::kCodes));
+        ++issued;
+        now = next;
       }
       // the copies under way land before the block's memory is given up, also after a failure
       const uint64_t t0 = globaltimer_ns();
-      for (int i = issued > L::kCodes ? issued - L::kCodes : 0; i < issued; ++i)
-        while (!mbar_try_wait(code_full(i % L::kCodes), (i / L::kCodes) & 1) && globaltimer_ns() - t0 < 1000000000ull) {
+      for (int e = issued > L::kCodes ? issued - L::kCodes : 0; e < issued; ++e)
+        while (!mbar_try_wait(code_full(e % L::kCodes), (e / L::kCodes) & 1) && globaltimer_ns() - t0 < 1000000000ull) {
         }
     } else if (warp >= L::kFillWarp0) {
       // ======== codes to operands ========
       const int ft = tid - 32 * L::kFillWarp0;
       // Eight lanes take 4 neighbouring chunks of 16 codes of the rows r and r ^ 5 (so that they read and write
-      // different banks); pass k of a thread is column group k % (D / 64) of row my_row or my_row + 64.
+      // different banks); a thread takes a column group of the rows my_row and my_row + 64 at a time.
       const int pair = (ft >> 3) & 3, low = (ft >> 2) & 1;
       const int my_row = ((ft >> 5) << 3) + (low ? pair ^ 5 : pair), my_chunk = ft & 3;
       // where a chunk's codes lie (128-byte rows: column groups side by side; 64-byte rows: one after the other),
       // and where the two halves of its operands go in a column group's 128 rows
-      auto code_at = [&](int d, int group, int row) -> uint32_t {
-        if (d == 128) return row * 128 + (((4 * group + my_chunk) ^ (row & 7)) << 4);
-        return group * (kTile * 64) + row * 64 + ((my_chunk ^ ((row >> 1) & 3)) << 4);
+      const uint32_t at128 = my_row * 128 + ((my_chunk ^ (my_row & 7)) << 4);
+      const uint32_t at64 = my_row * 64 + ((my_chunk ^ ((my_row >> 1) & 3)) << 4);
+      auto code_at = [&](int d, int group, int half) -> uint32_t {
+        return d == 128 ? (at128 ^ (group << 6)) + half * (64 * 128) : at64 + group * (kTile * 64) + half * (64 * 64);
       };
       const uint32_t out0 = my_row * 128 + (((2 * my_chunk) ^ (my_row & 7)) << 4);
       const uint32_t out1 = my_row * 128 + (((2 * my_chunk + 1) ^ (my_row & 7)) << 4);
-      constexpr int kGroupsK = DQK / 64, kGroupsV = DV / 64;
       auto to_f16 = [&](uint32_t from, uint32_t (&f)[8]) {
         const uint4 v = lds128(from);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -571,32 +597,29 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
       auto slot_done = [&](int e) {
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(kv_full(e % L::kSlots));
+        if (lane == 0) {
+          mbar_arrive(kv_full(e % L::kSlots));
+          mbar_arrive(code_empty(e % L::kCodes));
+        }
       };
-      for (int i = 0; i < count; ++i) {
-        const int stage = i % L::kCodes;
-        if (!__all_sync(0xffffffffu, tc_wait(code_full(stage), (i / L::kCodes) & 1, wc))) break;
-        const uint32_t k_codes = smem0 + L::oCodes + stage * L::kCodeBytes, v_codes = k_codes + kTile * DQK;
-        const bool wide = tiles[i & 7].wide != 0, masked = tiles[i & 7].masked != 0;
-
-        if (!slot_free(2 * i)) break;
-        const uint32_t k_tile = smem0 + L::oRing + L::slot_offset((2 * i) % L::kSlots);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int c = 0; c < kGroupsK; ++c) {
-            uint32_t f[8];
-            to_f16(k_codes + code_at(DQK, c, my_row + 64 * h), f);
-            put(k_tile + c * L::kChunk + h * 64 * 128, f);
-          }
-        slot_done(2 * i);
-
-        if (masked) {  // hidden from some row: no value may be NaN (a thread's own chunks, in place)
+      // an entry's codes, or 0 after a failure
+      auto codes_of = [&](int e) -> uint32_t {
+        const int place = e % L::kCodes;
+        if (!__all_sync(0xffffffffu, tc_wait(code_full(place), (e / L::kCodes) & 1, wc)) || !slot_free(e)) return 0;
+        return smem0 + L::oCodes + place * L::kCodeBytes;
+      };
+      // One short loop for K and V: what bounds this kernel more than anything else is the fetching of instructions.
+      for (int e = 0; e < 2 * count; ++e) {
+        const uint32_t codes = codes_of(e);
+        if (codes == 0) break;
+        const int i = e >> 1, d = e & 1 ? DV : DQK;
+        const uint32_t to = smem0 + L::oRing + L::slot_offset(e % L::kSlots);
+        if ((e & 1) && tiles[i & 7].masked != 0) {  // hidden from some row: no value may be NaN (own chunks, in place)
           const int left = tiles[i & 7].left;
 #pragma unroll 1
-          for (int k = 0; k < 2 * kGroupsV; ++k) {
-            const int row = my_row + 64 * (k / kGroupsV);
-            const uint32_t at = v_codes + code_at(DV, k % kGroupsV, row);
+          for (int k = 0; k < 2 * (DV / 64); ++k) {
+            const int row = my_row + 64 * (k & 1);
+            const uint32_t at = codes + code_at(DV, k >> 1, k & 1);
             uint4 v = lds128(at);
             uint32_t* w = &v.x;
             const bool inside = row < left;
@@ -611,36 +634,31 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                          : "memory");
           }
-          fence_proxy_async_smem();  // the next copy into the same place comes by TMA
         }
-        if (!slot_free(2 * i + 1)) break;
         // cleared for a tile far enough ahead that neither its conversion has begun nor the softmax of the
         // last tile that used these words is still under way
-        if (ft < 4) poison[(i + 4) & 7][ft] = 0;
-        const uint32_t v_tile = smem0 + L::oRing + L::slot_offset((2 * i + 1) % L::kSlots);
-        if (!wide) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int c = 0; c < kGroupsV; ++c) {
-              uint32_t f[8];
-              to_f16(v_codes + code_at(DV, c, my_row + 64 * h), f);
-              put(v_tile + c * L::kChunk + h * 64 * 128, f);
-            }
+        if ((e & 1) && ft < 4) poison[(i + 4) & 7][ft] = 0;
+        if (!(e & 1) || tiles[i & 7].wide == 0) {
+#pragma unroll 1
+          for (int c = 0; c < d / 64; ++c) {
+            uint32_t f[2][8];
+            to_f16(codes + code_at(d, c, 0), f[0]);
+            to_f16(codes + code_at(d, c, 1), f[1]);
+            put(to + c * L::kChunk, f[0]);
+            put(to + c * L::kChunk + 64 * 128, f[1]);
+          }
         } else {
 #pragma unroll 1
-          for (int k = 0; k < 2 * kGroupsV; ++k) {
-            const int row = my_row + 64 * (k / kGroupsV);
-            const float scale = pow2(tiles[i & 7].vk[row >> 4]);
+          for (int k = 0; k < 2 * (DV / 64); ++k) {
+            const float scale = pow2(tiles[i & 7].vk[(my_row + 64 * (k & 1)) >> 4]);
             uint32_t f[8];
-            to_f16(v_codes + code_at(DV, k % kGroupsV, row), f);
+            to_f16(codes + code_at(DV, k >> 1, k & 1), f);
 #pragma unroll
             for (int x = 0; x < 8; ++x) f[x] = scaled_bf16x2(f[x], scale);
-            put(v_tile + (k % kGroupsV) * L::kChunk + (k / kGroupsV) * 64 * 128, f);
+            put(to + (k >> 1) * L::kChunk + (k & 1) * 64 * 128, f);
           }
         }
-        slot_done(2 * i + 1);
-        if (lane == 0) mbar_arrive(code_empty(stage));  // behind slot_done's __syncwarp: the warp has read it
+        slot_done(e);
       }
     } else {
       // ======== MMA ========
@@ -657,7 +675,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
       auto issue_s = [&](int i) {  // S of tile i; its K slot is free after it
         const int slot = (2 * i) % L::kSlots;
         const uint32_t k_at = base + L::oRing + L::slot_offset(slot);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < DQK / 64; ++c) {
           const uint32_t co = opaque_u32(static_cast<uint32_t>(c * L::kChunk));
           mma_ss_x4<2, 2>(t0_mem + 128 * (i & 1), smem_desc_sw128(base + co, 16, 1024), smem_desc_sw128(k_at + co, 16, 1024),
@@ -690,19 +708,12 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
         const uint32_t v_at = base + L::oRing + L::slot_offset(slot);
         const uint32_t begun = i != 0 && tile != 0 ? 1u : 0u;  // O holds tiles of this unit
         const uint32_t p_at = t0_mem + L::kColP + 64 * (i & 1);
-        if (uniform(tiles[i & 7].wide) == 0) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            mma_ts_x4<(16 * 128 >> 4)>(t0_mem + L::kColO, p_at + 32 * h,
-                                       smem_desc_sw128(opaque_u32(v_at + static_cast<uint32_t>(h * 64 * 128)), L::kChunk, 1024),
-                                       kIdescO, h != 0 ? 1u : begun, leader);
-        } else {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            mma_ts_x4<(16 * 128 >> 4)>(t0_mem + L::kColO, p_at + 32 * h,
-                                       smem_desc_sw128(opaque_u32(v_at + static_cast<uint32_t>(h * 64 * 128)), L::kChunk, 1024),
-                                       kIdescWide, h != 0 ? 1u : begun, leader);
-        }
+        const uint32_t idesc = uniform(tiles[i & 7].wide) == 0 ? kIdescO : kIdescWide;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h)
+          mma_ts_x4<(16 * 128 >> 4)>(t0_mem + L::kColO, p_at + 32 * h,
+                                     smem_desc_sw128(v_at + static_cast<uint32_t>(h * 64 * 128), L::kChunk, 1024), idesc,
+                                     h != 0 ? 1u : begun, leader);
         mma_commit(o_full(i & 1), leader);
         mma_commit(kv_empty(slot), leader);
         if (++tile == unit_tiles && i + 1 < n) {
