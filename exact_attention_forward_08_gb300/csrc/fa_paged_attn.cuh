@@ -199,12 +199,15 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
 struct PagedCursor {
   PagedSeq s;
   int b, head, tile;
+  long long at;  // on the line, where units have a start that costs something
 };
 
 // To the next tile (the caller knows that there is one).
-template <int TILE>
+template <int TILE, int START = 0>
 __device__ __forceinline__ void paged_next(const PagedParams& p, PagedCursor& c) {
+  if constexpr (START > 0) ++c.at;
   if (++c.tile < c.s.tiles) return;
+  if constexpr (START > 0) c.at += START;
   c.tile = 0;
   if (++c.head < p.heads_kv) return;
   c.head = 0;
@@ -214,14 +217,16 @@ __device__ __forceinline__ void paged_next(const PagedParams& p, PagedCursor& c)
   } while (c.s.rows == 0);
 }
 
-// The line of tiles of all sequences and heads, and its equal pieces.
+// The line of tiles of all sequences and heads, and its equal pieces.  A unit,
+// a (sequence, head), takes as many places as it has tiles and START more in
+// front of them, for what its start and its end cost.
 struct PagedLine {
-  long long total, per, used;  // tiles, tiles of a piece, pieces that hold tiles
+  long long total, per, used;  // places, places of a piece, pieces that hold some
   int teams_used;              // of a block
   __device__ __forceinline__ long long piece(int team) const {
     return static_cast<long long>(blockIdx.x) * teams_used + team;
   }
-  __device__ __forceinline__ int count(int team) const {  // tiles of a team of this block
+  __device__ __forceinline__ int count(int team) const {  // places of a team of this block
     const long long left = total - piece(team) * per;
     return team >= teams_used || left <= 0 ? 0 : static_cast<int>(left < per ? left : per);
   }
@@ -229,29 +234,34 @@ struct PagedLine {
 
 // By all threads of the block: cuts the line, finds the places where this
 // block's pieces begin, and says that no piece leaves anything to join yet.
-// Ends with a barrier.
-template <int TILE, int THREADS, int TEAMS>
+// With START > 0 (one team) also counts the piece's tiles.  Ends with a barrier.
+template <int TILE, int THREADS, int TEAMS, int START>
 __device__ __forceinline__ void paged_line(const PagedParams& p, long long* scan, long long* warp_sum,
-                                           PagedCursor* begin_at, PagedLine& line) {
+                                           PagedCursor* begin_at, int* tiles, PagedLine& line) {
+  static_assert(START == 0 || TEAMS == 1, "tiles are counted for one team");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  auto scan_block = [&](int base) -> long long {  // inclusive scan of THREADS sequences' tiles into scan[]
+  if (START > 0 && tid == 0) *tiles = 0;
+  PagedSeq mine;
+  long long v;                                   // places of this thread's sequence
+  auto scan_block = [&](int base) -> long long {  // inclusive scan of THREADS sequences' places into scan[]
     const int b = base + tid;
-    long long v = 0;
+    v = 0;
     if (b < p.batch) {
-      const PagedSeq s = paged_seq<TILE>(p, b);
-      if (s.bad && blockIdx.x == 0) paged_error(p.status, kSitePagedSeq, b);
-      v = s.rows > 0 ? static_cast<long long>(s.tiles) * p.heads_kv : 0;
+      mine = paged_seq<TILE>(p, b);
+      if (mine.bad && blockIdx.x == 0) paged_error(p.status, kSitePagedSeq, b);
+      v = mine.rows > 0 ? (static_cast<long long>(mine.tiles) + START) * p.heads_kv : 0;
     }
+    long long sum = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += y;
+      const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
     }
-    if (lane == 31) warp_sum[warp] = v;
+    if (lane == 31) warp_sum[warp] = sum;
     __syncthreads();
     long long before = 0;
     for (int w = 0; w < warp; ++w) before += warp_sum[w];
-    scan[tid] = before + v;
+    scan[tid] = before + sum;
     __syncthreads();
     return scan[THREADS - 1];
   };
@@ -268,7 +278,26 @@ __device__ __forceinline__ void paged_line(const PagedParams& p, long long* scan
   for (int base = 0; base < p.batch; base += THREADS) {
     if (p.batch > THREADS) scan_block(base);
     const long long sum = scan[THREADS - 1];
-    if (tid < TEAMS && line.count(tid) > 0) {
+    if constexpr (START > 0) {  // each thread for its own sequence
+      const long long before = offset + scan[tid] - v, x0 = line.piece(0) * line.per;
+      const long long x1 = x0 + line.per < line.total ? x0 + line.per : line.total;
+      const long long lo = (x0 > before ? x0 : before) - before, hi = (x1 < before + v ? x1 : before + v) - before;
+      if (lo < hi) {
+        const long long unit = mine.tiles + START;
+        const long long head0 = lo / unit, in0 = lo - head0 * unit - START;
+        const long long head1 = hi / unit, in1 = hi - head1 * unit - START;
+        atomicAdd(tiles, static_cast<int>((head1 - head0) * mine.tiles + (in1 > 0 ? in1 : 0) - (in0 > 0 ? in0 : 0)));
+        if (lo + before == x0) {
+          PagedCursor c;
+          c.s = mine;
+          c.b = base + tid;
+          c.head = static_cast<int>(head0);
+          c.tile = static_cast<int>(in0 > 0 ? in0 : 0);
+          c.at = x0 + (in0 < 0 ? -in0 : 0);
+          *begin_at = c;
+        }
+      }
+    } else if (tid < TEAMS && line.count(tid) > 0) {
       const long long x = line.piece(tid) * line.per - offset;
       if (x >= 0 && x < sum) {  // the first sequence whose inclusive sum exceeds x
         int lo = 0, hi = THREADS - 1;
@@ -324,7 +353,7 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT, TW>::kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   PagedLine line;
-  paged_line<kTile, kThreads, kTeams>(p, scan, warp_sum, begin_at, line);
+  paged_line<kTile, kThreads, kTeams, 0>(p, scan, warp_sum, begin_at, nullptr, line);
 
   const int team = warp / TW, sub = warp % TW;
   const int g = lane >> 2, c = lane & 3;

@@ -40,6 +40,7 @@ namespace fa {
 template <int DQK, int DV>
 struct TcShape {
   static constexpr int kTile = 128, kRows = 128;
+  static constexpr int kStart = 5;  // tiles that a unit's start and end cost
   static constexpr int kFillWarps = 8, kFillThreads = 32 * kFillWarps;
   static constexpr int kMmaWarp = 4, kLoadWarp = 5, kFillWarp0 = 6;
   static constexpr int kThreads = 32 * (kFillWarp0 + kFillWarps);
@@ -54,10 +55,11 @@ struct TcShape {
     return (slot >> 1) * (kKBytes + kVBytes) + (slot & 1) * kKBytes;
   }
   static constexpr int kCodeBytes = kTile * (DQK > DV ? DQK : DV);  // codes of K or V of a tile
-  static constexpr int kCodes = 3;                                  // of them under way, K and V by turns
-  static constexpr int oRing = kQBytes, oCodes = oRing + kRingBytes;
-  static constexpr int kBytes = oCodes + kCodes * kCodeBytes + 1024;
-  static_assert(kBytes <= 227 * 1024 - 10 * 1024, "shared memory");
+  static constexpr int kCodes = 4;                                  // of them under way, K and V by turns
+  static constexpr int oRing = kQBytes < 32 * 1024 ? 32 * 1024 : kQBytes, oCodes = oRing + kRingBytes;
+  static constexpr int kBytes = oCodes + kCodes * kCodeBytes;  // from a 1024-byte boundary
+  static_assert(kBytes + 3 * 1024 <= 227 * 1024, "shared memory, with what the kernel declares itself");
+  static_assert(kThreads * 8 <= oRing && 128 * 64 * 4 <= oRing, "the scan of the sequences and sums of copies come there");
   static constexpr uint32_t kColO = 256, kColP = 384;  // TMEM columns (S: 0 and 128)
 };
 
@@ -65,6 +67,10 @@ struct TcShape {
 __device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t f16x2, float scale) {
   const float2 x = f16x2_float2(f16x2);
   return pack_bf16x2(x.x * scale, x.y * scale);
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 // 2^k for any k, 0 or infinity beyond fp32
@@ -91,18 +97,18 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
     paged_tc_kernel(const __grid_constant__ TcParams p) {
   using L = TcShape<DQK, DV>;
   constexpr int kTile = L::kTile;
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem_tc[];
   __shared__ __align__(8) uint64_t bars[2 * L::kSlots + 9 + 2 * L::kCodes];
   __shared__ __align__(16) TcTile tiles[8];  // of eight tiles
   __shared__ uint32_t poison[8][4];       // tokens of a masked tile whose values hold a NaN, for eight tiles
   __shared__ PagedCursor begin_at;
-  __shared__ long long scan[L::kThreads];
+  __shared__ int tile_count;
   __shared__ long long warp_sum[L::kThreads / 32];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t smem0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t smem0 = smem_u32(smem_tc);
   const uint32_t bar0 = smem_u32(bars);
   auto kv_full = [&](int slot) { return bar0 + 8 * slot; };
   auto kv_empty = [&](int slot) { return bar0 + 8 * (L::kSlots + slot); };
@@ -148,8 +154,9 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
 
   // ---- the line of tiles, as in paged_attn_kernel with one team a block ----
   PagedLine line;
-  paged_line<kTile, L::kThreads, 1>(p, scan, warp_sum, &begin_at, line);
-  const int count = line.count(0);
+  paged_line<kTile, L::kThreads, 1, L::kStart>(p, reinterpret_cast<long long*>(smem_tc), warp_sum, &begin_at, &tile_count,
+                                               line);
+  const int count = tile_count;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -181,33 +188,37 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
         const bool active = warp * 32 - copy * copy_rows < cur.s.rows;  // some row of this warp is one of the sequence's
         if (first) {
           started_here = cur.tile == 0;
-          // this thread's query row as f16, divided by the power of two of its largest value
-          uint4 raw[DQK / 8];
+          // this thread's query row as f16, divided by the power of two of its largest value, by way of its place
           const int pos = r / p.ratio;
+          const uint32_t at = smem0 + tid * 128;
+          auto column = [&](int c) { return at + (c >> 3) * L::kChunk + (((c & 7) ^ (tid & 7)) << 4); };
+          uint32_t top = 0;  // exponents of two columns
           if (r < cur.s.rows) {
             const __nv_bfloat16* src =
                 p.q + (static_cast<int64_t>(cur.s.cu0 + pos) * p.heads_q + cur.head * p.ratio + (r - pos * p.ratio)) * DQK;
-#pragma unroll
-            for (int c = 0; c < DQK / 8; ++c) raw[c] = __ldg(reinterpret_cast<const uint4*>(src) + c);
-          } else {
-#pragma unroll
-            for (int c = 0; c < DQK / 8; ++c) raw[c] = make_uint4(0, 0, 0, 0);
-          }
-          uint32_t top = 0;
-#pragma unroll
-          for (int c = 0; c < DQK / 8; ++c) {
-            const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t a = w[k] & 0x7f80u, b = (w[k] >> 16) & 0x7f80u;
-              top = top > a ? top : a;
-              top = top > b ? top : b;
+#pragma unroll 1
+            for (int c = 0; c < DQK / 8; ++c) cp_async16(column(c), src + 8 * c);
+            cp_async_commit();
+            cp_async_wait<0>();
+#pragma unroll 2
+            for (int c = 0; c < DQK / 8; ++c) {
+              const uint4 x = lds128(column(c));
+              top = __vmaxu2(__vmaxu2(top, x.x & 0x7f807f80u), x.y & 0x7f807f80u);
+              top = __vmaxu2(__vmaxu2(top, x.z & 0x7f807f80u), x.w & 0x7f807f80u);
             }
           }
-          int ex = static_cast<int>(top >> 7);
+          int ex = static_cast<int>(((top & 0xffffu) > (top >> 16) ? top & 0xffffu : top >> 16) >> 7);
           ex = ex == 0 || ex == 255 ? 127 : ex;  // a row of zeros, or one that holds no numbers
           const float down = scale_of(254 - ex);
           fac = p.scale_log2 * scale_of(ex);
+#pragma unroll 2
+          for (int c = 0; c < DQK / 8; ++c) {
+            const uint4 x = r < cur.s.rows ? lds128(column(c)) : make_uint4(0, 0, 0, 0);
+            auto half = [&](uint32_t w) {
+              return pack_f16x2(__uint_as_float(w << 16) * down, __uint_as_float(w & 0xffff0000u) * down);
+            };
+            sts128(column(c), make_uint4(half(x.x), half(x.y), half(x.z), half(x.w)));
+          }
           ref = -INFINITY;
           sum = 0.f;
           min_limit = least_limit(cur.s);
@@ -215,18 +226,6 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
           if (p.causal && r < cur.s.rows) {
             limit = cur.s.len - cur.s.n + pos + 1;
             limit = limit < 0 ? 0 : limit > cur.s.len ? cur.s.len : limit;
-          }
-#pragma unroll
-          for (int c = 0; c < DQK / 8; ++c) {
-            const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
-            uint32_t f[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              f[k] = pack_f16x2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             smem0 + (c >> 3) * L::kChunk + tid * 128 + (((c & 7) ^ (tid & 7)) << 4)),
-                         "r"(f[0]), "r"(f[1]), "r"(f[2]), "r"(f[3])
-                         : "memory");
           }
           fence_proxy_async_smem();
           mbar_arrive(bar_q);
@@ -338,7 +337,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
           const bool whole = started_here && unit_end;
           if (!whole && started_here && tid == 0) {
             PagedJoin j;
-            j.last = static_cast<int>((piece * line.per + i + (cur.s.tiles - 1 - cur.tile)) / line.per);
+            j.last = static_cast<int>((cur.at + (cur.s.tiles - 1 - cur.tile)) / line.per);
             j.cu0 = cur.s.cu0;
             j.head = cur.head;
             j.rows = cur.s.rows;
@@ -347,96 +346,101 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
           ok = __all_sync(0xffffffffu, tc_wait(o_full(buf), (i >> 1) & 1, wc));
           if (!ok) break;
           tc_fence_after();
-          // Copies are added up in halves, upper ones into lower ones, through the queries' place in shared memory,
-          // which the MMAs are done with: row `place` of it, in 16-byte steps that spread over the banks.
-          auto meet = [&]() {  // all softmax threads
-            mbar_arrive(bar_x);
-            return __all_sync(0xffffffffu, tc_wait(bar_x, x_phase++ & 1, wc));
-          };
-          for (int half = copies >> 1; half > 0 && ok; half >>= 1) {
-            const bool gives = copy >= half && copy < 2 * half, takes = copy < half;
-            // a step's upper copies write where they read before, so that nobody else can still be reading there
-            const int place = (half == 1 ? copies / 2 - 1 : gives ? copy - half : copy) * copy_rows + r;
-            const uint32_t at = smem0 + place * (DV * 4);
-            if (gives) {
-              copy_ml[place] = make_float2(ref, sum);
-#pragma unroll 1
-              for (int c = 0; c < DV; c += 32) {
-                uint32_t v[32];
-                tmem_ld32_wait(t_o + c, v);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((c / 4 + k) ^ (r & 7)) << 4)),
-                               "r"(v[4 * k]), "r"(v[4 * k + 1]), "r"(v[4 * k + 2]), "r"(v[4 * k + 3])
-                               : "memory");
-              }
-            }
-            ok = meet();
-            if (ok && takes) {
-              const float2 other = copy_ml[place];
-              const float m = fmaxf(ref, other.x);
-              const float a = m == -INFINITY ? 1.f : ex2_approx(ref - m), b = m == -INFINITY ? 1.f : ex2_approx(other.x - m);
-              ref = m;
-              sum = a * sum + b * other.y;
-#pragma unroll 1
-              for (int c = 0; c < DV; c += 32) {
-                uint32_t v[32];
-                tmem_ld32_wait(t_o + c, v);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const uint4 w = lds128(at + (((c / 4 + k) ^ (r & 7)) << 4));
-                  v[4 * k] = __float_as_uint(fmaf(b, __uint_as_float(w.x), a * __uint_as_float(v[4 * k])));
-                  v[4 * k + 1] = __float_as_uint(fmaf(b, __uint_as_float(w.y), a * __uint_as_float(v[4 * k + 1])));
-                  v[4 * k + 2] = __float_as_uint(fmaf(b, __uint_as_float(w.z), a * __uint_as_float(v[4 * k + 2])));
-                  v[4 * k + 3] = __float_as_uint(fmaf(b, __uint_as_float(w.w), a * __uint_as_float(v[4 * k + 3])));
-                }
-                tmem_st32(t_o + c, v);
-              }
-              tmem_wait_st();
-            }
-          }
-          if (copies > 1 && ok) ok = meet();  // read before the next queries come there
-          if (!ok) break;
-          if (active && copy == 0) {
-            const int64_t part = 2 * piece + (started_here ? 1 : 0);
+          const float unit = pow2(unit_k0);
+          // `out` columns from c on of this thread's row, as sums of all copies or as a part
+          auto write = [&](auto columns, const float* v, int c, float rf, float l) {
+            constexpr int N = decltype(columns)::value;
             const int pos = r / p.ratio, hq = cur.head * p.ratio + (r - pos * p.ratio);
-            const int64_t token = cur.s.cu0 + pos;
-            const float rf = sum != 0.f && ref == -INFINITY ? 0.f : ref;
-            const float unit = pow2(unit_k0);
-            const float inv = sum == 0.f ? 0.f : unit / sum;
+            const int64_t token = cur.s.cu0 + pos, part = 2 * piece + (started_here ? 1 : 0);
+            if (whole) {
+              // a row without a key multiplied nothing: its O is whatever P V of zeros left
+              const float inv = l == 0.f ? 0.f : unit / l;
+              uint4* dst = reinterpret_cast<uint4*>(p.o + (token * p.heads_q + hq) * DV + c);
+#pragma unroll
+              for (int k = 0; k < N / 8; ++k) {
+                uint32_t w[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) w[x] = pack_bf16x2(v[8 * k + 2 * x] * inv, v[8 * k + 2 * x + 1] * inv);
+                dst[k] = l == 0.f ? make_uint4(0, 0, 0, 0) : make_uint4(w[0], w[1], w[2], w[3]);
+              }
+              if (c == 0 && p.lse != nullptr)
+                p.lse[hq * p.total_q + token] = l == 0.f ? -INFINITY : (rf + log2f(l)) * 0.6931471805599453f;
+            } else {
+              float4* dst = reinterpret_cast<float4*>(p.part_o + (part * L::kRows + r) * DV + c);
+#pragma unroll
+              for (int k = 0; k < N / 4; ++k)
+                dst[k] = make_float4(v[4 * k] * unit, v[4 * k + 1] * unit, v[4 * k + 2] * unit, v[4 * k + 3] * unit);
+              if (c == 0) p.part_ml[part * L::kRows + r] = make_float2(rf + kPShift, l);
+            }
+          };
+          if (copies == 1) {
+            if (active) {
+              const float rf = sum != 0.f && ref == -INFINITY ? 0.f : ref;
 #pragma unroll 1
-            for (int c = 0; c < DV; c += 32) {
-              uint32_t v[32];
-              tmem_ld32_wait(t_o + c, v);
-              if (r < cur.s.rows) {
-                if (whole) {
-                  uint4* dst = reinterpret_cast<uint4*>(p.o + (token * p.heads_q + hq) * DV + c);
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                      w[x] = pack_bf16x2(__uint_as_float(v[8 * k + 2 * x]) * inv, __uint_as_float(v[8 * k + 2 * x + 1]) * inv);
-                    // a row without a key multiplied nothing: its O is whatever P V of zeros left
-                    dst[k] = sum == 0.f ? make_uint4(0, 0, 0, 0) : make_uint4(w[0], w[1], w[2], w[3]);
-                  }
-                } else {
-                  uint4* dst = reinterpret_cast<uint4*>(p.part_o + (part * L::kRows + r) * DV + c);
-#pragma unroll
-                  for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * unit);
-#pragma unroll
-                  for (int k = 0; k < 8; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-                }
+              for (int c = 0; c < DV; c += 16) {
+                uint32_t v[16];
+                tmem_ld16_wait(t_o + c, v);
+                if (r < cur.s.rows) write(std::integral_constant<int, 16>{}, reinterpret_cast<const float*>(v), c, rf, sum);
               }
             }
-            if (r < cur.s.rows) {
-              if (!whole) p.part_ml[part * L::kRows + r] = make_float2(rf + kPShift, sum);
-              else if (p.lse != nullptr)
-                p.lse[hq * p.total_q + token] = sum == 0.f ? -INFINITY : (rf + log2f(sum)) * 0.6931471805599453f;
+          } else {
+            // Copies are added up through the queries' place in shared memory, which the MMAs are done with: 64 columns
+            // of all 128 lanes at a time, of which copy c takes 64 / copies.  16-byte steps of a lane spread over the
+            // banks.
+            auto meet = [&]() {  // all softmax threads
+              mbar_arrive(bar_x);
+              return __all_sync(0xffffffffu, tc_wait(bar_x, x_phase++ & 1, wc));
+            };
+            const float rf0 = sum != 0.f && ref == -INFINITY ? 0.f : ref;
+            copy_ml[tid] = make_float2(rf0, sum);
+            const int mine = 64 / copies;
+#pragma unroll 1
+            for (int c0 = 0; c0 < DV && ok; c0 += 64) {
+#pragma unroll 1
+              for (int c = 0; c < 64; c += 16) {
+                uint32_t v[16];
+                tmem_ld16_wait(t_o + c0 + c, v);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  sts128(smem0 + tid * 256 + (((c / 4 + k) ^ (tid & 15)) << 4),
+                         make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
+              }
+              ok = meet();
+              if (ok && r < cur.s.rows) {
+                float rf = -INFINITY, l = 0.f;
+                for (int k = 0; k < copies; ++k) rf = fmaxf(rf, copy_ml[k * copy_rows + r].x);
+                const float base = rf == -INFINITY ? 0.f : rf;
+                for (int k = 0; k < copies; ++k) {
+                  const float2 ml = copy_ml[k * copy_rows + r];
+                  l = fmaf(ex2_approx(ml.x - base), ml.y, l);
+                }
+#pragma unroll 1
+                for (int c = copy * mine; c < (copy + 1) * mine; c += 16) {
+                  float v[16];
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) v[k] = 0.f;
+#pragma unroll 1
+                  for (int k = 0; k < copies; ++k) {
+                    const int from = k * copy_rows + r;
+                    const float w = ex2_approx(copy_ml[from].x - base);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                      const uint4 y = lds128(smem0 + from * 256 + (((c / 4 + x) ^ (from & 15)) << 4));
+                      v[4 * x] = fmaf(w, __uint_as_float(y.x), v[4 * x]);
+                      v[4 * x + 1] = fmaf(w, __uint_as_float(y.y), v[4 * x + 1]);
+                      v[4 * x + 2] = fmaf(w, __uint_as_float(y.z), v[4 * x + 2]);
+                      v[4 * x + 3] = fmaf(w, __uint_as_float(y.w), v[4 * x + 3]);
+                    }
+                  }
+                  write(std::integral_constant<int, 16>{}, v, c0 + c, rf, l);
+                }
+              }
+              if (ok) ok = meet();  // read before the next columns or queries come there
             }
+            if (!ok) break;
           }
         }
-        if (i + 1 < count) paged_next<kTile>(p, cur);
+        if (i + 1 < count) paged_next<kTile, L::kStart>(p, cur);
       }
     } else if (warp == L::kLoadWarp) {
       // ======== loads ========
@@ -482,6 +486,37 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
         }
         return a;
       };
+      auto advance = [&]() {
+        const int b = cur.b, head = cur.head;
+        paged_next<kTile, L::kStart>(p, cur);
+        const int page = (cur.tile * kTile) >> p.page_shift;
+        if (cur.b != b || (cur.head != head && page0 != 0) || page + kTile / 16 > page0 + 32) load_pages(page);
+      };
+      // what the other warps read of a tile
+      auto tell = [&](int i, const Ahead& a) {
+        // the unit of O: 2^-3 of the largest of the values' scales in the piece's first tile of the sequence, kept
+        // moderate; a scale that is NaN makes the keys' NaN
+        const bool none = 16 * (lane & 7) >= a.left, nan = !none && a.ev == 255;
+        int vk = none || nan ? -1000 : a.ev - 127;
+        if (a.first) {
+          k0 = __reduce_max_sync(0xffffffffu, vk);
+          k0 = k0 == -1000 ? 0 : k0 - 3;
+          k0 = k0 < -20 ? -20 : k0 > 30 ? 30 : k0;
+        }
+        vk = none || nan ? 0 : vk - k0;
+        const bool wide = __any_sync(0xffffffffu, vk < -3 || vk > 6);
+        TcTile& t = tiles[i & 7];
+        if (lane < 8) {
+          t.ks[lane] = none ? 1.f : scale_of(nan ? 255 : a.ek);
+          t.vk[lane] = vk;
+        }
+        if (lane == 0) {
+          t.k0 = k0;
+          t.wide = wide;
+          t.masked = a.masked;
+          t.left = a.left;
+        }
+      };
       load_pages((cur.tile * kTile) >> p.page_shift);
       Ahead now = look_ahead(true);
       // an entry's codes: even ones K, odd ones V; each copy announces its own bytes
@@ -509,36 +544,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
               tma_load_4d(dst + c * kTile * 64 + row * 64, &p.tm_k, full, 64 * c, 0, now.head, now.entry);
           }
         }
-        // the next tile's pages and scales are asked for before this one's are used
-        Ahead next = now;
-        if (i + 1 < count) {
-          const int b = cur.b, head = cur.head;
-          paged_next<kTile>(p, cur);
-          const int page = (cur.tile * kTile) >> p.page_shift;
-          if (cur.b != b || (cur.head != head && page0 != 0) || page + kTile / 16 > page0 + 32) load_pages(page);
-          next = look_ahead(false);
-        }
-        // the unit of O: 2^-3 of the largest of the values' scales in the piece's first tile of the sequence, kept
-        // moderate; a scale that is NaN makes the keys' NaN
-        const bool none = 16 * (lane & 7) >= now.left, nan = !none && now.ev == 255;
-        int vk = none || nan ? -1000 : now.ev - 127;
-        if (now.first) {
-          k0 = __reduce_max_sync(0xffffffffu, vk);
-          k0 = k0 == -1000 ? 0 : k0 - 3;
-          k0 = k0 < -20 ? -20 : k0 > 30 ? 30 : k0;
-        }
-        vk = none || nan ? 0 : vk - k0;
-        const bool wide = __any_sync(0xffffffffu, vk < -3 || vk > 6);
-        if (lane < 8) {
-          tiles[i & 7].ks[lane] = none ? 1.f : scale_of(nan ? 255 : now.ek);
-          tiles[i & 7].vk[lane] = vk;
-          if (lane == 0) {
-            tiles[i & 7].k0 = k0;
-            tiles[i & 7].wide = wide;
-            tiles[i & 7].masked = now.masked;
-            tiles[i & 7].left = now.left;
-          }
-        }
+        tell(i, now);
         __syncwarp();
         if (lane == 0) mbar_arrive(code_full((2 * i) % L::kCodes));
         ++issued;
@@ -549,7 +555,10 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(code_full((2 * i + 1) % L::kCodes));
         ++issued;
-        now = next;
+        if (i + 1 < count) {
+          advance();
+          now = look_ahead(false);
+        }
       }
       // the copies under way land before the block's memory is given up, also after a failure
       const uint64_t t0 = globaltimer_ns();
@@ -582,12 +591,8 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
         }
       };
       auto put = [&](uint32_t at, const uint32_t (&f)[8]) {
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + out0), "r"(f[0]), "r"(f[1]), "r"(f[2]),
-                     "r"(f[3])
-                     : "memory");
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + out1), "r"(f[4]), "r"(f[5]), "r"(f[6]),
-                     "r"(f[7])
-                     : "memory");
+        sts128(at + out0, make_uint4(f[0], f[1], f[2], f[3]));
+        sts128(at + out1, make_uint4(f[4], f[5], f[6], f[7]));
       };
       // an entry's slot of the ring is free once the MMA on its last use is done
       auto slot_free = [&](int e) {
@@ -631,8 +636,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
               w[x] = inside ? w[x] & ~((bad >> 7) * 0xffu) : 0u;
             }
             if (any != 0 && inside) atomicOr(&poison[i & 7][row >> 5], 1u << (row & 31));
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                         : "memory");
+            sts128(at, v);
           }
         }
         // cleared for a tile far enough ahead that neither its conversion has begun nor the softmax of the
@@ -718,7 +722,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
         mma_commit(kv_empty(slot), leader);
         if (++tile == unit_tiles && i + 1 < n) {
           cur.tile = cur.s.tiles - 1;
-          paged_next<kTile>(p, cur);
+          paged_next<kTile, L::kStart>(p, cur);
           tile = 0;
           unit_tiles = uniform(cur.s.tiles);
         }
