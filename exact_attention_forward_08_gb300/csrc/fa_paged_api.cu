@@ -259,7 +259,6 @@ int fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse, c
   p.page_shift = page_shift(c.page_size);
   p.causal = causal ? 1 : 0;
   p.timeout_ns = 1000000000ull;
-  p.copies = 1;
   p.max_n = max_seqlen_q;
   p.row_limit = fa::kPagedRowLimit;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);

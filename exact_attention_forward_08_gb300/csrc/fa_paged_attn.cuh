@@ -53,7 +53,7 @@ struct PagedParams {
   int64_t total_q;
   int batch, heads_q, heads_kv, ratio, num_pages, max_pages, page_shift, causal;
   unsigned long long timeout_ns;  // of a wait (paged_tc_kernel)
-  int copies;     // of the rows in the 128 lanes (paged_tc_kernel), each with its share of the tokens
+  int copy_shift;  // 2^this copies of the rows in the 128 lanes (paged_tc_kernel), each with its share of the tokens
   int max_n;      // longest sequence of new tokens allowed
   int row_limit;  // sequences with more rows (new tokens x ratio) are not this kernel's
   float scale_log2;

@@ -25,9 +25,9 @@ inline int paged_allow_smem(const void* kernel, int smem, bool (&ready)[64]) {
 
 // The merge's blocks may be placed while the attention kernel still runs; they wait for its end.
 template <int DV, int ROWS>
-int paged_merge_launch(const PagedParams& p, int pieces, cudaStream_t stream) {
+int paged_merge_launch(const PagedParams& p, int rows, int pieces, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(pieces, ROWS / 8, 1);
+  cfg.gridDim = dim3(pieces, (rows + 7) / 8, 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -47,7 +47,7 @@ int paged_launch(const PagedParams& p, int grid, cudaStream_t stream) {
   if (rc != FA_OK) return rc;
   kernel<<<grid, Shape::kThreads, Shape::kBytes, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  return paged_merge_launch<DV, Shape::kRows>(p, grid * Shape::kTeams, stream);
+  return paged_merge_launch<DV, Shape::kRows>(p, Shape::kRows, grid * Shape::kTeams, stream);
 }
 
 // Codes viewed as (d, token, head, page); a box is a page of one head, `columns` wide.
@@ -70,13 +70,13 @@ int paged_tc_launch(const PagedParams& shared, const fa_kv_cache& c, int rows, i
   if (rc != FA_OK) return rc;
   TcParams p;
   static_cast<PagedParams&>(p) = shared;
-  p.copies = rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
+  p.copy_shift = rows <= 32 ? 2 : rows <= 64 ? 1 : 0;
   rc = paged_encode(&p.tm_k, c.k, c.k_stride, c, DQK, DQK == 128 ? 128 : 64);
   if (rc == FA_OK) rc = paged_encode(&p.tm_v, c.v, c.v_stride, c, DV, DV);
   if (rc != FA_OK) return rc;
   kernel<<<grid, Shape::kThreads, Shape::kBytes, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  return paged_merge_launch<DV, Shape::kRows>(p, grid, stream);
+  return paged_merge_launch<DV, Shape::kRows>(p, rows, grid, stream);
 }
 
 // rows: the most that a sequence has

@@ -177,8 +177,9 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
       const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
       const uint32_t t_o = t_lane + L::kColO;
       // lanes' copies of the rows: this thread's row, and the tokens of a tile that its copy takes
-      const int copies = p.copies, copy_rows = 128 / copies, copy = tid / copy_rows, r = tid - copy * copy_rows;
-      const int groups = 8 / copies, group0 = copy * groups;  // of 16 tokens
+      const int copies = 1 << p.copy_shift, copy_rows = 128 >> p.copy_shift, copy = tid >> (7 - p.copy_shift);
+      const int r = tid & (copy_rows - 1);
+      const int groups = 8 >> p.copy_shift, group0 = copy * groups;  // of 16 tokens
       float fac = 0.f, ref = -INFINITY, sum = 0.f;
       int limit = 0, min_limit = 0, unit_k0 = 0, x_phase = 0;
       bool started_here = false;
@@ -188,19 +189,29 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
         const bool active = warp * 32 - copy * copy_rows < cur.s.rows;  // some row of this warp is one of the sequence's
         if (first) {
           started_here = cur.tile == 0;
-          // this thread's query row as f16, divided by the power of two of its largest value, by way of its place
+          // this thread's query row as f16, divided by the power of two of its largest value, by way of its place;
+          // eight lanes fetch 128 bytes of a row
           const int pos = r / p.ratio;
           const uint32_t at = smem0 + tid * 128;
           auto column = [&](int c) { return at + (c >> 3) * L::kChunk + (((c & 7) ^ (tid & 7)) << 4); };
           uint32_t top = 0;  // exponents of two columns
-          if (r < cur.s.rows) {
-            const __nv_bfloat16* src =
-                p.q + (static_cast<int64_t>(cur.s.cu0 + pos) * p.heads_q + cur.head * p.ratio + (r - pos * p.ratio)) * DQK;
+          const int64_t row_at =
+              (static_cast<int64_t>(cur.s.cu0 + pos) * p.heads_q + cur.head * p.ratio + (r - pos * p.ratio)) * DQK;
 #pragma unroll 1
-            for (int c = 0; c < DQK / 8; ++c) cp_async16(column(c), src + 8 * c);
-            cp_async_commit();
-            cp_async_wait<0>();
-#pragma unroll 2
+          for (int k = 0; k < 32; k += 4) {
+            const int from = k + (lane >> 3), there = __shfl_sync(0xffffffffu, r, from);
+            const __nv_bfloat16* src = p.q + __shfl_sync(0xffffffffu, row_at, from) + 8 * (lane & 7);
+            const uint32_t dst = smem0 + (warp * 32 + from) * 128 + (((lane & 7) ^ (from & 7)) << 4);
+            if (there < cur.s.rows) {
+#pragma unroll
+              for (int c = 0; c < DQK / 64; ++c) cp_async16(dst + c * L::kChunk, src + 64 * c);
+            }
+          }
+          cp_async_commit();
+          cp_async_wait<0>();
+          __syncwarp();
+          if (r < cur.s.rows) {
+#pragma unroll 4
             for (int c = 0; c < DQK / 8; ++c) {
               const uint4 x = lds128(column(c));
               top = __vmaxu2(__vmaxu2(top, x.x & 0x7f807f80u), x.y & 0x7f807f80u);
@@ -211,7 +222,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
           ex = ex == 0 || ex == 255 ? 127 : ex;  // a row of zeros, or one that holds no numbers
           const float down = scale_of(254 - ex);
           fac = p.scale_log2 * scale_of(ex);
-#pragma unroll 2
+#pragma unroll 4
           for (int c = 0; c < DQK / 8; ++c) {
             const uint4 x = r < cur.s.rows ? lds128(column(c)) : make_uint4(0, 0, 0, 0);
             auto half = [&](uint32_t w) {
@@ -247,10 +258,10 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
         }
         if (!ok) break;
         tc_fence_after();
+        if (first) unit_k0 = tiles[i & 7].k0;
         if (active) {
           const uint32_t t_s = t_lane + 128 * buf, t_p = t_lane + L::kColP + 64 * buf;
           const bool wide = tiles[i & 7].wide != 0;
-          if (first) unit_k0 = tiles[i & 7].k0;
           float mx = -INFINITY, part = 0.f;
           // weights of the tile with the present reference, their sum, and the scores' maximum
           auto weights = [&](auto with_mask) {
@@ -346,99 +357,82 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
           ok = __all_sync(0xffffffffu, tc_wait(o_full(buf), (i >> 1) & 1, wc));
           if (!ok) break;
           tc_fence_after();
-          const float unit = pow2(unit_k0);
-          // `out` columns from c on of this thread's row, as sums of all copies or as a part
-          auto write = [&](auto columns, const float* v, int c, float rf, float l) {
-            constexpr int N = decltype(columns)::value;
-            const int pos = r / p.ratio, hq = cur.head * p.ratio + (r - pos * p.ratio);
-            const int64_t token = cur.s.cu0 + pos, part = 2 * piece + (started_here ? 1 : 0);
-            if (whole) {
-              // a row without a key multiplied nothing: its O is whatever P V of zeros left
-              const float inv = l == 0.f ? 0.f : unit / l;
-              uint4* dst = reinterpret_cast<uint4*>(p.o + (token * p.heads_q + hq) * DV + c);
-#pragma unroll
-              for (int k = 0; k < N / 8; ++k) {
-                uint32_t w[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) w[x] = pack_bf16x2(v[8 * k + 2 * x] * inv, v[8 * k + 2 * x + 1] * inv);
-                dst[k] = l == 0.f ? make_uint4(0, 0, 0, 0) : make_uint4(w[0], w[1], w[2], w[3]);
-              }
-              if (c == 0 && p.lse != nullptr)
-                p.lse[hq * p.total_q + token] = l == 0.f ? -INFINITY : (rf + log2f(l)) * 0.6931471805599453f;
-            } else {
-              float4* dst = reinterpret_cast<float4*>(p.part_o + (part * L::kRows + r) * DV + c);
-#pragma unroll
-              for (int k = 0; k < N / 4; ++k)
-                dst[k] = make_float4(v[4 * k] * unit, v[4 * k + 1] * unit, v[4 * k + 2] * unit, v[4 * k + 3] * unit);
-              if (c == 0) p.part_ml[part * L::kRows + r] = make_float2(rf + kPShift, l);
-            }
+          auto meet = [&]() {  // all softmax threads
+            mbar_arrive(bar_x);
+            return __all_sync(0xffffffffu, tc_wait(bar_x, x_phase++ & 1, wc));
           };
-          if (copies == 1) {
-            if (active) {
-              const float rf = sum != 0.f && ref == -INFINITY ? 0.f : ref;
-#pragma unroll 1
-              for (int c = 0; c < DV; c += 16) {
-                uint32_t v[16];
-                tmem_ld16_wait(t_o + c, v);
-                if (r < cur.s.rows) write(std::integral_constant<int, 16>{}, reinterpret_cast<const float*>(v), c, rf, sum);
-              }
-            }
-          } else {
-            // Copies are added up through the queries' place in shared memory, which the MMAs are done with: 64 columns
-            // of all 128 lanes at a time, of which copy c takes 64 / copies.  16-byte steps of a lane spread over the
-            // banks.
-            auto meet = [&]() {  // all softmax threads
-              mbar_arrive(bar_x);
-              return __all_sync(0xffffffffu, tc_wait(bar_x, x_phase++ & 1, wc));
-            };
-            const float rf0 = sum != 0.f && ref == -INFINITY ? 0.f : ref;
-            copy_ml[tid] = make_float2(rf0, sum);
-            const int mine = 64 / copies;
-#pragma unroll 1
-            for (int c0 = 0; c0 < DV && ok; c0 += 64) {
-#pragma unroll 1
-              for (int c = 0; c < 64; c += 16) {
-                uint32_t v[16];
-                tmem_ld16_wait(t_o + c0 + c, v);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  sts128(smem0 + tid * 256 + (((c / 4 + k) ^ (tid & 15)) << 4),
-                         make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
-              }
-              ok = meet();
-              if (ok && r < cur.s.rows) {
-                float rf = -INFINITY, l = 0.f;
-                for (int k = 0; k < copies; ++k) rf = fmaxf(rf, copy_ml[k * copy_rows + r].x);
-                const float base = rf == -INFINITY ? 0.f : rf;
-                for (int k = 0; k < copies; ++k) {
-                  const float2 ml = copy_ml[k * copy_rows + r];
-                  l = fmaf(ex2_approx(ml.x - base), ml.y, l);
-                }
-#pragma unroll 1
-                for (int c = copy * mine; c < (copy + 1) * mine; c += 16) {
-                  float v[16];
-#pragma unroll
-                  for (int k = 0; k < 16; ++k) v[k] = 0.f;
-#pragma unroll 1
-                  for (int k = 0; k < copies; ++k) {
-                    const int from = k * copy_rows + r;
-                    const float w = ex2_approx(copy_ml[from].x - base);
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                      const uint4 y = lds128(smem0 + from * 256 + (((c / 4 + x) ^ (from & 15)) << 4));
-                      v[4 * x] = fmaf(w, __uint_as_float(y.x), v[4 * x]);
-                      v[4 * x + 1] = fmaf(w, __uint_as_float(y.y), v[4 * x + 1]);
-                      v[4 * x + 2] = fmaf(w, __uint_as_float(y.z), v[4 * x + 2]);
-                      v[4 * x + 3] = fmaf(w, __uint_as_float(y.w), v[4 * x + 3]);
-                    }
-                  }
-                  write(std::integral_constant<int, 16>{}, v, c0 + c, rf, l);
-                }
-              }
-              if (ok) ok = meet();  // read before the next columns or queries come there
-            }
+          const float rf = sum != 0.f && ref == -INFINITY ? 0.f : ref;
+          const int64_t part = 2 * piece + (started_here ? 1 : 0);
+          float top = rf, l = sum;
+          if (copies > 1) {
+            copy_ml[tid] = make_float2(rf, sum);
+            ok = meet();
             if (!ok) break;
+            for (int k = 0; k < copies; ++k) top = fmaxf(top, copy_ml[k * copy_rows + r].x);
           }
+          const float base = top == -INFINITY ? 0.f : top;
+          if (copies > 1) {
+            l = 0.f;
+            for (int k = 0; k < copies; ++k) {
+              const float2 ml = copy_ml[k * copy_rows + r];
+              l = fmaf(ex2_approx(ml.x - base), ml.y, l);
+            }
+          }
+          const float unit = pow2(unit_k0);
+          const float scale = ex2_approx(rf - base) * (!whole ? unit : l == 0.f ? 0.f : unit / l);
+          if (copy == 0 && r < cur.s.rows) {
+            if (!whole) {
+              p.part_ml[part * L::kRows + r] = make_float2(top + kPShift, l);
+            } else if (p.lse != nullptr) {
+              const int pos = r / p.ratio;
+              p.lse[static_cast<int64_t>(cur.head * p.ratio + (r - pos * p.ratio)) * p.total_q + cur.s.cu0 + pos] =
+                  l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+            }
+          }
+          // All lanes' O goes through the queries' place in shared memory, which the MMAs are done with, 64 columns at
+          // a time in 16-byte steps that spread over the banks; half a warp then takes a row, adds up its copies and
+          // writes 64 columns side by side.  A lane of no weight (a row without a key) multiplied nothing: its O is
+          // whatever P V of zeros left.
+          const int step = lane & 15;
+#pragma unroll 1
+          for (int c0 = 0; c0 < DV && ok; c0 += 64) {
+#pragma unroll 1
+            for (int c = 0; c < 64; c += 16) {
+              uint32_t v[16];
+              tmem_ld16_wait(t_o + c0 + c, v);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] = scale == 0.f ? 0u : __float_as_uint(__uint_as_float(v[k]) * scale);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                sts128(smem0 + tid * 256 + (((c / 4 + k) ^ (tid & 15)) << 4),
+                       make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
+            }
+            ok = meet();
+            if (!ok) break;
+#pragma unroll 1
+            for (int row = 2 * warp + (lane >> 4); row < cur.s.rows; row += 8) {
+              auto lane_o = [&](int k) {
+                const int from = k * copy_rows + row;
+                const uint4 y = lds128(smem0 + from * 256 + ((step ^ (from & 15)) << 4));
+                return make_float4(__uint_as_float(y.x), __uint_as_float(y.y), __uint_as_float(y.z), __uint_as_float(y.w));
+              };
+              float4 v = lane_o(0);
+              for (int k = 1; k < copies; ++k) {
+                const float4 y = lane_o(k);
+                v = make_float4(v.x + y.x, v.y + y.y, v.z + y.z, v.w + y.w);
+              }
+              const int c = c0 + 4 * step;
+              if (whole) {
+                const int pos = row / p.ratio, hq = cur.head * p.ratio + (row - pos * p.ratio);
+                *reinterpret_cast<uint2*>(p.o + (static_cast<int64_t>(cur.s.cu0 + pos) * p.heads_q + hq) * DV + c) =
+                    make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+              } else {
+                *reinterpret_cast<float4*>(p.part_o + (part * L::kRows + row) * DV + c) = v;
+              }
+            }
+            ok = meet();  // read before the next columns or queries come there
+          }
+          if (!ok) break;
         }
         if (i + 1 < count) paged_next<kTile, L::kStart>(p, cur);
       }
