@@ -15,12 +15,11 @@
 //
 // Work: a tile is 32 or 64 tokens of one key/value head; the tiles of all
 // sequences and heads form one line that is cut into equal pieces, one for
-// each team (1 to 4 warps of 8 or 16 rows each that read the same tiles).  A
-// team streams its piece through its own ring of slots, K and V tiles by turns,
-// filled by asynchronous 16-byte copies kSlots - 1 slots ahead, independently
-// of the other teams.  A (sequence, head) that lies in one piece is written out
-// at once, one that is cut leaves unnormalised parts that paged_merge_kernel
-// joins.
+// each warp ("team").  A warp streams its piece through its own ring of slots,
+// K and V tiles by turns, filled by asynchronous 16-byte copies kSlots - 1 slots
+// ahead, independently of the others.  A (sequence, head) that lies in one piece
+// is written out at once, one that is cut leaves unnormalised parts that
+// paged_merge_kernel joins.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -69,17 +68,17 @@ constexpr int kMinTokens = 64;        // a piece is not cut smaller
 constexpr float kPShift = 7.f;        // P is scaled by 2^7: f16 then holds weights down to 2^-31
 constexpr float kRefLag = 8.f;        // the reference follows the maximum when it lags by more (log2 units)
 
-// NT groups of 8 rows a warp, TW warps a team.  64 tokens a tile halve what a
+// NT groups of 8 rows.  64 tokens a tile halve what a
 // tile costs beside its products (B8 x 32768, 32/8 heads of 128: 93 us against
 // 97 with 32; 16 heads of 64 in pages of 16: 123 against 150); more rows or
 // wider keys leave registers for 32.  Two warps a scheduler: with three, 168
 // registers a thread spill (116 us for the first of these).
-template <int DQK, int DV, int NT, int TW>
+template <int DQK, int DV, int NT>
 struct PagedShape {
-  static constexpr int kRows = 8 * NT * TW;  // rows of a team
+  static constexpr int kRows = 8 * NT;
   static constexpr int kTile = NT == 1 && DQK <= 128 ? 64 : 32;  // tokens
   static constexpr int kWarps = 8, kThreads = 32 * kWarps;
-  static constexpr int kTeams = kWarps / TW;
+  static constexpr int kTeams = kWarps;  // each warp streams a piece of its own
   static constexpr int kSlotBytes = kTile * (DQK > DV ? DQK : DV);
   static constexpr int kSlots = 206 * 1024 / kSlotBytes / kTeams;  // of a team's ring
   static constexpr int kBytes = kTeams * kSlots * kSlotBytes + 128;
@@ -328,10 +327,10 @@ __device__ __forceinline__ void paged_line(const PagedParams& p, long long* scan
 }
 
 // G16: pages of 16 tokens, each with its own scale; else a scale holds for 32 tokens at least.
-template <int DQK, int DV, int NT, int TW, bool G16>
-__global__ void __launch_bounds__(PagedShape<DQK, DV, NT, TW>::kThreads, 1)
+template <int DQK, int DV, int NT, bool G16>
+__global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
     paged_attn_kernel(const __grid_constant__ PagedParams p) {
-  using Shape = PagedShape<DQK, DV, NT, TW>;
+  using Shape = PagedShape<DQK, DV, NT>;
   constexpr int kTile = Shape::kTile;
   constexpr int kSteps = DQK / 64;       // 64-column groups of K
   constexpr int kVWords = DV / 32;       // 32-bit words of V codes a lane reads per token
@@ -355,7 +354,7 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT, TW>::kThreads, 1)
   PagedLine line;
   paged_line<kTile, kThreads, kTeams, 0>(p, scan, warp_sum, begin_at, nullptr, line);
 
-  const int team = warp / TW, sub = warp % TW;
+  const int team = warp;
   const int g = lane >> 2, c = lane & 3;
   const int count = line.count(team);
   if (count == 0) return;
@@ -363,9 +362,8 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT, TW>::kThreads, 1)
   PagedCursor cur = begin_at[team];
   const uint32_t ring = smem0 + team * kSlots * Shape::kSlotBytes;
 
-  // ---- the team fills its ring: tile after tile, K and V by turns, each warp its share of the tokens ----
-  constexpr int kShare = kTile / TW;
-  constexpr int kRun = kShare < (G16 ? 16 : 32) ? kShare : (G16 ? 16 : 32);  // tokens that surely lie in one page
+  // ---- the warp fills its ring: tile after tile, K and V by turns ----
+  constexpr int kRun = G16 ? 16 : 32;  // tokens that surely lie in one page
   PagedCursor ahead = cur;  // the tile that is filled in next
   int filled = 0;           // slots filled so far
   int fill_slot = 0;
@@ -402,7 +400,7 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT, TW>::kThreads, 1)
   };
   // scale k of a slot belongs to 16 tokens: their page's lane, counted from the tile's first
   const int scale_lane = G16 ? lane : lane >> (p.page_shift - 4);
-  // This warp's tokens of a tile, 16 bytes a lane; pages behind the last are left out.  Lane l's chunks in a run
+  // The tokens of a tile, 16 bytes a lane; pages behind the last are left out.  Lane l's chunks in a run
   // of tokens are l, l + 32, ..: with rows of 4 or 8 chunks they are one column, with 12 the rows repeat by 8.
   auto lane_offset = [&](int d, uint32_t token_stride, int i) -> uint32_t {
     const int at = i * 32 + lane, chunks = d / 16;
@@ -424,8 +422,8 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT, TW>::kThreads, 1)
     static_assert(kRun * kChunks % 32 == 0, "whole warps of chunks");
     const uint32_t ts = kK ? p.k_token : p.v_token;
 #pragma unroll
-    for (int r0 = 0; r0 < kShare; r0 += kRun) {
-      const int row0 = sub * kShare + r0, t = token + row0;
+    for (int row0 = 0; row0 < kTile; row0 += kRun) {
+      const int t = token + row0;
       const int e = __shfl_sync(0xffffffffu, entry, (t >> p.page_shift) - page0);
       if (t < ahead.s.len) {
         const uint8_t* src = (kK ? k_at : v_at) + e * (kK ? p.k_page : p.v_page) +
@@ -452,7 +450,7 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT, TW>::kThreads, 1)
         fresh = false;
       }
       const float scale = __shfl_sync(0xffffffffu, is_k ? ks : vs, (token >> p.page_shift) - page0 + scale_lane);
-      if (sub == 0 && lane < kTile / 16) slot_scale[team * kSlots + fill_slot][lane] = scale;
+      if (lane < kTile / 16) slot_scale[team * kSlots + fill_slot][lane] = scale;
       ++filled;
       if (++fill_slot == kSlots) fill_slot = 0;
       if (!is_k && filled < 2 * count) {  // on to the next tile
@@ -470,11 +468,10 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT, TW>::kThreads, 1)
   load_pages((ahead.tile * kTile) >> p.page_shift);
   for (int e = 0; e < kSlots - 1; ++e) fill();
   int slot = -1;
-  // The next slot's tokens are there for the whole team, which has read the slot before: that one is refilled.
+  // The next slot's tokens are there for all lanes, which have read the slot before: that one is refilled.
   auto advance = [&]() {
     cp_async_wait<kSlots - 2>();
-    if constexpr (TW == 1) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(32 * TW) : "memory");
+    __syncwarp();
     if (++slot == kSlots) slot = 0;
     fill();
   };
@@ -490,11 +487,10 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT, TW>::kThreads, 1)
     if (i == 0 || cur.tile == 0) {
       // ---- a new (sequence, head): the query rows as B fragments ----
       started_here = cur.tile == 0;
-      const int row0 = sub * 8 * NT;
       min_limit = cur.s.len;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const int r = row0 + nt * 8 + g;
+        const int r = nt * 8 + g;
         uint4 raw[kSteps * 2];
         if (r < cur.s.rows) {
           const int pos = r / p.ratio, hr = r - pos * p.ratio;
@@ -550,7 +546,7 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT, TW>::kThreads, 1)
           qfac[nt][k] = p.scale_log2 * scale_of(e);
           ref[nt][k] = -INFINITY;
           sum[nt][k] = 0.f;
-          const int rr = row0 + nt * 8 + 2 * c + k;
+          const int rr = nt * 8 + 2 * c + k;
           int lim = cur.s.len;
           if (p.causal && rr < cur.s.rows) {
             lim = cur.s.len - cur.s.n + rr / p.ratio + 1;
@@ -764,7 +760,7 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT, TW>::kThreads, 1)
     if (unit_end || i + 1 == count) {
       const bool whole = started_here && unit_end;
       const int64_t part = 2 * piece + (started_here ? 1 : 0);
-      if (!whole && started_here && sub == 0 && lane == 0) {
+      if (!whole && started_here && lane == 0) {
         // the rest of the unit lies in the pieces that follow
         PagedJoin j;
         j.last = static_cast<int>((begin + i + (cur.s.tiles - 1 - cur.tile)) / line.per);
@@ -781,7 +777,7 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT, TW>::kThreads, 1)
           l += __shfl_xor_sync(0xffffffffu, l, 4);
           l += __shfl_xor_sync(0xffffffffu, l, 8);
           l += __shfl_xor_sync(0xffffffffu, l, 16);
-          const int r = sub * 8 * NT + nt * 8 + 2 * c + k;
+          const int r = nt * 8 + 2 * c + k;
           const float rf = l != 0.f && ref[nt][k] == -INFINITY ? kPShift : ref[nt][k];
           if (r < cur.s.rows) {
             if (whole) {

@@ -38,11 +38,11 @@ int paged_merge_launch(const PagedParams& p, int rows, int pieces, cudaStream_t 
   return cudaLaunchKernelEx(&cfg, paged_merge_kernel<DV, ROWS>, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-template <int DQK, int DV, int NT, int TW, bool G16>
+template <int DQK, int DV, int NT, bool G16>
 int paged_launch(const PagedParams& p, int grid, cudaStream_t stream) {
-  using Shape = PagedShape<DQK, DV, NT, TW>;
+  using Shape = PagedShape<DQK, DV, NT>;
   static bool ready[64] = {};
-  auto* kernel = paged_attn_kernel<DQK, DV, NT, TW, G16>;
+  auto* kernel = paged_attn_kernel<DQK, DV, NT, G16>;
   const int rc = paged_allow_smem(reinterpret_cast<const void*>(kernel), Shape::kBytes, ready);
   if (rc != FA_OK) return rc;
   kernel<<<grid, Shape::kThreads, Shape::kBytes, stream>>>(p);
@@ -82,8 +82,8 @@ int paged_tc_launch(const PagedParams& shared, const fa_kv_cache& c, int rows, i
 // rows: the most that a sequence has
 template <int DQK, int DV, bool G16>
 int paged_launch_rows(const PagedParams& p, const fa_kv_cache& c, int rows, int grid, cudaStream_t stream) {
-  if (rows <= 8) return paged_launch<DQK, DV, 1, 1, G16>(p, grid, stream);
-  if (rows <= 16) return paged_launch<DQK, DV, 2, 1, G16>(p, grid, stream);
+  if (rows <= 8) return paged_launch<DQK, DV, 1, G16>(p, grid, stream);
+  if (rows <= 16) return paged_launch<DQK, DV, 2, G16>(p, grid, stream);
   return paged_tc_launch<DQK, DV>(p, c, rows, grid, stream);
 }
 
