@@ -60,27 +60,32 @@ int page_shift(int page_size) { return page_size == 16 ? 4 : page_size == 32 ? 5
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
-// The workspace: parts, references and sums, and joins of the cut units, then
-// (for calls with long sequences) offsets, unpacked keys and values, and the
-// variable-length forward's own workspace.
+// The workspace: for each of the two kernels the parts, references and sums, and
+// joins of its cut units, then (for calls with long sequences) offsets, unpacked
+// keys and values, and the variable-length forward's own workspace.
 struct Workspace {
-  size_t part_ml, joins, cu_k, k, v, varlen, varlen_bytes, bytes;
+  size_t part_o[2], part_ml[2], joins[2], cu_k, k, v, varlen, varlen_bytes, bytes;
 };
 
-// rows of a team of the attention kernel's build for sequences of `rows` rows
-int team_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 128; }
-
-Workspace workspace_of(int batch, int heads_q, int heads_kv, int64_t total_q, int64_t rows, int64_t total_k, int d_qk,
+Workspace workspace_of(int batch, int heads_q, int heads_kv, int64_t total_q, int max_n, int64_t total_k, int d_qk,
                        int d_v) {
   Workspace w;
   std::memset(&w, 0, sizeof(w));
-  const int tr = team_rows(rows);
-  const size_t pieces = static_cast<size_t>(fa::kPagedMaxBlocks) * (tr <= 16 ? fa::kPagedMaxTeams : 1);
-  size_t at = up256(2 * pieces * tr * d_v * sizeof(float));
-  w.part_ml = at;
-  at += up256(2 * pieces * tr * sizeof(float2));
-  w.joins = at;
-  at += up256(pieces * sizeof(fa::PagedJoin));
+  const int ratio = heads_q / heads_kv;
+  const int64_t rows = static_cast<int64_t>(max_n) * ratio;
+  const fa::PagedSplit split = fa::paged_split(rows, ratio, batch, max_n, -1);  // enough for any total_q
+  size_t at = 0;
+  for (int i = 0; i < 2; ++i) {
+    if ((i == 0 ? split.few : split.many) == 0) continue;
+    const size_t pieces = static_cast<size_t>(fa::kPagedMaxBlocks) * (i == 0 ? fa::kPagedMaxTeams : 1);
+    const size_t part_rows = i == 0 ? fa::paged_few_rows(split.few) : fa::kPagedRowLimit;
+    w.part_o[i] = at;
+    at += up256(2 * pieces * part_rows * d_v * sizeof(float));
+    w.part_ml[i] = at;
+    at += up256(2 * pieces * part_rows * sizeof(float2));
+    w.joins[i] = at;
+    at += up256(pieces * sizeof(fa::PagedJoin));
+  }
   if (rows > fa::kPagedRowLimit) {
     w.cu_k = at;
     at += up256((static_cast<size_t>(batch) + 1) * sizeof(int));
@@ -148,8 +153,7 @@ size_t fa_fwd_paged_workspace_size(int batch, int heads_q, int heads_kv, int64_t
   if (batch < 0 || heads_q < 1 || heads_kv < 1 || heads_q % heads_kv != 0 || total_q < 0 || max_seqlen_q < 0 ||
       total_k < 0 || !dims_supported(d_qk, d_v))
     return 0;
-  const int64_t rows = static_cast<int64_t>(max_seqlen_q) * (heads_q / heads_kv);
-  return workspace_of(batch, heads_q, heads_kv, total_q, rows, total_k, d_qk, d_v).bytes;
+  return workspace_of(batch, heads_q, heads_kv, total_q, max_seqlen_q, total_k, d_qk, d_v).bytes;
 }
 
 int fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse, const int* cu_seqlens_q, int batch,
@@ -174,7 +178,7 @@ int fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse, c
   if (q == nullptr || o == nullptr || cu_seqlens_q == nullptr || workspace == nullptr) return FA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16) || !aligned(workspace, 16) || !aligned(cu_seqlens_q, 4))
     return FA_ERR_INVALID_ARG;
-  const Workspace w = workspace_of(batch, heads_q, c.heads_kv, total_q, rows, total_k, c.d_qk, c.d_v);
+  const Workspace w = workspace_of(batch, heads_q, c.heads_kv, total_q, max_seqlen_q, total_k, c.d_qk, c.d_v);
   if (workspace_bytes < w.bytes) return FA_ERR_INVALID_ARG;
   if (scale == 0.f) scale = 1.0f / std::sqrt(static_cast<float>(c.d_qk));
 
@@ -227,7 +231,6 @@ int fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse, c
 
   fa::PagedParams p;
   std::memset(&p, 0, sizeof(p));
-  const int most = rows < fa::kPagedRowLimit ? static_cast<int>(rows) : fa::kPagedRowLimit;
   p.k = static_cast<const uint8_t*>(c.k);
   p.v = static_cast<const uint8_t*>(c.v);
   p.k_page = c.k_stride[0];
@@ -246,9 +249,6 @@ int fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse, c
   p.seqlens = c.seqlens_k;
   p.cu = cu_seqlens_q;
   p.status = host.status;
-  p.part_o = reinterpret_cast<float*>(ws);
-  p.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
-  p.joins = reinterpret_cast<fa::PagedJoin*>(ws + w.joins);
   p.total_q = total_q;
   p.batch = batch;
   p.heads_q = heads_q;
@@ -260,12 +260,18 @@ int fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse, c
   p.causal = causal ? 1 : 0;
   p.timeout_ns = 1000000000ull;
   p.max_n = max_seqlen_q;
-  p.row_limit = fa::kPagedRowLimit;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   const int grid = host.sms < fa::kPagedMaxBlocks ? host.sms : fa::kPagedMaxBlocks;
-  if (c.d_qk == 64) return fa::paged_launch_d64(p, c, c.d_v, most, grid, stream);
-  if (c.d_qk == 128) return fa::paged_launch_d128(p, c, c.d_v, most, grid, stream);
-  return fa::paged_launch_d192(p, c, c.d_v, most, grid, stream);
+  fa::PagedParts parts[2];
+  for (int i = 0; i < 2; ++i) {
+    parts[i].o = reinterpret_cast<float*>(ws + w.part_o[i]);
+    parts[i].ml = reinterpret_cast<float2*>(ws + w.part_ml[i]);
+    parts[i].joins = reinterpret_cast<fa::PagedJoin*>(ws + w.joins[i]);
+  }
+  const fa::PagedSplit split = fa::paged_split(rows, ratio, batch, max_seqlen_q, total_q);
+  if (c.d_qk == 64) return fa::paged_launch_d64(p, parts, c, split, grid, stream);
+  if (c.d_qk == 128) return fa::paged_launch_d128(p, parts, c, split, grid, stream);
+  return fa::paged_launch_d192(p, parts, c, split, grid, stream);
 }
 
 }  // extern "C"

@@ -27,6 +27,7 @@
 #include <type_traits>
 
 #include "fa_paged.cuh"
+#include "fa_paged.h"
 #include "ptx.cuh"
 
 namespace fa {
@@ -46,15 +47,14 @@ struct PagedParams {
   const int* seqlens;
   const int* cu;
   unsigned int* status;
-  float* part_o;   // [2 * pieces][rows][DV]
-  float2* part_ml;  // [2 * pieces][rows] {reference, sum}
-  struct PagedJoin* joins;  // [pieces]
+  PagedParts part;
   int64_t total_q;
   int batch, heads_q, heads_kv, ratio, num_pages, max_pages, page_shift, causal;
   unsigned long long timeout_ns;  // of a wait (paged_tc_kernel)
   int copy_shift;  // 2^this copies of the rows in the 128 lanes (paged_tc_kernel), each with its share of the tokens
   int max_n;      // longest sequence of new tokens allowed
-  int row_limit;  // sequences with more rows (new tokens x ratio) are not this kernel's
+  int row_least, row_limit;  // sequences with fewer or more rows (new tokens x ratio) are not this kernel's
+  int after;                 // launched while the kernel before it may still run: ends after that (paged_tc_kernel)
   float scale_log2;
 };
 
@@ -189,7 +189,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
   s.bad = s.cu0 < 0 || c1 < s.cu0 || c1 > p.total_q || s.n > p.max_n || s.len < 0 ||
           s.len > (static_cast<int64_t>(p.max_pages) << p.page_shift);
   const int64_t rows = s.bad ? 0 : static_cast<int64_t>(s.n) * p.ratio;
-  s.rows = rows > p.row_limit ? 0 : static_cast<int>(rows);
+  s.rows = rows > p.row_limit || rows < p.row_least ? 0 : static_cast<int>(rows);
   s.tiles = s.len > 0 ? (s.len + TILE - 1) / TILE : 1;  // without a key: one tile that is masked
   return s;
 }
@@ -319,9 +319,9 @@ __device__ __forceinline__ void paged_line(const PagedParams& p, long long* scan
   }
   // pieces beyond the used ones are cleared in plain order
   if (tid < TEAMS) {
-    if (line.count(tid) > 0) p.joins[line.piece(tid)].last = -1;
+    if (line.count(tid) > 0) p.part.joins[line.piece(tid)].last = -1;
     const long long plain = static_cast<long long>(blockIdx.x) * TEAMS + tid;
-    if (plain >= line.used) p.joins[plain].last = -1;
+    if (plain >= line.used) p.part.joins[plain].last = -1;
   }
   __syncthreads();
 }
@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
         j.cu0 = cur.s.cu0;
         j.head = cur.head;
         j.rows = cur.s.rows;
-        p.joins[piece] = j;
+        p.part.joins[piece] = j;
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -795,11 +795,11 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
                 p.lse[hq * p.total_q + token] =
                     l == 0.f ? -INFINITY : (rf - kPShift + log2f(l)) * 0.6931471805599453f;
             } else {
-              float4* dst = reinterpret_cast<float4*>(p.part_o + (part * kRows + r) * DV + g * (DV / 8));
+              float4* dst = reinterpret_cast<float4*>(p.part.o + (part * kRows + r) * DV + g * (DV / 8));
 #pragma unroll
               for (int v = 0; v < kVTiles / 2; ++v)
                 dst[v] = make_float4(o[nt][2 * v][k], o[nt][2 * v][k + 2], o[nt][2 * v + 1][k], o[nt][2 * v + 1][k + 2]);
-              if (g == 0) p.part_ml[part * kRows + r] = make_float2(rf, l);
+              if (g == 0) p.part.ml[part * kRows + r] = make_float2(rf, l);
             }
           }
         }
@@ -813,20 +813,35 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
 //     O = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
 // One block for each piece and 8 rows, a warp a row; parts are taken in their
 // order, so the result does not depend on timing.
-template <int DV, int ROWS>
-__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedParams p) {
+struct PagedMerge {
+  struct Set {
+    PagedParts part;
+    int blocks, row_blocks, rows;  // blocks in all, of a piece; rows that the parts are laid out for
+  } set[2];
+  __nv_bfloat16* o;
+  float* lse;
+  int64_t total_q;
+  int heads_q, ratio;
+};
+
+template <int DV>
+__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedMerge p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int kPer = DV / 32;
-  const int piece = blockIdx.x;
-  const PagedJoin j = p.joins[piece];
+  const bool second = static_cast<int>(blockIdx.x) >= p.set[0].blocks;
+  const PagedParts part = second ? p.set[1].part : p.set[0].part;
+  const int rows = second ? p.set[1].rows : p.set[0].rows, row_blocks = second ? p.set[1].row_blocks : p.set[0].row_blocks;
+  const int block = blockIdx.x - (second ? p.set[0].blocks : 0);
+  const int piece = block / row_blocks;
+  const PagedJoin j = part.joins[piece];
   if (j.last < 0) return;
   const int lane = threadIdx.x & 31;
-  const int local = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int local = (block - piece * row_blocks) * 8 + (threadIdx.x >> 5);
   if (local >= j.rows) return;
   const int parts = j.last - piece + 1;
-  auto row = [&](int i) { return (2 * static_cast<int64_t>(piece + i) + (i == 0 ? 1 : 0)) * ROWS + local; };
+  auto row = [&](int i) { return (2 * static_cast<int64_t>(piece + i) + (i == 0 ? 1 : 0)) * rows + local; };
   float top = -INFINITY;
-  for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.part_ml[row(i)].x);
+  for (int i = lane; i < parts; i += 32) top = fmaxf(top, part.ml[row(i)].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const float base = top == -INFINITY ? 0.f : top;
@@ -837,7 +852,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
   for (int i0 = 0; i0 < parts; i0 += 32) {
     float w = 0.f;
     if (i0 + lane < parts) {
-      const float2 ml = p.part_ml[row(i0 + lane)];
+      const float2 ml = part.ml[row(i0 + lane)];
       w = ex2_approx(ml.x - base);
       l += w * ml.y;
     }
@@ -845,7 +860,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
 #pragma unroll 8
     for (int i = 0; i < n; ++i) {
       const float wi = __shfl_sync(0xffffffffu, w, i);
-      const float* src = p.part_o + row(i0 + i) * DV + lane * kPer;
+      const float* src = part.o + row(i0 + i) * DV + lane * kPer;
       if constexpr (kPer == 4) {
         const float4 x = *reinterpret_cast<const float4*>(src);
         acc[0] = fmaf(wi, x.x, acc[0]), acc[1] = fmaf(wi, x.y, acc[1]);

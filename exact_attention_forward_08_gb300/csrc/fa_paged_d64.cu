@@ -3,8 +3,9 @@
 
 namespace fa {
 
-int paged_launch_d64(const PagedParams& p, const fa_kv_cache& c, int d_v, int rows, int grid, cudaStream_t stream) {
-  if (d_v == 64) return paged_launch_pages<64, 64>(p, c, rows, grid, stream);
+int paged_launch_d64(const PagedParams& p, const PagedParts* parts, const fa_kv_cache& c, PagedSplit split, int grid,
+                     cudaStream_t stream) {
+  if (c.d_v == 64) return paged_launch_pages<64, 64>(p, parts, c, split, grid, stream);
   return FA_ERR_UNSUPPORTED;
 }
 

@@ -23,31 +23,30 @@ inline int paged_allow_smem(const void* kernel, int smem, bool (&ready)[64]) {
   return FA_OK;
 }
 
-// The merge's blocks may be placed while the attention kernel still runs; they wait for its end.
-template <int DV, int ROWS>
-int paged_merge_launch(const PagedParams& p, int rows, int pieces, cudaStream_t stream) {
+// `early`: the blocks may be placed while the kernel before this one on the stream still runs.
+template <typename P>
+int paged_start(void (*kernel)(P), const P& p, int grid, int threads, int smem, bool early, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(pieces, (rows + 7) / 8, 1);
-  cfg.blockDim = dim3(256, 1, 1);
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].val.programmaticStreamSerializationAllowed = early ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<DV, ROWS>, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 template <int DQK, int DV, int NT, bool G16>
-int paged_launch(const PagedParams& p, int grid, cudaStream_t stream) {
+int paged_few_launch(const PagedParams& p, int grid, cudaStream_t stream) {
   using Shape = PagedShape<DQK, DV, NT>;
   static bool ready[64] = {};
   auto* kernel = paged_attn_kernel<DQK, DV, NT, G16>;
   const int rc = paged_allow_smem(reinterpret_cast<const void*>(kernel), Shape::kBytes, ready);
   if (rc != FA_OK) return rc;
-  kernel<<<grid, Shape::kThreads, Shape::kBytes, stream>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  return paged_merge_launch<DV, Shape::kRows>(p, Shape::kRows, grid * Shape::kTeams, stream);
+  return paged_start(kernel, p, grid, Shape::kThreads, Shape::kBytes, false, stream);
 }
 
 // Codes viewed as (d, token, head, page); a box is a page of one head, `columns` wide.
@@ -62,7 +61,7 @@ inline int paged_encode(CUtensorMap* m, const void* base, const int64_t* s, cons
 }
 
 template <int DQK, int DV>
-int paged_tc_launch(const PagedParams& shared, const fa_kv_cache& c, int rows, int grid, cudaStream_t stream) {
+int paged_many_launch(const PagedParams& shared, const fa_kv_cache& c, int rows, int grid, cudaStream_t stream) {
   using Shape = TcShape<DQK, DV>;
   static bool ready[64] = {};
   auto* kernel = paged_tc_kernel<DQK, DV>;
@@ -74,23 +73,49 @@ int paged_tc_launch(const PagedParams& shared, const fa_kv_cache& c, int rows, i
   rc = paged_encode(&p.tm_k, c.k, c.k_stride, c, DQK, DQK == 128 ? 128 : 64);
   if (rc == FA_OK) rc = paged_encode(&p.tm_v, c.v, c.v_stride, c, DV, DV);
   if (rc != FA_OK) return rc;
-  kernel<<<grid, Shape::kThreads, Shape::kBytes, stream>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  return paged_merge_launch<DV, Shape::kRows>(p, rows, grid, stream);
+  return paged_start(kernel, p, grid, Shape::kThreads, Shape::kBytes, shared.after != 0, stream);
 }
 
-// rows: the most that a sequence has
-template <int DQK, int DV, bool G16>
-int paged_launch_rows(const PagedParams& p, const fa_kv_cache& c, int rows, int grid, cudaStream_t stream) {
-  if (rows <= 8) return paged_launch<DQK, DV, 1, G16>(p, grid, stream);
-  if (rows <= 16) return paged_launch<DQK, DV, 2, G16>(p, grid, stream);
-  return paged_tc_launch<DQK, DV>(p, c, rows, grid, stream);
-}
-
+// The kernel for few rows, the one for many, and the merge of what both cut: each may begin before the one in front
+// of it has ended, and ends after it.
 template <int DQK, int DV>
-int paged_launch_pages(const PagedParams& p, const fa_kv_cache& c, int rows, int grid, cudaStream_t stream) {
-  return p.page_shift == 4 ? paged_launch_rows<DQK, DV, true>(p, c, rows, grid, stream)
-                           : paged_launch_rows<DQK, DV, false>(p, c, rows, grid, stream);
+int paged_launch_pages(const PagedParams& shared, const PagedParts* parts, const fa_kv_cache& c, PagedSplit split,
+                       int grid, cudaStream_t stream) {
+  PagedMerge m = {};
+  PagedParams p = shared;
+  if (split.few > 0) {
+    p.part = parts[0];
+    p.row_least = 1;
+    p.row_limit = split.few;
+    int rc;
+    if (p.page_shift == 4)
+      rc = split.few <= 8 ? paged_few_launch<DQK, DV, 1, true>(p, grid, stream) : paged_few_launch<DQK, DV, 2, true>(p, grid, stream);
+    else
+      rc = split.few <= 8 ? paged_few_launch<DQK, DV, 1, false>(p, grid, stream) : paged_few_launch<DQK, DV, 2, false>(p, grid, stream);
+    if (rc != FA_OK) return rc;
+    m.set[0].part = parts[0];
+    m.set[0].rows = paged_few_rows(split.few);
+    m.set[0].row_blocks = m.set[0].rows / 8;
+    m.set[0].blocks = grid * PagedShape<DQK, DV, 1>::kTeams * m.set[0].row_blocks;
+  }
+  if (split.many > 0) {
+    p.part = parts[1];
+    p.row_least = split.few + 1;
+    p.row_limit = split.many;
+    p.after = split.few > 0;
+    const int rc = paged_many_launch<DQK, DV>(p, c, split.many, grid, stream);
+    if (rc != FA_OK) return rc;
+    m.set[1].part = parts[1];
+    m.set[1].rows = TcShape<DQK, DV>::kRows;
+    m.set[1].row_blocks = (split.many + 7) / 8;
+    m.set[1].blocks = grid * m.set[1].row_blocks;
+  }
+  m.o = p.o;
+  m.lse = p.lse;
+  m.total_q = p.total_q;
+  m.heads_q = p.heads_q;
+  m.ratio = p.ratio;
+  return paged_start(paged_merge_kernel<DV>, m, m.set[0].blocks + m.set[1].blocks, 256, 0, true, stream);
 }
 
 }  // namespace fa

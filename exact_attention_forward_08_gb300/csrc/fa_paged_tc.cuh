@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
             j.cu0 = cur.s.cu0;
             j.head = cur.head;
             j.rows = cur.s.rows;
-            p.joins[piece] = j;
+            p.part.joins[piece] = j;
           }
           ok = __all_sync(0xffffffffu, tc_wait(o_full(buf), (i >> 1) & 1, wc));
           if (!ok) break;
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
           const float scale = ex2_approx(rf - base) * (!whole ? unit : l == 0.f ? 0.f : unit / l);
           if (copy == 0 && r < cur.s.rows) {
             if (!whole) {
-              p.part_ml[part * L::kRows + r] = make_float2(top + kPShift, l);
+              p.part.ml[part * L::kRows + r] = make_float2(top + kPShift, l);
             } else if (p.lse != nullptr) {
               const int pos = r / p.ratio;
               p.lse[static_cast<int64_t>(cur.head * p.ratio + (r - pos * p.ratio)) * p.total_q + cur.s.cu0 + pos] =
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
                 *reinterpret_cast<uint2*>(p.o + (static_cast<int64_t>(cur.s.cu0 + pos) * p.heads_q + hq) * DV + c) =
                     make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
               } else {
-                *reinterpret_cast<float4*>(p.part_o + (part * L::kRows + row) * DV + c) = v;
+                *reinterpret_cast<float4*>(p.part.o + (part * L::kRows + row) * DV + c) = v;
               }
             }
             ok = meet();  // read before the next columns or queries come there
@@ -738,6 +738,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if (p.after) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace fa

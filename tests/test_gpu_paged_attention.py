@@ -123,6 +123,22 @@ def test_prompts_and_tokens_in_one_batch(fa, page):
     check(fa, [200, 77, 40, 500, 129, 0, 65], [1, 0, 32, 300, 33, 3, 65], 8, 2, (128, 128), page)
 
 
+@pytest.mark.parametrize("dims", [(64, 64), (128, 64), (192, 128)])
+@pytest.mark.parametrize("ratio", [1, 4, 8, 9])
+def test_few_and_many_rows_in_one_batch(fa, dims, ratio):
+    # up to 8 rows, and up to 128, next to each other, each kind with units that are cut
+    new = [1, 128 // ratio, 8 // ratio or 1, 0, 2, 17, 1, 30 // ratio]
+    check(fa, [5000, 3000, 77, 0, 4000, 17, 1, 900], new, 2 * ratio, 2, dims, 64, seed=ratio)
+
+
+@pytest.mark.parametrize("rows", [24, 56, 120])
+def test_cut_where_a_unit_starts(fa, rows):
+    """Lengths of one tile more and less, so that pieces begin and end at and near the ends of units."""
+    for batch in (3, 29, 37, 61):
+        lens = [(128 * (i % 5) + (-1, 0, 1)[i % 3]) or 1 for i in range(batch)]
+        check(fa, [max(n, 1) for n in lens], [1] * batch, 4 * rows, 4, (64, 64), 128, seed=batch)
+
+
 def test_prompt_without_keys(fa):
     check(fa, [0, 0], [100, 1], 4, 4, (64, 64), 16)
 
@@ -280,6 +296,63 @@ def test_side_stream_and_graph_replay(fa):
     o2, l2 = fa.attention_forward_paged(q, *dev, cu, 1, stream=side)
     side.synchronize()
     assert torch.equal(o2, out) and torch.equal(l2, lse)
+
+
+def test_replay_with_another_split_of_the_tokens(fa):
+    """A captured call of both kernels on pages, replayed with tokens that belong to other sequences, then with fewer."""
+    lens, new = [700, 300, 1500], [1, 20, 19]
+    cache = ref.Cache(lens, 2, 32, 128, 128, seed=7)
+    dev = cache.to_device("cuda")
+    q = queries(new, 8, 128).cuda()
+    cu = torch.tensor(offsets(new), dtype=torch.int32, device="cuda")
+    ws = torch.empty(fa.fa_fwd_paged_workspace_size(3, 8, 2, 40, 30, 0, 128, 128), dtype=torch.uint8, device="cuda")
+    out = torch.empty(40, 8, 128, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(8, 40, device="cuda")
+    call = lambda: fa.attention_forward_paged(q, *dev, cu, 30, out=out, lse=lse, workspace=ws)  # noqa: E731
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call()
+    for now in (new, [30, 2, 8], [0, 1, 30], [2, 2, 1]):
+        cu.copy_(torch.tensor(offsets(now), dtype=torch.int32))
+        out.fill_(-3.0)
+        lse.fill_(-3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert fa.fa_device_status()[0] == 0
+        used = sum(now)
+        want = ref.attention(q[:used], cache.k, cache.v, cache.k_scale, cache.v_scale, cache.table, lens, offsets(now),
+                             32, True)
+        ref.check_attention(out[:used], lse[:, :used], want, EPS_F16, f"replay {now}")
+        assert (out[used:] == -3.0).all() and (lse[:, used:] == -3.0).all()
+
+
+def test_two_calls_at_once(fa):
+    """Two streams, each with its own workspace, outputs and batch."""
+    batches = [([900, 40, 3000], [1, 1, 1]), ([500, 2500, 60], [6, 1, 20])]
+    streams, got, want = [torch.cuda.Stream(), torch.cuda.Stream()], [], []
+    for i, (lens, new) in enumerate(batches):
+        cache = ref.Cache(lens, 2, 64, 128, 128, seed=i)
+        q = queries(new, 8, 128, i)
+        want.append(ref.attention(q, cache.k, cache.v, cache.k_scale, cache.v_scale, cache.table, lens, offsets(new), 64,
+                                  True))
+        got.append((q.cuda(), cache.to_device("cuda"), torch.tensor(offsets(new), dtype=torch.int32, device="cuda"), max(new)))
+    torch.cuda.synchronize()
+    results = [[], []]
+    for _ in range(20):
+        for i, (q, dev, cu, most) in enumerate(got):
+            with torch.cuda.stream(streams[i]):
+                results[i].append(fa.attention_forward_paged(q, *dev, cu, most))
+    torch.cuda.synchronize()
+    assert fa.fa_device_status()[0] == 0
+    for i in range(2):
+        ref.check_attention(*results[i][0], want[i], EPS_F16, f"stream {i}")
+        for o, lse in results[i][1:]:
+            assert torch.equal(o, results[i][0][0]) and torch.equal(lse, results[i][0][1])
 
 
 @pytest.mark.parametrize("n", [1, 10, 80])
