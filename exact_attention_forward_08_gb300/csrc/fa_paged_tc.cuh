@@ -7,11 +7,12 @@
 // then holds its bf16 values), and the keys' scales, one for 16 tokens,
 // multiply the scores.  The values' scales are powers of two too: they go into
 // the exponents of the weights, P' = 2^(x - m + k - k0) with k the scale's
-// exponent and 2^k0 the unit that O is kept in, rounded to f16.  That holds for
-// scales between 2^(k0-3) and 2^(k0+6) (weights then lose bits only below
-// 2^-11 of the largest, vanish below 2^-21); a tile with others ("wide") takes its
-// V as code * 2^(k-k0) and its P in bf16, which has the exponents for them.
-// S, maxima, sums and O are fp32.
+// exponent and 2^k0 the unit that O is kept in, rounded to f16.  2^(k0 + 3) is
+// the largest scale of the first tile, so a weight under it keeps 11 bits down
+// to 2^-17 of the reference and vanishes below 2^-28.  That serves scales between
+// 2^(k0-3) and 2^(k0+6); a tile with others ("wide") takes its V as code * 2^(k-k0)
+// and its P in bf16, which has the exponents for them.  S, maxima, sums and O
+// are fp32.
 //
 // Work: the tiles of 128 tokens of all sequences and heads form one line that
 // is cut into equal pieces, one for each block; cut (sequence, head)s are
@@ -25,13 +26,21 @@
 //               takes a half or a quarter of every tile's tokens, with weights
 //               of 0 for the others, and the copies are added up at the end.
 //   warp 4      issues the MMAs, S of the next tile before P V of this one.
-//   warp 5      loads: block table, scales, and the codes by TMA ahead of their use.
+//   warp 5      loads: block table, scales, and the codes by TMA, two tiles ahead.
 //   warps 6-13  codes to operands, in the tensor cores' swizzled layout.
-// TMEM: S of even and odd tiles, O, P of even and odd tiles.  What bounds it:
-// per 128 tokens and head 32 KB of codes come in (about 1400 cycles at this
-// GPU's bandwidth), the two products take about 1000 cycles, the shared memory
-// carries 230 KB (1800 cycles), and the conversion issues about 400
-// instructions a scheduler.
+// TMEM: S of even and odd tiles, O, P of even and odd tiles.
+//
+// What bounds it: per 128 tokens and head of 128, 32 KB of codes come in (1300
+// cycles at the measured copy rate) and 16 MMAs take 75 cycles each; a tile
+// takes about 2600, a chain of load, conversion (700 each of K and V), S (800),
+// softmax (1000) and P V (900) with two tiles in flight, whose warps still wait
+// for instructions (six roles share the instruction caches) and for TMEM.  Short
+// loops were worth more than anything else: the same work unrolled took 90.8 us
+// where it takes 70.6.  Starting and ending a (sequence, head) takes 12000
+// cycles; counting them as kStart tiles when the line is cut was worth 17 %.
+// 16 sequences of 5 new tokens, 32/8 heads of 128, 500 to 8000 keys: 58 us, 2.5
+// TB/s of codes; 32 of 32/1 heads: 30 us, of which half is the start and the end;
+// 32 x 8000 keys of 2 heads with 64 rows: 57 us, 2.3 TB/s.
 #pragma once
 #include "fa_paged_attn.cuh"
 

@@ -422,7 +422,8 @@ size_t fa_noalloc_scratch_bytes(void);
  *               new tokens the new ones among them
  *
  * k_stride and v_stride hold the bytes between pages, heads and tokens
- * (multiples of 16; a token's codes are contiguous), so other orders of the
+ * (multiples of 16, at least d; below 2^24 between tokens, below 2^40 between
+ * the others; a token's codes are contiguous), so other orders of the
  * first three dimensions, and a cache that is part of a larger allocation,
  * are fine.  k and v are 16-byte aligned device memory.  page_size is 16, 32,
  * 64 or 128, (d_qk, d_v) one of fa_fwd's pairs.  An e8m0 byte e stands for
@@ -510,7 +511,9 @@ int fa_kv_append(const fa_kv_cache* cache, const void* q, const void* k, const v
  * workspace: device memory of fa_fwd_paged_workspace_size(...) bytes, 16-byte
  * aligned; it needs no initialisation, and calls that may overlap (captured
  * graphs that run at the same time among them) need different ones.
- * Deterministic: no atomics on results.
+ * Deterministic: no atomics on results.  The weights of the softmax are
+ * rounded to 16 bits for the second product (f16, or bf16 where the values'
+ * scales of a sequence are far apart); scores, maxima, sums and O are fp32.
  */
 size_t fa_fwd_paged_workspace_size(int batch, int heads_q, int heads_kv, int64_t total_q, int max_seqlen_q,
                                    int64_t total_k, int d_qk, int d_v);
@@ -543,7 +546,10 @@ int fa_device_status(fa_stream_t stream, int* out);
  * site, block or sequence index}, the site being the wait or check that
  * failed: 101-404 a forward wait (role * 100 + barrier: 1 softmax,
  * 2 correction, 3 MMA, 4 TMA), 501 bad cu_seqlens, 502 a varlen batch with
- * more tasks than the workspace holds, 601-623 a backward wait,
+ * more tasks than the workspace holds, 511 a bad sequence of a call on a paged
+ * cache, 512 a page outside the cache (the index is the sequence's in both),
+ * 513 more keys than total_k, 520 a wait of the paged attention kernel, 601-623
+ * a backward wait,
  * 701-707 a range check and 710 + i a hand-off count of the checking build.
  */
 int fa_device_status_detail(fa_stream_t stream, int* out, unsigned int detail[3]);
