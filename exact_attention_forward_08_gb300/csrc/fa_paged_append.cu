@@ -15,6 +15,14 @@
 // the caches, to round and store them (a warp with one block keeps it).  More
 // warps a unit where there are few units.  Nothing waits on anything but the
 // team's one maximum, so loads of many units are under way at a time.
+//
+// Bound by the latency of loads: 80 registers let 24 warps on an SM.  8191 tokens
+// of 32/8 heads of 128: 39 us, 4.8 TB/s of what has to move (28 us at the copy
+// rate); 24 prompts of 1 to 900 tokens, 16/16 heads of 192/128: 56 us (38.5);
+// one token of one or of 128 sequences: 3 and 5 us.  Queries take three heads a
+// lane at once and ask for the first before their token's sequence is known: 42.0
+// and 57.9 us with two, afterwards.  Registers for 16 warps: 45.6 and 64.5, for 32:
+// 40.5 and 58.4.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -52,7 +60,7 @@ struct AppendParams {
 
 constexpr int kBlockRows = 8;  // rows a warp holds at a time
 constexpr int kWarps = 8;      // of a block
-constexpr int kTeamWarps = 32;  // warps an SM that units are spread over
+constexpr int kTeamWarps = 64;  // warps an SM that units are spread over (8191 tokens: 38.8 us, with 32 39.5)
 
 // The sequence's range of new positions [start, start + n) if it can be
 // appended: offsets ordered and inside the batch, positions inside the block
@@ -349,34 +357,39 @@ __device__ __forceinline__ void append_unit(const AppendParams& p, int kv, int h
 // cosines and sines for all heads that it turns.
 template <int D>
 __device__ __forceinline__ void append_query(const AppendParams& p, int64_t unit, int parts) {
-  constexpr int kRowItems = D / 16, kRows = 32 / kRowItems, kBatch = 2;  // heads a warp, and heads a lane, at once
+  constexpr int kRowItems = D / 16, kRows = 32 / kRowItems, kBatch = 3;  // heads a warp, and heads a lane, at once
   const int lane = threadIdx.x & 31;
   const int64_t t = unit / parts;
   if (t >= p.total) return;
   const int part = static_cast<int>(unit - t * parts);
-  const int b = warp_search(p.batch, t, [&](int i) { return static_cast<int64_t>(p.cu[i]); });
-  int c0, start, n;
-  if (!append_range(p, b, c0, start, n) || t < c0 || t >= c0 + n) return;
-  if (lane >= kRows * kRowItems) return;  // 12 columns: 24 lanes
+  const bool has_item = lane < kRows * kRowItems;  // 12 columns: 24 lanes
   const int i = lane % kRowItems;
   int ca, cb;
   item_columns<D>(i, p.rot, ca, cb);
-  float cs[16];
-  const bool turned = i * 16 < p.rot;
-  if (turned) load_cos_sin(cs, p.cos_sin + (start + (t - c0)) * p.rot, i, p.rot, p.interleaved);
   const __nv_bfloat16* src = p.q + t * p.q_stride;
   __nv_bfloat16* dst = p.q_out + t * (static_cast<int64_t>(p.heads_q) * D);
   const int end = p.heads_q < (part + 1) * p.q_heads ? p.heads_q : (part + 1) * p.q_heads;
-  for (int h0 = part * p.q_heads + lane / kRowItems; h0 < end; h0 += kBatch * kRows) {
-    uint4 raw[kBatch][2];
+  uint4 raw[kBatch][2];
+  auto load = [&](int h0) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int h = h0 + k * kRows;
-      if (h < end) {
+      if (h < end && has_item) {
         raw[k][0] = *reinterpret_cast<const uint4*>(src + h * D + ca);
         raw[k][1] = *reinterpret_cast<const uint4*>(src + h * D + cb);
       }
     }
+  };
+  const int h_first = part * p.q_heads + lane / kRowItems;
+  load(h_first);  // on the way while the token's sequence is looked up
+  const int b = warp_search(p.batch, t, [&](int i) { return static_cast<int64_t>(p.cu[i]); });
+  int c0, start, n;
+  if (!append_range(p, b, c0, start, n) || t < c0 || t >= c0 + n || !has_item) return;
+  float cs[16];
+  const bool turned = i * 16 < p.rot;
+  if (turned) load_cos_sin(cs, p.cos_sin + (start + (t - c0)) * p.rot, i, p.rot, p.interleaved);
+  for (int h0 = h_first; h0 < end; h0 += kBatch * kRows) {
+    if (h0 != h_first) load(h0);
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int h = h0 + k * kRows;

@@ -2,8 +2,9 @@
 // unpacked to bf16 rows, which the variable-length forward then reads.  A code
 // times a power of two is a bf16 number, so nothing is rounded here.  With n
 // new tokens the attention reads each key n x ratio times; unpacking moves it
-// once, 1 byte in and 2 out, which from a few hundred rows on is small beside
-// the products.
+// once, 1 byte in and 2 out: bound by bandwidth, 23 us for 16384 tokens of 8
+// heads of 128 and 128 (101 MB, 4.4 TB/s) where the forward of 2 x 2048 new tokens
+// takes 381.
 #include <cuda_runtime.h>
 
 #include "fa.h"
