@@ -816,12 +816,17 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
 // Joins the parts of the cut units: with references m_i and sums l_i of the
 // parts and M = max m_i,
 //     O = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
-// One block for each piece and 8 rows, a warp a row; parts are taken in their
-// order, so the result does not depend on timing.
+// A block takes the rows of a few pieces' units, a warp a row; parts are taken in
+// their order, so the result does not depend on timing.  Bound by latency (4 us
+// beside the launch): loads of a row's first FIRST parts do not wait for its
+// weights, and there are few blocks, for most pieces leave nothing to join.  Eight
+// parts where only few rows are joined, four (80 registers, not 127) where blocks
+// are many: single tokens over 1026 keys 10.7 and 11.7 us, 128 rows of 32 x 8000 keys
+// 50.5 and 48.1.
 struct PagedMerge {
   struct Set {
     PagedParts part;
-    int blocks, row_blocks, rows;  // blocks in all, of a piece; rows that the parts are laid out for
+    int blocks, pieces, shares, rows;  // blocks; pieces of a block, blocks that share them; rows of the parts' layout
   } set[2];
   __nv_bfloat16* o;
   float* lse;
@@ -829,52 +834,51 @@ struct PagedMerge {
   int heads_q, ratio;
 };
 
-template <int DV>
-__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedMerge p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+template <int DV, int FIRST>
+__device__ __forceinline__ void paged_merge_row(const PagedMerge& p, const PagedParts& part, int rows, int piece,
+                                                const PagedJoin& j, int local) {
   constexpr int kPer = DV / 32;
-  const bool second = static_cast<int>(blockIdx.x) >= p.set[0].blocks;
-  const PagedParts part = second ? p.set[1].part : p.set[0].part;
-  const int rows = second ? p.set[1].rows : p.set[0].rows, row_blocks = second ? p.set[1].row_blocks : p.set[0].row_blocks;
-  const int block = blockIdx.x - (second ? p.set[0].blocks : 0);
-  const int piece = block / row_blocks;
-  const PagedJoin j = part.joins[piece];
-  if (j.last < 0) return;
+  using Vec = std::conditional_t<kPer == 4, float4, float2>;
   const int lane = threadIdx.x & 31;
-  const int local = (block - piece * row_blocks) * 8 + (threadIdx.x >> 5);
-  if (local >= j.rows) return;
   const int parts = j.last - piece + 1;
   auto row = [&](int i) { return (2 * static_cast<int64_t>(piece + i) + (i == 0 ? 1 : 0)) * rows + local; };
-  float top = -INFINITY;
-  for (int i = lane; i < parts; i += 32) top = fmaxf(top, part.ml[row(i)].x);
+  auto values = [&](int i) { return *reinterpret_cast<const Vec*>(part.o + row(i) * DV + lane * kPer); };
+  float2 ml = make_float2(-INFINITY, 0.f);
+  if (lane < parts) ml = part.ml[row(lane)];
+  Vec first[FIRST];
+#pragma unroll
+  for (int i = 0; i < FIRST; ++i)
+    if (i < parts) first[i] = values(i);
+  float top = ml.x;
+  for (int i = lane + 32; i < parts; i += 32) top = fmaxf(top, part.ml[row(i)].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const float base = top == -INFINITY ? 0.f : top;
   float acc[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+  auto add = [&](float w, const Vec& x) {
+    acc[0] = fmaf(w, x.x, acc[0]), acc[1] = fmaf(w, x.y, acc[1]);
+    if constexpr (kPer == 4) acc[2] = fmaf(w, x.z, acc[2]), acc[3] = fmaf(w, x.w, acc[3]);
+  };
   float l = 0.f;
   for (int i0 = 0; i0 < parts; i0 += 32) {
     float w = 0.f;
     if (i0 + lane < parts) {
-      const float2 ml = part.ml[row(i0 + lane)];
+      if (i0 > 0) ml = part.ml[row(i0 + lane)];
       w = ex2_approx(ml.x - base);
       l += w * ml.y;
     }
     const int n = parts - i0 < 32 ? parts - i0 : 32;
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      const float* src = part.o + row(i0 + i) * DV + lane * kPer;
-      if constexpr (kPer == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src);
-        acc[0] = fmaf(wi, x.x, acc[0]), acc[1] = fmaf(wi, x.y, acc[1]);
-        acc[2] = fmaf(wi, x.z, acc[2]), acc[3] = fmaf(wi, x.w, acc[3]);
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(src);
-        acc[0] = fmaf(wi, x.x, acc[0]), acc[1] = fmaf(wi, x.y, acc[1]);
+    if (i0 == 0) {
+#pragma unroll
+      for (int i = 0; i < FIRST; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        if (i < parts) add(wi, first[i]);
       }
     }
+#pragma unroll 8
+    for (int i = i0 == 0 ? FIRST : 0; i < n; ++i) add(__shfl_sync(0xffffffffu, w, i), values(i0 + i));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -886,6 +890,36 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
   for (int k = 0; k < kPer / 2; ++k) dst[k] = pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
   if (lane == 0 && p.lse != nullptr)
     p.lse[hq * p.total_q + token] = l == 0.f ? -INFINITY : (base - kPShift + log2f(l)) * 0.6931471805599453f;
+}
+
+template <int DV, int FIRST>
+__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedMerge p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const bool second = static_cast<int>(blockIdx.x) >= p.set[0].blocks;
+  const PagedMerge::Set& set = p.set[second ? 1 : 0];
+  const int block = blockIdx.x - (second ? p.set[0].blocks : 0);
+  const int piece0 = block / set.shares * set.pieces, share = block % set.shares;
+  const int lane = threadIdx.x & 31;
+  PagedJoin mine = {-1, 0, 0, 0};  // lane l: of the piece piece0 + l
+  if (lane < set.pieces) mine = set.part.joins[piece0 + lane];
+  const int rows = mine.last < 0 ? 0 : mine.rows;
+  int upto = rows;  // rows of the lanes up to this one
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  const int total = __shfl_sync(0xffffffffu, upto, 31);
+  for (int item = 8 * share + (threadIdx.x >> 5); item < total; item += 8 * set.shares) {
+    const int from = __popc(__ballot_sync(0xffffffffu, upto <= item));
+    PagedJoin j;
+    j.last = __shfl_sync(0xffffffffu, mine.last, from);
+    j.cu0 = __shfl_sync(0xffffffffu, mine.cu0, from);
+    j.head = __shfl_sync(0xffffffffu, mine.head, from);
+    j.rows = __shfl_sync(0xffffffffu, rows, from);
+    const int local = item - (__shfl_sync(0xffffffffu, upto, from) - j.rows);
+    paged_merge_row<DV, FIRST>(p, set.part, set.rows, piece0 + from, j, local);
+  }
 }
 
 }  // namespace fa

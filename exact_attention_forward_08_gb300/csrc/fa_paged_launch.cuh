@@ -89,14 +89,17 @@ int paged_launch_pages(const PagedParams& shared, const PagedParts* parts, const
     p.row_limit = split.few;
     int rc;
     if (p.page_shift == 4)
-      rc = split.few <= 8 ? paged_few_launch<DQK, DV, 1, true>(p, grid, stream) : paged_few_launch<DQK, DV, 2, true>(p, grid, stream);
+      rc = split.few <= 8 ? paged_few_launch<DQK, DV, 1, true>(p, grid, stream)
+                          : paged_few_launch<DQK, DV, 2, true>(p, grid, stream);
     else
-      rc = split.few <= 8 ? paged_few_launch<DQK, DV, 1, false>(p, grid, stream) : paged_few_launch<DQK, DV, 2, false>(p, grid, stream);
+      rc = split.few <= 8 ? paged_few_launch<DQK, DV, 1, false>(p, grid, stream)
+                          : paged_few_launch<DQK, DV, 2, false>(p, grid, stream);
     if (rc != FA_OK) return rc;
     m.set[0].part = parts[0];
     m.set[0].rows = paged_few_rows(split.few);
-    m.set[0].row_blocks = m.set[0].rows / 8;
-    m.set[0].blocks = grid * PagedShape<DQK, DV, 1>::kTeams * m.set[0].row_blocks;
+    m.set[0].pieces = PagedShape<DQK, DV, 1>::kTeams;
+    m.set[0].shares = m.set[0].rows / 4;
+    m.set[0].blocks = grid * m.set[0].shares;
   }
   if (split.many > 0) {
     p.part = parts[1];
@@ -107,15 +110,18 @@ int paged_launch_pages(const PagedParams& shared, const PagedParts* parts, const
     if (rc != FA_OK) return rc;
     m.set[1].part = parts[1];
     m.set[1].rows = TcShape<DQK, DV>::kRows;
-    m.set[1].row_blocks = (split.many + 7) / 8;
-    m.set[1].blocks = grid * m.set[1].row_blocks;
+    m.set[1].pieces = 1;
+    m.set[1].shares = (split.many + 7) / 8;
+    m.set[1].blocks = grid * m.set[1].shares;
   }
   m.o = p.o;
   m.lse = p.lse;
   m.total_q = p.total_q;
   m.heads_q = p.heads_q;
   m.ratio = p.ratio;
-  return paged_start(paged_merge_kernel<DV>, m, m.set[0].blocks + m.set[1].blocks, 256, 0, true, stream);
+  const int blocks = m.set[0].blocks + m.set[1].blocks;
+  if (split.many > 0) return paged_start(paged_merge_kernel<DV, 4>, m, blocks, 256, 0, true, stream);
+  return paged_start(paged_merge_kernel<DV, 8>, m, blocks, 256, 0, true, stream);
 }
 
 }  // namespace fa
