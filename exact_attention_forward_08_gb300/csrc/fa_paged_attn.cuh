@@ -21,8 +21,8 @@
 // is written out at once, one that is cut leaves unnormalised parts that
 // paged_merge_kernel joins.
 //
-// Bound by DRAM: B8 x 32767 keys, 32/8 heads of 128: 95 us with the merge, 5.7
-// TB/s of codes (the copies alone: 84 us); 16 heads of 192/128: 61 us, 5.4 TB/s;
+// Bound by DRAM: B8 x 32767 keys, 32/8 heads of 128: 93 us with the merge, 5.8
+// TB/s of codes (the copies alone: 84 us); 16 heads of 192/128: 59 us, 5.6 TB/s;
 // 16 heads of 64 in pages of 16, copies of 1 KB: 123 us, 4.4 TB/s (copies alone
 // 102).
 #pragma once
