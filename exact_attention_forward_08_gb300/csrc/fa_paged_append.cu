@@ -32,6 +32,7 @@
 #include "fa.h"
 #include "fa_host.h"
 #include "fa_paged.cuh"
+#include "fa_paged_range.h"
 #include "ptx.cuh"
 
 namespace fa {
@@ -67,11 +68,9 @@ constexpr int kTeamWarps = 64;  // warps an SM that units are spread over (8191 
 // table and the rotation table.
 __device__ __forceinline__ bool append_range(const AppendParams& p, int b, int& c0, int& start, int& n) {
   c0 = p.cu[b];
-  const int c1 = p.cu[b + 1], len = p.seqlens[b];
-  n = c1 - c0;
-  start = len - n;
-  return c0 >= 0 && c1 >= c0 && c1 <= p.total && start >= 0 &&
-         len <= (static_cast<int64_t>(p.max_pages) << p.page_shift) && (p.rot == 0 || len <= p.max_pos);
+  int64_t most = static_cast<int64_t>(p.max_pages) << p.page_shift;
+  if (p.rot > 0 && p.max_pos < most) most = p.max_pos;
+  return paged_append_range(c0, p.cu[b + 1], p.seqlens[b], p.total, most, start, n);
 }
 
 // Item i of a row holds 16 values: two groups of 8, at columns c0 and c1.  The

@@ -33,6 +33,7 @@
 
 #include "fa_paged.cuh"
 #include "fa_paged.h"
+#include "fa_paged_range.h"
 #include "ptx.cuh"
 
 namespace fa {
@@ -188,14 +189,12 @@ template <int TILE>
 __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
   PagedSeq s;
   s.cu0 = p.cu[b];
-  const int c1 = p.cu[b + 1];
   s.len = p.seqlens[b];
-  s.n = c1 - s.cu0;
-  s.bad = s.cu0 < 0 || c1 < s.cu0 || c1 > p.total_q || s.n > p.max_n || s.len < 0 ||
-          s.len > (static_cast<int64_t>(p.max_pages) << p.page_shift);
+  s.bad = !paged_attend_range(s.cu0, p.cu[b + 1], s.len, p.total_q, p.max_n,
+                              static_cast<int64_t>(p.max_pages) << p.page_shift, s.n);
   const int64_t rows = s.bad ? 0 : static_cast<int64_t>(s.n) * p.ratio;
   s.rows = rows > p.row_limit || rows < p.row_least ? 0 : static_cast<int>(rows);
-  s.tiles = s.len > 0 ? (s.len + TILE - 1) / TILE : 1;  // without a key: one tile that is masked
+  s.tiles = s.len > 0 ? (s.len - 1) / TILE + 1 : 1;  // without a key: one tile that is masked
   return s;
 }
 

@@ -10,6 +10,7 @@
 #include "fa.h"
 #include "fa_paged.cuh"
 #include "fa_paged.h"
+#include "fa_paged_range.h"
 
 namespace fa {
 namespace {
@@ -29,9 +30,10 @@ __global__ void __launch_bounds__(kPlanThreads) unpack_plan_kernel(const UnpackP
     const int b = base + tid;
     long long v = 0;
     if (b < p.batch) {
-      const int c0 = p.cu_q[b], c1 = p.cu_q[b + 1], len = p.seqlens[b], n = c1 - c0;
-      if (c0 < 0 || c1 < c0 || c1 > p.total_q || n > p.max_n || len < 0 ||
-          len > (static_cast<long long>(p.max_pages) << p.page_shift)) {
+      const int len = p.seqlens[b];
+      int n;
+      if (!paged_attend_range(p.cu_q[b], p.cu_q[b + 1], len, p.total_q, p.max_n,
+                              static_cast<int64_t>(p.max_pages) << p.page_shift, n)) {
         paged_error(p.status, kSitePagedSeq, b);
         bad = 1;
       } else if (static_cast<long long>(n) * p.ratio > p.row_limit) {

@@ -1,0 +1,54 @@
+"""Edges of the paged 8-bit cache that need no GPU: the range checks of the kernels, compiled for the host, and the
+checks and defaults of the Python binding."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "exact_attention_forward_08_gb300", "csrc")
+
+RANGE_PROGRAM = r"""
+#include <cstdio>
+#include "fa_paged_range.h"
+int main() {
+  int kind, c0, c1, len, max_new;
+  long long total, most;
+  while (std::scanf("%d %d %d %d %lld %d %lld", &kind, &c0, &c1, &len, &total, &max_new, &most) == 7) {
+    int start = 0, n = 0;
+    const bool ok = kind == 0 ? fa::paged_append_range(c0, c1, len, total, most, start, n)
+                              : fa::paged_attend_range(c0, c1, len, total, max_new, most, n);
+    std::printf("%d %d %d\n", ok ? 1 : 0, start, n);
+  }
+}
+"""
+
+
+def test_range_checks_hold_for_any_offsets_and_lengths(tmp_path):
+    """Offsets and lengths are device memory and may hold anything: the checks agree with unbounded integers and no step of
+    them overflows (a signed overflow stops the program)."""
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no host compiler")
+    source, program = tmp_path / "range.cpp", tmp_path / "range"
+    source.write_text(RANGE_PROGRAM)
+    subprocess.run([gxx, "-std=c++17", "-O1", "-fsanitize=signed-integer-overflow", "-fsanitize-undefined-trap-on-error", "-I",
+                    CSRC, str(source), "-o", str(program)], check=True)
+    low, high = -2 ** 31, 2 ** 31 - 1
+    offsets = [low, low + 1, -7, -1, 0, 1, 20, 24, 25, high - 1, high]
+    lengths = [low, low + 1, low + 20, -21, -20, -1, 0, 1, 19, 20, 21, 44, 45, 46, 1 << 30, high - 20, high]
+    cases = [(kind, c0, c1, length, total, max_new, most) for kind in (0, 1) for c0 in offsets for c1 in offsets
+             for length in lengths for total in (24, high) for max_new in (1, 24) for most in (45, 1 << 30)]
+    run = subprocess.run([str(program)], input="\n".join(" ".join(map(str, c)) for c in cases), text=True, capture_output=True)
+    assert run.returncode == 0, "an overflow"
+    got = [tuple(map(int, line.split())) for line in run.stdout.splitlines()]
+    assert len(got) == len(cases)
+    for (kind, c0, c1, length, total, max_new, most), (ok, start, n) in zip(cases, got):
+        new, rows = c1 - c0, 0 <= c0 <= c1 <= total
+        if kind == 0:
+            want = rows and new <= length <= most
+        else:
+            want = rows and new <= max_new and 0 <= length <= most
+        assert ok == want, (kind, c0, c1, length, total, max_new, most)
+        if ok:
+            assert n == new and (kind == 1 or start == length - new)
