@@ -55,6 +55,21 @@ __device__ __forceinline__ float scale_of(int e) {
   return __uint_as_float(e == 0 ? 0x00400000u : e == 255 ? 0x7fc00000u : static_cast<uint32_t>(e) << 23);
 }
 
+// A query row whose largest biased bf16 exponent is `top`, as f16: values times
+// 2^x, x = 14 - (exponent), which puts the largest into [2^14, 2^15).  Its bf16
+// values are then exact down to 2^-31 of 2^exponent (2^-17, 8 bits above f16's
+// smallest step of 2^-24); below that they are off by at most 2^-39 of it.  Rows
+// whose largest is below 2^-94 are all multiplied by 2^109, which makes the
+// smallest bf16 number f16's smallest.  Infinities stay what they are (255: the
+// finite values beside them must not become infinite).
+struct QueryScale {
+  float down, up;  // the factor, and its inverse
+};
+__device__ __forceinline__ QueryScale query_scale(int top) {
+  const int e = top < 32 ? 32 : top > 254 ? 254 : top;
+  return {scale_of(268 - e), scale_of(e - 14)};
+}
+
 __device__ __forceinline__ float2 f16x2_float2(uint32_t v) {
   float2 r;
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"

@@ -8,9 +8,13 @@
 // S) or value columns (for O) the large one (m16):
 //     S^T[16 tokens x 8 rows] += K[16 x 16] Q^T[16 x 8]
 //     O^T[16 columns x 8 rows] += V^T[16 x 16 tokens] P^T[16 x 8]
-// Codes become f16 exactly; a query row is divided by a power of two first so
-// that f16 holds its bf16 values (below 2^-24 of the row's largest they round);
-// P is rounded to f16 scaled by 2^7, 11 bits where bf16 would keep 8.
+// Codes become f16 exactly.  A query row is multiplied by a power of two that
+// puts its largest value at the top of f16's range, so that its bf16 values are
+// exact down to 2^-31 of the largest and off by at most 2^-39 of it below (what
+// counts against keys that are 0 where the query is large; with the largest at 1
+// rounding began at 2^-18).  P is rounded to f16 scaled by 2^7: 11 bits where
+// bf16 would keep 8, for weights down to 2^-21 of the row's reference; below that
+// a weight is off by at most 2^-32, whatever the scales of its values.
 // Scores, maxima, sums and O stay in fp32.
 //
 // Work: a tile is 32 or 64 tokens of one key/value head; the tiles of all
@@ -509,7 +513,7 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
 #pragma unroll
           for (int s = 0; s < kSteps * 2; ++s) raw[s] = make_uint4(0, 0, 0, 0);
         }
-        // the row's largest exponent: its values divided by that power of two fit f16
+        // the row's largest exponent: its values times a power of two fit f16
         uint32_t top = 0;
 #pragma unroll
         for (int s = 0; s < kSteps * 2; ++s) {
@@ -525,9 +529,8 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
         top = top > y ? top : y;
         y = __shfl_xor_sync(0xffffffffu, top, 2);
         top = top > y ? top : y;
-        int ex = static_cast<int>(top >> 7);  // biased
-        ex = ex == 0 || ex == 255 ? 127 : ex;  // a row of zeros, or one that holds no numbers
-        const float down = scale_of(254 - ex);
+        const QueryScale qs = query_scale(static_cast<int>(top >> 7));
+        const float down = qs.down;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
           uint32_t f[8];
@@ -546,8 +549,7 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {  // this lane's columns of S^T are rows 2 c and 2 c + 1
-          const int e = __shfl_sync(0xffffffffu, ex, (2 * c + k) * 4);
-          qfac[nt][k] = p.scale_log2 * scale_of(e);
+          qfac[nt][k] = p.scale_log2 * __shfl_sync(0xffffffffu, qs.up, (2 * c + k) * 4);
           ref[nt][k] = -INFINITY;
           sum[nt][k] = 0.f;
           const int rr = nt * 8 + 2 * c + k;

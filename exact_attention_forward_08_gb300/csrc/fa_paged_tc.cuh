@@ -3,9 +3,9 @@
 // tiles, which cost the same for any number of rows and read each key once.
 //
 //     S[128 rows x 128 tokens] = Q K^T,   O[128 rows x DV] += P V
-// Codes become f16 exactly; a query row is divided by a power of two first (f16
-// then holds its bf16 values), and the keys' scales, one for 16 tokens,
-// multiply the scores.  The values' scales are powers of two too: they go into
+// Codes become f16 exactly; a query row is multiplied by a power of two first
+// (query_scale: exact down to 2^-31 of its largest value), and the keys' scales,
+// one for 16 tokens, multiply the scores.  The values' scales are powers of two too: they go into
 // the exponents of the weights, P' = 2^(x - m + k - k0) with k the scale's
 // exponent and 2^k0 the unit that O is kept in, rounded to f16.  2^(k0 + 3) is
 // the largest scale of the first tile, so a weight under it keeps 11 bits down
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
         const bool active = warp * 32 - copy * copy_rows < cur.s.rows;  // some row of this warp is one of the sequence's
         if (first) {
           started_here = cur.tile == 0;
-          // this thread's query row as f16, divided by the power of two of its largest value, by way of its place;
+          // this thread's query row as f16, its largest value at the top of the range, by way of its place;
           // eight lanes fetch 128 bytes of a row
           const int pos = r / p.ratio;
           const uint32_t at = smem0 + tid * 128;
@@ -227,10 +227,10 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
               top = __vmaxu2(__vmaxu2(top, x.z & 0x7f807f80u), x.w & 0x7f807f80u);
             }
           }
-          int ex = static_cast<int>(((top & 0xffffu) > (top >> 16) ? top & 0xffffu : top >> 16) >> 7);
-          ex = ex == 0 || ex == 255 ? 127 : ex;  // a row of zeros, or one that holds no numbers
-          const float down = scale_of(254 - ex);
-          fac = p.scale_log2 * scale_of(ex);
+          const QueryScale qs =
+              query_scale(static_cast<int>(((top & 0xffffu) > (top >> 16) ? top & 0xffffu : top >> 16) >> 7));
+          const float down = qs.down;
+          fac = p.scale_log2 * qs.up;
 #pragma unroll 4
           for (int c = 0; c < DQK / 8; ++c) {
             const uint4 x = r < cur.s.rows ? lds128(column(c)) : make_uint4(0, 0, 0, 0);

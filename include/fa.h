@@ -511,9 +511,19 @@ int fa_kv_append(const fa_kv_cache* cache, const void* q, const void* k, const v
  * workspace: device memory of fa_fwd_paged_workspace_size(...) bytes, 16-byte
  * aligned; it needs no initialisation, and calls that may overlap (captured
  * graphs that run at the same time among them) need different ones.
- * Deterministic: no atomics on results.  The weights of the softmax are
- * rounded to 16 bits for the second product (f16, or bf16 where the values'
- * scales of a sequence are far apart); scores, maxima, sums and O are fp32.
+ * Deterministic: no atomics on results.  Scores, maxima, sums and O are fp32;
+ * rounded to 16 bits on the way are
+ *   the queries of up to 128 rows, to f16 after a power of two for each row:
+ *     exact for values down to 2^-31 of the row's largest power of two, off by
+ *     at most 2^-39 of it below.  Longer sequences keep their bf16 queries.
+ *   the weights of the softmax for the second product, relative to the row's
+ *     largest.  Up to 16 rows (up to 8 or none in calls that allow more) f16:
+ *     off by half a step, 2^-11, or by 2^-32 of the largest if that is more,
+ *     whatever the values' scales.  Up to 128 rows f16 too, where the second
+ *     figure is 2^-28 S / s, s the scale of the weight's values and S the
+ *     largest scale among the first 128 tokens that a block takes of the
+ *     sequence (2^-17 or 2^33 where it lies beyond these); 128 tokens with an s
+ *     below S / 64 or above 8 S take bf16 instead (2^-8).  Above 128 rows bf16.
  */
 size_t fa_fwd_paged_workspace_size(int batch, int heads_q, int heads_kv, int64_t total_q, int max_seqlen_q,
                                    int64_t total_k, int d_qk, int d_v);

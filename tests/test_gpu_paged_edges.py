@@ -50,3 +50,47 @@ def test_append_leaves_out_lengths_far_below_zero(fa, length):
     mine = cache.table[1, :2].tolist()
     for now, was in zip(dev[:4], before):
         assert torch.equal(now.view(torch.uint8)[mine], was[mine])
+
+
+EPS_F16, EPS_BF16 = 2.0 ** -11, 2.0 ** -8  # what a weight of the softmax may lose: the kernels on pages, the unpacked keys
+
+
+def attend(fa, cache, new, q, causal=True, **kw):
+    o, lse = fa.attention_forward_paged(q.cuda(), *cache.to_device("cuda"), cuda_offsets(new), max(new), causal=causal, **kw)
+    torch.cuda.synchronize()
+    code, detail = fa.fa_device_status()
+    assert code == 0, f"device status {code} {detail}"
+    return o, lse
+
+
+def reference(q, cache, new, causal=True):
+    return ref.attention(q, cache.k, cache.v, cache.k_scale, cache.v_scale, cache.table, cache.lens, offsets(new), cache.page,
+                         causal)
+
+
+@pytest.mark.parametrize("exponent", [17, 20, 24])
+@pytest.mark.parametrize("n", [1, 20, 80])
+@pytest.mark.parametrize("dims", [(64, 64), (128, 128), (192, 128)])
+def test_a_large_query_column_that_meets_no_key(fa, dims, n, exponent):
+    """One column of the queries is 2^exponent and all keys are 0 there: the scores are those of the other columns, in all
+    their bits (values down to 2^-31 of the row's largest are held exactly; the others here are 2^-6 and more)."""
+    cache = ref.Cache([200], 2, 32, *dims, seed=3)
+    cache.k.view(torch.uint8)[..., 0] = 0
+    q = normal(n, 4, dims[0], seed=n)
+    q = torch.where(q.abs() < 2.0 ** -6, torch.full_like(q, 2.0 ** -6), q)
+    q[..., 0] = 2.0 ** exponent
+    o, lse = attend(fa, cache, [n], q)
+    # the reference's bound counts the products that are not 0 only
+    ref.check_attention(o, lse, reference(q, cache, [n]), EPS_F16 if 2 * n <= 128 else EPS_BF16)
+
+
+@pytest.mark.parametrize("n", [1, 20])
+@pytest.mark.parametrize("q_exp,k_exp", [(-128, 118), (-105, 98), (-95, 88), (-90, 83), (100, -107), (124, -127)])
+def test_queries_at_the_ends_of_the_exponents(fa, n, q_exp, k_exp):
+    """Queries from bf16's subnormal numbers to its largest, against keys whose scales bring the scores back."""
+    cache = ref.Cache([200], 2, 32, 64, 64, seed=5)
+    cache.k_scale = ref.e8m0(torch.full(cache.k_scale.shape, k_exp))
+    q = (normal(n, 4, 64, seed=n).double() * 2.0 ** q_exp).to(torch.bfloat16)
+    assert q.abs().max() > 0 and torch.isfinite(q).all()
+    o, lse = attend(fa, cache, [n], q)
+    ref.check_attention(o, lse, reference(q, cache, [n]), EPS_F16)
