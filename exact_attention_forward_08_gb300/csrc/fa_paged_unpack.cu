@@ -17,8 +17,10 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 
-// One block: the key offsets of the sequences that take this path (others get
-// no keys), -1 throughout when something is out of range, so that nothing is computed.
+// One block: the key offsets of the sequences that take this path.  Others get no
+// keys, also those whose length or number of new tokens is out of range: the rest is
+// computed.  -1 throughout, so that nothing is, where the offsets of the new tokens
+// are broken or the keys do not fit.
 __global__ void __launch_bounds__(kPlanThreads) unpack_plan_kernel(const UnpackParams p) {
   __shared__ long long warp_sum[32];
   __shared__ int bad;
@@ -35,7 +37,7 @@ __global__ void __launch_bounds__(kPlanThreads) unpack_plan_kernel(const UnpackP
       if (!paged_attend_range(p.cu_q[b], p.cu_q[b + 1], len, p.total_q, p.max_n,
                               static_cast<int64_t>(p.max_pages) << p.page_shift, n)) {
         paged_error(p.status, kSitePagedSeq, b);
-        bad = 1;
+        if (n < 0) bad = 1;  // the variable-length forward reads the same offsets
       } else if (static_cast<long long>(n) * p.ratio > p.row_limit) {
         v = len;
       }

@@ -434,6 +434,9 @@ size_t fa_noalloc_scratch_bytes(void);
  * left out (site 511 and its index in the status word), a page index outside
  * [0, num_pages) is never followed (site 512); fa_device_status then reports
  * FA_ERR_INVALID_ARG, and outputs of the sequences concerned are not valid.
+ * The status names one of them; the call's other sequences are computed.  Only
+ * new-token offsets that descend or leave [0, total] concern the whole call,
+ * whose outputs are then not valid.
  */
 typedef struct fa_kv_cache {
   void* k;

@@ -94,3 +94,34 @@ def test_queries_at_the_ends_of_the_exponents(fa, n, q_exp, k_exp):
     assert q.abs().max() > 0 and torch.isfinite(q).all()
     o, lse = attend(fa, cache, [n], q)
     ref.check_attention(o, lse, reference(q, cache, [n]), EPS_F16)
+
+
+@pytest.mark.parametrize("ratio", [2, 40])
+@pytest.mark.parametrize("what", ["length", "negative length", "page", "new tokens", "short one"])
+def test_a_bad_sequence_leaves_its_neighbours_right_beside_prompts(fa, what, ratio):
+    """Sequences of more rows than are read from the pages, one of which (or a single token between them) is bad."""
+    lens, new = [100, 64, 200, 50, 70], [80, 60, 90, 1, 65]
+    most, index, site = 90, 1, 511
+    cache = ref.Cache(lens, 2, 32, 64, 64, seed=2)
+    dev, cu = list(cache.to_device("cuda")), offsets(new)
+    q = normal(sum(new), 2 * ratio, 64, seed=4)
+    if what == "length":
+        dev[5][1] = cache.width * 32 + 1
+    elif what == "negative length":
+        dev[5][1] = -5
+    elif what == "page":
+        dev[4][1, 1], site = cache.num_pages, 512
+    elif what == "new tokens":
+        most, index = 85, 2
+    else:
+        dev[5][3], index = -1, 3
+    o, lse = fa.attention_forward_paged(q.cuda(), *dev, cuda_offsets(new), most, total_k=sum(lens))
+    torch.cuda.synchronize()
+    code, detail = fa.fa_device_status()
+    assert code == fa.FA_ERR_INVALID_ARG and detail[1:] == (site, index), (code, detail)
+    want = reference(q, cache, new)
+    for b in range(5):
+        if b != index:
+            keep = slice(cu[b], cu[b + 1])
+            part = (want[0][keep], want[1][:, keep], want[2][keep], want[3][keep], want[4][keep])
+            ref.check_attention(o[keep], lse[:, keep], part, EPS_BF16, f"sequence {b}")
