@@ -60,6 +60,10 @@ int page_shift(int page_size) { return page_size == 16 ? 4 : page_size == 32 ? 5
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
+// Rows of the unpacked keys.  At least one: without any the variable-length
+// forward takes all queries for rows without a key, those of no sequence too.
+int64_t unpacked_keys(int64_t total_k) { return total_k > 0 ? total_k : 1; }
+
 // The workspace: for each of the two kernels the parts, references and sums, and
 // joins of its cut units, then (for calls with long sequences) offsets, unpacked
 // keys and values, and the variable-length forward's own workspace.
@@ -89,10 +93,11 @@ Workspace workspace_of(int batch, int heads_q, int heads_kv, int64_t total_q, in
   if (rows > fa::kPagedRowLimit) {
     w.cu_k = at;
     at += up256((static_cast<size_t>(batch) + 1) * sizeof(int));
+    const size_t keys = static_cast<size_t>(unpacked_keys(total_k));
     w.k = at;
-    at += up256(static_cast<size_t>(total_k) * heads_kv * d_qk * 2);
+    at += up256(keys * heads_kv * d_qk * 2);
     w.v = at;
-    at += up256(static_cast<size_t>(total_k) * heads_kv * d_v * 2);
+    at += up256(keys * heads_kv * d_v * 2);
     w.varlen = at;
     w.varlen_bytes = fa_varlen_workspace_size(batch, heads_q, total_q);
     at += up256(w.varlen_bytes);
@@ -224,8 +229,8 @@ int fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse, c
     rc = fa::unpack_launch(u, c.d_qk, c.d_v, host.sms, stream);
     if (rc != FA_OK) return rc;
     // rows of the short sequences get no keys here and are written below
-    rc = fa_fwd_varlen(q, u.dst[0], u.dst[1], o, lse, cu_seqlens_q, u.cu_k, batch, total_q, total_k, heads_q,
-                       c.heads_kv, c.d_qk, c.d_v, causal, scale, ws + w.varlen, w.varlen_bytes, stream_);
+    rc = fa_fwd_varlen(q, u.dst[0], u.dst[1], o, lse, cu_seqlens_q, u.cu_k, batch, total_q, unpacked_keys(total_k),
+                       heads_q, c.heads_kv, c.d_qk, c.d_v, causal, scale, ws + w.varlen, w.varlen_bytes, stream_);
     if (rc != FA_OK) return rc;
   }
 

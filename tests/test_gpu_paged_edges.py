@@ -125,3 +125,32 @@ def test_a_bad_sequence_leaves_its_neighbours_right_beside_prompts(fa, what, rat
             keep = slice(cu[b], cu[b + 1])
             part = (want[0][keep], want[1][:, keep], want[2][keep], want[3][keep], want[4][keep])
             ref.check_attention(o[keep], lse[:, keep], part, EPS_BF16, f"sequence {b}")
+
+
+@pytest.mark.parametrize("total_k", [0, 1, None])
+def test_prompts_without_keys_leave_rows_behind_the_last_sequence(fa, total_k):
+    """No key in any sequence, more rows than are read from the pages: the sequences' rows are written, no others."""
+    new = [90, 2]
+    cache = ref.Cache([0, 0], 2, 32, 64, 64)
+    q = normal(sum(new) + 7, 8, 64)
+    out = torch.full((sum(new) + 7, 8, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((8, sum(new) + 7), 3.0, device="cuda")
+    attend(fa, cache, new, q, out=out, lse=lse, total_k=total_k)
+    assert (out[:sum(new)] == 0).all() and torch.isneginf(lse[:, :sum(new)]).all()
+    assert (out[sum(new):] == 3.0).all() and (lse[:, sum(new):] == 3.0).all()
+
+
+def test_keys_where_none_were_said(fa):
+    """total_k 0 and a prompt that has keys: reported, and nothing of it is written; the single token is computed."""
+    lens, new = [100, 64], [90, 1]
+    cache = ref.Cache(lens, 2, 32, 64, 64)
+    q = normal(sum(new), 8, 64)
+    out = torch.full((sum(new), 8, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((8, sum(new)), 3.0, device="cuda")
+    fa.attention_forward_paged(q.cuda(), *cache.to_device("cuda"), cuda_offsets(new), 90, total_k=0, out=out, lse=lse)
+    torch.cuda.synchronize()
+    code, detail = fa.fa_device_status()
+    assert code == fa.FA_ERR_INVALID_ARG and detail[1] == 513, (code, detail)
+    assert (out[:90] == 3.0).all() and (lse[:, :90] == 3.0).all()
+    o, l, *rest = reference(q, cache, new)
+    ref.check_attention(out[90:], lse[:, 90:], (o[90:], l[:, 90:], *(x[90:] for x in rest)), EPS_F16)
