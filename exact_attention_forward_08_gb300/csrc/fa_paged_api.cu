@@ -265,6 +265,7 @@ int fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse, c
   p.causal = causal ? 1 : 0;
   p.timeout_ns = 1000000000ull;
   p.max_n = max_seqlen_q;
+  p.unpacked = unpack ? 1 : 0;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   const int grid = host.sms < fa::kPagedMaxBlocks ? host.sms : fa::kPagedMaxBlocks;
   fa::PagedParts parts[2];

@@ -119,9 +119,13 @@ int paged_launch_pages(const PagedParams& shared, const PagedParts* parts, const
   m.total_q = p.total_q;
   m.heads_q = p.heads_q;
   m.ratio = p.ratio;
+  m.cu = p.cu;
+  m.batch = p.batch;
+  m.max_n = p.max_n;
   const int blocks = m.set[0].blocks + m.set[1].blocks;
-  if (split.many > 0) return paged_start(paged_merge_kernel<DV, 4>, m, blocks, 256, 0, true, stream);
-  return paged_start(paged_merge_kernel<DV, 8>, m, blocks, 256, 0, true, stream);
+  if (p.unpacked) return paged_start(paged_merge_kernel<DV, 4, true>, m, blocks, 256, 0, true, stream);
+  if (split.many > 0) return paged_start(paged_merge_kernel<DV, 4, false>, m, blocks, 256, 0, true, stream);
+  return paged_start(paged_merge_kernel<DV, 8, false>, m, blocks, 256, 0, true, stream);
 }
 
 }  // namespace fa

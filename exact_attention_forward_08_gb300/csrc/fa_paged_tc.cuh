@@ -370,6 +370,17 @@ __global__ void __launch_bounds__(TcShape<DQK, DV>::kThreads, 1)
             mbar_arrive(bar_x);
             return __all_sync(0xffffffffu, tc_wait(bar_x, x_phase++ & 1, wc));
           };
+          // A value that is no number makes its whole row so, here as where its tile is masked.  (A lane of no weight
+          // saw none: its O is not looked at.)
+          bool nan = false;
+#pragma unroll 1
+          for (int c = 0; c < DV; c += 32) {
+            uint32_t v[32];
+            tmem_ld32_wait(t_o + c, v);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) nan |= isnan(__uint_as_float(v[k]));
+          }
+          if (nan && sum != 0.f) sum = __uint_as_float(0x7fc00000u);
           const float rf = sum != 0.f && ref == -INFINITY ? 0.f : ref;
           const int64_t part = 2 * piece + (started_here ? 1 : 0);
           float top = rf, l = sum;

@@ -32,12 +32,12 @@ __global__ void __launch_bounds__(kPlanThreads) unpack_plan_kernel(const UnpackP
     const int b = base + tid;
     long long v = 0;
     if (b < p.batch) {
-      const int len = p.seqlens[b];
+      const int c0 = p.cu_q[b], c1 = p.cu_q[b + 1], len = p.seqlens[b];
       int n;
-      if (!paged_attend_range(p.cu_q[b], p.cu_q[b + 1], len, p.total_q, p.max_n,
+      if (!paged_attend_range(c0, c1, len, p.total_q, p.max_n,
                               static_cast<int64_t>(p.max_pages) << p.page_shift, n)) {
         paged_error(p.status, kSitePagedSeq, b);
-        if (n < 0) bad = 1;  // the variable-length forward reads the same offsets
+        if (!paged_offsets_ok(c0, c1, p.total_q)) bad = 1;  // the variable-length forward reads the same offsets
       } else if (static_cast<long long>(n) * p.ratio > p.row_limit) {
         v = len;
       }

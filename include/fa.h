@@ -509,7 +509,8 @@ int fa_kv_append(const fa_kv_cache* cache, const void* q, const void* k, const v
  * fa_fwd_varlen's kernel.  Both kinds may be in one batch.
  *
  * A token whose keys or values hold a NaN (or whose scale is NaN) makes NaN
- * of the rows that see it, and of no others.
+ * of the rows that see it, of all their columns of O and of their lse, and of
+ * no others.  So does a query row that holds a NaN, of itself.
  *
  * workspace: device memory of fa_fwd_paged_workspace_size(...) bytes, 16-byte
  * aligned; it needs no initialisation, and calls that may overlap (captured

@@ -154,3 +154,45 @@ def test_keys_where_none_were_said(fa):
     assert (out[:90] == 3.0).all() and (lse[:, :90] == 3.0).all()
     o, l, *rest = reference(q, cache, new)
     ref.check_attention(out[90:], lse[:, 90:], (o[90:], l[:, 90:], *(x[90:] for x in rest)), EPS_F16)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("token", [3, 200, 997])
+@pytest.mark.parametrize("length,n", [(1000, 1), (1000, 4), (1000, 30), (1000, 60), (1000, 80), (9000, 1), (9000, 20)])
+@pytest.mark.parametrize("dims", [(64, 64), (128, 128), (192, 128)])
+def test_a_value_that_is_no_number_makes_whole_rows_so(fa, dims, length, n, token, causal):
+    """One NaN code among a token's values, wherever the token lies and whichever kernel the rows select: every column and
+    the log-sum-exp of the rows that see it are NaN, other rows and heads are what they are without it."""
+    page, new = 16, [n]
+    clean = ref.Cache([length], 2, page, *dims, seed=6)
+    bad = ref.Cache([length], 2, page, *dims, seed=6)
+    bad.v.view(torch.uint8)[int(bad.table[0, token // page]), 1, token % page, 5] = 0xFF
+    q = normal(n, 4, dims[0], seed=1)
+    o0, l0 = attend(fa, clean, new, q, causal)
+    o1, l1 = attend(fa, bad, new, q, causal)
+    assert torch.isfinite(o0).all() and torch.isfinite(l0).all()
+    sees = torch.arange(n) + length - n >= token if causal else torch.ones(n, dtype=torch.bool)
+    assert torch.isnan(o1[sees][:, 2:]).all() and torch.isnan(l1[2:][:, sees]).all()
+    assert torch.equal(o1[:, :2], o0[:, :2]) and torch.equal(l1[:2], l0[:2])
+    assert torch.equal(o1[~sees], o0[~sees]) and torch.equal(l1[:, ~sees], l0[:, ~sees])
+
+
+@pytest.mark.parametrize("n", [1, 20, 80])
+@pytest.mark.parametrize("what", ["key", "query"])
+def test_a_key_or_query_that_is_no_number_makes_whole_rows_so(fa, what, n):
+    clean, new = ref.Cache([500, 0], 2, 32, 128, 64, seed=6), [n, 1]
+    bad = ref.Cache([500, 0], 2, 32, 128, 64, seed=6)
+    q = normal(n + 1, 4, 128, seed=1)
+    o0, l0 = attend(fa, clean, new, q)
+    if what == "key":
+        bad.k.view(torch.uint8)[int(bad.table[0, 1]), 1, 3, 7] = 0x7F
+        hit = torch.zeros(n + 1, 4, dtype=torch.bool)
+        hit[:n, 2:] = True
+    else:
+        q[n // 2, 1, 9] = float("nan")
+        hit = torch.zeros(n + 1, 4, dtype=torch.bool)
+        hit[n // 2, 1] = True
+    o1, l1 = attend(fa, bad, new, q)
+    assert torch.isnan(o1[hit]).all() and torch.isnan(l1.t()[hit]).all()
+    assert torch.equal(o1[~hit], o0[~hit]) and torch.equal(l1.t()[~hit], l0.t()[~hit])
+    assert (o1[n] == 0).all() and torch.isneginf(l1[:, n]).all()  # without a key
