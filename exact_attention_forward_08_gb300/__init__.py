@@ -633,7 +633,7 @@ def _paged_cache(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, cu_
 
     f8, e8, i32 = torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.int32
     kd, vd, td = k_cache.shape, v_cache.shape, block_table.shape
-    if not (len(kd) == 4 and kd[:3] == vd[:3] and k_cache.dtype is f8 and v_cache.dtype is f8 and
+    if not (len(kd) == 4 and len(vd) == 4 and kd[:3] == vd[:3] and k_cache.dtype is f8 and v_cache.dtype is f8 and
             k_scale.dtype is e8 and v_scale.dtype is e8 and k_scale.shape == kd[:2] and v_scale.shape == kd[:2] and
             k_scale.is_contiguous() and v_scale.is_contiguous() and len(td) == 2 and block_table.dtype is i32 and
             seqlens_k.dtype is i32 and cu_seqlens.dtype is i32 and seqlens_k.shape == td[:1] and
@@ -730,7 +730,7 @@ def kv_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, 
                              interleaved, q_out, stream)
     cache, heads, d_qk, d_v, batch, _ = _paged_cache(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k,
                                                      cu_seqlens, index)
-    total = k.shape[0]
+    total = k.shape[0] if k.dim() else 0
     ks = _token_stride("k", k, total, heads, d_qk)
     vs = _token_stride("v", v, total, heads, d_v)
     rot = positions = 0

@@ -196,3 +196,18 @@ def test_a_key_or_query_that_is_no_number_makes_whole_rows_so(fa, what, n):
     assert torch.isnan(o1[hit]).all() and torch.isnan(l1.t()[hit]).all()
     assert torch.equal(o1[~hit], o0[~hit]) and torch.equal(l1.t()[~hit], l0.t()[~hit])
     assert (o1[n] == 0).all() and torch.isneginf(l1[:, n]).all()  # without a key
+
+
+def test_new_tokens_of_any_rank_are_refused(fa):
+    cache = ref.Cache([5], 2, 16, 64, 64)
+    dev, cu = cache.to_device("cuda"), cuda_offsets([2])
+    good = {"k": normal(2, 2, 64).cuda(), "v": normal(2, 2, 64).cuda(), "q": normal(2, 4, 64).cuda()}
+    for name in good:
+        for change in (lambda t: t[0], lambda t: t[None], lambda t: t[..., 0], lambda t: t.flatten()[0]):
+            bad = {**good, name: change(good[name])}
+            with pytest.raises(fa.FaError):
+                fa.kv_append(bad["k"], bad["v"], *dev, cu, q=bad["q"])
+            if name == "q":
+                with pytest.raises(fa.FaError):
+                    fa.attention_forward_paged(bad["q"], *dev, cu, 2)
+    assert fa.fa_device_status()[0] == 0

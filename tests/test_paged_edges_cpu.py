@@ -52,3 +52,28 @@ def test_range_checks_hold_for_any_offsets_and_lengths(tmp_path):
         assert ok == want, (kind, c0, c1, length, total, max_new, most)
         if ok:
             assert n == new and (kind == 1 or start == length - new)
+
+
+def paged_tensors(pages=3, heads=2, page=16, d_qk=64, d_v=64, batch=2):
+    """The cache's tensors as the binding takes them, on the CPU."""
+    torch = pytest.importorskip("torch")
+    f8, e8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+    u8 = dict(dtype=torch.uint8)
+    return dict(k_cache=torch.zeros(pages, heads, page, d_qk, **u8).view(f8),
+                v_cache=torch.zeros(pages, heads, page, d_v, **u8).view(f8),
+                k_scale=torch.zeros(pages, heads, **u8).view(e8), v_scale=torch.zeros(pages, heads, **u8).view(e8),
+                block_table=torch.zeros(batch, 4, dtype=torch.int32), seqlens_k=torch.zeros(batch, dtype=torch.int32),
+                cu_seqlens=torch.zeros(batch + 1, dtype=torch.int32))
+
+
+def test_tensors_of_any_rank_are_refused_by_name():
+    """A dimension too few or too many in any of the cache's tensors is an FaError that names it, nothing else."""
+    import exact_attention_forward_08_gb300 as fa
+    good = paged_tensors()
+    assert fa._paged_cache(*good.values(), -1)[1:] == (2, 64, 64, 2, 64)
+    for name in good:
+        for change in (lambda t: t[0], lambda t: t[None], lambda t: t[..., 0], lambda t: t[..., None], lambda t: t.flatten()[0]):
+            bad = dict(good)
+            bad[name] = change(good[name])
+            with pytest.raises(fa.FaError, match=name):
+                fa._paged_cache(*bad.values(), -1)
