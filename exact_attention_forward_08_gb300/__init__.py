@@ -690,6 +690,15 @@ def _empty(shape, dtype, index, ptr, current):
         return torch.empty(shape, dtype=dtype, device=index)
 
 
+# rows (new tokens x query heads a key/value head) up to which a sequence is read straight from the pages
+_PAGED_ROWS = 128
+
+
+def _paged_total_k(batch, capacity, total_q, ratio):
+    """The most keys that the sequences of more than _PAGED_ROWS rows can have, if each can have `capacity`."""
+    return min(batch, total_q // (_PAGED_ROWS // ratio + 1)) * capacity
+
+
 @functools.lru_cache(maxsize=256)
 def _paged_workspace_bytes(*sizes):
     return load_library().fa_fwd_paged_workspace_size(*sizes)
@@ -767,8 +776,9 @@ def attention_forward_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, 
     """O (and LSE) of new tokens over a paged 8-bit cache (``fa_fwd_paged`` of include/fa.h).
 
     q [total_q,Hq,dqk] bf16 (packed, cu_seqlens_q int32 [B+1], at most ``max_seqlen_q`` tokens a sequence); the cache
-    as ``kv_append`` fills it, seqlens_k the lengths with the new tokens.  ``total_k``: an upper limit of their sum,
-    which bounds the workspace of calls with long sequences of new tokens (default: what the block table can hold).
+    as ``kv_append`` fills it, seqlens_k the lengths with the new tokens.  ``total_k``: an upper limit of their sum over
+    the sequences of more than 128 rows (new tokens x query heads a key/value head), whose unpacked keys the workspace
+    holds (default: what the block table can hold of as many such sequences as total_q tokens can make).
     Allocates ``out`` [total_q,Hq,dv] bf16, ``lse`` [Hq,total_q] fp32 and the workspace (uint8) when not given.
     Offsets, lengths and pages out of range are detected on the device and reported by ``fa_device_status``.
     """
@@ -788,7 +798,7 @@ def attention_forward_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, 
     if d != d_qk:
         _bad(f"q must be [total_q, heads_q, {d_qk}]")
     if total_k is None:
-        total_k = batch * capacity
+        total_k = _paged_total_k(batch, capacity, total_q, max(heads_q // max(heads, 1), 1))
     ptr, current = _call_stream(index, stream)
     if out is None:
         out = _empty((total_q, heads_q, d_v), torch.bfloat16, index, ptr, current)

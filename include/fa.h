@@ -498,10 +498,11 @@ int fa_kv_append(const fa_kv_cache* cache, const void* q, const void* k, const v
  *   bottom-right inside each sequence: new token i of n sees token j iff
  *   j <= i + seqlens_k[b] - n.  A row without a key gets O = 0, lse = -inf.
  *   max_seqlen_q: an upper limit of the new tokens of a sequence (a longer one
- *   is left out: site 511).  total_k: an upper limit of the sum of seqlens_k;
- *   it bounds the workspace where max_seqlen_q * heads_q / heads_kv > 128 and
- *   is not used below (a larger sum: nothing of the longer sequences is
- *   computed, site 513).
+ *   is left out: site 511).  total_k: an upper limit of the sum of seqlens_k
+ *   over the sequences of more than 128 rows (new tokens x query heads a
+ *   key/value head); it bounds the workspace where max_seqlen_q * heads_q /
+ *   heads_kv > 128 and is not used below (a larger sum: nothing of these
+ *   sequences is computed, site 513).
  *
  * Sequences of up to 128 rows (new tokens x query heads a key/value head) are
  * computed straight from the pages, their keys split over the whole GPU;

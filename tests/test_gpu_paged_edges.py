@@ -211,3 +211,20 @@ def test_new_tokens_of_any_rank_are_refused(fa):
                 with pytest.raises(fa.FaError):
                     fa.attention_forward_paged(bad["q"], *dev, cu, 2)
     assert fa.fa_device_status()[0] == 0
+
+
+def test_default_workspace_has_room_for_the_long_sequences_only(fa):
+    """64 sequences with room for 32768 tokens each, one of them a prompt that is unpacked: without total_k the call asks
+    for what the sequences of that many new tokens could hold, not for the whole block table (8.6 GB here)."""
+    new, lens = [33] + [1] * 63, [40] + [1 + i for i in range(63)]
+    cache = ref.Cache(lens, 8, 64, 128, 128, width=512)
+    q = normal(sum(new), 32, 128)
+    dev, cu, qd = cache.to_device("cuda"), cuda_offsets(new), q.cuda()
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    o, lse = fa.attention_forward_paged(qd, *dev, cu, 33)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status()[0] == 0
+    assert torch.cuda.max_memory_allocated() - before < 1 << 30
+    ref.check_attention(o, lse, reference(q, cache, new), EPS_BF16)

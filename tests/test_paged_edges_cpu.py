@@ -77,3 +77,26 @@ def test_tensors_of_any_rank_are_refused_by_name():
             bad[name] = change(good[name])
             with pytest.raises(fa.FaError, match=name):
                 fa._paged_cache(*bad.values(), -1)
+
+
+def test_default_limit_of_keys_covers_every_batch():
+    """What attention_forward_paged takes for total_k when none is given: never below the keys that the sequences of more
+    than 128 rows can have, whatever the lengths (checked over all splits of the new tokens), and no more than that."""
+    import exact_attention_forward_08_gb300 as fa
+
+    def longest(batch, total, least, at=0):  # most sequences of `least` tokens or more among all splits of `total`
+        if at == batch:
+            return 0
+        return max((n >= least) + longest(batch, total - n, least, at + 1) for n in range(total + 1))
+
+    for ratio, most in ((128, 7), (64, 8), (43, 9), (129, 6), (40, 9)):  # 2, 3, 3, 1 and 4 tokens are more than 128 rows
+        least = 128 // ratio + 1
+        assert (least - 1) * ratio <= 128 < least * ratio
+        for batch in (1, 2, 3):
+            for total in range(most):
+                assert fa._paged_total_k(batch, 1000, total, ratio) == 1000 * longest(batch, total, least)
+    assert fa._paged_total_k(64, 32768, 96, 4) == 2 * 32768  # one prompt of 33 tokens and 63 single ones
+    # the row limit is the library's: one row more than it asks for room for unpacked keys
+    size = fa.fa_fwd_paged_workspace_size
+    rows = fa._PAGED_ROWS
+    assert size(1, 1, 1, rows, rows, 1 << 20, 64, 64) < 1 << 28 <= size(1, 1, 1, rows + 1, rows + 1, 1 << 20, 64, 64)
