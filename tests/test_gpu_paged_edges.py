@@ -228,3 +228,48 @@ def test_default_workspace_has_room_for_the_long_sequences_only(fa):
     assert fa.fa_device_status()[0] == 0
     assert torch.cuda.max_memory_allocated() - before < 1 << 30
     ref.check_attention(o, lse, reference(q, cache, new), EPS_BF16)
+
+
+@pytest.mark.parametrize("rows", [17, 32, 33, 64, 100, 128])
+@pytest.mark.parametrize("dims", [(64, 64), (128, 64), (128, 128), (192, 64), (192, 128)])
+def test_weights_keep_eleven_bits_from_the_pages(fa, dims, rows):
+    """17 to 128 rows and values' scales close to each other: the weights are f16, not bf16.  Sequences of few keys, where
+    many of O's elements are small against their terms, show the difference.
+
+    The bound: half a step of f16 for a weight (2^-11), what the scores' and sums' fp32 leaves (as in paged_ref), and for
+    weights in f16's subnormal range 2^-25 of the unit they are kept in, which for a value of the tile's largest scale s
+    is an eighth of 1 / s: 2^-28 of 448 s for each key."""
+    lens = [2, 3, 4, 5, 6, 8, 11, 300, 1000]
+    cache = ref.Cache(lens, 2, 64, *dims, seed=rows)
+    new = [1] * len(lens)
+    q = normal(len(lens), 2 * rows, dims[0], seed=rows)
+    o, lse = attend(fa, cache, new, q)
+    want = reference(q, cache, new)
+    ow, lw, weight, delta, count = want
+    tail = count[:, None, None] * 2.0 ** -28 * 448 * ref.scale_values(cache.v_scale).max()
+    rel = EPS_F16 + 2.0 ** -20 + 2 * delta[..., None] + count[:, None, None] * 2.0 ** -24
+    bound = (2.0 ** -8 * ow.abs() + (weight * rel + tail) * (1 + 2.0 ** -8)) * ref.SLACK
+    worst = ((o.double().cpu() - ow).abs() / bound).max().item()
+    assert worst <= 1.0, f"O off by {worst:.3f} of its bound"
+    ref.check_attention(o, lse, want, EPS_BF16)
+
+
+@pytest.mark.parametrize("n,eps,tail", [(1, EPS_F16, 2.0 ** -32), (8, EPS_F16, 2.0 ** -32), (20, EPS_BF16, 2.0 ** -22),
+                                        (80, EPS_BF16, 0.0)])
+def test_small_weights_of_large_values(fa, n, eps, tail):
+    """Scores that differ by 2^60 and values' scales that differ as much: what a weight may lose is what the header says.
+
+    Up to 16 rows the larger of 2^-11 of the weight and 2^-32 of the largest one, whatever its values; up to 128 rows 2^-8
+    of it where the scales are far apart, or 2^-11 and 2^-28 S / s, at most 2^-22, where they are not; above 2^-8."""
+    cache = ref.Cache([160], 2, 16, 64, 64, seed=4)
+    g = torch.Generator().manual_seed(9)
+    cache.v_scale = ref.e8m0(torch.randint(-40, 20, cache.v_scale.shape, generator=g))
+    cache.k_scale = ref.e8m0(torch.randint(-4, -1, cache.k_scale.shape, generator=g))
+    q = normal(n, 4, 64, seed=n)
+    o, lse = attend(fa, cache, [n], q)
+    ow, lw, weight, delta, count = reference(q, cache, [n])
+    size = ref.dense(cache.v, cache.v_scale, cache.table[0], 160, 16).abs().sum(1).repeat_interleave(2, 0)  # [heads_q, d_v]
+    rel = eps + 2.0 ** -20 + 2 * delta[..., None] + count[:, None, None] * 2.0 ** -24
+    bound = (2.0 ** -8 * ow.abs() + (weight * rel + tail * size) * (1 + 2.0 ** -8)) * ref.SLACK
+    worst = ((o.double().cpu() - ow).abs() / bound).max().item()
+    assert worst <= 1.0, f"O off by {worst:.3f} of its bound"
