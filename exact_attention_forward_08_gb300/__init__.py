@@ -722,7 +722,7 @@ def kv_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, 
 
     k [total,Hkv,dqk], v [total,Hkv,dv] and, to be rotated along with the keys, q [total,Hq,dqk] are bf16 CUDA tensors
     whose tokens may lie apart (views of one projection's output); k_cache, v_cache float8_e4m3fn
-    [num_pages,Hkv,page_size,d] of any strides with contiguous codes, k_scale, v_scale float8_e8m0fnu [num_pages,Hkv];
+    [num_pages,Hkv,page_size,d] with contiguous codes and strides of multiples of 16, k_scale, v_scale float8_e8m0fnu [num_pages,Hkv];
     block_table int32 [B,max_pages], seqlens_k int32 [B] (lengths with the new tokens), cu_seqlens int32 [B+1];
     cos_sin fp32 [positions, rot_dim] or None (no rotation).  The cache is updated in place; returns q_out (allocated
     when not given; may be q), None without q.  Launches on ``stream`` (default: torch's current stream).  Offsets,

@@ -19,10 +19,11 @@
 // Bound by the latency of loads: 80 registers let 24 warps on an SM.  8191 tokens
 // of 32/8 heads of 128: 39 us, 4.8 TB/s of what has to move (28 us at the copy
 // rate); 24 prompts of 1 to 900 tokens, 16/16 heads of 192/128: 56 us (38.5);
-// one token of one or of 128 sequences: 3 and 5 us.  Queries take three heads a
+// one token of one or of 128 sequences: 3.5 and 5.3 us.  Queries take three heads a
 // lane at once and ask for the first before their token's sequence is known: 42.0
 // and 57.9 us with two, afterwards.  Registers for 16 warps: 45.6 and 64.5, for 32:
-// 40.5 and 58.4.
+// 40.5 and 58.4.  With those for 24 a thread spills 8 bytes at d_qk = 128 and 40 at
+// 192 (136 read back), nothing at 64.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -61,7 +62,14 @@ struct AppendParams {
 
 constexpr int kBlockRows = 8;  // rows a warp holds at a time
 constexpr int kWarps = 8;      // of a block
-constexpr int kTeamWarps = 64;  // warps an SM that units are spread over (8191 tokens: 38.8 us, with 32 39.5)
+// Warps an SM that units are spread over: a unit gets two, four or eight where
+// there are fewer units than that.  us with 32 / 64 / 128:
+//   8191 tokens, 32/8 heads of 128, pages of 64        39.5 / 38.9 / 38.9
+//   24 prompts of 1..900, 16/16 of 192/128, pages of 32  55.8 / 55.8 / 61.5
+//   16 prompts of 450..900, 16/16 of 192/128, of 64      68.6 / 65.6 / 69.2
+//   64 prompts of 50..100, 32/8 of 128, of 64            22.6 / 25.9 / 31.9
+//   4 prompts of 256..512, 16/4 of 64, and one of 2000, 32/8 of 128: within 0.4 %
+constexpr int kTeamWarps = 64;
 
 // The sequence's range of new positions [start, start + n) if it can be
 // appended: offsets ordered and inside the batch, positions inside the block

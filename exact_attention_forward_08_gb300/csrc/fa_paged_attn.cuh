@@ -25,8 +25,8 @@
 // is written out at once, one that is cut leaves unnormalised parts that
 // paged_merge_kernel joins.
 //
-// Bound by DRAM: B8 x 32767 keys, 32/8 heads of 128: 93 us with the merge, 5.8
-// TB/s of codes (the copies alone: 84 us); 16 heads of 192/128: 59 us, 5.6 TB/s;
+// Bound by DRAM: B8 x 32767 keys, 32/8 heads of 128: 94 us with the merge, 5.7
+// TB/s of codes (the copies alone: 84 us); 16 heads of 192/128: 60 us, 5.5 TB/s;
 // 16 heads of 64 in pages of 16, copies of 1 KB: 123 us, 4.4 TB/s (copies alone
 // 102).
 #pragma once
@@ -83,7 +83,9 @@ constexpr float kRefLag = 8.f;        // the reference follows the maximum when 
 // tile costs beside its products (B8 x 32768, 32/8 heads of 128: 93 us against
 // 97 with 32; 16 heads of 64 in pages of 16: 123 against 150); more rows or
 // wider keys leave registers for 32.  Two warps a scheduler: with three, 168
-// registers a thread spill (116 us for the first of these).
+// registers a thread spill (116 us for the first of these).  With two, 255 spill 12
+// to 24 bytes at (128, 128) and 8 rows, 100 to 116 at (128, 128) and (192, 128) and 16
+// rows, nothing elsewhere.
 template <int DQK, int DV, int NT>
 struct PagedShape {
   static constexpr int kRows = 8 * NT;
@@ -828,9 +830,9 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
 // their order, so the result does not depend on timing.  Bound by latency (4 us
 // beside the launch): loads of a row's first FIRST parts do not wait for its
 // weights, and there are few blocks, for most pieces leave nothing to join.  Eight
-// parts where only few rows are joined, four (80 registers, not 127) where blocks
-// are many: single tokens over 1026 keys 10.7 and 11.7 us, 128 rows of 32 x 8000 keys
-// 50.5 and 48.1.
+// parts where only few rows are joined (127 registers, 80 at d_v = 64), four (64)
+// where blocks are many: single tokens over 1026 keys 10.7 and 11.7 us, 128 rows of
+// 32 x 8000 keys 50.5 and 48.1.
 struct PagedMerge {
   struct Set {
     PagedParts part;

@@ -39,7 +39,7 @@
 // where it takes 70.6.  Starting and ending a (sequence, head) takes 12000
 // cycles; counting them as kStart tiles when the line is cut was worth 17 %.
 // 16 sequences of 5 new tokens, 32/8 heads of 128, 500 to 8000 keys: 58 us, 2.5
-// TB/s of codes; 32 of 32/1 heads: 30 us, of which half is the start and the end;
+// TB/s of codes; 32 of 32/1 heads: 31 us, of which half is the start and the end;
 // 32 x 8000 keys of 2 heads with 64 rows: 57 us, 2.3 TB/s.
 #pragma once
 #include "fa_paged_attn.cuh"
@@ -49,7 +49,12 @@ namespace fa {
 template <int DQK, int DV>
 struct TcShape {
   static constexpr int kTile = 128, kRows = 128;
-  static constexpr int kStart = 5;  // tiles that a unit's start and end cost
+  // Tiles that a unit's start and end cost.  us with 3 / 5 / 8, 16 sequences of 5 new tokens and 500 to 8000 keys, 32/8
+  // heads: 48.0 / 48.5 / 50.9 at (64, 64), 60.7 / 58.5 / 59.3 at (128, 128), 79.8 / 83.4 / 87.6 at (192, 64), 86.2 / 89.3 /
+  // 93.5 at (192, 128), where a tile costs more; 64 sequences of 100 to 600 keys: 44.2 / 41.3 / 41.1, 57.9 / 52.1 / 52.4 and
+  // 62.1 / 64.1 / 66.1 at (64, 64), (128, 128) and (192, 128); 32 of 3000 to 9000 keys, 32/1 heads, one token: 25.9 / 24.4 /
+  // 25.6, 33.0 / 30.6 / 31.6 and 39.4 / 39.7 / 42.3.  One value within 4.5 % of the best of the three in all.
+  static constexpr int kStart = 5;
   static constexpr int kFillWarps = 8, kFillThreads = 32 * kFillWarps;
   static constexpr int kMmaWarp = 4, kLoadWarp = 5, kFillWarp0 = 6;
   static constexpr int kThreads = 32 * (kFillWarp0 + kFillWarps);

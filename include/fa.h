@@ -478,8 +478,8 @@ typedef struct fa_kv_cache {
  * finite are stored as NaN and do not count for the scale.  Bytes behind a
  * sequence's last token are left as they were.
  *
- * A page that receives tokens may belong to one sequence of the call only
- * (full pages may be shared).  One launch; no workspace.  A sequence with
+ * A page that receives tokens may belong to one sequence of the call only, and
+ * stand in its row once (full pages may be shared).  One launch; no workspace.  A sequence with
  * positions beyond max_positions (rot_dim > 0) or beyond its row of the block
  * table is left out and reported as above.
  */
