@@ -529,6 +529,8 @@ int fa_kv_append(const fa_kv_cache* cache, const void* q, const void* k, const v
  *     largest scale among the first 128 tokens that a block takes of the
  *     sequence (2^-17 or 2^33 where it lies beyond these); 128 tokens with an s
  *     below S / 64 or above 8 S take bf16 instead (2^-8).  Above 128 rows bf16.
+ * The sums hold weights of up to 2^15 before they are normalised, in units of
+ * 2^-20 at least: values up to 2^64 in magnitude cannot overflow them.
  */
 size_t fa_fwd_paged_workspace_size(int batch, int heads_q, int heads_kv, int64_t total_q, int max_seqlen_q,
                                    int64_t total_k, int d_qk, int d_v);

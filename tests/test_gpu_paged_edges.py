@@ -273,3 +273,17 @@ def test_small_weights_of_large_values(fa, n, eps, tail):
     bound = (2.0 ** -8 * ow.abs() + (weight * rel + tail * size) * (1 + 2.0 ** -8)) * ref.SLACK
     worst = ((o.double().cpu() - ow).abs() / bound).max().item()
     assert worst <= 1.0, f"O off by {worst:.3f} of its bound"
+
+
+@pytest.mark.parametrize("small", [-63, 55])
+@pytest.mark.parametrize("n", [1, 20, 80])
+def test_values_up_to_two_to_the_sixty_fourth(fa, n, small):
+    """Values' scales of 2^55 throughout, and next to pages of the smallest scale that the append writes."""
+    cache = ref.Cache([300], 2, 32, 128, 128, seed=4)
+    exps = torch.full(cache.v_scale.shape, 55)
+    exps[cache.table[0, :5].long()] = small  # the first tile's pages and one more
+    cache.v_scale = ref.e8m0(exps)
+    q = normal(n, 4, 128, seed=n)
+    o, lse = attend(fa, cache, [n], q)
+    wide = small != 55 and n == 20  # bf16 weights from the second tile on
+    ref.check_attention(o, lse, reference(q, cache, [n]), EPS_F16 if n * 2 <= 128 and not wide else EPS_BF16)
