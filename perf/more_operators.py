@@ -460,7 +460,8 @@ def _own_select(s):
     import exact_attention_forward_08_gb300 as fa
 
     c = s["case"]
-    fa.kv_bounds(s["k_cache"], s["k_bounds"], s["block_table"], s["seqlens_k"], s["cu_seqlens"])
+    fa.kv_bounds(s["k_cache"], s["k_bounds"], s["block_table"], s["seqlens_k"], s["cu_seqlens"],
+                 s["q"].shape[0])
     lists, lens = fa.kv_select(s["q"], s["k_bounds"], s["k_scale"], s["block_table"], s["seqlens_k"], s["cu_seqlens"],
                                c["new"], c["page"], c["top"], keep_first=c["first"], keep_last=c["last"],
                                lists=s["lists"], list_lens=s["list_lens"])
