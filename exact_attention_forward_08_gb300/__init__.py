@@ -10,12 +10,20 @@ library is missing or a call fails, an exception is raised.
     o, lse = attention_forward_varlen(q, k, v, cu_q, cu_k)  # q [total_q,Hq,d], cu_q int32 [B+1]
     kv_append(k, v, k_cache, v_cache, k_scale, v_scale, table, lens, cu_q)  # paged 8-bit cache
     o, lse = attention_forward_paged(q, k_cache, v_cache, k_scale, v_scale, table, lens, cu_q, max_seqlen_q)
+    table = rotary_table(positions, rot_dim); q, k = rotary(q, k, table)   # dq, dk = rotary_backward(dq, dk, table)
+    kv_bounds(k_cache, k_bounds, table, lens, cu_q)                         # sparse attention over selected pages
+    lists, list_lens = kv_select(q, k_bounds, k_scale, table, lens, cu_q, max_seqlen_q, page_size, top)
+    o, lse = attention_forward_lists(q, k_cache, v_cache, k_scale, v_scale, lists, list_lens)
+    table, lens, refs = kv_fork(parents, k_cache, v_cache, k_scale, v_scale, table, lens, refs)  # the cache's pages
+    table, refs, page_map, used = kv_compact(k_cache, v_cache, k_scale, v_scale, table, lens, refs)
 
 Raw entry points with the C names: ``fa_fwd``, ``fa_fwd_ex``, ``fa_fwd_varlen``,
 ``fa_fwd_varlen_ex``, ``fa_varlen_workspace_size``, ``fa_varlen_plan_host``,
 ``fa_device_status``, ``fa_status_string``, ``fa_make_plan``, ``fa_plan_task``, ``fa_plan_set_grid``,
 ``fa_plan_block_masked``, ``fa_plan_first_masked_block``, ``fa_version``, ``fa_kv_append``, ``fa_fwd_paged``,
-``fa_fwd_paged_workspace_size``.
+``fa_fwd_paged_workspace_size``, ``fa_rotary_table``, ``fa_rotary``, ``fa_kv_bounds``, ``fa_kv_select``,
+``fa_kv_select_workspace_size``, ``fa_fwd_lists``, ``fa_fwd_lists_workspace_size``, ``fa_kv_fork``, ``fa_kv_compact``,
+``fa_kv_pages_workspace_size``.
 """
 from __future__ import annotations
 
@@ -35,7 +43,11 @@ __all__ = ["fa_fwd", "fa_fwd_ex", "fa_fwd_varlen", "fa_fwd_varlen_ex", "fa_varle
            "fa_plan_task", "fa_plan_set_grid", "fa_plan_block_masked", "fa_plan_first_masked_block", "fa_version", "FaOptions", "FaPlan",
            "FaTask", "FaVarlenTask", "attention_forward", "attention_forward_varlen", "FaError", "load_library",
            "LIB_PATH", "STATUS", "VARLEN_HEADER_BYTES", "FaKvCache", "fa_kv_append", "fa_fwd_paged",
-           "fa_fwd_paged_workspace_size", "kv_append", "attention_forward_paged"]
+           "fa_fwd_paged_workspace_size", "kv_append", "attention_forward_paged", "FaRotaryScaling", "ROTARY_SCALING",
+           "fa_rotary_table", "fa_rotary", "rotary_table", "rotary", "rotary_backward", "fa_kv_bounds", "fa_kv_select",
+           "fa_kv_select_workspace_size", "fa_fwd_lists", "fa_fwd_lists_workspace_size", "kv_bounds", "kv_select",
+           "attention_forward_lists", "fa_kv_fork", "fa_kv_compact", "fa_kv_pages_workspace_size", "kv_fork",
+           "kv_compact"]
 
 LIB_PATH = _build.LIB
 STATUS = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED", 3: "FA_ERR_CUDA",
@@ -84,6 +96,15 @@ class FaKvCache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "block_table", "seqlens_k")] + \
                [("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3), ("table_stride", ctypes.c_int64)] + \
                [(n, ctypes.c_int) for n in ("num_pages", "page_size", "heads_kv", "d_qk", "d_v", "max_pages")]
+
+
+class FaRotaryScaling(ctypes.Structure):
+    """``fa_rotary_scaling`` of include/fa.h."""
+    _fields_ = [("kind", ctypes.c_int)] + [(n, ctypes.c_double) for n in ("factor", "original", "low", "high", "magnitude")]
+
+
+# names of the kinds of scaling (enum fa_rotary_kind)
+ROTARY_SCALING = {"none": 0, "linear": 1, "base": 2, "by_parts": 3}
 
 
 # a varlen workspace holds the task count at byte 0 and the task records from this offset
@@ -179,6 +200,26 @@ def load_library(path: str | None = None):
     lib.fa_fwd_paged.restype = _I
     lib.fa_fwd_paged_workspace_size.argtypes = [_I, _I, _I, i64, _I, i64, _I, _I]
     lib.fa_fwd_paged_workspace_size.restype = ctypes.c_size_t
+    lib.fa_rotary_table.argtypes = [_P, _I, _I, ctypes.c_double, ctypes.POINTER(FaRotaryScaling), _P]
+    lib.fa_rotary_table.restype = _I
+    lib.fa_rotary.argtypes = [_P, _P, _P, _P, i64, i64, i64, i64, _P, _P, _I, i64, i64, _I, _I, _I, _P, _I, _I, _I, _I, _P]
+    lib.fa_rotary.restype = _I
+    lib.fa_kv_bounds.argtypes = [_P, _P, _P, _I, i64, _P]
+    lib.fa_kv_bounds.restype = _I
+    lib.fa_kv_select_workspace_size.argtypes = [_I, i64, _I, _I]
+    lib.fa_kv_select_workspace_size.restype = ctypes.c_size_t
+    lib.fa_kv_select.argtypes = [_P, _P, _P, _P, i64, _P, _P, _I, i64] + [_I] * 11 + [_P, _P, _P, ctypes.c_size_t, _P]
+    lib.fa_kv_select.restype = _I
+    lib.fa_fwd_lists_workspace_size.argtypes = [_I, _I, _I]
+    lib.fa_fwd_lists_workspace_size.restype = ctypes.c_size_t
+    lib.fa_fwd_lists.argtypes = [_P, _P, _P, _P, _I, _P, _P, i64, _I, ctypes.c_float, _P, ctypes.c_size_t, _P]
+    lib.fa_fwd_lists.restype = _I
+    lib.fa_kv_pages_workspace_size.argtypes = [_I, _I, _I]
+    lib.fa_kv_pages_workspace_size.restype = ctypes.c_size_t
+    lib.fa_kv_fork.argtypes = [_P, _P, _P, _I, _P, _P, _I, _P, i64, _P, _P, _P, ctypes.c_size_t, _P]
+    lib.fa_kv_fork.restype = _I
+    lib.fa_kv_compact.argtypes = [_P, _P, _P, _I, _P, i64, _P, _P, _P, _P, ctypes.c_size_t, _P]
+    lib.fa_kv_compact.restype = _I
     if path is None:
         _lib = lib
     return lib
@@ -822,3 +863,501 @@ def attention_forward_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, 
     if rc != FA_OK:
         raise FaError(rc, "fa_fwd_paged")
     return (out, lse) if return_lse else out
+
+
+# ---------------------------------------------------------------------------
+# rotary positions
+# ---------------------------------------------------------------------------
+
+def fa_rotary_table(cos_sin, positions, rot_dim, base, scaling: FaRotaryScaling | None, stream) -> int:
+    """``fa_rotary_table`` of include/fa.h; pointer arguments are integers (device addresses)."""
+    return load_library().fa_rotary_table(cos_sin, positions, rot_dim, float(base),
+                                          ctypes.byref(scaling) if scaling is not None else None, stream)
+
+
+def fa_rotary(q, k, q_out, k_out, q_stride, k_stride, q_out_stride, k_out_stride, positions, cu_seqlens, batch, seqlen,
+              total, heads_q, heads_k, d, cos_sin, max_positions, rot_dim, interleaved, backward, stream) -> int:
+    """``fa_rotary`` of include/fa.h; pointer arguments are integers (device addresses)."""
+    return load_library().fa_rotary(q, k, q_out, k_out, q_stride, k_stride, q_out_stride, k_out_stride, positions,
+                                    cu_seqlens, batch, seqlen, total, heads_q, heads_k, d, cos_sin, max_positions, rot_dim,
+                                    int(interleaved), int(backward), stream)
+
+
+def rotary_table(positions: int, rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                 original: float = 0.0, low: float = 1.0, high: float = 32.0, magnitude: float = 1.0, out=None, device=None,
+                 stream=None):
+    """Cosines and sines of positions 0 .. positions - 1 (``fa_rotary_table`` of include/fa.h), fp32 [positions, rot_dim],
+    as ``kv_append`` and ``rotary`` take them.
+
+    ``scaling`` is "none", "linear", "base" or "by_parts" (with ``factor``, and for the last ``original``, the trained
+    length, and ``low`` and ``high``, turns within it); every value is multiplied by ``magnitude``.  Allocates ``out`` on
+    ``device`` (default: the current CUDA device) when not given."""
+    import torch
+
+    if scaling not in ROTARY_SCALING:
+        _bad(f"scaling must be one of {', '.join(ROTARY_SCALING)}")
+    if out is not None:
+        if out.dtype is not torch.float32 or out.shape != (positions, rot_dim) or not out.is_contiguous() or not out.is_cuda:
+            _bad(f"out must be a contiguous fp32 CUDA tensor [{positions}, {rot_dim}]")
+        index = out.get_device()
+    else:
+        device = torch.device("cuda" if device is None else device)
+        if device.type != "cuda":
+            _bad("device must be a CUDA device")
+        index = torch._C._cuda_getDevice() if device.index is None else device.index
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return rotary_table(positions, rot_dim, base, scaling, factor, original, low, high, magnitude, out, index, stream)
+    ptr, current = _call_stream(index, stream)
+    if out is None:
+        if positions < 0 or rot_dim < 0:
+            _bad("positions and rot_dim must not be negative")
+        out = _empty((positions, rot_dim), torch.float32, index, ptr, current)
+    spec = FaRotaryScaling(ROTARY_SCALING[scaling], factor, original, low, high, magnitude)
+    rc = fa_rotary_table(out.data_ptr(), positions, rot_dim, base, spec, ptr)
+    if rc != FA_OK:
+        raise FaError(rc, "fa_rotary_table")
+    return out
+
+
+def _rotary_rows(name, t, tokens, dims):
+    """(heads, stride from token to token) of a bf16 tensor whose `dims` leading dimensions are tokens."""
+    import torch
+
+    if t.dtype is not torch.bfloat16 or t.dim() != dims + 1 or t.shape[:-2] != tokens:
+        _bad(f"{name} must be a bf16 tensor {list(tokens)} x heads x d")
+    st, shape = t.stride(), t.shape
+    heads, d = shape[-2], shape[-1]
+    row = heads * d
+    if t.numel() == 0:
+        return heads, row
+    if (st[-1] != 1 and d > 1) or (st[-2] != d and heads > 1):
+        _bad(f"{name}: a token's heads must be contiguous")
+    if dims == 2:
+        return heads, st[0] if shape[0] > 1 else row
+    if shape[0] > 1 and shape[1] > 1 and st[0] != shape[1] * st[1]:
+        _bad(f"{name}: the step from sequence to sequence must be that of seqlen tokens")
+    return heads, st[1] if shape[1] > 1 else st[0] if shape[0] > 1 else row
+
+
+def _rotary(q, k, cos_sin, positions, cu_seqlens, interleaved, q_out, k_out, stream, backward):
+    import torch
+
+    ref = q if q is not None else k
+    if ref is None:
+        _bad("neither q nor k")
+    index = ref.get_device()
+    if index < 0:
+        _bad("q and k must be CUDA tensors")
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return _rotary(q, k, cos_sin, positions, cu_seqlens, interleaved, q_out, k_out, stream, backward)
+    dims = ref.dim() - 1
+    if dims not in (2, 3):
+        _bad("q and k must be [total, heads, d] or [batch, seqlen, heads, d]")
+    tokens, d = ref.shape[:-2], ref.shape[-1]
+    total = 1
+    for n in tokens:
+        total *= n
+    if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        _bad("cos_sin must be a contiguous 2-D fp32 tensor")
+    pos = cu = None
+    batch = seqlen = 0
+    if positions is not None:
+        if cu_seqlens is not None:
+            _bad("positions and cu_seqlens exclude each other")
+        if positions.dtype is not torch.int32 or positions.shape != tokens or not positions.is_contiguous():
+            _bad(f"positions must be a contiguous int32 tensor {list(tokens)}")
+        pos = positions.data_ptr()
+    elif cu_seqlens is not None:
+        if dims != 2 or cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or \
+                not cu_seqlens.is_contiguous():
+            _bad("cu_seqlens must be a contiguous int32 tensor of batch + 1 offsets into [total, heads, d]")
+        batch, cu = cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
+    elif dims == 3:
+        seqlen = max(tokens[1], 1)
+    else:
+        seqlen = max(total, 1)  # one sequence
+    ptr, current = _call_stream(index, stream)
+    got, args = [], []
+    for name, x, out in (("q", q, q_out), ("k", k, k_out)):
+        if x is None:
+            if out is not None:
+                _bad(f"{name}_out without {name}")
+            got.append(None)
+            args.append((None, None, 0, 0, 0))
+            continue
+        heads, stride = _rotary_rows(name, x, tokens, dims)
+        if x.shape[-1] != d:
+            _bad("q and k must have the same d")
+        if out is None:
+            out = _empty(x.shape, torch.bfloat16, index, ptr, current)
+        if out.shape != x.shape:
+            _bad(f"{name}_out must have {name}'s shape")
+        _, out_stride = _rotary_rows(name + "_out", out, tokens, dims)
+        got.append(out)
+        args.append((x.data_ptr(), out.data_ptr(), stride, out_stride, heads))
+    (qp, qo, qs, qos, hq), (kp, ko, ks, kos, hk) = args
+    rc = load_library().fa_rotary(qp, kp, qo, ko, qs, ks, qos, kos, pos, cu, batch, seqlen, total, hq, hk, d,
+                                  cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0,
+                                  backward, ptr)
+    if rc != FA_OK:
+        raise FaError(rc, "fa_rotary")
+    return tuple(got)
+
+
+def rotary(q, k, cos_sin, positions=None, cu_seqlens=None, interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """(q, k) rotated by their positions (``fa_rotary`` of include/fa.h); either may be None.
+
+    bf16 CUDA tensors [total,H,d] or [B,S,H,d] whose tokens may lie apart (views of one projection's output); cos_sin fp32
+    [max_positions, rot_dim] as ``rotary_table`` makes it.  Positions: ``positions`` int32 of the tokens' shape, or the
+    index in the sequence that ``cu_seqlens`` int32 [B+1] gives (rows of no sequence are left as they are), or without both
+    the index in the sequence [B,S] (in the whole of [total]).  ``q_out`` and ``k_out`` (allocated when not given) may be q
+    and k.  Positions outside the table are detected on the device and reported by ``fa_device_status``."""
+    return _rotary(q, k, cos_sin, positions, cu_seqlens, interleaved, q_out, k_out, stream, 0)
+
+
+def rotary_backward(dq, dk, cos_sin, positions=None, cu_seqlens=None, interleaved: bool = False, q_out=None, k_out=None,
+                    stream=None):
+    """The gradients of ``rotary``'s q and k from those of its results: the transposed rotation, arguments alike."""
+    return _rotary(dq, dk, cos_sin, positions, cu_seqlens, interleaved, q_out, k_out, stream, 1)
+
+
+# ---------------------------------------------------------------------------
+# sparse attention over selected pages
+# ---------------------------------------------------------------------------
+
+def fa_kv_bounds(cache: FaKvCache, k_bounds, cu_seqlens, batch, total, stream) -> int:
+    """``fa_kv_bounds`` of include/fa.h; pointer arguments are integers (device addresses)."""
+    return load_library().fa_kv_bounds(ctypes.byref(cache) if cache is not None else None, k_bounds, cu_seqlens, batch,
+                                       total, stream)
+
+
+def fa_kv_select_workspace_size(batch: int, total_q: int, heads_kv: int, max_pages: int) -> int:
+    return load_library().fa_kv_select_workspace_size(batch, total_q, heads_kv, max_pages)
+
+
+def fa_kv_select(q, k_bounds, k_scale, block_table, table_stride, seqlens_k, cu_seqlens_q, batch, total_q, max_seqlen_q,
+                 heads_q, heads_kv, d_qk, num_pages, page_size, max_pages, causal, top, keep_first, keep_last, lists,
+                 list_lens, workspace, workspace_bytes, stream) -> int:
+    """``fa_kv_select`` of include/fa.h; pointer arguments are integers (device addresses)."""
+    return load_library().fa_kv_select(q, k_bounds, k_scale, block_table, table_stride, seqlens_k, cu_seqlens_q, batch,
+                                       total_q, max_seqlen_q, heads_q, heads_kv, d_qk, num_pages, page_size, max_pages,
+                                       int(causal), top, keep_first, keep_last, lists, list_lens, workspace,
+                                       workspace_bytes, stream)
+
+
+def fa_fwd_lists_workspace_size(heads_q: int, heads_kv: int, d_v: int) -> int:
+    return load_library().fa_fwd_lists_workspace_size(heads_q, heads_kv, d_v)
+
+
+def fa_fwd_lists(q, cache: FaKvCache, lists, list_lens, width, o, lse, total_q, heads_q, scale, workspace, workspace_bytes,
+                 stream) -> int:
+    """``fa_fwd_lists`` of include/fa.h; pointer arguments are integers (device addresses)."""
+    return load_library().fa_fwd_lists(q, ctypes.byref(cache) if cache is not None else None, lists, list_lens, width, o,
+                                       lse, total_q, heads_q, float(scale), workspace, workspace_bytes, stream)
+
+
+def _int32(name, t, shape):
+    """Checks a contiguous int32 tensor of a shape (None: any extent)."""
+    import torch
+
+    if t.dtype is not torch.int32 or len(t.shape) != len(shape) or not t.is_contiguous() or \
+            any(n is not None and m != n for m, n in zip(t.shape, shape)):
+        _bad(f"{name} must be a contiguous int32 tensor [{', '.join('*' if n is None else str(n) for n in shape)}]")
+
+
+def _table_rows(block_table, seqlens_k):
+    """(batch, max_pages, row stride) of a block table beside its lengths."""
+    import torch
+
+    td = block_table.shape
+    if block_table.dtype is not torch.int32 or len(td) != 2 or (block_table.stride(1) != 1 and td[1] > 1):
+        _bad("block_table must be a 2-D int32 tensor whose rows are contiguous")
+    _int32("seqlens_k", seqlens_k, (td[0],))
+    return td[0], td[1], block_table.stride(0) if td[0] > 1 else td[1]
+
+
+def _bounds(k_bounds, pages, heads, d):
+    import torch
+
+    if k_bounds.dtype is not torch.float8_e4m3fn or k_bounds.shape != (pages, heads, 2, d) or not k_bounds.is_contiguous():
+        _bad(f"k_bounds must be a contiguous float8_e4m3fn tensor [{pages}, {heads}, 2, {d}]")
+    return k_bounds.data_ptr()
+
+
+def _workspace(workspace, size, index, ptr, current):
+    """(pointer, bytes) of the caller's workspace, or of one of `size` bytes; and what keeps it."""
+    import torch
+
+    if workspace is None:
+        workspace = _empty((size or 16,), torch.uint8, index, ptr, current)
+    elif not workspace.is_contiguous():
+        _bad("workspace must be contiguous")
+    else:
+        size = workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), size, workspace
+
+
+def kv_bounds(k_cache, k_bounds, block_table, seqlens_k, cu_seqlens, total: int, stream=None):
+    """Update the bounds of the pages that hold a step's new tokens (``fa_kv_bounds`` of include/fa.h), after ``kv_append``.
+
+    k_bounds float8_e4m3fn [num_pages,Hkv,2,dqk] (largest and smallest code of each channel) is written in place and
+    returned; the other tensors as for ``kv_append``, cu_seqlens int32 [B+1] of the ``total`` new tokens."""
+    import torch
+
+    index = k_cache.get_device()
+    if index < 0 or k_cache.dtype is not torch.float8_e4m3fn or k_cache.dim() != 4:
+        _bad("k_cache must be a 4-D float8_e4m3fn CUDA tensor")
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return kv_bounds(k_cache, k_bounds, block_table, seqlens_k, cu_seqlens, total, stream)
+    pages, heads, page, d = k_cache.shape
+    batch, width, ts = _table_rows(block_table, seqlens_k)
+    _int32("cu_seqlens", cu_seqlens, (batch + 1,))
+    ks = k_cache.stride()
+    if ks[3] != 1 and d > 1:
+        _bad("the codes of a token must be contiguous")
+    bounds = _bounds(k_bounds, pages, heads, d)
+    ptr, _ = _call_stream(index, stream)
+    cache = _KV_CACHE.pack(k_cache.data_ptr(), 0, 0, 0, block_table.data_ptr(), seqlens_k.data_ptr(), ks[0], ks[1], ks[2],
+                           0, 0, 0, ts, pages, page, heads, d, 0, width)
+    rc = load_library().fa_kv_bounds(cache, bounds, cu_seqlens.data_ptr(), batch, total, ptr)
+    if rc != FA_OK:
+        raise FaError(rc, "fa_kv_bounds")
+    return k_bounds
+
+
+def kv_select(q, k_bounds, k_scale, block_table, seqlens_k, cu_seqlens_q, max_seqlen_q: int, page_size: int, top: int,
+              causal: bool = True, keep_first: int = 0, keep_last: int = 1, lists=None, list_lens=None, workspace=None,
+              stream=None):
+    """The ``top`` pages that each new token and key/value head attends to (``fa_kv_select`` of include/fa.h).
+
+    q [total_q,Hq,dqk] bf16 (packed by cu_seqlens_q int32 [B+1], at most ``max_seqlen_q`` tokens a sequence), k_bounds as
+    ``kv_bounds`` keeps it, k_scale float8_e8m0fnu [num_pages,Hkv], block_table and seqlens_k as for
+    ``attention_forward_paged``.  The first ``keep_first`` and the last ``keep_last`` (1 at least) pages that a token sees
+    are always taken, the others by the sum over the query heads of the largest score that a key within the bounds can
+    have.  Returns (lists int32 [total_q,Hkv,top], list_lens int32 [total_q]) for ``attention_forward_lists``, allocated
+    when not given, as is the workspace (uint8), which grows with total_q * Hkv * the width of block_table."""
+    import torch
+
+    index = q.get_device()
+    qd = q.shape
+    if index < 0 or q.dtype is not torch.bfloat16 or len(qd) != 3 or not q.is_contiguous():
+        _bad("q must be a contiguous 3-D bf16 CUDA tensor")
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return kv_select(q, k_bounds, k_scale, block_table, seqlens_k, cu_seqlens_q, max_seqlen_q, page_size, top,
+                             causal, keep_first, keep_last, lists, list_lens, workspace, stream)
+    total_q, heads_q, d = qd
+    if k_scale.dtype is not torch.float8_e8m0fnu or k_scale.dim() != 2 or not k_scale.is_contiguous():
+        _bad("k_scale must be a contiguous float8_e8m0fnu tensor [num_pages, heads_kv]")
+    pages, heads = k_scale.shape
+    bounds = _bounds(k_bounds, pages, heads, d)
+    batch, width, ts = _table_rows(block_table, seqlens_k)
+    _int32("cu_seqlens_q", cu_seqlens_q, (batch + 1,))
+    if top < 0:
+        _bad("top must not be negative")
+    ptr, current = _call_stream(index, stream)
+    if lists is None:
+        lists = _empty((total_q, heads, top), torch.int32, index, ptr, current)
+    else:
+        _int32("lists", lists, (total_q, heads, top))
+    if list_lens is None:
+        list_lens = _empty((total_q,), torch.int32, index, ptr, current)
+    else:
+        _int32("list_lens", list_lens, (total_q,))
+    size = load_library().fa_kv_select_workspace_size(batch, total_q, heads, width) if workspace is None else 0
+    ws, size, workspace = _workspace(workspace, size, index, ptr, current)
+    rc = load_library().fa_kv_select(q.data_ptr(), bounds, k_scale.data_ptr(), block_table.data_ptr(), ts,
+                                     seqlens_k.data_ptr(), cu_seqlens_q.data_ptr(), batch, total_q, max_seqlen_q, heads_q,
+                                     heads, d, pages, page_size, width, 1 if causal else 0, top, keep_first, keep_last,
+                                     lists.data_ptr(), list_lens.data_ptr(), ws, size, ptr)
+    if rc != FA_OK:
+        raise FaError(rc, "fa_kv_select")
+    return lists, list_lens
+
+
+def _pool(k_cache, v_cache, k_scale, v_scale, index, table, seqlens, width, table_stride):
+    """(fa_kv_cache as bytes, num_pages, heads_kv, page_size, d_qk, d_v) of the cache's tensors, which are checked."""
+    import torch
+
+    f8, e8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+    kd, vd = k_cache.shape, v_cache.shape
+    if len(kd) != 4 or len(vd) != 4 or kd[:3] != vd[:3] or k_cache.dtype is not f8 or v_cache.dtype is not f8:
+        _bad("k_cache and v_cache must be float8_e4m3fn [num_pages, heads_kv, page_size, d]")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t.dtype is not e8 or t.shape != kd[:2] or not t.is_contiguous():
+            _bad(f"{name} must be a contiguous float8_e8m0fnu tensor [num_pages, heads_kv]")
+    ks, vs = k_cache.stride(), v_cache.stride()
+    if (ks[3] != 1 and kd[3] > 1) or (vs[3] != 1 and vd[3] > 1):
+        _bad("the codes of a token must be contiguous")
+    packed = _KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), table, seqlens,
+                            ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], table_stride, kd[0], kd[2], kd[1], kd[3], vd[3], width)
+    return packed, kd[0], kd[1], kd[2], kd[3], vd[3]
+
+
+def attention_forward_lists(q, k_cache, v_cache, k_scale, v_scale, lists, list_lens, scale: float | None = None, out=None,
+                            lse=None, return_lse: bool = True, workspace=None, stream=None):
+    """O (and LSE) of tokens over lists of a paged 8-bit cache's pages (``fa_fwd_lists`` of include/fa.h).
+
+    q [total_q,Hq,dqk] bf16; lists int32 [total_q,Hkv,width] and list_lens int32 [total_q] from ``kv_select`` or made by
+    the caller: token t and key/value head h see the first list_lens[t] tokens of the pages lists[t,h].  Allocates ``out``
+    [total_q,Hq,dv] bf16, ``lse`` [Hq,total_q] fp32 and the workspace (uint8) when not given.  Lengths and pages out of
+    range are detected on the device and reported by ``fa_device_status``."""
+    import torch
+
+    index = q.get_device()
+    qd = q.shape
+    if index < 0 or q.dtype is not torch.bfloat16 or len(qd) != 3 or not q.is_contiguous():
+        _bad("q must be a contiguous 3-D bf16 CUDA tensor")
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return attention_forward_lists(q, k_cache, v_cache, k_scale, v_scale, lists, list_lens, scale, out, lse,
+                                           return_lse, workspace, stream)
+    total_q, heads_q, d = qd
+    _int32("lists", lists, (total_q, None, None))
+    _int32("list_lens", list_lens, (total_q,))
+    width = lists.shape[2]
+    cache, _, heads, _, d_qk, d_v = _pool(k_cache, v_cache, k_scale, v_scale, index, lists.data_ptr(), list_lens.data_ptr(),
+                                          width, width)
+    if d != d_qk or lists.shape[1] != heads:
+        _bad(f"q must be [total_q, heads_q, {d_qk}] and lists [total_q, {heads}, width]")
+    ptr, current = _call_stream(index, stream)
+    if out is None:
+        out = _empty((total_q, heads_q, d_v), torch.bfloat16, index, ptr, current)
+    elif out.dtype is not torch.bfloat16 or out.shape != (total_q, heads_q, d_v) or not out.is_contiguous():
+        _bad(f"out must be a contiguous bf16 tensor [total_q, heads_q, {d_v}]")
+    if lse is None:
+        if return_lse:
+            lse = _empty((heads_q, total_q), torch.float32, index, ptr, current)
+    elif lse.dtype is not torch.float32 or lse.shape != (heads_q, total_q) or not lse.is_contiguous():
+        _bad("lse must be a contiguous fp32 tensor [heads_q, total_q]")
+    size = load_library().fa_fwd_lists_workspace_size(heads_q, heads, d_v) if workspace is None else 0
+    ws, size, workspace = _workspace(workspace, size, index, ptr, current)
+    rc = load_library().fa_fwd_lists(q.data_ptr(), cache, lists.data_ptr(), list_lens.data_ptr(), width, out.data_ptr(),
+                                     lse.data_ptr() if lse is not None else None, total_q, heads_q,
+                                     0.0 if scale is None else scale, ws, size, ptr)
+    if rc != FA_OK:
+        raise FaError(rc, "fa_fwd_lists")
+    return (out, lse) if return_lse else out
+
+
+# ---------------------------------------------------------------------------
+# the cache's pages among the rows of a block table
+# ---------------------------------------------------------------------------
+
+def fa_kv_pages_workspace_size(batch: int, rows: int, num_pages: int) -> int:
+    return load_library().fa_kv_pages_workspace_size(batch, rows, num_pages)
+
+
+def fa_kv_fork(cache: FaKvCache, k_bounds, page_refs, batch, parents, new_tokens, rows, table_out, table_out_stride,
+               seqlens_out, refs_out, workspace, workspace_bytes, stream) -> int:
+    """``fa_kv_fork`` of include/fa.h; pointer arguments are integers (device addresses)."""
+    return load_library().fa_kv_fork(ctypes.byref(cache) if cache is not None else None, k_bounds, page_refs, batch,
+                                     parents, new_tokens, rows, table_out, table_out_stride, seqlens_out, refs_out,
+                                     workspace, workspace_bytes, stream)
+
+
+def fa_kv_compact(cache: FaKvCache, k_bounds, page_refs, batch, table_out, table_out_stride, refs_out, page_map, used,
+                  workspace, workspace_bytes, stream) -> int:
+    """``fa_kv_compact`` of include/fa.h; pointer arguments are integers (device addresses)."""
+    return load_library().fa_kv_compact(ctypes.byref(cache) if cache is not None else None, k_bounds, page_refs, batch,
+                                        table_out, table_out_stride, refs_out, page_map, used, workspace, workspace_bytes,
+                                        stream)
+
+
+def _table_out(table_out, rows, width, index, ptr, current):
+    """(tensor, row stride) of the table that is written."""
+    import torch
+
+    if table_out is None:
+        table_out = _empty((rows, width), torch.int32, index, ptr, current)
+    elif table_out.dtype is not torch.int32 or table_out.shape != (rows, width) or (table_out.stride(1) != 1 and width > 1):
+        _bad(f"table_out must be an int32 tensor [{rows}, {width}] whose rows are contiguous")
+    return table_out, table_out.stride(0) if rows > 1 else width
+
+
+def _int32_out(name, t, n, index, ptr, current):
+    import torch
+
+    if t is None:
+        return _empty((n,), torch.int32, index, ptr, current)
+    _int32(name, t, (n,))
+    return t
+
+
+def kv_fork(parents, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, page_refs, new_tokens=None, k_bounds=None,
+            table_out=None, seqlens_out=None, refs_out=None, workspace=None, stream=None):
+    """Rows of a block table taken over by others, with pages for new tokens (``fa_kv_fork`` of include/fa.h).
+
+    Row r of the result takes over row parents[r] (int32 [rows]; -1: it starts empty) and gets room for new_tokens[r]
+    (int32 [rows]) more tokens: beams that fork, requests that end (no row names them) or begin, sequences that grow.
+    Full pages are shared, page_refs (int32 [num_pages]) counts their uses; a last page that is not full stays with the
+    first heir, others get a copy.  Returns (table_out int32 [rows,max_pages], seqlens_out int32 [rows], refs_out int32
+    [num_pages]), allocated when not given; refs_out may be page_refs.  The cache (and ``k_bounds``, if given) changes in
+    new pages only.  Rows out of range and rows that find no free pages become empty, which ``fa_device_status`` reports."""
+    import torch
+
+    index = k_cache.get_device()
+    if index < 0:
+        _bad("k_cache must be a CUDA tensor")
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return kv_fork(parents, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, page_refs, new_tokens,
+                           k_bounds, table_out, seqlens_out, refs_out, workspace, stream)
+    batch, width, ts = _table_rows(block_table, seqlens_k)
+    cache, pages, heads, _, d_qk, _ = _pool(k_cache, v_cache, k_scale, v_scale, index, block_table.data_ptr(),
+                                            seqlens_k.data_ptr(), width, ts)
+    rows = parents.shape[0] if parents.dim() == 1 else -1
+    _int32("parents", parents, (None,))
+    _int32("page_refs", page_refs, (pages,))
+    if new_tokens is not None:
+        _int32("new_tokens", new_tokens, (rows,))
+    bounds = _bounds(k_bounds, pages, heads, d_qk) if k_bounds is not None else None
+    ptr, current = _call_stream(index, stream)
+    table_out, out_stride = _table_out(table_out, rows, width, index, ptr, current)
+    seqlens_out = _int32_out("seqlens_out", seqlens_out, rows, index, ptr, current)
+    refs_out = _int32_out("refs_out", refs_out, pages, index, ptr, current)
+    size = load_library().fa_kv_pages_workspace_size(batch, rows, pages) if workspace is None else 0
+    ws, size, workspace = _workspace(workspace, size, index, ptr, current)
+    rc = load_library().fa_kv_fork(cache, bounds, page_refs.data_ptr(), batch, parents.data_ptr(),
+                                   new_tokens.data_ptr() if new_tokens is not None else None, rows, table_out.data_ptr(),
+                                   out_stride, seqlens_out.data_ptr(), refs_out.data_ptr(), ws, size, ptr)
+    if rc != FA_OK:
+        raise FaError(rc, "fa_kv_fork")
+    return table_out, seqlens_out, refs_out
+
+
+def kv_compact(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, page_refs, k_bounds=None, table_out=None,
+               refs_out=None, page_map=None, used=None, workspace=None, stream=None):
+    """Move the cache's pages in use to its lowest indices (``fa_kv_compact`` of include/fa.h).
+
+    Returns (table_out, refs_out, page_map int32 [num_pages]: each page's new index, -1 for a free one, used int32 [1]),
+    allocated when not given; table_out may be block_table and refs_out page_refs."""
+    import torch
+
+    index = k_cache.get_device()
+    if index < 0:
+        _bad("k_cache must be a CUDA tensor")
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return kv_compact(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, page_refs, k_bounds, table_out,
+                              refs_out, page_map, used, workspace, stream)
+    batch, width, ts = _table_rows(block_table, seqlens_k)
+    cache, pages, heads, _, d_qk, _ = _pool(k_cache, v_cache, k_scale, v_scale, index, block_table.data_ptr(),
+                                            seqlens_k.data_ptr(), width, ts)
+    _int32("page_refs", page_refs, (pages,))
+    bounds = _bounds(k_bounds, pages, heads, d_qk) if k_bounds is not None else None
+    ptr, current = _call_stream(index, stream)
+    table_out, out_stride = _table_out(table_out, batch, width, index, ptr, current)
+    refs_out = _int32_out("refs_out", refs_out, pages, index, ptr, current)
+    page_map = _int32_out("page_map", page_map, pages, index, ptr, current)
+    used = _int32_out("used", used, 1, index, ptr, current)
+    size = load_library().fa_kv_pages_workspace_size(batch, 0, pages) if workspace is None else 0
+    ws, size, workspace = _workspace(workspace, size, index, ptr, current)
+    rc = load_library().fa_kv_compact(cache, bounds, page_refs.data_ptr(), batch, table_out.data_ptr(), out_stride,
+                                      refs_out.data_ptr(), page_map.data_ptr(), used.data_ptr(), ws, size, ptr)
+    if rc != FA_OK:
+        raise FaError(rc, "fa_kv_compact")
+    return table_out, refs_out, page_map, used

@@ -22,7 +22,8 @@ LIB = os.path.join(OUT_DIR, "libfa_gb300.so")
 SOURCES = ["fa_api.cu", "fa_inst_d64.cu", "fa_inst_d128.cu", "fa_inst_d192.cu", "fa_bwd.cu", "fa_dbg_trace.cu",
            "fa_dbg_check_a.cu", "fa_dbg_check_b.cu", "fa_var_stagger.cu", "fa_bwd_trace.cu",
            "fa_bwd_varlen.cu", "fa_paged_api.cu", "fa_paged_append.cu", "fa_paged_unpack.cu", "fa_paged_d64.cu",
-           "fa_paged_d128.cu", "fa_paged_d192.cu"]
+           "fa_paged_d128.cu", "fa_paged_d192.cu", "fa_lists_d64.cu", "fa_lists_d128.cu", "fa_lists_d192.cu", "fa_rotary.cu",
+           "fa_select.cu", "fa_pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

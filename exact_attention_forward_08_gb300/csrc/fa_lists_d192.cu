@@ -1,0 +1,11 @@
+// attention over lists of pages, d_qk = 192
+#include "fa_paged_launch.cuh"
+
+namespace fa {
+
+int lists_launch_d192(const PagedParams& p, int d_v, int grid, cudaStream_t stream) {
+  if (d_v == 64) return paged_launch_lists<192, 64>(p, grid, stream);
+  return paged_launch_lists<192, 128>(p, grid, stream);
+}
+
+}  // namespace fa

@@ -14,6 +14,8 @@ constexpr unsigned int kSitePagedSeq = 511;   // a sequence's offsets, length or
 constexpr unsigned int kSitePagedPage = 512;  // a block-table entry out of range (index: sequence)
 constexpr unsigned int kSitePagedWait = 520;  // a bounded wait of paged_tc_kernel expired
 constexpr unsigned int kSitePagedTotal = 513; // the lengths sum to more than total_k (index: 0)
+constexpr unsigned int kSiteRotaryPosition = 514;  // a position outside the rotation table (index: token)
+constexpr unsigned int kSitePagedFull = 515;  // too few free pages (index: the first row without)
 
 // the smallest scale that the append writes: 2^-63
 constexpr int kMinScale = 64;

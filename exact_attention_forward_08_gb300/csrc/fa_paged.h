@@ -58,6 +58,11 @@ int paged_launch_d128(const PagedParams& p, const PagedParts* parts, const fa_kv
 int paged_launch_d192(const PagedParams& p, const PagedParts* parts, const fa_kv_cache& c, PagedSplit split, int grid,
                       cudaStream_t stream);
 
+// fa_lists_d{64,128,192}.cu: attention over lists of pages and the merge
+int lists_launch_d64(const PagedParams& p, int grid, cudaStream_t stream);
+int lists_launch_d128(const PagedParams& p, int d_v, int grid, cudaStream_t stream);
+int lists_launch_d192(const PagedParams& p, int d_v, int grid, cudaStream_t stream);
+
 // fa_paged_unpack.cu: the codes of the long sequences as bf16 rows, packed, and their offsets
 struct UnpackParams {
   const uint8_t* src[2];

@@ -9,56 +9,13 @@
 #include "fa_host.h"
 #include "fa_paged.h"
 #include "fa_paged_attn.cuh"
+#include "fa_paged_check.h"
+
+using namespace fa;
 
 namespace {
 
-constexpr int kMaxBatch = 16384;
-
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-bool dims_supported(int d_qk, int d_v) {
-  return (d_qk == 64 && d_v == 64) || ((d_qk == 128 || d_qk == 192) && (d_v == 64 || d_v == 128));
-}
-
-// strides in bytes {page, head, token} of a cache of rows of d codes
-bool strides_ok(const int64_t* s, int pages, int heads, int d) {
-  const int64_t most = int64_t(1) << 40;
-  for (int i = 0; i < 3; ++i)
-    if (s[i] < 0 || s[i] % 16 != 0 || s[i] >= most) return false;
-  if (s[2] < d || s[2] >= int64_t(1) << 24) return false;  // offsets inside a page are counted in 32 bits
-  return (heads == 1 || s[1] >= d) && (pages == 1 || s[0] >= d);
-}
-
-int check_cache(const fa_kv_cache* c) {
-  if (c == nullptr) return FA_ERR_INVALID_ARG;
-  if (c->heads_kv < 1 || c->num_pages < 1 || c->max_pages < 1 || c->table_stride < c->max_pages) return FA_ERR_INVALID_ARG;
-  if (!dims_supported(c->d_qk, c->d_v)) return FA_ERR_UNSUPPORTED;
-  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) return FA_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(c->max_pages) * c->page_size > (int64_t(1) << 30)) return FA_ERR_INVALID_ARG;
-  if (!strides_ok(c->k_stride, c->num_pages, c->heads_kv, c->d_qk) ||
-      !strides_ok(c->v_stride, c->num_pages, c->heads_kv, c->d_v))
-    return FA_ERR_INVALID_ARG;
-  return FA_OK;
-}
-
-int check_cache_pointers(const fa_kv_cache* c) {
-  if (c->k == nullptr || c->v == nullptr || c->k_scale == nullptr || c->v_scale == nullptr ||
-      c->block_table == nullptr || c->seqlens_k == nullptr)
-    return FA_ERR_INVALID_ARG;
-  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->block_table, 4) || !aligned(c->seqlens_k, 4))
-    return FA_ERR_INVALID_ARG;
-  return FA_OK;
-}
-
-bool cache_on_device(const fa_kv_cache* c, int dev) {
-  return fa::host_is_device_ptr(c->k, dev) && fa::host_is_device_ptr(c->v, dev) &&
-         fa::host_is_device_ptr(c->k_scale, dev) && fa::host_is_device_ptr(c->v_scale, dev) &&
-         fa::host_is_device_ptr(c->block_table, dev) && fa::host_is_device_ptr(c->seqlens_k, dev);
-}
-
-int page_shift(int page_size) { return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7; }
-
-size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+constexpr int64_t kMaxListTokens = int64_t(1) << 20;  // each block of the attention over lists looks at all lengths
 
 // Rows of the unpacked keys.  At least one: without any the variable-length
 // forward takes all queries for rows without a key, those of no sequence too.
@@ -103,6 +60,53 @@ Workspace workspace_of(int batch, int heads_q, int heads_kv, int64_t total_q, in
     at += up256(w.varlen_bytes);
   }
   w.bytes = at;
+  return w;
+}
+
+// What the kernels on pages take of the cache and the call alike.
+void fill_params(fa::PagedParams& p, const fa_kv_cache& c, const void* q, void* o, float* lse, int64_t total_q,
+                 int heads_q, float scale, unsigned int* status) {
+  std::memset(&p, 0, sizeof(p));
+  p.k = static_cast<const uint8_t*>(c.k);
+  p.v = static_cast<const uint8_t*>(c.v);
+  p.k_page = c.k_stride[0];
+  p.k_head = c.k_stride[1];
+  p.k_token = static_cast<uint32_t>(c.k_stride[2]);
+  p.v_page = c.v_stride[0];
+  p.v_head = c.v_stride[1];
+  p.v_token = static_cast<uint32_t>(c.v_stride[2]);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.k_scale = c.k_scale;
+  p.v_scale = c.v_scale;
+  p.status = status;
+  p.total_q = total_q;
+  p.heads_q = heads_q;
+  p.num_pages = c.num_pages;
+  p.page_shift = page_shift(c.page_size);
+  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+}
+
+// Groups of a key head's query heads whose rows fit a tile of 16.
+int list_groups(int ratio) {
+  int groups = (ratio + 15) / 16;
+  while (ratio % groups != 0) ++groups;
+  return groups;
+}
+
+// The workspace of attention over lists: parts, references and sums, joins.
+struct ListsWorkspace {
+  size_t part_o, part_ml, joins, bytes;
+};
+ListsWorkspace lists_workspace(int rows, int d_v) {
+  ListsWorkspace w;
+  const size_t pieces = static_cast<size_t>(fa::kPagedMaxBlocks) * fa::kPagedMaxTeams;
+  const size_t part_rows = fa::paged_few_rows(rows);
+  w.part_o = 0;
+  w.part_ml = w.part_o + up256(2 * pieces * part_rows * d_v * sizeof(float));
+  w.joins = w.part_ml + up256(2 * pieces * part_rows * sizeof(float2));
+  w.bytes = w.joins + up256(pieces * sizeof(fa::PagedJoin));
   return w;
 }
 
@@ -235,38 +239,19 @@ int fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse, c
   }
 
   fa::PagedParams p;
-  std::memset(&p, 0, sizeof(p));
-  p.k = static_cast<const uint8_t*>(c.k);
-  p.v = static_cast<const uint8_t*>(c.v);
-  p.k_page = c.k_stride[0];
-  p.k_head = c.k_stride[1];
-  p.k_token = static_cast<uint32_t>(c.k_stride[2]);
-  p.v_page = c.v_stride[0];
-  p.v_head = c.v_stride[1];
-  p.v_token = static_cast<uint32_t>(c.v_stride[2]);
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.o = static_cast<__nv_bfloat16*>(o);
-  p.lse = lse;
-  p.k_scale = c.k_scale;
-  p.v_scale = c.v_scale;
+  fill_params(p, c, q, o, lse, total_q, heads_q, scale, host.status);
   p.table = c.block_table;
   p.table_stride = c.table_stride;
   p.seqlens = c.seqlens_k;
   p.cu = cu_seqlens_q;
-  p.status = host.status;
-  p.total_q = total_q;
   p.batch = batch;
-  p.heads_q = heads_q;
   p.heads_kv = c.heads_kv;
   p.ratio = ratio;
-  p.num_pages = c.num_pages;
   p.max_pages = c.max_pages;
-  p.page_shift = page_shift(c.page_size);
   p.causal = causal ? 1 : 0;
   p.timeout_ns = 1000000000ull;
   p.max_n = max_seqlen_q;
   p.unpacked = unpack ? 1 : 0;
-  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   const int grid = host.sms < fa::kPagedMaxBlocks ? host.sms : fa::kPagedMaxBlocks;
   fa::PagedParts parts[2];
   for (int i = 0; i < 2; ++i) {
@@ -278,6 +263,61 @@ int fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse, c
   if (c.d_qk == 64) return fa::paged_launch_d64(p, parts, c, split, grid, stream);
   if (c.d_qk == 128) return fa::paged_launch_d128(p, parts, c, split, grid, stream);
   return fa::paged_launch_d192(p, parts, c, split, grid, stream);
+}
+
+size_t fa_fwd_lists_workspace_size(int heads_q, int heads_kv, int d_v) {
+  if (heads_q < 1 || heads_kv < 1 || heads_q % heads_kv != 0 || (d_v != 64 && d_v != 128)) return 0;
+  const int ratio = heads_q / heads_kv;
+  return lists_workspace(ratio / list_groups(ratio), d_v).bytes;
+}
+
+int fa_fwd_lists(const void* q, const fa_kv_cache* cache, const int* lists, const int* list_lens, int width, void* o,
+                 float* lse, int64_t total_q, int heads_q, float scale, void* workspace, size_t workspace_bytes,
+                 fa_stream_t stream_) {
+  if (cache == nullptr) return FA_ERR_INVALID_ARG;
+  fa_kv_cache c = *cache;
+  c.block_table = lists;
+  c.seqlens_k = list_lens;
+  c.table_stride = c.max_pages = width;
+  int rc = check_cache(&c);
+  if (rc != FA_OK) return rc;
+  if (total_q < 0 || total_q > kMaxListTokens || heads_q < 1 || heads_q % c.heads_kv != 0) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || scale < 0.f) return FA_ERR_INVALID_ARG;
+  if (total_q == 0) return FA_OK;
+  rc = check_cache_pointers(&c);
+  if (rc != FA_OK) return rc;
+  if (q == nullptr || o == nullptr || workspace == nullptr) return FA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16) || !aligned(workspace, 16)) return FA_ERR_INVALID_ARG;
+  const int ratio = heads_q / c.heads_kv, groups = list_groups(ratio);
+  const ListsWorkspace w = lists_workspace(ratio / groups, c.d_v);
+  if (workspace_bytes < w.bytes) return FA_ERR_INVALID_ARG;
+  if (scale == 0.f) scale = 1.0f / std::sqrt(static_cast<float>(c.d_qk));
+  fa::HostDevice host;
+  rc = fa::host_device(&host);
+  if (rc != FA_OK) return rc;
+  if (!cache_on_device(&c, host.dev) || !fa::host_is_device_ptr(q, host.dev) || !fa::host_is_device_ptr(o, host.dev) ||
+      !fa::host_is_device_ptr(workspace, host.dev) || (lse != nullptr && !fa::host_is_device_ptr(lse, host.dev)))
+    return FA_ERR_INVALID_ARG;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  fa::PagedParams p;
+  fill_params(p, c, q, o, lse, total_q, heads_q, scale, host.status);
+  p.lists = lists;
+  p.seqlens = list_lens;
+  p.lists_heads = c.heads_kv;
+  p.groups = groups;
+  p.batch = static_cast<int>(total_q);
+  p.heads_kv = c.heads_kv * groups;
+  p.ratio = ratio / groups;
+  p.max_pages = width;
+  p.max_n = 1;
+  p.part.o = reinterpret_cast<float*>(ws + w.part_o);
+  p.part.ml = reinterpret_cast<float2*>(ws + w.part_ml);
+  p.part.joins = reinterpret_cast<fa::PagedJoin*>(ws + w.joins);
+  const int grid = host.sms < fa::kPagedMaxBlocks ? host.sms : fa::kPagedMaxBlocks;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (c.d_qk == 64) return fa::lists_launch_d64(p, grid, stream);
+  if (c.d_qk == 128) return fa::lists_launch_d128(p, c.d_v, grid, stream);
+  return fa::lists_launch_d192(p, c.d_v, grid, stream);
 }
 
 }  // extern "C"

@@ -56,6 +56,10 @@ struct PagedParams {
   int64_t table_stride;
   const int* seqlens;
   const int* cu;
+  // lists of pages in place of the table (LISTS): [total_q][lists_heads][max_pages], seqlens the tokens of each list,
+  // a key head's query heads in `groups` groups that count as heads of their own
+  const int* lists;
+  int lists_heads, groups;
   unsigned int* status;
   PagedParts part;
   int64_t total_q;
@@ -192,9 +196,18 @@ struct PagedSeq {
   bool bad;
 };
 
-template <int TILE>
+template <int TILE, bool LISTS = false>
 __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
   PagedSeq s;
+  if constexpr (LISTS) {  // each token by itself
+    s.cu0 = b;
+    s.n = 1;
+    s.len = p.seqlens[b];
+    s.bad = s.len < 0 || s.len > static_cast<int64_t>(p.max_pages) << p.page_shift;
+    s.rows = s.bad ? 0 : p.ratio;
+    s.tiles = s.len > 0 ? (s.len - 1) / TILE + 1 : 1;
+    return s;
+  }
   s.cu0 = p.cu[b];
   s.len = p.seqlens[b];
   s.bad = !paged_attend_range(s.cu0, p.cu[b + 1], s.len, p.total_q, p.max_n,
@@ -213,7 +226,7 @@ struct PagedCursor {
 };
 
 // To the next tile (the caller knows that there is one).
-template <int TILE, int START = 0>
+template <int TILE, int START = 0, bool LISTS = false>
 __device__ __forceinline__ void paged_next(const PagedParams& p, PagedCursor& c) {
   if constexpr (START > 0) ++c.at;
   if (++c.tile < c.s.tiles) return;
@@ -223,7 +236,7 @@ __device__ __forceinline__ void paged_next(const PagedParams& p, PagedCursor& c)
   c.head = 0;
   do {
     if (c.b + 1 >= p.batch) return;
-    c.s = paged_seq<TILE>(p, ++c.b);
+    c.s = paged_seq<TILE, LISTS>(p, ++c.b);
   } while (c.s.rows == 0);
 }
 
@@ -245,7 +258,7 @@ struct PagedLine {
 // By all threads of the block: cuts the line, finds the places where this
 // block's pieces begin, and says that no piece leaves anything to join yet.
 // With START > 0 (one team) also counts the piece's tiles.  Ends with a barrier.
-template <int TILE, int THREADS, int TEAMS, int START>
+template <int TILE, int THREADS, int TEAMS, int START, bool LISTS = false>
 __device__ __forceinline__ void paged_line(const PagedParams& p, long long* scan, long long* warp_sum,
                                            PagedCursor* begin_at, int* tiles, PagedLine& line) {
   static_assert(START == 0 || TEAMS == 1, "tiles are counted for one team");
@@ -257,7 +270,7 @@ __device__ __forceinline__ void paged_line(const PagedParams& p, long long* scan
     const int b = base + tid;
     v = 0;
     if (b < p.batch) {
-      mine = paged_seq<TILE>(p, b);
+      mine = paged_seq<TILE, LISTS>(p, b);
       if (mine.bad && blockIdx.x == 0) paged_error(p.status, kSitePagedSeq, b);
       v = mine.rows > 0 ? (static_cast<long long>(mine.tiles) + START) * p.heads_kv : 0;
     }
@@ -318,7 +331,7 @@ __device__ __forceinline__ void paged_line(const PagedParams& p, long long* scan
         }
         PagedCursor c;
         c.b = base + lo;
-        c.s = paged_seq<TILE>(p, c.b);
+        c.s = paged_seq<TILE, LISTS>(p, c.b);
         const long long in = x - (lo > 0 ? scan[lo - 1] : 0);
         c.head = static_cast<int>(in / c.s.tiles);
         c.tile = static_cast<int>(in - static_cast<long long>(c.head) * c.s.tiles);
@@ -338,7 +351,8 @@ __device__ __forceinline__ void paged_line(const PagedParams& p, long long* scan
 }
 
 // G16: pages of 16 tokens, each with its own scale; else a scale holds for 32 tokens at least.
-template <int DQK, int DV, int NT, bool G16>
+// LISTS: each token and key head has a list of pages of its own.
+template <int DQK, int DV, int NT, bool G16, bool LISTS>
 __global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
     paged_attn_kernel(const __grid_constant__ PagedParams p) {
   using Shape = PagedShape<DQK, DV, NT>;
@@ -363,7 +377,7 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   PagedLine line;
-  paged_line<kTile, kThreads, kTeams, 0>(p, scan, warp_sum, begin_at, nullptr, line);
+  paged_line<kTile, kThreads, kTeams, 0, LISTS>(p, scan, warp_sum, begin_at, nullptr, line);
 
   const int team = warp;
   const int g = lane >> 2, c = lane & 3;
@@ -383,10 +397,13 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
   int page0 = 0, entry = 0, ks_next = 127, vs_next = 127;
   float ks = 1.f, vs = 1.f;
   bool fresh = true;  // the pages' scales are still to be taken over
+  // the key head of a head on the line, and how many there are
+  auto key_head = [&](int head) { return LISTS ? head / p.groups : head; };
+  const int key_heads = LISTS ? p.lists_heads : p.heads_kv;
   auto load_scales = [&](int head) {
     ks_next = vs_next = 127;
     if (((page0 + lane) << p.page_shift) < ahead.s.len) {
-      const int64_t at = static_cast<int64_t>(entry) * p.heads_kv + head;
+      const int64_t at = static_cast<int64_t>(entry) * key_heads + key_head(head);
       ks_next = p.k_scale[at];
       vs_next = p.v_scale[at];
     }
@@ -394,13 +411,16 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
   auto take_scales = [&]() {
     ks = vs_next == 255 ? scale_of(255) : scale_of(ks_next);  // NaN in either: NaN scores
     vs = vs_next == 255 ? 1.f : scale_of(vs_next);
-    if (ahead.head + 1 < p.heads_kv) load_scales(ahead.head + 1);
+    if (!LISTS && ahead.head + 1 < p.heads_kv) load_scales(ahead.head + 1);
   };
   auto load_pages = [&](int first) {
     page0 = first;
     entry = 0;
     if (((first + lane) << p.page_shift) < ahead.s.len) {
-      entry = p.table[ahead.b * p.table_stride + first + lane];
+      if constexpr (LISTS)
+        entry = p.lists[(static_cast<int64_t>(ahead.b) * key_heads + key_head(ahead.head)) * p.max_pages + first + lane];
+      else
+        entry = p.table[ahead.b * p.table_stride + first + lane];
       if (entry < 0 || entry >= p.num_pages) {
         paged_error(p.status, kSitePagedPage, ahead.b);
         entry = 0;
@@ -424,8 +444,8 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
   const uint32_t v_off = lane_offset(DV, p.v_token, 0);
   const uint8_t *k_at, *v_at;  // of the cursor's head
   auto set_head = [&]() {
-    k_at = p.k + ahead.head * p.k_head;
-    v_at = p.v + ahead.head * p.v_head;
+    k_at = p.k + key_head(ahead.head) * p.k_head;
+    v_at = p.v + key_head(ahead.head) * p.v_head;
   };
   auto copy = [&](auto is_k, uint32_t dst, int token) {
     constexpr bool kK = decltype(is_k)::value;
@@ -466,10 +486,10 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
       if (++fill_slot == kSlots) fill_slot = 0;
       if (!is_k && filled < 2 * count) {  // on to the next tile
         const int b = ahead.b, head = ahead.head;
-        paged_next<kTile>(p, ahead);
+        paged_next<kTile, 0, LISTS>(p, ahead);
         if (ahead.head != head) set_head();
         const int next = (ahead.tile * kTile) >> p.page_shift;
-        if (ahead.b == b && ahead.head == head + 1 && page0 == 0) take_scales();  // the same pages, the next head
+        if (!LISTS && ahead.b == b && ahead.head == head + 1 && page0 == 0) take_scales();  // the same pages, the next head
         else if (ahead.b != b || ahead.head != head || next + kTile / 16 > page0 + 32) load_pages(next);
       }
     }
@@ -819,7 +839,7 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
           }
         }
     }
-    if (i + 1 < count) paged_next<kTile>(p, cur);
+    if (i + 1 < count) paged_next<kTile, 0, LISTS>(p, cur);
   }
 }
 

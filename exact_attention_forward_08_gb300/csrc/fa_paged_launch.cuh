@@ -39,14 +39,34 @@ int paged_start(void (*kernel)(P), const P& p, int grid, int threads, int smem, 
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-template <int DQK, int DV, int NT, bool G16>
+template <int DQK, int DV, int NT, bool G16, bool LISTS>
 int paged_few_launch(const PagedParams& p, int grid, cudaStream_t stream) {
   using Shape = PagedShape<DQK, DV, NT>;
   static bool ready[64] = {};
-  auto* kernel = paged_attn_kernel<DQK, DV, NT, G16>;
+  auto* kernel = paged_attn_kernel<DQK, DV, NT, G16, LISTS>;
   const int rc = paged_allow_smem(reinterpret_cast<const void*>(kernel), Shape::kBytes, ready);
   if (rc != FA_OK) return rc;
   return paged_start(kernel, p, grid, Shape::kThreads, Shape::kBytes, false, stream);
+}
+
+// The instantiation for `rows` rows, 16 at most.
+template <int DQK, int DV, bool LISTS>
+int paged_few_start(const PagedParams& p, int rows, int grid, cudaStream_t stream) {
+  if (p.page_shift == 4)
+    return rows <= 8 ? paged_few_launch<DQK, DV, 1, true, LISTS>(p, grid, stream)
+                     : paged_few_launch<DQK, DV, 2, true, LISTS>(p, grid, stream);
+  return rows <= 8 ? paged_few_launch<DQK, DV, 1, false, LISTS>(p, grid, stream)
+                   : paged_few_launch<DQK, DV, 2, false, LISTS>(p, grid, stream);
+}
+
+// Where the merge finds what the kernel for few rows cut.
+template <int DQK, int DV>
+void paged_few_parts(PagedMerge& m, const PagedParts& part, int rows, int grid) {
+  m.set[0].part = part;
+  m.set[0].rows = paged_few_rows(rows);
+  m.set[0].pieces = PagedShape<DQK, DV, 1>::kTeams;
+  m.set[0].shares = m.set[0].rows / 4;
+  m.set[0].blocks = grid * m.set[0].shares;
 }
 
 // Codes viewed as (d, token, head, page); a box is a page of one head, `columns` wide.
@@ -76,6 +96,28 @@ int paged_many_launch(const PagedParams& shared, const fa_kv_cache& c, int rows,
   return paged_start(kernel, p, grid, Shape::kThreads, Shape::kBytes, shared.after != 0, stream);
 }
 
+inline void paged_merge_outputs(PagedMerge& m, const PagedParams& p) {
+  m.o = p.o;
+  m.lse = p.lse;
+  m.total_q = p.total_q;
+  m.heads_q = p.heads_q;
+  m.ratio = p.ratio;
+  m.cu = p.cu;
+  m.batch = p.batch;
+  m.max_n = p.max_n;
+}
+
+// Attention over lists of pages: the kernel for few rows and the merge.
+template <int DQK, int DV>
+int paged_launch_lists(const PagedParams& p, int grid, cudaStream_t stream) {
+  const int rc = paged_few_start<DQK, DV, true>(p, p.ratio, grid, stream);
+  if (rc != FA_OK) return rc;
+  PagedMerge m = {};
+  paged_few_parts<DQK, DV>(m, p.part, p.ratio, grid);
+  paged_merge_outputs(m, p);
+  return paged_start(paged_merge_kernel<DV, 8, false>, m, m.set[0].blocks, 256, 0, true, stream);
+}
+
 // The kernel for few rows, the one for many, and the merge of what both cut: each may begin before the one in front
 // of it has ended, and ends after it.
 template <int DQK, int DV>
@@ -87,19 +129,9 @@ int paged_launch_pages(const PagedParams& shared, const PagedParts* parts, const
     p.part = parts[0];
     p.row_least = 1;
     p.row_limit = split.few;
-    int rc;
-    if (p.page_shift == 4)
-      rc = split.few <= 8 ? paged_few_launch<DQK, DV, 1, true>(p, grid, stream)
-                          : paged_few_launch<DQK, DV, 2, true>(p, grid, stream);
-    else
-      rc = split.few <= 8 ? paged_few_launch<DQK, DV, 1, false>(p, grid, stream)
-                          : paged_few_launch<DQK, DV, 2, false>(p, grid, stream);
+    const int rc = paged_few_start<DQK, DV, false>(p, split.few, grid, stream);
     if (rc != FA_OK) return rc;
-    m.set[0].part = parts[0];
-    m.set[0].rows = paged_few_rows(split.few);
-    m.set[0].pieces = PagedShape<DQK, DV, 1>::kTeams;
-    m.set[0].shares = m.set[0].rows / 4;
-    m.set[0].blocks = grid * m.set[0].shares;
+    paged_few_parts<DQK, DV>(m, parts[0], split.few, grid);
   }
   if (split.many > 0) {
     p.part = parts[1];
@@ -114,14 +146,7 @@ int paged_launch_pages(const PagedParams& shared, const PagedParts* parts, const
     m.set[1].shares = (split.many + 7) / 8;
     m.set[1].blocks = grid * m.set[1].shares;
   }
-  m.o = p.o;
-  m.lse = p.lse;
-  m.total_q = p.total_q;
-  m.heads_q = p.heads_q;
-  m.ratio = p.ratio;
-  m.cu = p.cu;
-  m.batch = p.batch;
-  m.max_n = p.max_n;
+  paged_merge_outputs(m, p);
   const int blocks = m.set[0].blocks + m.set[1].blocks;
   if (p.unpacked) return paged_start(paged_merge_kernel<DV, 4, true>, m, blocks, 256, 0, true, stream);
   if (split.many > 0) return paged_start(paged_merge_kernel<DV, 4, false>, m, blocks, 256, 0, true, stream);

@@ -1,0 +1,582 @@
+// fa_kv_fork and fa_kv_compact: which rows of a block table use which pages of
+// the 8-bit cache, decided on the device.
+//
+// Both are integer work on a few thousand numbers with several steps that each
+// need all of the step before, and after that copies of whole or part pages.
+// The steps run in one cluster of 8 blocks, whose barrier takes less time than a
+// launch; the copies in a second kernel over the whole GPU, which is placed while
+// the first still runs.
+//
+// Every result is determined by the inputs alone: sums by atomics are of
+// integers, a parent's first heir is found as a minimum, pages are numbered by
+// scans in order of rows and of pages.
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstring>
+
+#include "fa.h"
+#include "fa_host.h"
+#include "fa_paged.cuh"
+#include "fa_paged_check.h"
+
+namespace fa {
+namespace {
+
+constexpr int kCluster = 8;       // blocks that decide
+constexpr int kThreads = 1024;    // of each
+constexpr int kAll = kCluster * kThreads;
+constexpr int kCopyBits = 20;     // of a row's packed numbers: copies below, pages needed above
+
+struct PagesHead {
+  long long need;   // pages that all rows need
+  int copies;       // pages to copy
+  int used;         // pages in use (compaction)
+  int used_low;     // those among the first `used`
+  int count[kCluster];
+};
+
+struct PagesParams {
+  const int* table;
+  int64_t table_stride;
+  const int* seqlens;
+  const int* refs;
+  const int* parents;
+  const int* grow;
+  int* table_out;
+  int64_t out_stride;
+  int* seqlens_out;
+  int* refs_out;
+  int* page_map;
+  int* used;
+  unsigned int* status;
+  PagesHead* head;
+  int* heirs;          // [batch], -1: a row that is not valid
+  int* first;          // [batch] the first heir
+  long long* start;    // [rows] pages needed by the rows before
+  int* list;           // [num_pages] free pages in order; compaction: holes
+  int *src, *dst, *tokens;  // copies
+  int batch, rows, num_pages, max_pages, page_shift;
+};
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Inclusive scan over the block's threads; `total` is the sum.  All threads call.
+__device__ __forceinline__ long long block_scan(long long v, long long* warp_sum, long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  __syncthreads();  // the sums of the scan before have been read
+  if (lane == 31) warp_sum[warp] = v;
+  __syncthreads();
+  long long w = warp_sum[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
+  }
+  total = __shfl_sync(0xffffffffu, w, 31);
+  const long long before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+  return v + (warp > 0 ? before : 0);
+}
+
+// The pages that thread `tid` of block `rank` counts: equal runs in order.
+struct PageRun {
+  int64_t begin, end;
+};
+__device__ __forceinline__ PageRun page_run(const PagesParams& p, int rank) {
+  const int64_t per = (p.num_pages + kAll - 1) / kAll;
+  const int64_t begin = (static_cast<int64_t>(rank) * kThreads + threadIdx.x) * per;
+  const int64_t end = begin + per;
+  return {begin < p.num_pages ? begin : p.num_pages, end < p.num_pages ? end : p.num_pages};
+}
+
+// A row of the new table as far as it does not depend on other rows.
+struct ForkRow {
+  int src, len, held, total;  // parent (-1: none), its tokens, its pages, pages of the new row
+  bool bad;
+};
+__device__ __forceinline__ ForkRow fork_row(const PagesParams& p, int r) {
+  ForkRow w = {p.parents[r], 0, 0, 0, false};
+  const int64_t most = static_cast<int64_t>(p.max_pages) << p.page_shift;
+  const int grow = p.grow != nullptr ? p.grow[r] : 0;
+  w.bad = w.src < -1 || w.src >= p.batch || grow < 0;
+  if (!w.bad && w.src >= 0) {
+    w.bad = __ldcg(p.heirs + w.src) < 0;
+    w.len = w.bad ? 0 : p.seqlens[w.src];
+  }
+  w.bad = w.bad || static_cast<int64_t>(w.len) + grow > most;
+  if (w.bad) return {-1, 0, 0, 0, true};
+  const int round = (1 << p.page_shift) - 1;
+  w.held = (w.len + round) >> p.page_shift;
+  w.total = static_cast<int>((static_cast<int64_t>(w.len) + grow + round) >> p.page_shift);
+  return w;
+}
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
+    kv_fork_kernel(const __grid_constant__ PagesParams p) {
+  __shared__ long long warp_sum[32];
+  const int rank = blockIdx.x, tid = rank * kThreads + threadIdx.x;
+  const int lane = threadIdx.x & 31, warp = tid >> 5;
+  const int part_mask = (1 << p.page_shift) - 1;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // ---- counts start from the old ones; a warp looks at an old row's pages ----
+  for (int i = tid; i < p.num_pages; i += kAll) p.refs_out[i] = p.refs[i];
+  for (int b = warp; b < p.batch; b += kAll / 32) {
+    const int len = p.seqlens[b];
+    const bool fits = len >= 0 && len <= static_cast<int64_t>(p.max_pages) << p.page_shift;
+    bool page_bad = false;
+    if (fits) {
+      const int pages = (len + part_mask) >> p.page_shift;
+      const int* row = p.table + b * p.table_stride;
+      for (int j = lane; j < pages; j += 32) page_bad |= row[j] < 0 || row[j] >= p.num_pages;
+    }
+    page_bad = __any_sync(0xffffffffu, page_bad);
+    if (lane == 0) {
+      if (!fits || page_bad) paged_error(p.status, fits ? kSitePagedPage : kSitePagedSeq, b);
+      p.heirs[b] = fits && !page_bad ? 0 : -1;
+      p.first[b] = INT_MAX;
+    }
+  }
+  cluster_sync();
+  for (int r = tid; r < p.rows; r += kAll) {
+    const ForkRow w = fork_row(p, r);
+    if (w.bad) paged_error(p.status, kSitePagedSeq, r);
+    if (w.src >= 0) {
+      atomicAdd(p.heirs + w.src, 1);
+      atomicMin(p.first + w.src, r);
+    }
+  }
+  cluster_sync();
+
+  // ---- block 0 numbers the pages that rows need and the copies; all move the counts of old pages ----
+  if (rank == 0) {
+    long long before = 0;
+    for (int base = 0; base < p.rows; base += kThreads) {
+      const int r = base + threadIdx.x;
+      long long v = 0;
+      if (r < p.rows) {
+        const ForkRow w = fork_row(p, r);
+        const bool copy = w.src >= 0 && (w.len & part_mask) != 0 && __ldcg(p.first + w.src) != r;
+        v = (static_cast<long long>(w.total - w.held + (copy ? 1 : 0)) << kCopyBits) | (copy ? 1 : 0);
+      }
+      long long total;
+      const long long upto = block_scan(v, warp_sum, total);
+      if (r < p.rows) p.start[r] = before + upto - v;
+      before += total;
+    }
+    if (threadIdx.x == 0) {
+      p.head->need = before >> kCopyBits;
+      p.head->copies = static_cast<int>(before & ((1 << kCopyBits) - 1));
+    }
+  }
+  for (int b = warp; b < p.batch; b += kAll / 32) {
+    const int heirs = __ldcg(p.heirs + b);
+    if (heirs < 0) continue;
+    const int len = p.seqlens[b], full = len >> p.page_shift;
+    const int* row = p.table + b * p.table_stride;
+    if (heirs != 1)
+      for (int j = lane; j < full; j += 32) atomicAdd(p.refs_out + row[j], heirs - 1);
+    if (heirs == 0 && (len & part_mask) != 0 && lane == 0) atomicAdd(p.refs_out + row[full], -1);
+  }
+  cluster_sync();
+
+  // ---- the lowest free pages, as many as are needed, in order ----
+  const PageRun run = page_run(p, rank);
+  int mine = 0;
+  for (int64_t i = run.begin; i < run.end; ++i) mine += __ldcg(p.refs_out + i) <= 0;
+  long long total;
+  long long at = block_scan(mine, warp_sum, total) - mine;
+  if (threadIdx.x == 0) p.head->count[rank] = static_cast<int>(total);
+  cluster_sync();
+  long long free_pages = 0;
+#pragma unroll
+  for (int i = 0; i < kCluster; ++i) {
+    const int n = __ldcg(&p.head->count[i]);
+    if (i < rank) at += n;
+    free_pages += n;
+  }
+  const long long need = __ldcg(&p.head->need);
+  for (int64_t i = run.begin; i < run.end && mine > 0 && at < need; ++i)
+    if (__ldcg(p.refs_out + i) <= 0) p.list[at++] = static_cast<int>(i);
+  cluster_sync();
+
+  // ---- a warp writes a row ----
+  for (int r = warp; r < p.rows; r += kAll / 32) {
+    const ForkRow w = fork_row(p, r);
+    const long long packed = __ldcg(p.start + r);
+    const long long start = packed >> kCopyBits;
+    const bool part = (w.len & part_mask) != 0;
+    const bool heir = w.src >= 0 && __ldcg(p.first + w.src) == r;
+    const bool copy = w.src >= 0 && part && !heir;
+    const int kept = w.held - (copy ? 1 : 0);
+    const int fresh = w.total - kept;
+    const bool fails = fresh > 0 && start + fresh > free_pages;
+    const int* row = p.table + (w.src >= 0 ? w.src : 0) * p.table_stride;
+    int* out = p.table_out + r * p.out_stride;
+    if (fails && lane == 0 && start <= free_pages) paged_error(p.status, kSitePagedFull, r);
+    for (int j = lane; j < p.max_pages; j += 32) {
+      int page = -1;
+      if (j < kept) {
+        page = row[j];
+        if (fails) {  // the row stays empty: it gives back what it shares
+          if (j < w.len >> p.page_shift || heir) atomicAdd(p.refs_out + page, -1);
+          page = -1;
+        }
+      } else if (j < w.total && !fails) {
+        page = __ldcg(p.list + start + (j - kept));
+        p.refs_out[page] = 1;
+      }
+      out[j] = page;
+    }
+    if (lane == 0) {
+      p.seqlens_out[r] = fails || w.bad ? 0 : w.len + (p.grow != nullptr ? p.grow[r] : 0);
+      if (copy) {
+        const int c = static_cast<int>(packed & ((1 << kCopyBits) - 1));
+        p.src[c] = fails ? -1 : row[kept];
+        p.dst[c] = fails ? -1 : __ldcg(p.list + start);
+        p.tokens[c] = w.len & part_mask;
+      }
+    }
+  }
+}
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
+    kv_compact_kernel(const __grid_constant__ PagesParams p) {
+  __shared__ long long warp_sum[32];
+  const int rank = blockIdx.x, tid = rank * kThreads + threadIdx.x;
+  const int lane = threadIdx.x & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // ---- pages in use: how many, and before each page ----
+  const PageRun run = page_run(p, rank);
+  int mine = 0;
+  for (int64_t i = run.begin; i < run.end; ++i) mine += p.refs[i] > 0;
+  long long total;
+  long long before = block_scan(mine, warp_sum, total) - mine;
+  if (threadIdx.x == 0) p.head->count[rank] = static_cast<int>(total);
+  cluster_sync();
+  int used = 0;
+#pragma unroll
+  for (int i = 0; i < kCluster; ++i) {
+    const int n = __ldcg(&p.head->count[i]);
+    if (i < rank) before += n;
+    used += n;
+  }
+  // those among the first `used`
+  if (run.begin <= used && used < run.end) {
+    int low = static_cast<int>(before);
+    for (int64_t i = run.begin; i < used; ++i) low += p.refs[i] > 0;
+    p.head->used_low = low;
+  }
+  if (tid == 0) {
+    if (used == p.num_pages) p.head->used_low = used;
+    p.used[0] = used;
+  }
+  cluster_sync();
+  const int low = __ldcg(&p.head->used_low);
+  // ---- pages behind go to the holes before, both in order ----
+  for (int64_t i = run.begin; i < run.end; ++i) {
+    const bool in_use = p.refs[i] > 0;
+    if (i < used) {
+      if (!in_use) p.dst[i - before] = static_cast<int>(i);
+    } else if (in_use) {
+      p.src[before - low] = static_cast<int>(i);
+    }
+    p.page_map[i] = in_use ? static_cast<int>(i) : -1;
+    before += in_use;
+  }
+  cluster_sync();
+  // counts of the pages that stay and of the free ones behind, then of those that move (refs_out may be refs)
+  for (int i = tid; i < p.num_pages; i += kAll)
+    if (i < used) {
+      if (__ldcg(p.page_map + i) >= 0) p.refs_out[i] = p.refs[i];
+    } else if (__ldcg(p.page_map + i) < 0) {
+      p.refs_out[i] = 0;
+    }
+  cluster_sync();
+  const int moves = used - low;
+  for (int i = tid; i < moves; i += kAll) {
+    const int from = __ldcg(p.src + i), to = __ldcg(p.dst + i);
+    const int n = p.refs[from];
+    p.refs_out[to] = n;
+    p.refs_out[from] = 0;
+    p.page_map[from] = to;
+  }
+  if (tid == 0) p.head->copies = moves;
+  cluster_sync();
+
+  // ---- the table follows ----
+  for (int b = warp; b < p.batch; b += kAll / 32) {
+    const int len = p.seqlens[b];
+    const bool fits = len >= 0 && len <= static_cast<int64_t>(p.max_pages) << p.page_shift;
+    const int pages = fits ? static_cast<int>((static_cast<int64_t>(len) + (1 << p.page_shift) - 1) >> p.page_shift) : 0;
+    const int* row = p.table + b * p.table_stride;
+    int* out = p.table_out + b * p.out_stride;
+    if (!fits && lane == 0) paged_error(p.status, kSitePagedSeq, b);
+    for (int j = lane; j < p.max_pages; j += 32) {
+      int page = -1;
+      if (j < pages) {
+        page = row[j];
+        page = page >= 0 && page < p.num_pages ? __ldcg(p.page_map + page) : -1;
+        if (page < 0) paged_error(p.status, kSitePagedPage, b);
+      }
+      out[j] = page;
+    }
+  }
+}
+
+struct CopyParams {
+  uint8_t* base[2];
+  int64_t page_stride[2], head_stride[2];
+  uint32_t token_stride[2];
+  uint8_t* scale[2];
+  uint8_t* bounds;
+  const PagesHead* head;
+  const int *src, *dst, *tokens;  // tokens NULL: whole pages
+  int heads, page, num_pages, d_qk;
+};
+
+constexpr int kCopyWarps = 8;   // of a block
+constexpr int kCopyBlocks = 4;  // of an SM
+constexpr int kCopyAhead = 8;   // 16-byte loads of a lane under way
+
+// The first `tokens` tokens of one head's D codes by a warp, in columns of 128 or 64 bytes.
+template <int D>
+__device__ __forceinline__ void copy_codes(const uint8_t* src, uint8_t* dst, uint32_t ts, int tokens) {
+  constexpr int kChunks = D == 128 ? 8 : 4, kRows = 32 / kChunks;
+  const int lane = threadIdx.x & 31;
+  const uint32_t step = kRows * ts;
+#pragma unroll 1
+  for (int column = 0; column < D; column += kChunks * 16) {
+    uint32_t at = (lane / kChunks) * ts + column + (lane % kChunks) * 16;
+    int row = lane / kChunks;
+#pragma unroll 1
+    for (; row + (kCopyAhead - 1) * kRows < tokens; row += kRows * kCopyAhead) {
+      uint4 v[kCopyAhead];
+#pragma unroll
+      for (int k = 0; k < kCopyAhead; ++k) v[k] = *reinterpret_cast<const uint4*>(src + (at + k * step));
+#pragma unroll
+      for (int k = 0; k < kCopyAhead; ++k) *reinterpret_cast<uint4*>(dst + (at + k * step)) = v[k];
+      at += kCopyAhead * step;
+    }
+#pragma unroll 1
+    for (; row < tokens; row += kRows, at += step)
+      *reinterpret_cast<uint4*>(dst + at) = *reinterpret_cast<const uint4*>(src + at);
+  }
+}
+
+// A warp copies one head's keys or values of a page, with their scale (and the bounds of the keys).
+template <int DQK, int DV>
+__global__ void __launch_bounds__(32 * kCopyWarps, kCopyBlocks) kv_copy_kernel(const __grid_constant__ CopyParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int64_t units = static_cast<int64_t>(p.head->copies) * p.heads * 2;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kCopyWarps;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kCopyWarps + (threadIdx.x >> 5); u < units; u += step) {
+    const int x = static_cast<int>(u & 1);
+    const int64_t copy = (u >> 1) / p.heads;
+    const int head = static_cast<int>((u >> 1) - copy * p.heads);
+    const int from = p.src[copy], to = p.dst[copy];
+    if (from < 0) continue;
+    const int tokens = p.tokens != nullptr ? p.tokens[copy] : p.page;
+    const uint8_t* src = p.base[x] + from * p.page_stride[x] + head * p.head_stride[x];
+    uint8_t* dst = p.base[x] + to * p.page_stride[x] + head * p.head_stride[x];
+    const int64_t from_head = static_cast<int64_t>(from) * p.heads + head, to_head = static_cast<int64_t>(to) * p.heads + head;
+    if (lane == 0) p.scale[x][to_head] = p.scale[x][from_head];
+    if (x == 0 && p.bounds != nullptr && lane < DQK / 8)
+      reinterpret_cast<uint4*>(p.bounds)[to_head * (DQK / 8) + lane] =
+          reinterpret_cast<const uint4*>(p.bounds)[from_head * (DQK / 8) + lane];
+    if (x == 0) copy_codes<DQK>(src, dst, p.token_stride[0], tokens);
+    else copy_codes<DV>(src, dst, p.token_stride[1], tokens);
+  }
+}
+
+struct PagesWorkspace {
+  size_t head, heirs, first, start, list, src, dst, tokens, bytes;
+};
+PagesWorkspace pages_workspace(int batch, int rows, int num_pages) {
+  PagesWorkspace w;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t here = at;
+    at += up256(n);
+    return here;
+  };
+  const size_t copies = static_cast<size_t>(rows > num_pages ? rows : num_pages);
+  w.head = take(sizeof(PagesHead));
+  w.heirs = take(sizeof(int) * batch);
+  w.first = take(sizeof(int) * batch);
+  w.start = take(sizeof(long long) * rows);
+  w.list = take(sizeof(int) * num_pages);
+  w.src = take(sizeof(int) * copies);
+  w.dst = take(sizeof(int) * copies);
+  w.tokens = take(sizeof(int) * rows);
+  w.bytes = at;
+  return w;
+}
+
+void pages_fill(PagesParams& p, uint8_t* ws, int batch, int rows, const fa_kv_cache& c) {
+  const PagesWorkspace w = pages_workspace(batch, rows, c.num_pages);
+  p.head = reinterpret_cast<PagesHead*>(ws + w.head);
+  p.heirs = reinterpret_cast<int*>(ws + w.heirs);
+  p.first = reinterpret_cast<int*>(ws + w.first);
+  p.start = reinterpret_cast<long long*>(ws + w.start);
+  p.list = reinterpret_cast<int*>(ws + w.list);
+  p.src = reinterpret_cast<int*>(ws + w.src);
+  p.dst = reinterpret_cast<int*>(ws + w.dst);
+  p.tokens = reinterpret_cast<int*>(ws + w.tokens);
+  p.table = c.block_table;
+  p.table_stride = c.table_stride;
+  p.seqlens = c.seqlens_k;
+  p.batch = batch;
+  p.rows = rows;
+  p.num_pages = c.num_pages;
+  p.max_pages = c.max_pages;
+  p.page_shift = page_shift(c.page_size);
+}
+
+template <int DQK, int DV>
+int copy_start(const CopyParams& p, int sms, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kCopyBlocks * sms, 1, 1);
+  cfg.blockDim = dim3(32 * kCopyWarps, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_copy_kernel<DQK, DV>, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int copy_launch(const PagesParams& m, const fa_kv_cache& c, uint8_t* bounds, bool whole, int sms, cudaStream_t stream) {
+  CopyParams p;
+  std::memset(&p, 0, sizeof(p));
+  for (int x = 0; x < 2; ++x) {
+    const int64_t* s = x == 0 ? c.k_stride : c.v_stride;
+    p.base[x] = static_cast<uint8_t*>(x == 0 ? c.k : c.v);
+    p.page_stride[x] = s[0];
+    p.head_stride[x] = s[1];
+    p.token_stride[x] = static_cast<uint32_t>(s[2]);
+    p.scale[x] = x == 0 ? c.k_scale : c.v_scale;
+  }
+  p.bounds = bounds;
+  p.head = m.head;
+  p.src = m.src;
+  p.dst = m.dst;
+  p.tokens = whole ? nullptr : m.tokens;
+  p.heads = c.heads_kv;
+  p.page = c.page_size;
+  p.num_pages = c.num_pages;
+  p.d_qk = c.d_qk;
+  if (c.d_qk == 64) return copy_start<64, 64>(p, sms, stream);
+  if (c.d_qk == 128) return c.d_v == 64 ? copy_start<128, 64>(p, sms, stream) : copy_start<128, 128>(p, sms, stream);
+  return c.d_v == 64 ? copy_start<192, 64>(p, sms, stream) : copy_start<192, 128>(p, sms, stream);
+}
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+size_t fa_kv_pages_workspace_size(int batch, int rows, int num_pages) {
+  if (batch < 0 || rows < 0 || num_pages < 1) return 0;
+  return pages_workspace(batch, rows, num_pages).bytes;
+}
+
+int fa_kv_fork(const fa_kv_cache* cache, void* k_bounds, const int* page_refs, int batch, const int* parents,
+               const int* new_tokens, int rows, int* table_out, int64_t table_out_stride, int* seqlens_out,
+               int* refs_out, void* workspace, size_t workspace_bytes, fa_stream_t stream_) {
+  int rc = check_cache(cache);
+  if (rc != FA_OK) return rc;
+  const fa_kv_cache& c = *cache;
+  if (batch < 1 || batch > kMaxBatch || rows < 1 || rows > kMaxBatch || table_out_stride < c.max_pages)
+    return FA_ERR_INVALID_ARG;
+  rc = check_cache_pointers(cache);
+  if (rc != FA_OK) return rc;
+  if (page_refs == nullptr || parents == nullptr || table_out == nullptr || seqlens_out == nullptr ||
+      refs_out == nullptr || workspace == nullptr)
+    return FA_ERR_INVALID_ARG;
+  // the old rows are read while the new ones are written
+  if (table_out == c.block_table || seqlens_out == c.seqlens_k) return FA_ERR_INVALID_ARG;
+  if (!aligned(k_bounds, 16) || !aligned(workspace, 16) || !aligned(page_refs, 4) || !aligned(parents, 4) ||
+      !aligned(new_tokens, 4) || !aligned(table_out, 4) || !aligned(seqlens_out, 4) || !aligned(refs_out, 4))
+    return FA_ERR_INVALID_ARG;
+  if (workspace_bytes < fa_kv_pages_workspace_size(batch, rows, c.num_pages)) return FA_ERR_INVALID_ARG;
+  HostDevice host;
+  rc = host_device(&host);
+  if (rc != FA_OK) return rc;
+  if (!cache_on_device(cache, host.dev) || !host_is_device_ptr(page_refs, host.dev) ||
+      !host_is_device_ptr(parents, host.dev) || (new_tokens != nullptr && !host_is_device_ptr(new_tokens, host.dev)) ||
+      (k_bounds != nullptr && !host_is_device_ptr(k_bounds, host.dev)) || !host_is_device_ptr(table_out, host.dev) ||
+      !host_is_device_ptr(seqlens_out, host.dev) || !host_is_device_ptr(refs_out, host.dev) ||
+      !host_is_device_ptr(workspace, host.dev))
+    return FA_ERR_INVALID_ARG;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  PagesParams p;
+  std::memset(&p, 0, sizeof(p));
+  pages_fill(p, static_cast<uint8_t*>(workspace), batch, rows, c);
+  p.refs = page_refs;
+  p.parents = parents;
+  p.grow = new_tokens;
+  p.table_out = table_out;
+  p.out_stride = table_out_stride;
+  p.seqlens_out = seqlens_out;
+  p.refs_out = refs_out;
+  p.status = host.status;
+  kv_fork_kernel<<<kCluster, kThreads, 0, stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  return copy_launch(p, c, static_cast<uint8_t*>(k_bounds), false, host.sms, stream);
+}
+
+int fa_kv_compact(const fa_kv_cache* cache, void* k_bounds, const int* page_refs, int batch, int* table_out,
+                  int64_t table_out_stride, int* refs_out, int* page_map, int* used, void* workspace,
+                  size_t workspace_bytes, fa_stream_t stream_) {
+  int rc = check_cache(cache);
+  if (rc != FA_OK) return rc;
+  const fa_kv_cache& c = *cache;
+  if (batch < 0 || batch > kMaxBatch || table_out_stride < c.max_pages) return FA_ERR_INVALID_ARG;
+  rc = check_cache_pointers(cache);
+  if (rc != FA_OK) return rc;
+  if (page_refs == nullptr || table_out == nullptr || refs_out == nullptr || page_map == nullptr || used == nullptr ||
+      workspace == nullptr || page_map == refs_out || page_map == page_refs)
+    return FA_ERR_INVALID_ARG;
+  if (table_out == c.block_table && table_out_stride != c.table_stride && batch > 1) return FA_ERR_INVALID_ARG;
+  if (!aligned(k_bounds, 16) || !aligned(workspace, 16) || !aligned(page_refs, 4) || !aligned(table_out, 4) ||
+      !aligned(refs_out, 4) || !aligned(page_map, 4) || !aligned(used, 4))
+    return FA_ERR_INVALID_ARG;
+  if (workspace_bytes < fa_kv_pages_workspace_size(batch, 0, c.num_pages)) return FA_ERR_INVALID_ARG;
+  HostDevice host;
+  rc = host_device(&host);
+  if (rc != FA_OK) return rc;
+  if (!cache_on_device(cache, host.dev) || !host_is_device_ptr(page_refs, host.dev) ||
+      (k_bounds != nullptr && !host_is_device_ptr(k_bounds, host.dev)) || !host_is_device_ptr(table_out, host.dev) ||
+      !host_is_device_ptr(refs_out, host.dev) || !host_is_device_ptr(page_map, host.dev) ||
+      !host_is_device_ptr(used, host.dev) || !host_is_device_ptr(workspace, host.dev))
+    return FA_ERR_INVALID_ARG;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  PagesParams p;
+  std::memset(&p, 0, sizeof(p));
+  pages_fill(p, static_cast<uint8_t*>(workspace), batch, 0, c);
+  p.refs = page_refs;
+  p.table_out = table_out;
+  p.out_stride = table_out_stride;
+  p.refs_out = refs_out;
+  p.page_map = page_map;
+  p.used = used;
+  p.status = host.status;
+  kv_compact_kernel<<<kCluster, kThreads, 0, stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  return copy_launch(p, c, static_cast<uint8_t*>(k_bounds), true, host.sms, stream);
+}
+
+}  // extern "C"

@@ -540,6 +540,187 @@ int fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse, c
                  void* workspace, size_t workspace_bytes, fa_stream_t stream);
 
 /*
+ * Rotary positions: a table of cosines and sines, and the rotation by it.
+ *
+ * fa_rotary_table writes cos_sin [positions, rot_dim] fp32, as fa_kv_append and
+ * fa_rotary take it: for position p the rot_dim / 2 values magnitude cos(p f_i),
+ * then as many magnitude sin(p f_i).  rot_dim is a multiple of 16 up to 192,
+ * base >= 1; f_i = base^(-2 i / rot_dim), scaled for contexts longer than the
+ * trained one (factor >= 1; scaling NULL: FA_ROTARY_PLAIN):
+ *   FA_ROTARY_PLAIN     f_i
+ *   FA_ROTARY_LINEAR    f_i / factor
+ *   FA_ROTARY_BASE      base * factor^(rot_dim / (rot_dim - 2)) in place of base
+ *   FA_ROTARY_BY_PARTS  w f_i + (1 - w) f_i / factor, where pair i makes
+ *                       r = original f_i / (2 pi) turns within the trained length
+ *                       and w = (r - low) / (high - low), kept in [0, 1]
+ *                       (0 <= low < high, original > 0)
+ * Angles are exact to 2^-64 turns a position, so values are off by a few units
+ * of the last place at any position.  magnitude is in [2^-64, 2^64].  One launch.
+ */
+enum fa_rotary_kind { FA_ROTARY_PLAIN = 0, FA_ROTARY_LINEAR = 1, FA_ROTARY_BASE = 2, FA_ROTARY_BY_PARTS = 3 };
+
+typedef struct fa_rotary_scaling {
+  int kind;
+  double factor, original, low, high;
+  double magnitude;  /* of every value, for each kind */
+} fa_rotary_scaling;
+
+int fa_rotary_table(float* cos_sin, int positions, int rot_dim, double base, const fa_rotary_scaling* scaling,
+                    fa_stream_t stream);
+
+/*
+ * Rotate queries and keys (or one of them: NULL for the other's input and
+ * output) by their positions, or with backward = 1 turn their gradients back
+ * (the transposed map; the table takes no gradient).
+ *
+ *   q, q_out [total, heads_q, d], k, k_out [total, heads_k, d] bf16; strides in
+ *      elements from token to token (multiples of 8, a token's heads are
+ *      contiguous); d is 64, 128 or 192; an output may be its input (with the
+ *      same stride), and overlaps nothing else
+ *   positions  int32 [total], or NULL and
+ *   cu_seqlens int32 [batch + 1]: a token's position is its index in its
+ *      sequence; tokens of no sequence are left as they are; or NULL too: a
+ *      token's position is its index modulo seqlen (dense batches [B, S, H, d])
+ *   cos_sin    [max_positions, rot_dim] fp32, columns and pairs as for
+ *      fa_kv_append (rot_dim >= 16); columns from rot_dim on are copied
+ *
+ * Products and sums are fp32, rounded to bf16 once.  A token whose position is
+ * outside the table is left as it is and reported (FA_ERR_INVALID_ARG, site 514
+ * and the token); bad offsets are site 511.  One launch; no workspace.
+ */
+int fa_rotary(const void* q, const void* k, void* q_out, void* k_out, int64_t q_stride, int64_t k_stride,
+              int64_t q_out_stride, int64_t k_out_stride, const int* positions, const int* cu_seqlens, int batch,
+              int64_t seqlen, int64_t total, int heads_q, int heads_k, int d, const float* cos_sin, int max_positions,
+              int rot_dim, int interleaved, int backward, fa_stream_t stream);
+
+/*
+ * Sparse attention over the paged cache.  A step over long contexts appends its
+ * tokens (fa_kv_append), updates the bounds of the pages that received them
+ * (fa_kv_bounds), selects pages for each new token and key/value head
+ * (fa_kv_select) and attends over those alone (fa_fwd_lists).
+ *
+ *   k_bounds [num_pages, heads_kv, 2, d_qk] e4m3, contiguous, 16-byte aligned: of
+ *      each page, head and channel the largest, then the smallest code of the
+ *      page's tokens (in units of the page's key scale); NaN where one is NaN.  A
+ *      zero may have either sign.
+ *
+ * fa_kv_bounds writes the bounds of every page that holds one of the new tokens
+ * (cu_seqlens as for fa_kv_append, after it), over all tokens of the page up to
+ * seqlens_k[b].  Of `cache` it reads k, k_stride, the table, seqlens_k and the
+ * sizes; values and scales are not looked at.  One launch, no workspace.
+ */
+int fa_kv_bounds(const fa_kv_cache* cache, void* k_bounds, const int* cu_seqlens, int batch, int64_t total,
+                 fa_stream_t stream);
+
+/*
+ * Pages for each new token t (q [total_q, heads_q, d_qk] bf16, packed by
+ * cu_seqlens_q, at most max_seqlen_q of a sequence) and key/value head h.  Token
+ * i of the n new ones of sequence b sees seqlens_k[b] - n + i + 1 tokens if
+ * causal, else all seqlens_k[b], in P pages of block_table's row.  If P <= top,
+ * all are taken.  Else the first keep_first, the last keep_last (1 at least) and,
+ * of the others, those with the largest
+ *     score_j = sum over the query heads g of h, over d, of
+ *               max(q_gd hi_jd, q_gd lo_jd) * k_scale[j, h]
+ * (hi and lo of k_bounds: no key of the page scores more), top in all; equal
+ * scores are taken from the lowest page on.  A score that is NaN counts as +inf.
+ * The choice is that of exact scores as far as sums of 2 d_qk products in fp64
+ * are exact.
+ *
+ *   lists     [total_q, heads_kv, top] int32: the pages taken (indices into the
+ *             cache, as in block_table), in the order of the sequence, then -1
+ *   list_lens [total_q] int32: tokens that they hold for the token to see, the
+ *             last page perhaps in part
+ * Rows of tokens of no sequence are left as they are.  A page outside the cache
+ * is never followed (site 512); it counts as the last choice, and stands in the
+ * list as -1 if it is taken all the same.
+ *
+ * heads_q * d_qk per token contiguous; table_stride in entries; sizes as in
+ * fa_kv_cache.  total_q * heads_kv < 2^31, top <= 2^24.
+ * workspace: fa_kv_select_workspace_size bytes, 16-byte aligned, no
+ * initialisation; calls that may overlap need different ones.  It grows with
+ * total_q * heads_kv * max_pages (12 bytes each): pass no wider rows of the table
+ * than the longest sequence needs.  Two launches, deterministic.
+ */
+size_t fa_kv_select_workspace_size(int batch, int64_t total_q, int heads_kv, int max_pages);
+
+int fa_kv_select(const void* q, const void* k_bounds, const uint8_t* k_scale, const int* block_table,
+                 int64_t table_stride, const int* seqlens_k, const int* cu_seqlens_q, int batch, int64_t total_q,
+                 int max_seqlen_q, int heads_q, int heads_kv, int d_qk, int num_pages, int page_size, int max_pages,
+                 int causal, int top, int keep_first, int keep_last, int* lists, int* list_lens, void* workspace,
+                 size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * Attention of each token over lists of pages: token t and key/value head h see
+ * the first list_lens[t] tokens of the pages lists[t, h, 0], lists[t, h, 1], ..
+ * (lists [total_q, heads_kv, width] int32 contiguous, list_lens [total_q] int32,
+ * from fa_kv_select or made by the caller; a page may stand in several lists).
+ * q, o, lse, scale, NaN, rounding and the workspace's rules as for fa_fwd_paged
+ * with up to 16 rows; no further mask.  A token with list_lens 0 gets O = 0,
+ * lse = -inf; one outside [0, width * page_size] is left out (site 511, its
+ * index), a page outside the cache is never followed (site 512, the token's
+ * index).  total_q <= 2^20, width * page_size <= 2^30.  Of `cache` the table, its
+ * sizes and seqlens_k are not read.  Two launches, deterministic.
+ */
+size_t fa_fwd_lists_workspace_size(int heads_q, int heads_kv, int d_v);
+
+int fa_fwd_lists(const void* q, const fa_kv_cache* cache, const int* lists, const int* list_lens, int width, void* o,
+                 float* lse, int64_t total_q, int heads_q, float scale, void* workspace, size_t workspace_bytes,
+                 fa_stream_t stream);
+
+/*
+ * The cache's pages among rows of the block table.  page_refs [num_pages] int32
+ * counts how often rows (of this table or anything else that holds pages) use
+ * each page; a page with a count of 0 or less is free.  A row holds
+ * ceil(seqlens_k[b] / page_size) pages.
+ *
+ * fa_kv_fork makes a table of `rows` rows out of cache's one of `batch`: row r
+ * takes over row parents[r] (-1: it starts empty), then gets room for
+ * new_tokens[r] more tokens (NULL: 0).  A parent may have any number of heirs
+ * among the rows; one without any is freed.  Full pages are shared by all heirs.
+ * A last page that is not full stays with the parent's first heir (the lowest r);
+ * each other heir gets a new page with a copy of its tokens, scales and (k_bounds
+ * not NULL) bounds, bytes behind them left as they were.  New pages, a row's copy
+ * first, are the lowest free ones after the old rows' uses were dropped, row by
+ * row.  So one call forks, reorders, frees and extends.
+ *   table_out   [rows, max_pages] int32, row stride table_out_stride, written
+ *               whole (-1 behind a row's pages); not cache's table
+ *   seqlens_out [rows] int32: with the new tokens, as fa_kv_append takes them
+ *   refs_out    [num_pages] int32: the new counts; may be page_refs
+ * cache->k, v, scales and k_bounds are written in pages that were free, or freed
+ * by this call, only.  A row with a parent, a length or new tokens out of range
+ * (site 511, the row), with a parent whose row is (511 or 512, the parent), or
+ * for which too few pages are free (site 515; rows before it are served, later
+ * ones that need pages are not) becomes empty, with length 0; pages of parents
+ * out of range keep their counts.
+ *
+ * fa_kv_compact moves pages so that those in use (a count above 0) are the first
+ * `used`: each page behind goes to a hole before, both in order, with its scales
+ * and bounds.
+ *   table_out   [batch, max_pages]: the new indices, -1 behind a row's pages;
+ *               may be cache's table (with its stride)
+ *   refs_out    [num_pages], may be page_refs
+ *   page_map    [num_pages]: each page's new index, -1 if it is free
+ *   used        [1]
+ * A row with a length out of range becomes -1 throughout (site 511), so does an
+ * entry outside the cache or of a free page (site 512).
+ *
+ * batch, rows <= 16384 (1 at least for fa_kv_fork).  workspace: at least
+ * fa_kv_pages_workspace_size(batch, rows, num_pages) bytes (rows 0 for
+ * fa_kv_compact), 16-byte aligned, no initialisation; calls that may overlap need
+ * different ones, and different caches.  Outputs overlap nothing but what is said
+ * above.  Two launches, deterministic.
+ */
+size_t fa_kv_pages_workspace_size(int batch, int rows, int num_pages);
+
+int fa_kv_fork(const fa_kv_cache* cache, void* k_bounds, const int* page_refs, int batch, const int* parents,
+               const int* new_tokens, int rows, int* table_out, int64_t table_out_stride, int* seqlens_out,
+               int* refs_out, void* workspace, size_t workspace_bytes, fa_stream_t stream);
+
+int fa_kv_compact(const fa_kv_cache* cache, void* k_bounds, const int* page_refs, int batch, int* table_out,
+                  int64_t table_out_stride, int* refs_out, int* page_map, int* used, void* workspace,
+                  size_t workspace_bytes, fa_stream_t stream);
+
+/*
  * Host-only copy of the planning kernel's task list (no CUDA call): the same
  * records in the same order, for host cu_seqlens arrays.  l2_bytes is the L2
  * budget of the causal sections (0 selects 64 MiB; the kernel uses half the
@@ -565,7 +746,8 @@ int fa_device_status(fa_stream_t stream, int* out);
  * 2 correction, 3 MMA, 4 TMA), 501 bad cu_seqlens, 502 a varlen batch with
  * more tasks than the workspace holds, 511 a bad sequence of a call on a paged
  * cache, 512 a page outside the cache (the index is the sequence's in both),
- * 513 more keys than total_k, 520 a wait of the paged attention kernel, 601-623
+ * 513 more keys than total_k, 514 a position outside the rotation table (the index is
+ * the token's), 515 too few free pages (the index is the row's), 520 a wait of the paged attention kernel, 601-623
  * a backward wait,
  * 701-707 a range check and 710 + i a hand-off count of the checking build.
  */
