@@ -71,7 +71,7 @@ class Server:
         full = want.all_bounds(c).float()
         for b, n in enumerate(c.lens):
             mine = c.table[b, :-(-n // self.page)].long()
-            assert torch.equal(self.bounds.cpu()[mine].float(), full[mine])
+            assert torch.equal(self.bounds.float().cpu()[mine], full[mine])
         ex, ex_lens = want.select(q.cpu(), self.bounds.cpu(), c.k_scale, c.table, c.lens, cu.tolist(), self.page, top, True, 1, 1)
         assert torch.equal(lists.long().cpu(), ex) and torch.equal(list_lens.long().cpu(), ex_lens)
         ref.check_attention(o, lse, want.lists_attention(q, c, lists, list_lens.tolist()), EPS_F16)
