@@ -920,24 +920,24 @@ def rotary_table(positions: int, rot_dim: int, base: float = 10000.0, scaling: s
     return out
 
 
-def _rotary_rows(name, t, tokens, dims):
-    """(heads, stride from token to token) of a bf16 tensor whose `dims` leading dimensions are tokens."""
+def _rotary_rows(name, t, tokens, d):
+    """(heads, stride from token to token) of a bf16 tensor [*tokens, heads, d]."""
     import torch
 
-    if t.dtype is not torch.bfloat16 or t.dim() != dims + 1 or t.shape[:-2] != tokens:
-        _bad(f"{name} must be a bf16 tensor {list(tokens)} x heads x d")
-    st, shape = t.stride(), t.shape
-    heads, d = shape[-2], shape[-1]
-    row = heads * d
-    if t.numel() == 0:
-        return heads, row
-    if (st[-1] != 1 and d > 1) or (st[-2] != d and heads > 1):
-        _bad(f"{name}: a token's heads must be contiguous")
-    if dims == 2:
-        return heads, st[0] if shape[0] > 1 else row
-    if shape[0] > 1 and shape[1] > 1 and st[0] != shape[1] * st[1]:
+    shape, st = t.shape, t.stride()
+    if t.dtype is not torch.bfloat16 or shape[:-2] != tokens or shape[-1] != d:
+        _bad(f"{name} must be a bf16 tensor of tokens {list(tokens)} with heads of {d}")
+    heads = shape[-2]
+    if st[-1] == 1 and (st[-2] == d or heads == 1):
+        if len(tokens) == 1:
+            return heads, st[0] if tokens[0] > 1 else heads * d
+        batch, seqlen = tokens
+        if batch <= 1 or seqlen <= 1 or st[0] == seqlen * st[1]:
+            return heads, st[1] if seqlen > 1 else st[0] if batch > 1 else heads * d
         _bad(f"{name}: the step from sequence to sequence must be that of seqlen tokens")
-    return heads, st[1] if shape[1] > 1 else st[0] if shape[0] > 1 else row
+    if t.numel() == 0:
+        return heads, heads * d
+    _bad(f"{name}: a token's heads must be contiguous")
 
 
 def _rotary(q, k, cos_sin, positions, cu_seqlens, interleaved, q_out, k_out, stream, backward):
@@ -952,58 +952,57 @@ def _rotary(q, k, cos_sin, positions, cu_seqlens, interleaved, q_out, k_out, str
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return _rotary(q, k, cos_sin, positions, cu_seqlens, interleaved, q_out, k_out, stream, backward)
-    dims = ref.dim() - 1
-    if dims not in (2, 3):
+    shape = ref.shape
+    if len(shape) not in (3, 4):
         _bad("q and k must be [total, heads, d] or [batch, seqlen, heads, d]")
-    tokens, d = ref.shape[:-2], ref.shape[-1]
-    total = 1
-    for n in tokens:
-        total *= n
-    if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+    tokens, d = shape[:-2], shape[-1]
+    total = tokens[0] if len(tokens) == 1 else tokens[0] * tokens[1]
+    table = cos_sin.shape
+    if cos_sin.dtype is not torch.float32 or len(table) != 2 or not cos_sin.is_contiguous():
         _bad("cos_sin must be a contiguous 2-D fp32 tensor")
     pos = cu = None
     batch = seqlen = 0
     if positions is not None:
         if cu_seqlens is not None:
             _bad("positions and cu_seqlens exclude each other")
-        if positions.dtype is not torch.int32 or positions.shape != tokens or not positions.is_contiguous():
-            _bad(f"positions must be a contiguous int32 tensor {list(tokens)}")
+        _int32("positions", positions, tokens)
         pos = positions.data_ptr()
     elif cu_seqlens is not None:
-        if dims != 2 or cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or \
-                not cu_seqlens.is_contiguous():
-            _bad("cu_seqlens must be a contiguous int32 tensor of batch + 1 offsets into [total, heads, d]")
-        batch, cu = cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
-    elif dims == 3:
-        seqlen = max(tokens[1], 1)
+        batch = cu_seqlens.numel() - 1
+        if len(tokens) != 1 or batch < 0:
+            _bad("cu_seqlens must hold batch + 1 offsets into [total, heads, d]")
+        _int32("cu_seqlens", cu_seqlens, (batch + 1,))
+        cu = cu_seqlens.data_ptr()
     else:
-        seqlen = max(total, 1)  # one sequence
+        seqlen = tokens[-1] or 1  # without a batch: one sequence
     ptr, current = _call_stream(index, stream)
-    got, args = [], []
-    for name, x, out in (("q", q, q_out), ("k", k, k_out)):
-        if x is None:
-            if out is not None:
-                _bad(f"{name}_out without {name}")
-            got.append(None)
-            args.append((None, None, 0, 0, 0))
-            continue
-        heads, stride = _rotary_rows(name, x, tokens, dims)
-        if x.shape[-1] != d:
-            _bad("q and k must have the same d")
-        if out is None:
-            out = _empty(x.shape, torch.bfloat16, index, ptr, current)
-        if out.shape != x.shape:
-            _bad(f"{name}_out must have {name}'s shape")
-        _, out_stride = _rotary_rows(name + "_out", out, tokens, dims)
-        got.append(out)
-        args.append((x.data_ptr(), out.data_ptr(), stride, out_stride, heads))
-    (qp, qo, qs, qos, hq), (kp, ko, ks, kos, hk) = args
+    qp = kp = qo = ko = None
+    hq = hk = qs = ks = qos = kos = 0
+    if q is not None:
+        hq, qs = _rotary_rows("q", q, tokens, d)
+        if q_out is None:
+            q_out = _empty(q.shape, torch.bfloat16, index, ptr, current)
+        ho, qos = _rotary_rows("q_out", q_out, tokens, d)
+        if ho != hq:
+            _bad("q_out must have q's shape")
+        qp, qo = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        _bad("q_out without q")
+    if k is not None:
+        hk, ks = _rotary_rows("k", k, tokens, d)
+        if k_out is None:
+            k_out = _empty(k.shape, torch.bfloat16, index, ptr, current)
+        ho, kos = _rotary_rows("k_out", k_out, tokens, d)
+        if ho != hk:
+            _bad("k_out must have k's shape")
+        kp, ko = k.data_ptr(), k_out.data_ptr()
+    elif k_out is not None:
+        _bad("k_out without k")
     rc = load_library().fa_rotary(qp, kp, qo, ko, qs, ks, qos, kos, pos, cu, batch, seqlen, total, hq, hk, d,
-                                  cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0,
-                                  backward, ptr)
+                                  cos_sin.data_ptr(), table[0], table[1], 1 if interleaved else 0, backward, ptr)
     if rc != FA_OK:
         raise FaError(rc, "fa_rotary")
-    return tuple(got)
+    return q_out, k_out
 
 
 def rotary(q, k, cos_sin, positions=None, cu_seqlens=None, interleaved: bool = False, q_out=None, k_out=None, stream=None):
@@ -1059,23 +1058,24 @@ def fa_fwd_lists(q, cache: FaKvCache, lists, list_lens, width, o, lse, total_q, 
 
 
 def _int32(name, t, shape):
-    """Checks a contiguous int32 tensor of a shape (None: any extent)."""
+    """Checks a contiguous int32 tensor of a shape."""
     import torch
 
-    if t.dtype is not torch.int32 or len(t.shape) != len(shape) or not t.is_contiguous() or \
-            any(n is not None and m != n for m, n in zip(t.shape, shape)):
-        _bad(f"{name} must be a contiguous int32 tensor [{', '.join('*' if n is None else str(n) for n in shape)}]")
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
+        _bad(f"{name} must be a contiguous int32 tensor {list(shape)}")
 
 
 def _table_rows(block_table, seqlens_k):
     """(batch, max_pages, row stride) of a block table beside its lengths."""
     import torch
 
-    td = block_table.shape
-    if block_table.dtype is not torch.int32 or len(td) != 2 or (block_table.stride(1) != 1 and td[1] > 1):
+    td, st = block_table.shape, block_table.stride()
+    if block_table.dtype is not torch.int32 or len(td) != 2 or (st[1] != 1 and td[1] > 1):
         _bad("block_table must be a 2-D int32 tensor whose rows are contiguous")
-    _int32("seqlens_k", seqlens_k, (td[0],))
-    return td[0], td[1], block_table.stride(0) if td[0] > 1 else td[1]
+    batch, width = td
+    if seqlens_k.dtype is not torch.int32 or seqlens_k.shape != td[:1] or not seqlens_k.is_contiguous():
+        _bad(f"seqlens_k must be a contiguous int32 tensor [{batch}]")
+    return batch, width, st[0] if batch > 1 else width
 
 
 def _bounds(k_bounds, pages, heads, d):
@@ -1086,17 +1086,16 @@ def _bounds(k_bounds, pages, heads, d):
     return k_bounds.data_ptr()
 
 
-def _workspace(workspace, size, index, ptr, current):
-    """(pointer, bytes) of the caller's workspace, or of one of `size` bytes; and what keeps it."""
-    import torch
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(name, *sizes):
+    """What the library's function `name` says, 16 at least; it depends on the sizes alone."""
+    return getattr(load_library(), name)(*sizes) or 16
 
-    if workspace is None:
-        workspace = _empty((size or 16,), torch.uint8, index, ptr, current)
-    elif not workspace.is_contiguous():
+
+def _given_workspace(workspace):
+    if not workspace.is_contiguous():
         _bad("workspace must be contiguous")
-    else:
-        size = workspace.numel() * workspace.element_size()
-    return workspace.data_ptr(), size, workspace
+    return workspace.numel() * workspace.element_size()
 
 
 def kv_bounds(k_cache, k_bounds, block_table, seqlens_k, cu_seqlens, total: int, stream=None):
@@ -1167,34 +1166,52 @@ def kv_select(q, k_bounds, k_scale, block_table, seqlens_k, cu_seqlens_q, max_se
         list_lens = _empty((total_q,), torch.int32, index, ptr, current)
     else:
         _int32("list_lens", list_lens, (total_q,))
-    size = load_library().fa_kv_select_workspace_size(batch, total_q, heads, width) if workspace is None else 0
-    ws, size, workspace = _workspace(workspace, size, index, ptr, current)
+    if workspace is None:
+        size = _workspace_bytes("fa_kv_select_workspace_size", batch, total_q, heads, width)
+        workspace = _empty((size,), torch.uint8, index, ptr, current)
+    else:
+        size = _given_workspace(workspace)
     rc = load_library().fa_kv_select(q.data_ptr(), bounds, k_scale.data_ptr(), block_table.data_ptr(), ts,
                                      seqlens_k.data_ptr(), cu_seqlens_q.data_ptr(), batch, total_q, max_seqlen_q, heads_q,
                                      heads, d, pages, page_size, width, 1 if causal else 0, top, keep_first, keep_last,
-                                     lists.data_ptr(), list_lens.data_ptr(), ws, size, ptr)
+                                     lists.data_ptr(), list_lens.data_ptr(), workspace.data_ptr(), size, ptr)
     if rc != FA_OK:
         raise FaError(rc, "fa_kv_select")
     return lists, list_lens
 
 
-def _pool(k_cache, v_cache, k_scale, v_scale, index, table, seqlens, width, table_stride):
-    """(fa_kv_cache as bytes, num_pages, heads_kv, page_size, d_qk, d_v) of the cache's tensors, which are checked."""
+def _pool(k_cache, v_cache, k_scale, v_scale, table, seqlens, width, table_stride):
+    """(fa_kv_cache as bytes, num_pages, heads_kv, d_qk, d_v) of the cache's tensors, which are checked."""
     import torch
 
     f8, e8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
     kd, vd = k_cache.shape, v_cache.shape
-    if len(kd) != 4 or len(vd) != 4 or kd[:3] != vd[:3] or k_cache.dtype is not f8 or v_cache.dtype is not f8:
-        _bad("k_cache and v_cache must be float8_e4m3fn [num_pages, heads_kv, page_size, d]")
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t.dtype is not e8 or t.shape != kd[:2] or not t.is_contiguous():
-            _bad(f"{name} must be a contiguous float8_e8m0fnu tensor [num_pages, heads_kv]")
+    head = kd[:2]
     ks, vs = k_cache.stride(), v_cache.stride()
-    if (ks[3] != 1 and kd[3] > 1) or (vs[3] != 1 and vd[3] > 1):
-        _bad("the codes of a token must be contiguous")
+    if not (len(kd) == 4 and len(vd) == 4 and kd[:3] == vd[:3] and k_cache.dtype is f8 and v_cache.dtype is f8 and
+            k_scale.dtype is e8 and v_scale.dtype is e8 and k_scale.shape == head and v_scale.shape == head and
+            k_scale.is_contiguous() and v_scale.is_contiguous() and ks[3] == 1 and vs[3] == 1):
+        _pool_error(k_cache, v_cache, k_scale, v_scale)
+    pages, heads, page, d_qk = kd
+    d_v = vd[3]
     packed = _KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), table, seqlens,
-                            ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], table_stride, kd[0], kd[2], kd[1], kd[3], vd[3], width)
-    return packed, kd[0], kd[1], kd[2], kd[3], vd[3]
+                            ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], table_stride, pages, page, heads, d_qk, d_v, width)
+    return packed, pages, heads, d_qk, d_v
+
+
+def _pool_error(k_cache, v_cache, k_scale, v_scale):
+    """Says which tensor is wrong."""
+    import torch
+
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype is not torch.float8_e4m3fn or t.dim() != 4 or t.stride(3) != 1:
+            _bad(f"{name} must be a 4-D float8_e4m3fn tensor whose tokens' codes are contiguous")
+    if k_cache.shape[:3] != v_cache.shape[:3]:
+        _bad("k_cache and v_cache must be [num_pages, heads_kv, page_size, d]")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t.dtype is not torch.float8_e8m0fnu or t.shape != k_cache.shape[:2] or not t.is_contiguous():
+            _bad(f"{name} must be a contiguous float8_e8m0fnu tensor [num_pages, heads_kv]")
+    _bad("the cache's tensors do not fit each other")
 
 
 def attention_forward_lists(q, k_cache, v_cache, k_scale, v_scale, lists, list_lens, scale: float | None = None, out=None,
@@ -1216,13 +1233,14 @@ def attention_forward_lists(q, k_cache, v_cache, k_scale, v_scale, lists, list_l
             return attention_forward_lists(q, k_cache, v_cache, k_scale, v_scale, lists, list_lens, scale, out, lse,
                                            return_lse, workspace, stream)
     total_q, heads_q, d = qd
-    _int32("lists", lists, (total_q, None, None))
-    _int32("list_lens", list_lens, (total_q,))
-    width = lists.shape[2]
-    cache, _, heads, _, d_qk, d_v = _pool(k_cache, v_cache, k_scale, v_scale, index, lists.data_ptr(), list_lens.data_ptr(),
-                                          width, width)
-    if d != d_qk or lists.shape[1] != heads:
+    ld = lists.shape
+    width = ld[2] if len(ld) == 3 else -1
+    cache, _, heads, d_qk, d_v = _pool(k_cache, v_cache, k_scale, v_scale, lists.data_ptr(), list_lens.data_ptr(), width,
+                                       width)
+    if d != d_qk or width < 0:
         _bad(f"q must be [total_q, heads_q, {d_qk}] and lists [total_q, {heads}, width]")
+    _int32("lists", lists, (total_q, heads, width))
+    _int32("list_lens", list_lens, (total_q,))
     ptr, current = _call_stream(index, stream)
     if out is None:
         out = _empty((total_q, heads_q, d_v), torch.bfloat16, index, ptr, current)
@@ -1233,11 +1251,14 @@ def attention_forward_lists(q, k_cache, v_cache, k_scale, v_scale, lists, list_l
             lse = _empty((heads_q, total_q), torch.float32, index, ptr, current)
     elif lse.dtype is not torch.float32 or lse.shape != (heads_q, total_q) or not lse.is_contiguous():
         _bad("lse must be a contiguous fp32 tensor [heads_q, total_q]")
-    size = load_library().fa_fwd_lists_workspace_size(heads_q, heads, d_v) if workspace is None else 0
-    ws, size, workspace = _workspace(workspace, size, index, ptr, current)
+    if workspace is None:
+        size = _workspace_bytes("fa_fwd_lists_workspace_size", heads_q, heads, d_v)
+        workspace = _empty((size,), torch.uint8, index, ptr, current)
+    else:
+        size = _given_workspace(workspace)
     rc = load_library().fa_fwd_lists(q.data_ptr(), cache, lists.data_ptr(), list_lens.data_ptr(), width, out.data_ptr(),
                                      lse.data_ptr() if lse is not None else None, total_q, heads_q,
-                                     0.0 if scale is None else scale, ws, size, ptr)
+                                     0.0 if scale is None else scale, workspace.data_ptr(), size, ptr)
     if rc != FA_OK:
         raise FaError(rc, "fa_fwd_lists")
     return (out, lse) if return_lse else out
@@ -1272,10 +1293,11 @@ def _table_out(table_out, rows, width, index, ptr, current):
     import torch
 
     if table_out is None:
-        table_out = _empty((rows, width), torch.int32, index, ptr, current)
-    elif table_out.dtype is not torch.int32 or table_out.shape != (rows, width) or (table_out.stride(1) != 1 and width > 1):
+        return _empty((rows, width), torch.int32, index, ptr, current), width
+    st = table_out.stride()
+    if table_out.dtype is not torch.int32 or table_out.shape != (rows, width) or (st[1] != 1 and width > 1):
         _bad(f"table_out must be an int32 tensor [{rows}, {width}] whose rows are contiguous")
-    return table_out, table_out.stride(0) if rows > 1 else width
+    return table_out, st[0] if rows > 1 else width
 
 
 def _int32_out(name, t, n, index, ptr, current):
@@ -1307,10 +1329,10 @@ def kv_fork(parents, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k,
             return kv_fork(parents, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, page_refs, new_tokens,
                            k_bounds, table_out, seqlens_out, refs_out, workspace, stream)
     batch, width, ts = _table_rows(block_table, seqlens_k)
-    cache, pages, heads, _, d_qk, _ = _pool(k_cache, v_cache, k_scale, v_scale, index, block_table.data_ptr(),
-                                            seqlens_k.data_ptr(), width, ts)
-    rows = parents.shape[0] if parents.dim() == 1 else -1
-    _int32("parents", parents, (None,))
+    cache, pages, heads, d_qk, _ = _pool(k_cache, v_cache, k_scale, v_scale, block_table.data_ptr(), seqlens_k.data_ptr(),
+                                         width, ts)
+    rows = parents.numel()
+    _int32("parents", parents, (rows,))
     _int32("page_refs", page_refs, (pages,))
     if new_tokens is not None:
         _int32("new_tokens", new_tokens, (rows,))
@@ -1319,11 +1341,14 @@ def kv_fork(parents, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k,
     table_out, out_stride = _table_out(table_out, rows, width, index, ptr, current)
     seqlens_out = _int32_out("seqlens_out", seqlens_out, rows, index, ptr, current)
     refs_out = _int32_out("refs_out", refs_out, pages, index, ptr, current)
-    size = load_library().fa_kv_pages_workspace_size(batch, rows, pages) if workspace is None else 0
-    ws, size, workspace = _workspace(workspace, size, index, ptr, current)
+    if workspace is None:
+        size = _workspace_bytes("fa_kv_pages_workspace_size", batch, rows, pages)
+        workspace = _empty((size,), torch.uint8, index, ptr, current)
+    else:
+        size = _given_workspace(workspace)
     rc = load_library().fa_kv_fork(cache, bounds, page_refs.data_ptr(), batch, parents.data_ptr(),
                                    new_tokens.data_ptr() if new_tokens is not None else None, rows, table_out.data_ptr(),
-                                   out_stride, seqlens_out.data_ptr(), refs_out.data_ptr(), ws, size, ptr)
+                                   out_stride, seqlens_out.data_ptr(), refs_out.data_ptr(), workspace.data_ptr(), size, ptr)
     if rc != FA_OK:
         raise FaError(rc, "fa_kv_fork")
     return table_out, seqlens_out, refs_out
@@ -1345,8 +1370,8 @@ def kv_compact(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, page_
             return kv_compact(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, page_refs, k_bounds, table_out,
                               refs_out, page_map, used, workspace, stream)
     batch, width, ts = _table_rows(block_table, seqlens_k)
-    cache, pages, heads, _, d_qk, _ = _pool(k_cache, v_cache, k_scale, v_scale, index, block_table.data_ptr(),
-                                            seqlens_k.data_ptr(), width, ts)
+    cache, pages, heads, d_qk, _ = _pool(k_cache, v_cache, k_scale, v_scale, block_table.data_ptr(), seqlens_k.data_ptr(),
+                                         width, ts)
     _int32("page_refs", page_refs, (pages,))
     bounds = _bounds(k_bounds, pages, heads, d_qk) if k_bounds is not None else None
     ptr, current = _call_stream(index, stream)
@@ -1354,10 +1379,13 @@ def kv_compact(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, page_
     refs_out = _int32_out("refs_out", refs_out, pages, index, ptr, current)
     page_map = _int32_out("page_map", page_map, pages, index, ptr, current)
     used = _int32_out("used", used, 1, index, ptr, current)
-    size = load_library().fa_kv_pages_workspace_size(batch, 0, pages) if workspace is None else 0
-    ws, size, workspace = _workspace(workspace, size, index, ptr, current)
+    if workspace is None:
+        size = _workspace_bytes("fa_kv_pages_workspace_size", batch, 0, pages)
+        workspace = _empty((size,), torch.uint8, index, ptr, current)
+    else:
+        size = _given_workspace(workspace)
     rc = load_library().fa_kv_compact(cache, bounds, page_refs.data_ptr(), batch, table_out.data_ptr(), out_stride,
-                                      refs_out.data_ptr(), page_map.data_ptr(), used.data_ptr(), ws, size, ptr)
+                                      refs_out.data_ptr(), page_map.data_ptr(), used.data_ptr(), workspace.data_ptr(), size, ptr)
     if rc != FA_OK:
         raise FaError(rc, "fa_kv_compact")
     return table_out, refs_out, page_map, used

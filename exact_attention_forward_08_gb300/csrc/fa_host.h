@@ -7,6 +7,9 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <mutex>
+
+#include "fa.h"
 
 namespace fa {
 
@@ -27,5 +30,19 @@ bool host_is_device_ptr(const void* p, int dev);
 // box, shared-memory swizzle of 128 or 64 bytes.  After host_device().
 int host_encode_bytes(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
                       const uint32_t* box, int swizzle);
+
+// Lets `kernel` use `smem` bytes of dynamic shared memory, once a device.
+inline int allow_smem(const void* kernel, int smem, bool (&ready)[64]) {
+  static std::mutex mutex;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FA_ERR_CUDA;
+  std::lock_guard<std::mutex> lock(mutex);
+  if (!ready[dev]) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      return FA_ERR_CUDA;
+    ready[dev] = true;
+  }
+  return FA_OK;
+}
 
 }  // namespace fa

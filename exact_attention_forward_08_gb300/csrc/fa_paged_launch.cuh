@@ -1,27 +1,11 @@
 // Launch of one instantiation of the paged attention kernel and its merge.
 #pragma once
-#include <mutex>
-
 #include "fa_host.h"
 #include "fa_paged.h"
 #include "fa_paged_attn.cuh"
 #include "fa_paged_tc.cuh"
 
 namespace fa {
-
-// Lets `kernel` use `smem` bytes of dynamic shared memory, once a device.
-inline int paged_allow_smem(const void* kernel, int smem, bool (&ready)[64]) {
-  static std::mutex mutex;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FA_ERR_CUDA;
-  std::lock_guard<std::mutex> lock(mutex);
-  if (!ready[dev]) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-      return FA_ERR_CUDA;
-    ready[dev] = true;
-  }
-  return FA_OK;
-}
 
 // `early`: the blocks may be placed while the kernel before this one on the stream still runs.
 template <typename P>
@@ -44,7 +28,7 @@ int paged_few_launch(const PagedParams& p, int grid, cudaStream_t stream) {
   using Shape = PagedShape<DQK, DV, NT>;
   static bool ready[64] = {};
   auto* kernel = paged_attn_kernel<DQK, DV, NT, G16, LISTS>;
-  const int rc = paged_allow_smem(reinterpret_cast<const void*>(kernel), Shape::kBytes, ready);
+  const int rc = allow_smem(reinterpret_cast<const void*>(kernel), Shape::kBytes, ready);
   if (rc != FA_OK) return rc;
   return paged_start(kernel, p, grid, Shape::kThreads, Shape::kBytes, false, stream);
 }
@@ -85,7 +69,7 @@ int paged_many_launch(const PagedParams& shared, const fa_kv_cache& c, int rows,
   using Shape = TcShape<DQK, DV>;
   static bool ready[64] = {};
   auto* kernel = paged_tc_kernel<DQK, DV>;
-  int rc = paged_allow_smem(reinterpret_cast<const void*>(kernel), Shape::kBytes, ready);
+  int rc = allow_smem(reinterpret_cast<const void*>(kernel), Shape::kBytes, ready);
   if (rc != FA_OK) return rc;
   TcParams p;
   static_cast<PagedParams&>(p) = shared;

@@ -23,16 +23,13 @@
 namespace fa {
 namespace {
 
-constexpr int kCluster = 8;       // blocks that decide
-constexpr int kThreads = 1024;    // of each
+constexpr int kCluster = 8;     // blocks that decide
+constexpr int kThreads = 1024;  // of each
 constexpr int kAll = kCluster * kThreads;
-constexpr int kCopyBits = 20;     // of a row's packed numbers: copies below, pages needed above
 
 struct PagesHead {
-  long long need;   // pages that all rows need
-  int copies;       // pages to copy
-  int used;         // pages in use (compaction)
-  int used_low;     // those among the first `used`
+  int copies;  // pages to copy
+  int skip;    // where their list begins
   int count[kCluster];
 };
 
@@ -51,10 +48,7 @@ struct PagesParams {
   int* used;
   unsigned int* status;
   PagesHead* head;
-  int* heirs;          // [batch], -1: a row that is not valid
-  int* first;          // [batch] the first heir
-  long long* start;    // [rows] pages needed by the rows before
-  int* list;           // [num_pages] free pages in order; compaction: holes
+  int* valid;               // [batch] 0: a row whose length or pages are out of range
   int *src, *dst, *tokens;  // copies
   int batch, rows, num_pages, max_pages, page_shift;
 };
@@ -85,7 +79,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* warp_sum
   return v + (warp > 0 ? before : 0);
 }
 
-// The pages that thread `tid` of block `rank` counts: equal runs in order.
+// The pages that a thread of block `rank` counts: equal runs in order.
 struct PageRun {
   int64_t begin, end;
 };
@@ -96,30 +90,55 @@ __device__ __forceinline__ PageRun page_run(const PagesParams& p, int rank) {
   return {begin < p.num_pages ? begin : p.num_pages, end < p.num_pages ? end : p.num_pages};
 }
 
+// Pages of all runs that hold something (of the pages counted: `mine` of this thread), and those before this thread's.
+__device__ __forceinline__ int cluster_scan(const PagesParams& p, int rank, int mine, long long* warp_sum, long long& before) {
+  long long total;
+  before = block_scan(mine, warp_sum, total) - mine;
+  if (threadIdx.x == 0) p.head->count[rank] = static_cast<int>(total);
+  cluster_sync();
+  int all = 0;
+#pragma unroll
+  for (int i = 0; i < kCluster; ++i) {
+    const int n = __ldcg(&p.head->count[i]);
+    if (i < rank) before += n;
+    all += n;
+  }
+  return all;
+}
+
+__device__ __forceinline__ bool length_fits(const PagesParams& p, int len) {
+  return len >= 0 && len <= static_cast<int64_t>(p.max_pages) << p.page_shift;
+}
+
 // A row of the new table as far as it does not depend on other rows.
 struct ForkRow {
-  int src, len, held, total;  // parent (-1: none), its tokens, its pages, pages of the new row
+  int src, len, held, total, grow;  // parent (-1: none), its tokens, its pages; pages of the new row; new tokens
   bool bad;
 };
 __device__ __forceinline__ ForkRow fork_row(const PagesParams& p, int r) {
-  ForkRow w = {p.parents[r], 0, 0, 0, false};
-  const int64_t most = static_cast<int64_t>(p.max_pages) << p.page_shift;
-  const int grow = p.grow != nullptr ? p.grow[r] : 0;
-  w.bad = w.src < -1 || w.src >= p.batch || grow < 0;
+  ForkRow w = {p.parents[r], 0, 0, 0, p.grow != nullptr ? p.grow[r] : 0, false};
+  w.bad = w.src < -1 || w.src >= p.batch || w.grow < 0;
   if (!w.bad && w.src >= 0) {
-    w.bad = __ldcg(p.heirs + w.src) < 0;
+    w.bad = __ldcg(p.valid + w.src) == 0;
     w.len = w.bad ? 0 : p.seqlens[w.src];
   }
-  w.bad = w.bad || static_cast<int64_t>(w.len) + grow > most;
-  if (w.bad) return {-1, 0, 0, 0, true};
+  w.bad = w.bad || static_cast<int64_t>(w.len) + w.grow > static_cast<int64_t>(p.max_pages) << p.page_shift;
+  if (w.bad) return {-1, 0, 0, 0, 0, true};
   const int round = (1 << p.page_shift) - 1;
   w.held = (w.len + round) >> p.page_shift;
-  w.total = static_cast<int>((static_cast<int64_t>(w.len) + grow + round) >> p.page_shift);
+  w.total = static_cast<int>((static_cast<int64_t>(w.len) + w.grow + round) >> p.page_shift);
   return w;
 }
 
+// Three barriers of the cluster.  What all rows need of one another (heirs, first
+// heirs, the pages needed before each row) every block works out for itself in
+// shared memory, which takes less time than an exchange; pages are shared out.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     kv_fork_kernel(const __grid_constant__ PagesParams p) {
+  extern __shared__ int fork_smem[];
+  int* const heirs = fork_smem;          // [batch], -1: not valid
+  int* const first = heirs + p.batch;    // [batch] the first heir
+  int* const start = first + p.batch;    // [rows + 1] pages that the rows before need
   __shared__ long long warp_sum[32];
   const int rank = blockIdx.x, tid = rank * kThreads + threadIdx.x;
   const int lane = threadIdx.x & 31, warp = tid >> 5;
@@ -127,10 +146,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- counts start from the old ones; a warp looks at an old row's pages ----
-  for (int i = tid; i < p.num_pages; i += kAll) p.refs_out[i] = p.refs[i];
+  if (tid == 0) p.head->copies = p.head->skip = 0;
   for (int b = warp; b < p.batch; b += kAll / 32) {
     const int len = p.seqlens[b];
-    const bool fits = len >= 0 && len <= static_cast<int64_t>(p.max_pages) << p.page_shift;
+    const bool fits = length_fits(p, len);
     bool page_bad = false;
     if (fits) {
       const int pages = (len + part_mask) >> p.page_shift;
@@ -140,109 +159,98 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     page_bad = __any_sync(0xffffffffu, page_bad);
     if (lane == 0) {
       if (!fits || page_bad) paged_error(p.status, fits ? kSitePagedPage : kSitePagedSeq, b);
-      p.heirs[b] = fits && !page_bad ? 0 : -1;
-      p.first[b] = INT_MAX;
+      p.valid[b] = fits && !page_bad ? 1 : 0;
     }
   }
-  cluster_sync();
-  for (int r = tid; r < p.rows; r += kAll) {
-    const ForkRow w = fork_row(p, r);
-    if (w.bad) paged_error(p.status, kSitePagedSeq, r);
-    if (w.src >= 0) {
-      atomicAdd(p.heirs + w.src, 1);
-      atomicMin(p.first + w.src, r);
-    }
-  }
+  for (int i = tid; i < p.num_pages; i += kAll) p.refs_out[i] = p.refs[i];
+  for (int b = threadIdx.x; b < p.batch; b += kThreads) heirs[b] = 0, first[b] = INT_MAX;
   cluster_sync();
 
-  // ---- block 0 numbers the pages that rows need and the copies; all move the counts of old pages ----
-  if (rank == 0) {
-    long long before = 0;
-    for (int base = 0; base < p.rows; base += kThreads) {
-      const int r = base + threadIdx.x;
-      long long v = 0;
-      if (r < p.rows) {
-        const ForkRow w = fork_row(p, r);
-        const bool copy = w.src >= 0 && (w.len & part_mask) != 0 && __ldcg(p.first + w.src) != r;
-        v = (static_cast<long long>(w.total - w.held + (copy ? 1 : 0)) << kCopyBits) | (copy ? 1 : 0);
-      }
-      long long total;
-      const long long upto = block_scan(v, warp_sum, total);
-      if (r < p.rows) p.start[r] = before + upto - v;
-      before += total;
-    }
-    if (threadIdx.x == 0) {
-      p.head->need = before >> kCopyBits;
-      p.head->copies = static_cast<int>(before & ((1 << kCopyBits) - 1));
+  // ---- heirs, and the pages that rows need ----
+  for (int r = threadIdx.x; r < p.rows; r += kThreads) {
+    const ForkRow w = fork_row(p, r);
+    if (w.bad && rank == 0) paged_error(p.status, kSitePagedSeq, r);
+    if (w.src >= 0) {
+      atomicAdd(heirs + w.src, 1);
+      atomicMin(first + w.src, r);
     }
   }
+  __syncthreads();
+  auto copies = [&](const ForkRow& w, int r) { return w.src >= 0 && (w.len & part_mask) != 0 && first[w.src] != r; };
+  long long needed = 0;
+  for (int base = 0; base < p.rows; base += kThreads) {
+    const int r = base + threadIdx.x;
+    int need = 0;
+    if (r < p.rows) {
+      const ForkRow w = fork_row(p, r);
+      need = w.total - w.held + (copies(w, r) ? 1 : 0);
+    }
+    long long total;
+    const long long upto = needed + block_scan(need, warp_sum, total);
+    if (r < p.rows) start[r + 1] = static_cast<int>(upto < INT_MAX ? upto : INT_MAX);
+    needed += total;
+  }
+  if (threadIdx.x == 0) start[0] = 0;
+
+  // ---- what the old rows' heirs make of their pages' counts ----
   for (int b = warp; b < p.batch; b += kAll / 32) {
-    const int heirs = __ldcg(p.heirs + b);
-    if (heirs < 0) continue;
+    const int n = heirs[b];
+    if (n == 1 || __ldcg(p.valid + b) == 0) continue;
     const int len = p.seqlens[b], full = len >> p.page_shift;
     const int* row = p.table + b * p.table_stride;
-    if (heirs != 1)
-      for (int j = lane; j < full; j += 32) atomicAdd(p.refs_out + row[j], heirs - 1);
-    if (heirs == 0 && (len & part_mask) != 0 && lane == 0) atomicAdd(p.refs_out + row[full], -1);
+    for (int j = lane; j < full; j += 32) atomicAdd(p.refs_out + row[j], n - 1);
+    if (n == 0 && (len & part_mask) != 0 && lane == 0) atomicAdd(p.refs_out + row[full], -1);
   }
   cluster_sync();
 
-  // ---- the lowest free pages, as many as are needed, in order ----
+  // ---- the lowest free pages go to the rows in order ----
   const PageRun run = page_run(p, rank);
   int mine = 0;
   for (int64_t i = run.begin; i < run.end; ++i) mine += __ldcg(p.refs_out + i) <= 0;
-  long long total;
-  long long at = block_scan(mine, warp_sum, total) - mine;
-  if (threadIdx.x == 0) p.head->count[rank] = static_cast<int>(total);
-  cluster_sync();
-  long long free_pages = 0;
-#pragma unroll
-  for (int i = 0; i < kCluster; ++i) {
-    const int n = __ldcg(&p.head->count[i]);
-    if (i < rank) at += n;
-    free_pages += n;
+  long long at;
+  const int free_pages = cluster_scan(p, rank, mine, warp_sum, at);
+  for (int64_t i = run.begin; i < run.end && mine > 0 && at < needed; ++i) {
+    if (__ldcg(p.refs_out + i) > 0) continue;
+    const int page = static_cast<int>(i), place = static_cast<int>(at++);
+    --mine;
+    int lo = 0, hi = p.rows - 1;  // the last row that starts at `place` or before
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (start[mid] <= place) lo = mid;
+      else hi = mid - 1;
+    }
+    if (start[lo + 1] > free_pages) continue;  // too few for the row
+    const ForkRow w = fork_row(p, lo);
+    const bool copy = copies(w, lo);
+    const int kept = w.held - (copy ? 1 : 0), j = kept + place - start[lo];
+    p.table_out[lo * p.out_stride + j] = page;
+    p.refs_out[page] = 1;
+    if (copy && j == kept) {
+      const int c = atomicAdd(&p.head->copies, 1);  // in any order: they are independent
+      p.src[c] = p.table[w.src * p.table_stride + kept];
+      p.dst[c] = page;
+      p.tokens[c] = w.len & part_mask;
+    }
   }
-  const long long need = __ldcg(&p.head->need);
-  for (int64_t i = run.begin; i < run.end && mine > 0 && at < need; ++i)
-    if (__ldcg(p.refs_out + i) <= 0) p.list[at++] = static_cast<int>(i);
-  cluster_sync();
+  const bool some_fail = needed > free_pages;
+  if (some_fail) cluster_sync();  // counts are lowered below, above they have been read
 
-  // ---- a warp writes a row ----
+  // ---- a warp writes the rest of a row ----
   for (int r = warp; r < p.rows; r += kAll / 32) {
     const ForkRow w = fork_row(p, r);
-    const long long packed = __ldcg(p.start + r);
-    const long long start = packed >> kCopyBits;
-    const bool part = (w.len & part_mask) != 0;
-    const bool heir = w.src >= 0 && __ldcg(p.first + w.src) == r;
-    const bool copy = w.src >= 0 && part && !heir;
-    const int kept = w.held - (copy ? 1 : 0);
-    const int fresh = w.total - kept;
-    const bool fails = fresh > 0 && start + fresh > free_pages;
+    const int kept = w.held - (copies(w, r) ? 1 : 0);
+    const bool fails = start[r + 1] > start[r] && start[r + 1] > free_pages;
     const int* row = p.table + (w.src >= 0 ? w.src : 0) * p.table_stride;
     int* out = p.table_out + r * p.out_stride;
-    if (fails && lane == 0 && start <= free_pages) paged_error(p.status, kSitePagedFull, r);
-    for (int j = lane; j < p.max_pages; j += 32) {
-      int page = -1;
-      if (j < kept) {
-        page = row[j];
-        if (fails) {  // the row stays empty: it gives back what it shares
-          if (j < w.len >> p.page_shift || heir) atomicAdd(p.refs_out + page, -1);
-          page = -1;
-        }
-      } else if (j < w.total && !fails) {
-        page = __ldcg(p.list + start + (j - kept));
-        p.refs_out[page] = 1;
-      }
-      out[j] = page;
-    }
     if (lane == 0) {
-      p.seqlens_out[r] = fails || w.bad ? 0 : w.len + (p.grow != nullptr ? p.grow[r] : 0);
-      if (copy) {
-        const int c = static_cast<int>(packed & ((1 << kCopyBits) - 1));
-        p.src[c] = fails ? -1 : row[kept];
-        p.dst[c] = fails ? -1 : __ldcg(p.list + start);
-        p.tokens[c] = w.len & part_mask;
-      }
+      p.seqlens_out[r] = fails ? 0 : w.len + w.grow;
+      if (fails && start[r] <= free_pages) paged_error(p.status, kSitePagedFull, r);
+    }
+    for (int j = lane; j < p.max_pages; j += 32) {
+      if (j < kept && !fails) out[j] = row[j];
+      else if (j >= w.total || fails) out[j] = -1;
+      // a row without enough pages gives back what it shares, a first heir the page that is partly filled too
+      if (j < kept && fails && (j < w.len >> p.page_shift || first[w.src] == r)) atomicAdd(p.refs_out + row[j], -1);
     }
   }
 }
@@ -258,52 +266,31 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   const PageRun run = page_run(p, rank);
   int mine = 0;
   for (int64_t i = run.begin; i < run.end; ++i) mine += p.refs[i] > 0;
-  long long total;
-  long long before = block_scan(mine, warp_sum, total) - mine;
-  if (threadIdx.x == 0) p.head->count[rank] = static_cast<int>(total);
-  cluster_sync();
-  int used = 0;
-#pragma unroll
-  for (int i = 0; i < kCluster; ++i) {
-    const int n = __ldcg(&p.head->count[i]);
-    if (i < rank) before += n;
-    used += n;
-  }
-  // those among the first `used`
-  if (run.begin <= used && used < run.end) {
-    int low = static_cast<int>(before);
-    for (int64_t i = run.begin; i < used; ++i) low += p.refs[i] > 0;
-    p.head->used_low = low;
-  }
+  long long before;
+  const int used = cluster_scan(p, rank, mine, warp_sum, before);
   if (tid == 0) {
-    if (used == p.num_pages) p.head->used_low = used;
     p.used[0] = used;
+    if (used == p.num_pages) p.head->skip = used;
   }
-  cluster_sync();
-  const int low = __ldcg(&p.head->used_low);
-  // ---- pages behind go to the holes before, both in order ----
+  // ---- pages behind go to the holes before, both in order; the k-th page in use stands at src[k] if it is behind ----
   for (int64_t i = run.begin; i < run.end; ++i) {
-    const bool in_use = p.refs[i] > 0;
+    const int n = p.refs[i];
+    if (i == used) p.head->skip = static_cast<int>(before);  // pages in use that stay
     if (i < used) {
-      if (!in_use) p.dst[i - before] = static_cast<int>(i);
-    } else if (in_use) {
-      p.src[before - low] = static_cast<int>(i);
-    }
-    p.page_map[i] = in_use ? static_cast<int>(i) : -1;
-    before += in_use;
-  }
-  cluster_sync();
-  // counts of the pages that stay and of the free ones behind, then of those that move (refs_out may be refs)
-  for (int i = tid; i < p.num_pages; i += kAll)
-    if (i < used) {
-      if (__ldcg(p.page_map + i) >= 0) p.refs_out[i] = p.refs[i];
-    } else if (__ldcg(p.page_map + i) < 0) {
+      if (n > 0) p.refs_out[i] = n;
+      else p.dst[i - before] = static_cast<int>(i);
+    } else if (n > 0) {
+      p.src[before] = static_cast<int>(i);
+    } else {
       p.refs_out[i] = 0;
     }
+    p.page_map[i] = n > 0 ? static_cast<int>(i) : -1;
+    before += n > 0;
+  }
   cluster_sync();
-  const int moves = used - low;
+  const int skip = __ldcg(&p.head->skip), moves = used - skip;
   for (int i = tid; i < moves; i += kAll) {
-    const int from = __ldcg(p.src + i), to = __ldcg(p.dst + i);
+    const int from = __ldcg(p.src + skip + i), to = __ldcg(p.dst + i);
     const int n = p.refs[from];
     p.refs_out[to] = n;
     p.refs_out[from] = 0;
@@ -315,7 +302,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   // ---- the table follows ----
   for (int b = warp; b < p.batch; b += kAll / 32) {
     const int len = p.seqlens[b];
-    const bool fits = len >= 0 && len <= static_cast<int64_t>(p.max_pages) << p.page_shift;
+    const bool fits = length_fits(p, len);
     const int pages = fits ? static_cast<int>((static_cast<int64_t>(len) + (1 << p.page_shift) - 1) >> p.page_shift) : 0;
     const int* row = p.table + b * p.table_stride;
     int* out = p.table_out + b * p.out_stride;
@@ -378,13 +365,13 @@ __global__ void __launch_bounds__(32 * kCopyWarps, kCopyBlocks) kv_copy_kernel(c
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int64_t units = static_cast<int64_t>(p.head->copies) * p.heads * 2;
+  const int* src_pages = p.src + p.head->skip;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kCopyWarps;
   for (int64_t u = static_cast<int64_t>(blockIdx.x) * kCopyWarps + (threadIdx.x >> 5); u < units; u += step) {
     const int x = static_cast<int>(u & 1);
     const int64_t copy = (u >> 1) / p.heads;
     const int head = static_cast<int>((u >> 1) - copy * p.heads);
-    const int from = p.src[copy], to = p.dst[copy];
-    if (from < 0) continue;
+    const int from = src_pages[copy], to = p.dst[copy];
     const int tokens = p.tokens != nullptr ? p.tokens[copy] : p.page;
     const uint8_t* src = p.base[x] + from * p.page_stride[x] + head * p.head_stride[x];
     uint8_t* dst = p.base[x] + to * p.page_stride[x] + head * p.head_stride[x];
@@ -399,25 +386,22 @@ __global__ void __launch_bounds__(32 * kCopyWarps, kCopyBlocks) kv_copy_kernel(c
 }
 
 struct PagesWorkspace {
-  size_t head, heirs, first, start, list, src, dst, tokens, bytes;
+  size_t head, valid, src, dst, tokens, bytes;
 };
 PagesWorkspace pages_workspace(int batch, int rows, int num_pages) {
   PagesWorkspace w;
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t here = at;
-    at += up256(n);
+    at += up256(n * sizeof(int));
     return here;
   };
   const size_t copies = static_cast<size_t>(rows > num_pages ? rows : num_pages);
-  w.head = take(sizeof(PagesHead));
-  w.heirs = take(sizeof(int) * batch);
-  w.first = take(sizeof(int) * batch);
-  w.start = take(sizeof(long long) * rows);
-  w.list = take(sizeof(int) * num_pages);
-  w.src = take(sizeof(int) * copies);
-  w.dst = take(sizeof(int) * copies);
-  w.tokens = take(sizeof(int) * rows);
+  w.head = take(sizeof(PagesHead) / sizeof(int));
+  w.valid = take(batch);
+  w.src = take(copies);
+  w.dst = take(copies);
+  w.tokens = take(rows);
   w.bytes = at;
   return w;
 }
@@ -425,10 +409,7 @@ PagesWorkspace pages_workspace(int batch, int rows, int num_pages) {
 void pages_fill(PagesParams& p, uint8_t* ws, int batch, int rows, const fa_kv_cache& c) {
   const PagesWorkspace w = pages_workspace(batch, rows, c.num_pages);
   p.head = reinterpret_cast<PagesHead*>(ws + w.head);
-  p.heirs = reinterpret_cast<int*>(ws + w.heirs);
-  p.first = reinterpret_cast<int*>(ws + w.first);
-  p.start = reinterpret_cast<long long*>(ws + w.start);
-  p.list = reinterpret_cast<int*>(ws + w.list);
+  p.valid = reinterpret_cast<int*>(ws + w.valid);
   p.src = reinterpret_cast<int*>(ws + w.src);
   p.dst = reinterpret_cast<int*>(ws + w.dst);
   p.tokens = reinterpret_cast<int*>(ws + w.tokens);
@@ -533,7 +514,10 @@ int fa_kv_fork(const fa_kv_cache* cache, void* k_bounds, const int* page_refs, i
   p.seqlens_out = seqlens_out;
   p.refs_out = refs_out;
   p.status = host.status;
-  kv_fork_kernel<<<kCluster, kThreads, 0, stream>>>(p);
+  static bool ready[64] = {};
+  rc = allow_smem(reinterpret_cast<const void*>(kv_fork_kernel), sizeof(int) * (3 * kMaxBatch + 1), ready);
+  if (rc != FA_OK) return rc;
+  kv_fork_kernel<<<kCluster, kThreads, sizeof(int) * (2 * static_cast<size_t>(batch) + rows + 1), stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   return copy_launch(p, c, static_cast<uint8_t*>(k_bounds), false, host.sms, stream);
 }

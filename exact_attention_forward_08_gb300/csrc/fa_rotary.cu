@@ -6,7 +6,9 @@
 // only the part behind the point counts: F_i as a 64-bit fraction times p, taken
 // modulo 2^64, is that part, exact but for F_i's own rounding.  The nearest
 // quarter turn is split off as an integer, so the sine and cosine are taken of an
-// angle of at most an eighth of a turn that has all its 24 bits, at any position.
+// angle x of at most an eighth of a turn that has all its 24 bits, at any position:
+// by Taylor's series, to x^9 and x^10, whose next terms are below 2^-28 and 2^-33 of
+// the values there.
 //
 // Rotation.  A pair (a, b) becomes (a cos - b sin, b cos + a sin) in fp32, each
 // product and sum rounded by itself, then rounded to bf16; the gradient turns
@@ -54,10 +56,20 @@ __global__ void __launch_bounds__(kTableThreads) rotary_table_kernel(const __gri
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint64_t t = static_cast<uint64_t>(pos) * turn[k];
-      const uint64_t quarter = (t + (1ull << 61)) >> 62;
-      const float x = __ll2float_rn(static_cast<long long>(t - (quarter << 62))) * 0x1p-63f;  // half turns
-      float sx, cx;
-      sincospif(x, &sx, &cx);
+      const uint32_t quarter = static_cast<uint32_t>((t + (1ull << 61)) >> 62);
+      const uint64_t rest = t - (static_cast<uint64_t>(quarter) << 62);  // signed, of 2^64 a turn
+      const float x = fmaf(static_cast<float>(static_cast<int>(rest >> 32)), 0x1p-32f * 6.28318530717958647692f,
+                           static_cast<float>(static_cast<uint32_t>(rest)) * (0x1p-64f * 6.28318530717958647692f));
+      const float x2 = x * x;
+      float sx = fmaf(x2, 1.f / 362880.f, -1.f / 5040.f);
+      sx = fmaf(sx, x2, 1.f / 120.f);
+      sx = fmaf(sx, x2, -1.f / 6.f);
+      sx = fmaf(sx * x2, x, x);
+      float cx = fmaf(x2, -1.f / 3628800.f, 1.f / 40320.f);
+      cx = fmaf(cx, x2, -1.f / 720.f);
+      cx = fmaf(cx, x2, 1.f / 24.f);
+      cx = fmaf(cx, x2, -0.5f);
+      cx = fmaf(cx, x2, 1.f);
       const float a = quarter & 1 ? sx : cx, b = quarter & 1 ? cx : sx;
       c[k] = p.magnitude * ((quarter + 1) & 2 ? -a : a);
       s[k] = p.magnitude * (quarter & 2 ? -b : b);

@@ -9,9 +9,9 @@
 // one product of length 2 d whatever the number of query heads.
 //
 // Which pages have the largest scores has to be decided exactly, equal scores by
-// the lowest index, and not by how fp32 rounds.  So scores are computed in fp32
-// and kept with 20 bits of their fraction; their error is below a bound eps known
-// from the inputs, and with T the k-th largest of them every page above T + 2 eps
+// the lowest index, and not by how fp32 rounds.  So scores are computed on the
+// tensor cores with sums in fp32 and kept with 20 bits of their fraction; their
+// error is below a bound eps known from the inputs, and with T the k-th largest of them every page above T + 2 eps
 // is in and every page below T - 2 eps is out.  The others, mostly none, get
 // scores in fp64, where sums of products of 8-bit and 4-bit fractions are exact
 // for all but extreme ranges.
@@ -23,6 +23,7 @@
 #include <cuda_runtime.h>
 
 #include <climits>
+#include <cstddef>
 #include <cstring>
 
 #include "fa.h"
@@ -155,7 +156,7 @@ cudaError_t bounds_launch(const BoundsParams& p, cudaStream_t stream) {
 }
 
 // ---------------------------------------------------------------------------
-// scores
+// selection
 // ---------------------------------------------------------------------------
 
 struct SelectParams {
@@ -169,42 +170,58 @@ struct SelectParams {
   unsigned int* status;
   uint32_t* keys;    // [total][heads][width] scores as ordered integers
   uint64_t* exact;   // the same in 64 bits, where they were needed
-  uint8_t* top_e;    // [batch][heads][groups] largest scale of 8 pages
+  int* top_e;        // [batch][heads][tiles] largest scale of a tile's pages
   int* lists;        // [total][heads][top]
   int* list_lens;    // [total]
   int64_t total;
   int batch, heads, ratio, num_pages, max_pages, page_shift, max_n, causal, top, first, last;
-  int width, groups;  // pages and groups of 8 pages that rows are laid out for
+  int tiles;     // of a sequence and head
+  double error;  // of a score, in terms of the largest that it could be
 };
 
-constexpr int kScoreWarps = 8, kScoreThreads = 32 * kScoreWarps;
-constexpr int kWarpPages = 8, kTilePages = kWarpPages * kScoreWarps;
+constexpr int kSelectWarps = 8, kSelectThreads = 32 * kSelectWarps;
+constexpr int kScoreBlocks = 4;    // of an SM
+constexpr int kChunk = 8;          // tokens whose queries a block holds
+constexpr int kWarpPages = 16;     // pages of a warp
+constexpr int kTilePages = kSelectWarps * kWarpPages;
+constexpr int kStagePages = 4096;  // keys of a token that are kept in shared memory
 
 struct SelectSeq {
-  int c0, n, len, pages;  // pages 0: no scores
+  int c0, n, len;
 };
 __device__ __forceinline__ SelectSeq select_seq(const SelectParams& p, int b, bool& bad) {
   SelectSeq s;
   s.c0 = p.cu[b];
   s.len = p.seqlens[b];
   bad = !paged_attend_range(s.c0, p.cu[b + 1], s.len, p.total, p.max_n, static_cast<int64_t>(p.max_pages) << p.page_shift, s.n);
-  const int round = (1 << p.page_shift) - 1;
-  s.pages = bad || s.n == 0 ? 0 : (s.len + round) >> p.page_shift;
   return s;
 }
+// tokens that new token i of a sequence sees
+__device__ __forceinline__ int select_seen(const SelectParams& p, const SelectSeq& s, int i) {
+  const int seen = p.causal ? s.len - s.n + i + 1 : s.len;
+  return seen < 0 ? 0 : seen;
+}
 
-// A score's place in the order: the upper half of its double's bits, made ordered.  NaN counts as +inf.
-__device__ __forceinline__ uint32_t score_key(double x) {
-  const uint32_t h = x != x ? 0x7ff00000u : static_cast<uint32_t>(__double2hiint(x));
-  return h & 0x80000000u ? ~h : h | 0x80000000u;
+// A score's place in the order: the upper half of the bits of x 2^shift as a double, made ordered.  NaN counts as
+// +inf; what is subnormal in fp32 is far below the error of a score and counts as 0.
+__device__ __forceinline__ uint32_t score_key(float x, int shift) {
+  const uint32_t u = __float_as_uint(x), e = (u >> 23) & 0xffu;
+  if (e == 0) return 0x80000000u;  // of either sign
+  const uint32_t h = e == 255 ? 0x7ff00000u : ((e + static_cast<uint32_t>(1023 - 127 + shift)) << 20) | ((u & 0x7fffffu) >> 3);
+  const bool negative = u >> 31 && !(e == 255 && (u & 0x7fffffu) != 0);
+  return negative ? ~(h | 0x80000000u) : h | 0x80000000u;
 }
 __device__ __forceinline__ double key_score(uint32_t k) {
   return __hiloint2double(static_cast<int>(k & 0x80000000u ? k ^ 0x80000000u : ~k), 0);
 }
-// the same of all 64 bits; both zeros are one
-__device__ __forceinline__ uint64_t score_key64(double x) {
+// all 64 bits of a double made ordered; NaN counts as +inf, both zeros are one
+__device__ __forceinline__ uint64_t order64(double x) {
   const uint64_t h = x != x ? 0x7ff0000000000000ull : static_cast<uint64_t>(__double_as_longlong(x + 0.0));
   return h >> 63 ? ~h : h | (1ull << 63);
+}
+// order64 of the score that a key stands for
+__device__ __forceinline__ uint64_t key_order64(uint32_t k) {
+  return static_cast<uint64_t>(k) << 32 | (k & 0x80000000u ? 0u : 0xffffffffu);
 }
 
 // 2^(e - 127) of an e8m0 byte; 255 is NaN
@@ -212,386 +229,367 @@ __device__ __forceinline__ double scale_double(int e) {
   return e == 255 ? __longlong_as_double(0x7ff8000000000000ll) : __longlong_as_double(static_cast<long long>(e - 127 + 1023) << 52);
 }
 
-// The power of two that brings queries whose largest biased exponent is `top` to at most 1; and its inverse.
-__device__ __forceinline__ float query_down(int top) {
-  return top >= 253 ? 0x1p-126f : top < 1 ? 0x1p126f : __uint_as_float(static_cast<uint32_t>(253 - top) << 23);
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))), "l"(src)
+               : "memory");
 }
-__device__ __forceinline__ double query_up(int top) {
-  return top >= 253 ? 0x1p126 : top < 1 ? 0x1p-126 : __longlong_as_double(static_cast<long long>(top - 126 + 1023) << 52);
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// waits until at most N of this thread's groups of copies are under way
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-
-// D / 16 codes of a page that belong to a lane
-template <int D>
-struct LaneCodes {
-  uint32_t w[D / 64];
-};
-template <int D>
-__device__ __forceinline__ LaneCodes<D> load_lane_codes(const uint8_t* row, int lane) {
-  LaneCodes<D> c;
-  if constexpr (D == 64) {
-    c.w[0] = __ldg(reinterpret_cast<const uint32_t*>(row) + lane);
-  } else {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(row) + lane);
-    c.w[0] = v.x, c.w[1] = v.y;
-    if constexpr (D == 192) c.w[2] = __ldg(reinterpret_cast<const uint32_t*>(row + 256) + lane);
-  }
-  return c;
-}
-// the place in a page's 2 D bounds of code i of a lane
-template <int D>
-__device__ __forceinline__ int lane_column(int lane, int i) {
-  if constexpr (D == 64) return 4 * lane + i;
-  return i < 8 ? 8 * lane + i : 256 + 4 * lane + (i - 8);
-}
-
-// TOK tokens at a time.  Blocks take equal runs of the line of tiles of 64 pages
-// of all sequences and heads; a warp has 8 pages, whose codes it loads together
-// and multiplies lane by lane, D / 16 codes each, the sums of 8 pages crossing the
-// warp in 9 exchanges.
-template <int D, int TOK>
-__global__ void __launch_bounds__(kScoreThreads, TOK == 1 ? 4 : 2) select_score_kernel(const __grid_constant__ SelectParams p) {
-  constexpr int kCodes = D / 16;
-  __shared__ float qs[TOK][2 * D];
-  __shared__ int q_top[TOK];
-  __shared__ long long scan[kScoreThreads], warp_sum[kScoreWarps];
-  __shared__ int begin_b, begin_head, begin_tile;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-  // ---- the run of this block ----
-  auto scan_block = [&](int base) -> long long {
-    long long v = 0;
-    if (base + tid < p.batch) {
-      bool bad;
-      const SelectSeq s = select_seq(p, base + tid, bad);
-      if (bad && blockIdx.x == 0) paged_error(p.status, kSitePagedSeq, base + tid);
-      v = static_cast<long long>((s.pages + kTilePages - 1) / kTilePages) * p.heads;
-    }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += y;
-    }
-    __syncthreads();
-    if (lane == 31) warp_sum[warp] = v;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) v += warp_sum[w];
-    scan[tid] = v;
-    __syncthreads();
-    return scan[kScoreThreads - 1];
-  };
-  long long total = 0;
-  for (int base = 0; base < p.batch; base += kScoreThreads) total += scan_block(base);
-  const long long per = (total + gridDim.x - 1) / gridDim.x, x0 = per * blockIdx.x;
-  const long long x1 = x0 + per < total ? x0 + per : total;
-  if (x0 >= x1) return;
-  long long offset = 0;
-  for (int base = 0; base < p.batch; base += kScoreThreads) {
-    if (p.batch > kScoreThreads) scan_block(base);
-    const long long before = offset + (tid > 0 ? scan[tid - 1] : 0), upto = offset + scan[tid];
-    if (before <= x0 && x0 < upto) {
-      bool bad;
-      const SelectSeq s = select_seq(p, base + tid, bad);
-      const int tiles = (s.pages + kTilePages - 1) / kTilePages;
-      begin_b = base + tid;
-      begin_head = static_cast<int>((x0 - before) / tiles);
-      begin_tile = static_cast<int>((x0 - before) % tiles);
-    }
-    offset += scan[kScoreThreads - 1];
-  }
-  __syncthreads();
-
-  int b = begin_b, head = begin_head, tile = begin_tile;
-  bool bad;
-  SelectSeq s = select_seq(p, b, bad);
-  int loaded_b = -1, loaded_head = -1, loaded_token = -1;
-  for (long long x = x0; x < x1; ++x) {
-    const int j0 = tile * kTilePages + warp * kWarpPages;
-    const int count = s.pages - j0 < kWarpPages ? s.pages - j0 : kWarpPages;  // pages of this warp
-    int entry = -1, e = 0;
-    if (lane < count) {
-      entry = p.table[b * p.table_stride + j0 + lane];
-      if (entry < 0 || entry >= p.num_pages) {
-        paged_error(p.status, kSitePagedPage, b);
-        entry = -1;
-      } else {
-        e = p.k_scale[static_cast<int64_t>(entry) * p.heads + head];
-      }
-    }
-    LaneCodes<D> codes[kWarpPages];
-#pragma unroll
-    for (int k = 0; k < kWarpPages; ++k) {
-      const int page = __shfl_sync(0xffffffffu, entry, k);
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i) codes[k].w[i] = 0;
-      if (page >= 0) codes[k] = load_lane_codes<D>(p.bounds + (static_cast<int64_t>(page) * p.heads + head) * 2 * D, lane);
-    }
-    if (count > 0) {
-      const int top = __reduce_max_sync(0xffffffffu, e == 255 ? 0 : e);
-      if (lane == 0)
-        p.top_e[(static_cast<int64_t>(b) * p.heads + head) * p.groups + j0 / kWarpPages] = static_cast<uint8_t>(top);
-    }
-
-    for (int t0 = 0; t0 < s.n; t0 += TOK) {
-      if (b != loaded_b || head != loaded_head || t0 != loaded_token) {
-        // ---- q+ and q- of TOK tokens ----
-        __syncthreads();
-        for (int w = warp; w < TOK; w += kScoreWarps) {
-          const bool there = t0 + w < s.n;
-          const __nv_bfloat16* row = p.q + ((static_cast<int64_t>(s.c0) + t0 + w) * p.heads + head) * p.ratio * D;
-          uint32_t top = 0;
-          if (there)
-            for (int i = lane; i < p.ratio * D / 8; i += 32) {
-              const uint4 v = __ldg(reinterpret_cast<const uint4*>(row) + i);
-              const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) top = max(top, max(u[k] & 0x7f80u, (u[k] >> 16) & 0x7f80u));
-            }
-          top = __reduce_max_sync(0xffffffffu, top) >> 7;
-          if (lane == 0) q_top[w] = static_cast<int>(top);
-          const float down = query_down(static_cast<int>(top));
-          for (int i = lane; i < D / 2; i += 32) {
-            float pos0 = 0.f, pos1 = 0.f, neg0 = 0.f, neg1 = 0.f;
-            if (there)
-              for (int h = 0; h < p.ratio; ++h) {
-                const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(row + h * D) + i);
-                const float a = __uint_as_float(u << 16) * down, c = __uint_as_float(u & 0xffff0000u) * down;
-                // a NaN goes into both
-                pos0 += a < 0.f ? 0.f : a, neg0 += a > 0.f ? 0.f : a;
-                pos1 += c < 0.f ? 0.f : c, neg1 += c > 0.f ? 0.f : c;
-              }
-            *reinterpret_cast<float2*>(&qs[w][2 * i]) = make_float2(pos0, pos1);
-            *reinterpret_cast<float2*>(&qs[w][D + 2 * i]) = make_float2(neg0, neg1);
-          }
-        }
-        loaded_b = b, loaded_head = head, loaded_token = t0;
-        __syncthreads();
-      }
-      if (count <= 0) continue;
-      float q[TOK][kCodes], acc[TOK][kWarpPages];
-#pragma unroll
-      for (int t = 0; t < TOK; ++t)
-#pragma unroll
-        for (int i = 0; i < kCodes; i += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(&qs[t][lane_column<D>(lane, i)]);
-          q[t][i] = v.x, q[t][i + 1] = v.y, q[t][i + 2] = v.z, q[t][i + 3] = v.w;
-        }
-#pragma unroll
-      for (int k = 0; k < kWarpPages; ++k) {
-        float x[kCodes];
-#pragma unroll
-        for (int i = 0; i < kCodes / 4; ++i) {
-          const float2 f0 = f16x2_float2(e4m3x2_f16x2(codes[k].w[i])), f1 = f16x2_float2(e4m3x2_hi_f16x2(codes[k].w[i]));
-          x[4 * i] = f0.x, x[4 * i + 1] = f0.y, x[4 * i + 2] = f1.x, x[4 * i + 3] = f1.y;
-        }
-#pragma unroll
-        for (int t = 0; t < TOK; ++t) {
-          float a = x[0] * q[t][0];
-#pragma unroll
-          for (int i = 1; i < kCodes; ++i) a = fmaf(x[i], q[t][i], a);
-          acc[t][k] = a;
-        }
-      }
-      // lane l ends with the sum of page (l >> 4 & 1) * 4 + (l >> 3 & 1) * 2 + (l >> 2 & 1)
-      const int mine = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
-      const int e_mine = __shfl_sync(0xffffffffu, e, mine), entry_mine = __shfl_sync(0xffffffffu, entry, mine);
-#pragma unroll
-      for (int t = 0; t < TOK; ++t) {
-        float(&a)[kWarpPages] = acc[t];
-#pragma unroll
-        for (int half = 4; half >= 1; half >>= 1) {
-          const bool upper = (lane & (4 * half)) != 0;
-#pragma unroll
-          for (int k = 0; k < half; ++k) {
-            const float give = upper ? a[k] : a[k + half];
-            const float keep = upper ? a[k + half] : a[k];
-            a[k] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * half);
-          }
-        }
-        float sum = a[0];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        if ((lane & 3) == 0 && mine < count && t0 + t < s.n) {
-          const uint32_t key = entry_mine < 0 ? 0u : score_key(static_cast<double>(sum) * scale_double(e_mine) * query_up(q_top[t]));
-          p.keys[((static_cast<int64_t>(s.c0) + t0 + t) * p.heads + head) * p.width + j0 + mine] = key;
-        }
-      }
-    }
-    // ---- the next tile ----
-    if (x + 1 < x1 && ++tile * kTilePages >= s.pages) {
-      tile = 0;
-      if (++head == p.heads) {
-        head = 0;
-        do s = select_seq(p, ++b, bad);
-        while (s.pages == 0 && b + 1 < p.batch);
-      }
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------
-// the choice
-// ---------------------------------------------------------------------------
-
-constexpr int kChooseWarps = 8, kChooseThreads = 32 * kChooseWarps;
-constexpr int kStagePages = 4096;  // keys of a row that are kept in shared memory
 
 // Sum over the block; two buffers by turns, one barrier a call.
-__device__ __forceinline__ int block_sum(int v, int (*buffer)[kChooseWarps], int& turn) {
+__device__ __forceinline__ int block_sum(int v, int (*buffer)[kSelectWarps], int& turn) {
   v = __reduce_add_sync(0xffffffffu, v);
   if ((threadIdx.x & 31) == 0) buffer[turn][threadIdx.x >> 5] = v;
   __syncthreads();
   int sum = 0;
 #pragma unroll
-  for (int w = 0; w < kChooseWarps; ++w) sum += buffer[turn][w];
+  for (int w = 0; w < kSelectWarps; ++w) sum += buffer[turn][w];
   turn ^= 1;
   return sum;
 }
 
+constexpr int kTokens = 4;    // tokens of one product: a column for the upper and one for the lower part of each
+constexpr int kQueryTop = 14; // q+ and q- are brought below 2^14
+
+template <int D>
+struct ScoreShared {
+  static constexpr int kRow = 2 * D * 2 + 16;  // bytes of a column: neighbours fall on other banks
+  alignas(16) uint8_t q[kChunk][2][kRow];      // f16 upper and lower parts of q+ and q- of each token
+  alignas(16) uint8_t codes[kSelectWarps][kWarpPages][2 * D];
+  int q_shift[kChunk];  // the power of two that they were divided by
+  int top_e;
+};
+
+// Where 16-byte chunk `chunk` of a page's bounds lies: two rows read together meet no bank twice.
+template <int D>
+__device__ __forceinline__ int code_place(int row, int chunk) {
+  return row * 2 * D + ((chunk ^ ((row & 1) << 2)) << 4);
+}
+
+__device__ __forceinline__ void mma_16x8x16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A block takes 128 pages of a sequence and one key head, 16 a warp, whose bounds it
+// asks for at once (4 KB a warp at d = 128) and keeps for all new tokens; it holds q+
+// and q- of 8 tokens at a time.  The codes are exact as f16; q+ and q- are the sums
+// of two f16, off by 2^-22 of themselves (2^-39 of the row's largest if that is
+// more).  So a warp's 16 pages are one operand of m16n8k16 products and 4 tokens,
+// an upper and a lower part each, the other, and a lane ends with both parts of a
+// token's score of two pages.  The order of columns is free: a lane takes those of
+// one 16-byte chunk for four products, which go to four sums.
+template <int D>
+__global__ void __launch_bounds__(kSelectThreads, kScoreBlocks) kv_score_kernel(const __grid_constant__ SelectParams p) {
+  static_assert(D % 64 == 0, "whole steps of four products");
+  using Shared = ScoreShared<D>;
+  static_assert(offsetof(Shared, codes) % 16 == 0 && Shared::kRow % 16 == 0, "16-byte copies");
+  extern __shared__ __align__(16) uint8_t smem[];
+  Shared& sh = *reinterpret_cast<Shared*>(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t bh = blockIdx.x / p.tiles;
+  const int tile = blockIdx.x - static_cast<int>(bh) * p.tiles;
+  const int b = static_cast<int>(bh / p.heads), head = static_cast<int>(bh - static_cast<int64_t>(b) * p.heads);
+  bool bad;
+  const SelectSeq s = select_seq(p, b, bad);
+  if (bad && tile == 0 && head == 0 && tid == 0) paged_error(p.status, kSitePagedSeq, b);
+  if (bad || s.n == 0) return;
+  const int round = (1 << p.page_shift) - 1;
+  const int pages = (select_seen(p, s, s.n - 1) + round) >> p.page_shift;  // that the last token sees
+  if (pages <= p.top || tile * kTilePages >= pages) return;
+
+  // ---- the pages ----
+  const int j0 = tile * kTilePages + warp * kWarpPages;
+  const int* row = p.table + b * p.table_stride;
+  int entry = -1;
+  if (lane < kWarpPages && j0 + lane < pages) {
+    entry = row[j0 + lane];
+    if (entry < 0 || entry >= p.num_pages) {
+      paged_error(p.status, kSitePagedPage, b);
+      entry = -1;
+    }
+  }
+  constexpr int kChunks = 2 * D / 16;
+  uint8_t* const codes = &sh.codes[warp][0][0];
+#pragma unroll
+  for (int k = 0; k < kWarpPages * kChunks / 32; ++k) {
+    const int i = 32 * k + lane, at = i / kChunks, chunk = i % kChunks;
+    const int page = __shfl_sync(0xffffffffu, entry, at);
+    if (page >= 0)
+      copy_async16(codes + code_place<D>(at, chunk),
+                   p.bounds + (static_cast<int64_t>(page) * p.heads + head) * 2 * D + chunk * 16);
+  }
+  copy_commit();
+  const int e = entry >= 0 ? p.k_scale[static_cast<int64_t>(entry) * p.heads + head] : 0;
+  if (tid == 0) sh.top_e = 0;
+  const int g = lane >> 2, c = lane & 3;
+  // this lane's pages of the result
+  const int e_g[2] = {__shfl_sync(0xffffffffu, e, g), __shfl_sync(0xffffffffu, e, g + 8)};
+  const int entry_g[2] = {__shfl_sync(0xffffffffu, entry, g), __shfl_sync(0xffffffffu, entry, g + 8)};
+
+  for (int t0 = 0; t0 < s.n; t0 += kChunk) {
+    const int tokens = s.n - t0 < kChunk ? s.n - t0 : kChunk;
+    const int64_t first_token = static_cast<int64_t>(s.c0) + t0;
+    if (t0 > 0) __syncthreads();
+    if (warp < tokens) {  // ---- q+ and q- ----
+      const __nv_bfloat16* q = p.q + ((first_token + warp) * p.heads + head) * p.ratio * D;
+      constexpr int kPairs = D / 64;  // pairs of columns of a lane
+      float pos[kPairs][2] = {}, neg[kPairs][2] = {};
+#pragma unroll 4
+      for (int h = 0; h < p.ratio; ++h)
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(q + h * D) + 32 * i + lane);
+          const float v[2] = {__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)};
+#pragma unroll
+          for (int x = 0; x < 2; ++x) pos[i][x] += v[x] < 0.f ? 0.f : v[x], neg[i][x] += v[x] > 0.f ? 0.f : v[x];  // a NaN goes into both
+        }
+      uint32_t top = 0;  // of their bits without signs
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) top = max(top, max(__float_as_uint(pos[i][x]), __float_as_uint(neg[i][x]) & 0x7fffffffu));
+      top = __reduce_max_sync(0xffffffffu, top) >> 23;
+      // 2^shift brings the largest, below 2^(top - 126), to 2^14; between 2^-126 and 2^127
+      int shift = kQueryTop + 126 - static_cast<int>(top);
+      shift = shift > 126 ? 126 : shift;
+      const float scale = __uint_as_float(static_cast<uint32_t>(shift + 127) << 23);
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i)
+#pragma unroll
+        for (int sign = 0; sign < 2; ++sign) {
+          const float u = (sign ? neg[i][0] : pos[i][0]) * scale, v = (sign ? neg[i][1] : pos[i][1]) * scale;
+          const __half2 upper = __floats2half2_rn(u, v);
+          const float2 back = __half22float2(upper);
+          const __half2 lower = __floats2half2_rn(u - back.x, v - back.y);
+          const int column = sign * D + 2 * (32 * i + lane);
+          *reinterpret_cast<__half2*>(&sh.q[warp][0][2 * column]) = upper;
+          *reinterpret_cast<__half2*>(&sh.q[warp][1][2 * column]) = lower;
+        }
+      if (lane == 0) sh.q_shift[warp] = shift;
+    }
+    if (t0 == 0) copy_wait<0>();
+    __syncthreads();
+    if (j0 >= pages) continue;
+#pragma unroll 1
+    for (int x0 = 0; x0 < tokens; x0 += kTokens) {
+      // column g of the second operand: part g & 1 of token x0 + g / 2 (of any content behind the last)
+      const uint8_t* q = &sh.q[x0 + (g >> 1)][g & 1][0];
+      float acc[4][4] = {};
+#pragma unroll 1
+      for (int st = 0; st < D / 32; ++st) {
+        const int chunk = 4 * st + c;
+        const uint4 lo = *reinterpret_cast<const uint4*>(codes + code_place<D>(g, chunk));
+        const uint4 hi = *reinterpret_cast<const uint4*>(codes + code_place<D>(g + 8, chunk));
+        const uint4 q0 = *reinterpret_cast<const uint4*>(q + 32 * chunk), q1 = *reinterpret_cast<const uint4*>(q + 32 * chunk + 16);
+        const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+        const uint32_t wq[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_16x8x16(acc[k], e4m3x2_f16x2(wl[k]), e4m3x2_f16x2(wh[k]), e4m3x2_hi_f16x2(wl[k]), e4m3x2_hi_f16x2(wh[k]),
+                      wq[2 * k], wq[2 * k + 1]);
+      }
+      const int x = x0 + c;  // this lane's token
+      if (x >= tokens) continue;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int j = j0 + g + 8 * half;
+        if (j >= pages) break;
+        const float upper = (acc[0][2 * half] + acc[1][2 * half]) + (acc[2][2 * half] + acc[3][2 * half]);
+        const float lower = (acc[0][2 * half + 1] + acc[1][2 * half + 1]) + (acc[2][2 * half + 1] + acc[3][2 * half + 1]);
+        const float sum = e_g[half] == 255 ? __uint_as_float(0x7fc00000u) : upper + lower;
+        p.keys[((first_token + x) * p.heads + head) * p.max_pages + j] =
+            entry_g[half] < 0 ? 0u : score_key(sum, e_g[half] - 127 - sh.q_shift[x]);
+      }
+    }
+  }
+  const int top_e = __reduce_max_sync(0xffffffffu, e == 255 ? 0 : e);
+  if (lane == 0) atomicMax(&sh.top_e, top_e);
+  __syncthreads();
+  if (tid == 0) p.top_e[bh * p.tiles + tile] = sh.top_e;
+}
+
+// ---- the choice ----
+
+constexpr int kBinBits = 11, kBins = 1 << kBinBits;
+
+struct ChooseShared {
+  uint32_t stage[kStagePages];  // keys
+  int bins[kBins], bin, rank;
+  double q[2 * 192];            // q+ and q- in 64 bits
+  int sums[2][kSelectWarps];
+  uint32_t least[kSelectWarps], most[kSelectWarps], near_low, near_high;
+  uint64_t least64[kSelectWarps], most64[kSelectWarps];
+  int count[kSelectWarps], ties[kSelectWarps], top_e[kSelectWarps];
+  float q_size[kSelectWarps];
+};
+
 // A block takes one token and key head.
 template <int D>
-__global__ void __launch_bounds__(kChooseThreads) select_choose_kernel(const __grid_constant__ SelectParams p) {
-  __shared__ uint32_t stage[kStagePages];
-  __shared__ double qd[2 * D];
-  __shared__ int sums[2][kChooseWarps];
-  __shared__ uint32_t least[kChooseWarps], most[kChooseWarps];
-  __shared__ uint64_t least64[kChooseWarps], most64[kChooseWarps];
-  __shared__ float q_sum[kChooseWarps];
-  __shared__ int warp_count[kChooseWarps], warp_ties[kChooseWarps];
+__global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_constant__ SelectParams p) {
+  __shared__ ChooseShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int turn = 0;
-  const int64_t unit = blockIdx.x;
-  const int64_t t = unit / p.heads;
+  const int64_t unit = blockIdx.x, t = unit / p.heads;
   const int head = static_cast<int>(unit - t * p.heads);
-
   const int b = warp_search(p.batch, t, [&](int i) { return p.cu[i]; });
   bool bad;
   const SelectSeq s = select_seq(p, b, bad);
-  if (bad || t < s.c0 || t >= s.c0 + s.n) {  // of no sequence: left as it is
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    return;
-  }
-  int seen = s.len;
-  if (p.causal) {
-    seen = s.len - s.n + static_cast<int>(t - s.c0) + 1;
-    seen = seen < 0 ? 0 : seen;
-  }
+  const bool mine = !bad && t >= s.c0 && t < s.c0 + s.n;
+  const int seen = mine ? select_seen(p, s, static_cast<int>(t - s.c0)) : 0;
   const int pages = (seen + (1 << p.page_shift) - 1) >> p.page_shift;
-  const int count = pages < p.top ? pages : p.top;
-  int* out = p.lists + unit * p.top;
-  if (head == 0 && tid == 0) p.list_lens[t] = seen - ((pages - count) << p.page_shift);
-  const int* row = p.table + b * p.table_stride;
+  const int* row = p.table + (mine ? b : 0) * p.table_stride;
   auto listed = [&](int j) {
     const int page = row[j];
     return page >= 0 && page < p.num_pages ? page : -1;
   };
-  for (int i = count + tid; i < p.top; i += kChooseThreads) out[i] = -1;
-  if (pages <= p.top) {
-    for (int i = tid; i < pages; i += kChooseThreads) out[i] = listed(i);
+  int* out = p.lists + unit * p.top;
+  if (mine && head == 0 && tid == 0) p.list_lens[t] = pages > p.top ? seen - ((pages - p.top) << p.page_shift) : seen;
+  if (pages <= p.top) {  // all of them; a token of no sequence is left as it is
+    for (int i = tid; mine && i < p.top; i += kSelectThreads) {
+      const int page = i < pages ? listed(i) : -1;
+      if (i < pages && page < 0) paged_error(p.status, kSitePagedPage, b);
+      out[i] = page;
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
   // pages first .. end - 1 compete for k places, which are fewer
   const int end = pages - p.last, k = p.top - p.first - p.last;
-
-  // ---- q+ and q- in 64 bits, and the bound of a score's error ----
+  const uint32_t* keys = p.keys + unit * p.max_pages;
+  uint64_t* exact = p.exact + unit * p.max_pages;
+  int turn = 0;
+  // the sum of the sizes of q+ and q-
+  float q_size = 0.f;
   {
-    const __nv_bfloat16* q = p.q + unit * p.ratio * D;
-    float part = 0.f;
-    for (int i = tid; i < D; i += kChooseThreads) {
-      double pos = 0.0, neg = 0.0;
-      for (int h = 0; h < p.ratio; ++h) {
-        const float a = __bfloat162float(q[h * D + i]);
-        pos += a < 0.f ? 0.0 : static_cast<double>(a), neg += a > 0.f ? 0.0 : static_cast<double>(a);
-      }
-      qd[i] = pos, qd[D + i] = neg;
-      part += __double2float_ru(pos) - __double2float_rd(neg);
+    const __nv_bfloat162* q = reinterpret_cast<const __nv_bfloat162*>(p.q + unit * p.ratio * D);
+    for (int i = tid; i < p.ratio * D / 2; i += kSelectThreads) {
+      const float2 v = __bfloat1622float2(q[i]);
+      q_size += fabsf(v.x) + fabsf(v.y);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-    if (lane == 0) q_sum[warp] = part;
+    for (int o = 16; o > 0; o >>= 1) q_size += __shfl_xor_sync(0xffffffffu, q_size, o);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores are there
-  const uint32_t* keys = p.keys + unit * p.width;
+  int top_e = 0;
+  {
+    const int* es = p.top_e + (static_cast<int64_t>(b) * p.heads + head) * p.tiles;
+    for (int i = tid; i * kTilePages < pages; i += kSelectThreads) top_e = max(top_e, __ldcg(es + i));
+    top_e = __reduce_max_sync(0xffffffffu, top_e);
+    if (lane == 0) sh.top_e[warp] = top_e, sh.q_size[warp] = q_size;
+  }
   uint32_t low = 0xffffffffu, high = 0;
   const bool staged = pages <= kStagePages;
-  for (int j = p.first + tid; j < end; j += kChooseThreads) {
-    const uint32_t x = __ldcg(keys + j);
-    if (staged) stage[j] = x;
-    low = min(low, x), high = max(high, x);
+  for (int j = p.first + tid; j < end; j += kSelectThreads) {
+    const uint32_t v = __ldcg(keys + j);
+    if (staged) sh.stage[j] = v;
+    low = min(low, v), high = max(high, v);
   }
-  int top_e = 0;
-  const uint8_t* es = p.top_e + (static_cast<int64_t>(b) * p.heads + head) * p.groups;
-  for (int i = tid; i < (pages + kWarpPages - 1) / kWarpPages; i += kChooseThreads) top_e = max(top_e, static_cast<int>(__ldcg(es + i)));
-  low = __reduce_min_sync(0xffffffffu, low);
-  high = __reduce_max_sync(0xffffffffu, high);
-  top_e = __reduce_max_sync(0xffffffffu, top_e);
-  if (lane == 0) least[warp] = low, most[warp] = high, warp_count[warp] = top_e;
-  __syncthreads();
-  double size = 0.0;
-#pragma unroll
-  for (int w = 0; w < kChooseWarps; ++w) {
-    low = min(low, least[w]), high = max(high, most[w]);
-    top_e = max(top_e, warp_count[w]);
-    size += q_sum[w];
-  }
-  auto key = [&](int j) { return staged ? stage[j] : __ldcg(keys + j); };
-  // No score is larger than `size`.  Of it, the sums of q+ and q- are off by `ratio` roundings of 2^-24, the products
-  // and their sum by 12 + 5, and the key drops what is below 2^-20; a few more for the rounding of `size` itself.
-  size *= 448.0 * scale_double(top_e);
-  const double margin = 2.0 * size * ((p.ratio + 24) * 0x1p-24 + 0x1p-20);
+  auto key = [&](int j) { return staged ? sh.stage[j] : __ldcg(keys + j); };
 
-  // ---- the least key of the k largest: [lo, hi) keeps count(>= lo) >= k > count(>= hi) ----
-  uint32_t lo = low, hi = high;  // hi: one below it, so that it fits
-  bool split = false;
-  int at_least = end - p.first;
-  while (k > 0 && !split && lo < hi) {
-    const uint32_t mid = lo + (hi - lo) / 2 + 1;
-    int n = 0;
-    for (int j = p.first + tid; j < end; j += kChooseThreads) n += key(j) >= mid;
-    n = block_sum(n, sums, turn);
-    if (n >= k) lo = mid, at_least = n, split = n == k;
-    else hi = mid - 1;
-  }
-  uint32_t cut = lo;  // in from here on, if nothing is near
-  if (k == 0) cut = 0xffffffffu, at_least = 0;
-  bool close = k > 0 && at_least != k;
-  double t_value = key_score(cut);
-  if (k > 0 && at_least == k) {
-    uint32_t in = 0xffffffffu, below = 0;
-    for (int j = p.first + tid; j < end; j += kChooseThreads) {
-      const uint32_t x = key(j);
-      if (x >= cut) in = min(in, x);
-      else below = max(below, x);
-    }
-    in = __reduce_min_sync(0xffffffffu, in);
-    below = __reduce_max_sync(0xffffffffu, below);
-    __syncthreads();
-    if (lane == 0) least[warp] = in, most[warp] = below;
+  // ---- T, the k-th largest key: a histogram of the keys from low to high, again of the bin that holds it ----
+  uint32_t near_low = 0xffffffffu, near_high = 0xffffffffu;
+  bool close = false;
+  if (k > 0) {
+    low = __reduce_min_sync(0xffffffffu, low);
+    high = __reduce_max_sync(0xffffffffu, high);
+    if (lane == 0) sh.least[warp] = low, sh.most[warp] = high;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kChooseWarps; ++w) in = min(in, least[w]), below = max(below, most[w]);
-    t_value = key_score(in);
-    close = !(key_score(below) < t_value - margin);
+    for (int w = 0; w < kSelectWarps; ++w) low = min(low, sh.least[w]), high = max(high, sh.most[w]);
+    int rank = k;
+    while (low < high) {
+      const int bits = 32 - __clz(high - low), shift = bits > kBinBits ? bits - kBinBits : 0;
+      for (int i = tid; i < kBins; i += kSelectThreads) sh.bins[i] = 0;
+      __syncthreads();
+      for (int j = p.first + tid; j < end; j += kSelectThreads) {
+        const uint32_t v = key(j);
+        if (v >= low && v <= high) atomicAdd(&sh.bins[(v - low) >> shift], 1);
+      }
+      __syncthreads();
+      // a thread's bins, the last thread's are the lowest; those above come from the scan
+      constexpr int kMine = kBins / kSelectThreads;
+      int count[kMine], mine_count = 0;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) mine_count += count[i] = sh.bins[kBins - 1 - (tid * kMine + i)];
+      int upto = mine_count;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      if (lane == 31) sh.count[warp] = upto;
+      __syncthreads();
+      for (int w = 0; w < warp; ++w) upto += sh.count[w];
+      int above = upto - mine_count;
+      if (above < rank && rank <= upto) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          if (above < rank && rank <= above + count[i]) {
+            sh.bin = kBins - 1 - (tid * kMine + i);
+            sh.rank = rank - above;
+          }
+          above += count[i];
+        }
+      }
+      __syncthreads();
+      rank = sh.rank;
+      const uint32_t from = low + (static_cast<uint32_t>(sh.bin) << shift), to = from + ((1u << shift) - 1);
+      high = to < from || to > high ? high : to;
+      low = from;
+    }
+    if (tid == 0) {
+      float q_all = 0.f;
+      for (int w = 0; w < kSelectWarps; ++w) q_all += sh.q_size[w], top_e = max(top_e, sh.top_e[w]);
+      // No score is larger than `size`; computed ones are off by `error` of it at most.  Queries as small as the second
+      // case are not scaled all the way: all pages are near then.
+      const double size = 448.0 * q_all * scale_double(top_e), margin = 2.0 * size * p.error;
+      const double middle = key_score(low), above = middle + margin, under = middle - margin;
+      uint32_t last_near = 0xffffffffu, first_near = 0;
+      if (above == above && under == under && q_all > 0x1p-90f) {
+        const uint64_t a = order64(above), u = order64(under);
+        last_near = static_cast<uint32_t>(a >> 32);  // the largest key that is not above
+        if (key_order64(last_near) > a) --last_near;
+        first_near = static_cast<uint32_t>(u >> 32);  // the smallest that is not below
+        if (key_order64(first_near) < u) ++first_near;
+      }
+      sh.near_low = first_near, sh.near_high = last_near;
+    }
+    __syncthreads();
+    near_low = sh.near_low, near_high = sh.near_high;
+    int n = 0;
+    for (int j = p.first + tid; j < end; j += kSelectThreads) n += key(j) >= near_low;
+    close = block_sum(n, sh.sums, turn) != k;
   }
 
   // ---- pages too near to tell get scores in 64 bits ----
-  const double sure_in = t_value + margin, sure_out = t_value - margin;
-  auto near = [&](int j) {
-    const double x = key_score(key(j));
-    return !(x > sure_in) && !(x < sure_out);
-  };
-  uint64_t* exact = p.exact + unit * p.width;
   uint64_t cut64 = 0;
   int ties = 0;  // of the pages at cut64, so many are in
   if (close) {
+    const __nv_bfloat16* q = p.q + unit * p.ratio * D;
+    for (int i = tid; i < D; i += kSelectThreads) {
+      double pos = 0.0, neg = 0.0;
+      for (int h = 0; h < p.ratio; ++h) {
+        const float v = __bfloat162float(q[h * D + i]);  // a NaN goes into both
+        pos += v < 0.f ? 0.0 : static_cast<double>(v), neg += v > 0.f ? 0.0 : static_cast<double>(v);
+      }
+      sh.q[i] = pos, sh.q[D + i] = neg;
+    }
+    __syncthreads();
     int in = 0;
     uint64_t low64 = ~0ull, high64 = 0;
-    for (int j0 = p.first + warp * 32; j0 < end; j0 += kChooseThreads) {
+    for (int j0 = p.first + warp * 32; j0 < end; j0 += kSelectThreads) {
       const int j = j0 + lane;
-      const bool is_near = j < end && near(j);
-      in += j < end && !is_near && key_score(key(j)) > sure_in;
-      uint32_t todo = __ballot_sync(0xffffffffu, is_near);
+      const uint32_t v = j < end ? key(j) : 0u;
+      in += j < end && v > near_high;
+      uint32_t todo = __ballot_sync(0xffffffffu, j < end && v >= near_low && v <= near_high);
       while (todo != 0) {
         const int at = j0 + __ffs(todo) - 1;
         todo &= todo - 1;
@@ -603,7 +601,7 @@ __global__ void __launch_bounds__(kChooseThreads) select_choose_kernel(const __g
           for (int i = lane; i < D / 2; i += 32) {
             const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(codes) + i);
             const float2 f0 = f16x2_float2(e4m3x2_f16x2(w)), f1 = f16x2_float2(e4m3x2_hi_f16x2(w));
-            sum += qd[4 * i] * f0.x + qd[4 * i + 1] * f0.y + qd[4 * i + 2] * f1.x + qd[4 * i + 3] * f1.y;
+            sum += sh.q[4 * i] * f0.x + sh.q[4 * i + 1] * f0.y + sh.q[4 * i + 2] * f1.x + sh.q[4 * i + 3] * f1.y;
           }
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -611,32 +609,34 @@ __global__ void __launch_bounds__(kChooseThreads) select_choose_kernel(const __g
         } else {
           sum = -__longlong_as_double(0x7ff0000000000000ll);
         }
-        const uint64_t x = score_key64(sum);
-        low64 = x < low64 ? x : low64, high64 = x > high64 ? x : high64;
-        if (lane == 0) exact[at] = x;
+        const uint64_t o = order64(sum);
+        low64 = o < low64 ? o : low64, high64 = o > high64 ? o : high64;
+        if (lane == 0) exact[at] = o;
       }
     }
-    in = block_sum(in, sums, turn);  // its barrier: the stores above are there for the block
-    if (lane == 0) least64[warp] = low64, most64[warp] = high64;
+    in = block_sum(in, sh.sums, turn);  // its barrier: the stores above are there for the block
+    if (lane == 0) sh.least64[warp] = low64, sh.most64[warp] = high64;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kChooseWarps; ++w) {
-      low64 = least64[w] < low64 ? least64[w] : low64;
-      high64 = most64[w] > high64 ? most64[w] : high64;
+    for (int w = 0; w < kSelectWarps; ++w) {
+      low64 = sh.least64[w] < low64 ? sh.least64[w] : low64;
+      high64 = sh.most64[w] > high64 ? sh.most64[w] : high64;
     }
     const int need = k - in;  // 1 at least, and no more than are near
     auto count64 = [&](uint64_t from) {
       int n = 0;
-      for (int j = p.first + tid; j < end; j += kChooseThreads) n += near(j) && exact[j] >= from;
-      return block_sum(n, sums, turn);
+      for (int j = p.first + tid; j < end; j += kSelectThreads) {
+        const uint32_t v = key(j);
+        n += v >= near_low && v <= near_high && exact[j] >= from;
+      }
+      return block_sum(n, sh.sums, turn);
     };
     int n = count64(low64);
-    bool found = n == need;
     uint64_t lo64 = low64, hi64 = high64;
-    while (!found && lo64 < hi64) {
+    while (n != need && lo64 < hi64) {
       const uint64_t mid = lo64 + (hi64 - lo64) / 2 + 1;
       const int m = count64(mid);
-      if (m >= need) lo64 = mid, n = m, found = m == need;
+      if (m >= need) lo64 = mid, n = m;
       else hi64 = mid - 1;
     }
     cut64 = lo64;
@@ -647,33 +647,34 @@ __global__ void __launch_bounds__(kChooseThreads) select_choose_kernel(const __g
   // ---- the chosen pages in order: a warp counts, then writes, a run of pages ----
   auto state = [&](int j) {  // 2: in, 1: a tie, 0: out
     if (j < p.first || j >= end) return 2;
-    if (!close) return key(j) >= cut ? 2 : 0;
-    if (!near(j)) return key_score(key(j)) > sure_in ? 2 : 0;
-    const uint64_t x = exact[j];
-    return x > cut64 ? 2 : x == cut64 ? (ties == INT_MAX ? 2 : 1) : 0;
+    const uint32_t v = key(j);
+    if (!close) return v >= near_low ? 2 : 0;
+    if (v > near_high) return 2;
+    if (v < near_low) return 0;
+    const uint64_t o = exact[j];
+    return o > cut64 ? 2 : o == cut64 ? (ties == INT_MAX ? 2 : 1) : 0;
   };
-  const int per = ((pages + kChooseThreads - 1) / kChooseThreads) * 32;  // pages of a warp
+  const int per = ((pages + kSelectThreads - 1) / kSelectThreads) * 32;  // pages of a warp
   const int j_begin = warp * per, j_end = j_begin + per < pages ? j_begin + per : pages;
   int sure = 0, tied = 0;
   for (int j0 = j_begin; j0 < j_end; j0 += 32) {
-    const int x = j0 + lane < j_end ? state(j0 + lane) : 0;
-    sure += __popc(__ballot_sync(0xffffffffu, x == 2));
-    tied += __popc(__ballot_sync(0xffffffffu, x == 1));
+    const int v = j0 + lane < j_end ? state(j0 + lane) : 0;
+    sure += __popc(__ballot_sync(0xffffffffu, v == 2));
+    tied += __popc(__ballot_sync(0xffffffffu, v == 1));
   }
-  __syncthreads();
-  if (lane == 0) warp_count[warp] = sure, warp_ties[warp] = tied;
+  if (lane == 0) sh.count[warp] = sure, sh.ties[warp] = tied;
   __syncthreads();
   int at = 0, ties_before = 0;
   for (int w = 0; w < warp; ++w) {
     const int left = ties - ties_before;
-    at += warp_count[w] + (warp_ties[w] < left ? warp_ties[w] : left > 0 ? left : 0);
-    ties_before += warp_ties[w];
+    at += sh.count[w] + (sh.ties[w] < left ? sh.ties[w] : left > 0 ? left : 0);
+    ties_before += sh.ties[w];
   }
   for (int j0 = j_begin; j0 < j_end; j0 += 32) {
-    const int x = j0 + lane < j_end ? state(j0 + lane) : 0;
-    const uint32_t tie_mask = __ballot_sync(0xffffffffu, x == 1);
+    const int v = j0 + lane < j_end ? state(j0 + lane) : 0;
+    const uint32_t tie_mask = __ballot_sync(0xffffffffu, v == 1);
     const uint32_t below = (1u << lane) - 1;
-    const bool in = x == 2 || (x == 1 && ties_before + __popc(tie_mask & below) < ties);
+    const bool in = v == 2 || (v == 1 && ties_before + __popc(tie_mask & below) < ties);
     const uint32_t mask = __ballot_sync(0xffffffffu, in);
     const int place = at + __popc(mask & below);
     if (in && place < p.top) out[place] = listed(j0 + lane);
@@ -691,28 +692,36 @@ SelectWorkspace select_workspace(int batch, int64_t total, int heads, int max_pa
   w.keys = 0;
   w.exact = up256(cells * sizeof(uint32_t));
   w.top_e = w.exact + up256(cells * sizeof(uint64_t));
-  w.bytes = w.top_e + up256(static_cast<size_t>(batch) * heads * ((max_pages + kWarpPages - 1) / kWarpPages));
+  w.bytes = w.top_e + up256(static_cast<size_t>(batch) * heads * ((max_pages + kTilePages - 1) / kTilePages) * sizeof(int));
   return w;
 }
 
+// Roundings of a score: 2^-24 for each addition to q+ and q-; 2^-22 and less than 2^-28 for their two parts; 2^-23 for
+// each of 2 d / 4 additions to a sum (single precision, rounded in any way) and the last five; 2^-20 for what the key
+// drops; 1 / 256 more of it all for the products of these factors and the rounding of the bound itself.
+double score_error(int ratio, int d) {
+  return (ratio * 0x1p-24 + 0x1p-22 + 0x1p-28 + (d / 2 + 5) * 0x1p-23 + 0x1p-20) * (1.0 + 0x1p-8);
+}
+
 template <int D>
-int select_launch(const SelectParams& p, int sms, cudaStream_t stream) {
-  const int64_t tiles = static_cast<int64_t>(p.batch) * p.heads * ((p.max_pages + kTilePages - 1) / kTilePages);
-  const int64_t most = static_cast<int64_t>(sms) * (p.max_n == 1 ? 4 : 2);
-  const int grid = static_cast<int>(tiles < most ? tiles : most);
-  if (p.max_n == 1) select_score_kernel<D, 1><<<grid, kScoreThreads, 0, stream>>>(p);
-  else select_score_kernel<D, 4><<<grid, kScoreThreads, 0, stream>>>(p);
+int select_launch(const SelectParams& p, cudaStream_t stream) {
+  const int64_t blocks = static_cast<int64_t>(p.batch) * p.heads * p.tiles;
+  if (blocks > INT_MAX) return FA_ERR_INVALID_ARG;
+  static bool ready[64] = {};
+  const int rc = allow_smem(reinterpret_cast<const void*>(kv_score_kernel<D>), sizeof(ScoreShared<D>), ready);
+  if (rc != FA_OK) return rc;
+  kv_score_kernel<D><<<static_cast<int>(blocks), kSelectThreads, sizeof(ScoreShared<D>), stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned int>(p.total * p.heads), 1, 1);
-  cfg.blockDim = dim3(kChooseThreads, 1, 1);
+  cfg.blockDim = dim3(kSelectThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, select_choose_kernel<D>, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kv_choose_kernel<D>, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 bool page_size_ok(int n) { return n == 16 || n == 32 || n == 64 || n == 128; }
@@ -823,7 +832,7 @@ int fa_kv_select(const void* q, const void* k_bounds, const uint8_t* k_scale, co
   p.status = host.status;
   p.keys = reinterpret_cast<uint32_t*>(ws + w.keys);
   p.exact = reinterpret_cast<uint64_t*>(ws + w.exact);
-  p.top_e = ws + w.top_e;
+  p.top_e = reinterpret_cast<int*>(ws + w.top_e);
   p.lists = lists;
   p.list_lens = list_lens;
   p.total = total_q;
@@ -838,12 +847,12 @@ int fa_kv_select(const void* q, const void* k_bounds, const uint8_t* k_scale, co
   p.top = top;
   p.first = keep_first;
   p.last = keep_last;
-  p.width = max_pages;
-  p.groups = (max_pages + kWarpPages - 1) / kWarpPages;
+  p.tiles = (max_pages + kTilePages - 1) / kTilePages;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  if (d_qk == 64) return select_launch<64>(p, host.sms, stream);
-  if (d_qk == 128) return select_launch<128>(p, host.sms, stream);
-  return select_launch<192>(p, host.sms, stream);
+  p.error = score_error(p.ratio, d_qk);
+  if (d_qk == 64) return select_launch<64>(p, stream);
+  if (d_qk == 128) return select_launch<128>(p, stream);
+  return select_launch<192>(p, stream);
 }
 
 }  // extern "C"
