@@ -908,7 +908,9 @@ def rotary_table(positions: int, rot_dim: int, base: float = 10000.0, scaling: s
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return rotary_table(positions, rot_dim, base, scaling, factor, original, low, high, magnitude, out, index, stream)
-    ptr, current = _call_stream(index, stream)
+    ptr = current = torch._C._cuda_getCurrentRawStream(index)
+    if stream is not None:
+        ptr, current = _call_stream(index, stream)
     if out is None:
         if positions < 0 or rot_dim < 0:
             _bad("positions and rot_dim must not be negative")
@@ -920,10 +922,8 @@ def rotary_table(positions: int, rot_dim: int, base: float = 10000.0, scaling: s
     return out
 
 
-def _rotary_rows(name, t, tokens, d):
+def _rotary_rows(torch, name, t, tokens, d):
     """(heads, stride from token to token) of a bf16 tensor [*tokens, heads, d]."""
-    import torch
-
     shape, st = t.shape, t.stride()
     if t.dtype is not torch.bfloat16 or shape[:-2] != tokens or shape[-1] != d:
         _bad(f"{name} must be a bf16 tensor of tokens {list(tokens)} with heads of {d}")
@@ -965,34 +965,36 @@ def _rotary(q, k, cos_sin, positions, cu_seqlens, interleaved, q_out, k_out, str
     if positions is not None:
         if cu_seqlens is not None:
             _bad("positions and cu_seqlens exclude each other")
-        _int32("positions", positions, tokens)
+        _int32(torch, "positions", positions, tokens)
         pos = positions.data_ptr()
     elif cu_seqlens is not None:
         batch = cu_seqlens.numel() - 1
         if len(tokens) != 1 or batch < 0:
             _bad("cu_seqlens must hold batch + 1 offsets into [total, heads, d]")
-        _int32("cu_seqlens", cu_seqlens, (batch + 1,))
+        _int32(torch, "cu_seqlens", cu_seqlens, (batch + 1,))
         cu = cu_seqlens.data_ptr()
     else:
         seqlen = tokens[-1] or 1  # without a batch: one sequence
-    ptr, current = _call_stream(index, stream)
+    ptr = current = torch._C._cuda_getCurrentRawStream(index)
+    if stream is not None:
+        ptr, current = _call_stream(index, stream)
     qp = kp = qo = ko = None
     hq = hk = qs = ks = qos = kos = 0
     if q is not None:
-        hq, qs = _rotary_rows("q", q, tokens, d)
+        hq, qs = _rotary_rows(torch, "q", q, tokens, d)
         if q_out is None:
             q_out = _empty(q.shape, torch.bfloat16, index, ptr, current)
-        ho, qos = _rotary_rows("q_out", q_out, tokens, d)
+        ho, qos = _rotary_rows(torch, "q_out", q_out, tokens, d)
         if ho != hq:
             _bad("q_out must have q's shape")
         qp, qo = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         _bad("q_out without q")
     if k is not None:
-        hk, ks = _rotary_rows("k", k, tokens, d)
+        hk, ks = _rotary_rows(torch, "k", k, tokens, d)
         if k_out is None:
             k_out = _empty(k.shape, torch.bfloat16, index, ptr, current)
-        ho, kos = _rotary_rows("k_out", k_out, tokens, d)
+        ho, kos = _rotary_rows(torch, "k_out", k_out, tokens, d)
         if ho != hk:
             _bad("k_out must have k's shape")
         kp, ko = k.data_ptr(), k_out.data_ptr()
@@ -1057,18 +1059,14 @@ def fa_fwd_lists(q, cache: FaKvCache, lists, list_lens, width, o, lse, total_q, 
                                        lse, total_q, heads_q, float(scale), workspace, workspace_bytes, stream)
 
 
-def _int32(name, t, shape):
+def _int32(torch, name, t, shape):
     """Checks a contiguous int32 tensor of a shape."""
-    import torch
-
     if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         _bad(f"{name} must be a contiguous int32 tensor {list(shape)}")
 
 
-def _table_rows(block_table, seqlens_k):
+def _table_rows(torch, block_table, seqlens_k):
     """(batch, max_pages, row stride) of a block table beside its lengths."""
-    import torch
-
     td, st = block_table.shape, block_table.stride()
     if block_table.dtype is not torch.int32 or len(td) != 2 or (st[1] != 1 and td[1] > 1):
         _bad("block_table must be a 2-D int32 tensor whose rows are contiguous")
@@ -1078,9 +1076,7 @@ def _table_rows(block_table, seqlens_k):
     return batch, width, st[0] if batch > 1 else width
 
 
-def _bounds(k_bounds, pages, heads, d):
-    import torch
-
+def _bounds(torch, k_bounds, pages, heads, d):
     if k_bounds.dtype is not torch.float8_e4m3fn or k_bounds.shape != (pages, heads, 2, d) or not k_bounds.is_contiguous():
         _bad(f"k_bounds must be a contiguous float8_e4m3fn tensor [{pages}, {heads}, 2, {d}]")
     return k_bounds.data_ptr()
@@ -1106,19 +1102,17 @@ def kv_bounds(k_cache, k_bounds, block_table, seqlens_k, cu_seqlens, total: int,
     import torch
 
     index = k_cache.get_device()
-    if index < 0 or k_cache.dtype is not torch.float8_e4m3fn or k_cache.dim() != 4:
-        _bad("k_cache must be a 4-D float8_e4m3fn CUDA tensor")
+    kd, ks = k_cache.shape, k_cache.stride()
+    if index < 0 or k_cache.dtype is not torch.float8_e4m3fn or len(kd) != 4 or ks[3] != 1:
+        _bad("k_cache must be a 4-D float8_e4m3fn CUDA tensor whose tokens' codes are contiguous")
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return kv_bounds(k_cache, k_bounds, block_table, seqlens_k, cu_seqlens, total, stream)
-    pages, heads, page, d = k_cache.shape
-    batch, width, ts = _table_rows(block_table, seqlens_k)
-    _int32("cu_seqlens", cu_seqlens, (batch + 1,))
-    ks = k_cache.stride()
-    if ks[3] != 1 and d > 1:
-        _bad("the codes of a token must be contiguous")
-    bounds = _bounds(k_bounds, pages, heads, d)
-    ptr, _ = _call_stream(index, stream)
+    pages, heads, page, d = kd
+    batch, width, ts = _table_rows(torch, block_table, seqlens_k)
+    _int32(torch, "cu_seqlens", cu_seqlens, (batch + 1,))
+    bounds = _bounds(torch, k_bounds, pages, heads, d)
+    ptr = torch._C._cuda_getCurrentRawStream(index) if stream is None else _call_stream(index, stream)[0]
     cache = _KV_CACHE.pack(k_cache.data_ptr(), 0, 0, 0, block_table.data_ptr(), seqlens_k.data_ptr(), ks[0], ks[1], ks[2],
                            0, 0, 0, ts, pages, page, heads, d, 0, width)
     rc = load_library().fa_kv_bounds(cache, bounds, cu_seqlens.data_ptr(), batch, total, ptr)
@@ -1141,34 +1135,37 @@ def kv_select(q, k_bounds, k_scale, block_table, seqlens_k, cu_seqlens_q, max_se
     import torch
 
     index = q.get_device()
-    qd = q.shape
+    qd, sd = q.shape, k_scale.shape
     if index < 0 or q.dtype is not torch.bfloat16 or len(qd) != 3 or not q.is_contiguous():
         _bad("q must be a contiguous 3-D bf16 CUDA tensor")
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return kv_select(q, k_bounds, k_scale, block_table, seqlens_k, cu_seqlens_q, max_seqlen_q, page_size, top,
                              causal, keep_first, keep_last, lists, list_lens, workspace, stream)
-    total_q, heads_q, d = qd
-    if k_scale.dtype is not torch.float8_e8m0fnu or k_scale.dim() != 2 or not k_scale.is_contiguous():
+    if k_scale.dtype is not torch.float8_e8m0fnu or len(sd) != 2 or not k_scale.is_contiguous():
         _bad("k_scale must be a contiguous float8_e8m0fnu tensor [num_pages, heads_kv]")
-    pages, heads = k_scale.shape
-    bounds = _bounds(k_bounds, pages, heads, d)
-    batch, width, ts = _table_rows(block_table, seqlens_k)
-    _int32("cu_seqlens_q", cu_seqlens_q, (batch + 1,))
+    total_q, heads_q, d = qd
+    pages, heads = sd
+    bounds = _bounds(torch, k_bounds, pages, heads, d)
+    batch, width, ts = _table_rows(torch, block_table, seqlens_k)
+    _int32(torch, "cu_seqlens_q", cu_seqlens_q, (batch + 1,))
     if top < 0:
         _bad("top must not be negative")
-    ptr, current = _call_stream(index, stream)
+    ptr = current = torch._C._cuda_getCurrentRawStream(index)
+    if stream is not None:
+        ptr, current = _call_stream(index, stream)
     if lists is None:
         lists = _empty((total_q, heads, top), torch.int32, index, ptr, current)
     else:
-        _int32("lists", lists, (total_q, heads, top))
+        _int32(torch, "lists", lists, (total_q, heads, top))
     if list_lens is None:
         list_lens = _empty((total_q,), torch.int32, index, ptr, current)
     else:
-        _int32("list_lens", list_lens, (total_q,))
+        _int32(torch, "list_lens", list_lens, (total_q,))
     if workspace is None:
         size = _workspace_bytes("fa_kv_select_workspace_size", batch, total_q, heads, width)
-        workspace = _empty((size,), torch.uint8, index, ptr, current)
+        workspace = (torch.empty((size,), dtype=torch.uint8, device=index) if ptr == current
+                     else _empty((size,), torch.uint8, index, ptr, current))
     else:
         size = _given_workspace(workspace)
     rc = load_library().fa_kv_select(q.data_ptr(), bounds, k_scale.data_ptr(), block_table.data_ptr(), ts,
@@ -1180,10 +1177,8 @@ def kv_select(q, k_bounds, k_scale, block_table, seqlens_k, cu_seqlens_q, max_se
     return lists, list_lens
 
 
-def _pool(k_cache, v_cache, k_scale, v_scale, table, seqlens, width, table_stride):
+def _pool(torch, k_cache, v_cache, k_scale, v_scale, table, seqlens, width, table_stride):
     """(fa_kv_cache as bytes, num_pages, heads_kv, d_qk, d_v) of the cache's tensors, which are checked."""
-    import torch
-
     f8, e8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
     kd, vd = k_cache.shape, v_cache.shape
     head = kd[:2]
@@ -1235,13 +1230,15 @@ def attention_forward_lists(q, k_cache, v_cache, k_scale, v_scale, lists, list_l
     total_q, heads_q, d = qd
     ld = lists.shape
     width = ld[2] if len(ld) == 3 else -1
-    cache, _, heads, d_qk, d_v = _pool(k_cache, v_cache, k_scale, v_scale, lists.data_ptr(), list_lens.data_ptr(), width,
+    cache, _, heads, d_qk, d_v = _pool(torch, k_cache, v_cache, k_scale, v_scale, lists.data_ptr(), list_lens.data_ptr(), width,
                                        width)
     if d != d_qk or width < 0:
         _bad(f"q must be [total_q, heads_q, {d_qk}] and lists [total_q, {heads}, width]")
-    _int32("lists", lists, (total_q, heads, width))
-    _int32("list_lens", list_lens, (total_q,))
-    ptr, current = _call_stream(index, stream)
+    _int32(torch, "lists", lists, (total_q, heads, width))
+    _int32(torch, "list_lens", list_lens, (total_q,))
+    ptr = current = torch._C._cuda_getCurrentRawStream(index)
+    if stream is not None:
+        ptr, current = _call_stream(index, stream)
     if out is None:
         out = _empty((total_q, heads_q, d_v), torch.bfloat16, index, ptr, current)
     elif out.dtype is not torch.bfloat16 or out.shape != (total_q, heads_q, d_v) or not out.is_contiguous():
@@ -1253,7 +1250,8 @@ def attention_forward_lists(q, k_cache, v_cache, k_scale, v_scale, lists, list_l
         _bad("lse must be a contiguous fp32 tensor [heads_q, total_q]")
     if workspace is None:
         size = _workspace_bytes("fa_fwd_lists_workspace_size", heads_q, heads, d_v)
-        workspace = _empty((size,), torch.uint8, index, ptr, current)
+        workspace = (torch.empty((size,), dtype=torch.uint8, device=index) if ptr == current
+                     else _empty((size,), torch.uint8, index, ptr, current))
     else:
         size = _given_workspace(workspace)
     rc = load_library().fa_fwd_lists(q.data_ptr(), cache, lists.data_ptr(), list_lens.data_ptr(), width, out.data_ptr(),
@@ -1288,10 +1286,8 @@ def fa_kv_compact(cache: FaKvCache, k_bounds, page_refs, batch, table_out, table
                                         stream)
 
 
-def _table_out(table_out, rows, width, index, ptr, current):
+def _table_out(torch, table_out, rows, width, index, ptr, current):
     """(tensor, row stride) of the table that is written."""
-    import torch
-
     if table_out is None:
         return _empty((rows, width), torch.int32, index, ptr, current), width
     st = table_out.stride()
@@ -1300,12 +1296,11 @@ def _table_out(table_out, rows, width, index, ptr, current):
     return table_out, st[0] if rows > 1 else width
 
 
-def _int32_out(name, t, n, index, ptr, current):
-    import torch
-
+def _int32_out(torch, name, t, n, index, ptr, current):
     if t is None:
         return _empty((n,), torch.int32, index, ptr, current)
-    _int32(name, t, (n,))
+    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous():
+        _bad(f"{name} must be a contiguous int32 tensor [{n}]")
     return t
 
 
@@ -1328,27 +1323,32 @@ def kv_fork(parents, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k,
         with torch.cuda.device(index):
             return kv_fork(parents, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, page_refs, new_tokens,
                            k_bounds, table_out, seqlens_out, refs_out, workspace, stream)
-    batch, width, ts = _table_rows(block_table, seqlens_k)
-    cache, pages, heads, d_qk, _ = _pool(k_cache, v_cache, k_scale, v_scale, block_table.data_ptr(), seqlens_k.data_ptr(),
+    batch, width, ts = _table_rows(torch, block_table, seqlens_k)
+    cache, pages, heads, d_qk, _ = _pool(torch, k_cache, v_cache, k_scale, v_scale, block_table.data_ptr(), seqlens_k.data_ptr(),
                                          width, ts)
     rows = parents.numel()
-    _int32("parents", parents, (rows,))
-    _int32("page_refs", page_refs, (pages,))
+    _int32(torch, "parents", parents, (rows,))
+    _int32(torch, "page_refs", page_refs, (pages,))
+    grow = None
     if new_tokens is not None:
-        _int32("new_tokens", new_tokens, (rows,))
-    bounds = _bounds(k_bounds, pages, heads, d_qk) if k_bounds is not None else None
-    ptr, current = _call_stream(index, stream)
-    table_out, out_stride = _table_out(table_out, rows, width, index, ptr, current)
-    seqlens_out = _int32_out("seqlens_out", seqlens_out, rows, index, ptr, current)
-    refs_out = _int32_out("refs_out", refs_out, pages, index, ptr, current)
+        _int32(torch, "new_tokens", new_tokens, (rows,))
+        grow = new_tokens.data_ptr()
+    bounds = _bounds(torch, k_bounds, pages, heads, d_qk) if k_bounds is not None else None
+    ptr = current = torch._C._cuda_getCurrentRawStream(index)
+    if stream is not None:
+        ptr, current = _call_stream(index, stream)
+    table_out, out_stride = _table_out(torch, table_out, rows, width, index, ptr, current)
+    seqlens_out = _int32_out(torch, "seqlens_out", seqlens_out, rows, index, ptr, current)
+    refs_out = _int32_out(torch, "refs_out", refs_out, pages, index, ptr, current)
     if workspace is None:
         size = _workspace_bytes("fa_kv_pages_workspace_size", batch, rows, pages)
-        workspace = _empty((size,), torch.uint8, index, ptr, current)
+        workspace = (torch.empty((size,), dtype=torch.uint8, device=index) if ptr == current
+                     else _empty((size,), torch.uint8, index, ptr, current))
     else:
         size = _given_workspace(workspace)
-    rc = load_library().fa_kv_fork(cache, bounds, page_refs.data_ptr(), batch, parents.data_ptr(),
-                                   new_tokens.data_ptr() if new_tokens is not None else None, rows, table_out.data_ptr(),
-                                   out_stride, seqlens_out.data_ptr(), refs_out.data_ptr(), workspace.data_ptr(), size, ptr)
+    rc = load_library().fa_kv_fork(cache, bounds, page_refs.data_ptr(), batch, parents.data_ptr(), grow, rows,
+                                   table_out.data_ptr(), out_stride, seqlens_out.data_ptr(), refs_out.data_ptr(),
+                                   workspace.data_ptr(), size, ptr)
     if rc != FA_OK:
         raise FaError(rc, "fa_kv_fork")
     return table_out, seqlens_out, refs_out
@@ -1369,19 +1369,22 @@ def kv_compact(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, page_
         with torch.cuda.device(index):
             return kv_compact(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, page_refs, k_bounds, table_out,
                               refs_out, page_map, used, workspace, stream)
-    batch, width, ts = _table_rows(block_table, seqlens_k)
-    cache, pages, heads, d_qk, _ = _pool(k_cache, v_cache, k_scale, v_scale, block_table.data_ptr(), seqlens_k.data_ptr(),
+    batch, width, ts = _table_rows(torch, block_table, seqlens_k)
+    cache, pages, heads, d_qk, _ = _pool(torch, k_cache, v_cache, k_scale, v_scale, block_table.data_ptr(), seqlens_k.data_ptr(),
                                          width, ts)
-    _int32("page_refs", page_refs, (pages,))
-    bounds = _bounds(k_bounds, pages, heads, d_qk) if k_bounds is not None else None
-    ptr, current = _call_stream(index, stream)
-    table_out, out_stride = _table_out(table_out, batch, width, index, ptr, current)
-    refs_out = _int32_out("refs_out", refs_out, pages, index, ptr, current)
-    page_map = _int32_out("page_map", page_map, pages, index, ptr, current)
-    used = _int32_out("used", used, 1, index, ptr, current)
+    _int32(torch, "page_refs", page_refs, (pages,))
+    bounds = _bounds(torch, k_bounds, pages, heads, d_qk) if k_bounds is not None else None
+    ptr = current = torch._C._cuda_getCurrentRawStream(index)
+    if stream is not None:
+        ptr, current = _call_stream(index, stream)
+    table_out, out_stride = _table_out(torch, table_out, batch, width, index, ptr, current)
+    refs_out = _int32_out(torch, "refs_out", refs_out, pages, index, ptr, current)
+    page_map = _int32_out(torch, "page_map", page_map, pages, index, ptr, current)
+    used = _int32_out(torch, "used", used, 1, index, ptr, current)
     if workspace is None:
         size = _workspace_bytes("fa_kv_pages_workspace_size", batch, 0, pages)
-        workspace = _empty((size,), torch.uint8, index, ptr, current)
+        workspace = (torch.empty((size,), dtype=torch.uint8, device=index) if ptr == current
+                     else _empty((size,), torch.uint8, index, ptr, current))
     else:
         size = _given_workspace(workspace)
     rc = load_library().fa_kv_compact(cache, bounds, page_refs.data_ptr(), batch, table_out.data_ptr(), out_stride,

@@ -112,33 +112,40 @@ __device__ __forceinline__ bool length_fits(const PagesParams& p, int len) {
 
 // A row of the new table as far as it does not depend on other rows.
 struct ForkRow {
-  int src, len, held, total, grow;  // parent (-1: none), its tokens, its pages; pages of the new row; new tokens
+  int src, len, grow;  // parent (-1: none), its tokens; new tokens (0 if not known)
   bool bad;
+  __device__ __forceinline__ uint64_t pack() const {  // without the new tokens
+    return static_cast<uint64_t>(src + 1) | static_cast<uint64_t>(len) << 16 | static_cast<uint64_t>(bad) << 63;
+  }
+  static __device__ __forceinline__ ForkRow unpack(uint64_t x) {
+    return {static_cast<int>(x & 0xffff) - 1, static_cast<int>(x >> 16 & 0x7fffffff), 0, (x >> 63) != 0};
+  }
 };
 __device__ __forceinline__ ForkRow fork_row(const PagesParams& p, int r) {
-  ForkRow w = {p.parents[r], 0, 0, 0, p.grow != nullptr ? p.grow[r] : 0, false};
+  ForkRow w = {p.parents[r], 0, p.grow != nullptr ? p.grow[r] : 0, false};
   w.bad = w.src < -1 || w.src >= p.batch || w.grow < 0;
   if (!w.bad && w.src >= 0) {
-    w.bad = __ldcg(p.valid + w.src) == 0;
-    w.len = w.bad ? 0 : p.seqlens[w.src];
+    const int valid = __ldcg(p.valid + w.src), len = p.seqlens[w.src];
+    w.bad = valid == 0;
+    w.len = w.bad ? 0 : len;
   }
   w.bad = w.bad || static_cast<int64_t>(w.len) + w.grow > static_cast<int64_t>(p.max_pages) << p.page_shift;
-  if (w.bad) return {-1, 0, 0, 0, 0, true};
-  const int round = (1 << p.page_shift) - 1;
-  w.held = (w.len + round) >> p.page_shift;
-  w.total = static_cast<int>((static_cast<int64_t>(w.len) + w.grow + round) >> p.page_shift);
-  return w;
+  return w.bad ? ForkRow{-1, 0, 0, true} : w;
 }
 
 // Three barriers of the cluster.  What all rows need of one another (heirs, first
 // heirs, the pages needed before each row) every block works out for itself in
-// shared memory, which takes less time than an exchange; pages are shared out.
+// shared memory, which takes less time than an exchange; pages are shared out.  Rows
+// are kept there once they are known (CACHED), as far as they fit.
+template <bool CACHED>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     kv_fork_kernel(const __grid_constant__ PagesParams p) {
   extern __shared__ int fork_smem[];
-  int* const heirs = fork_smem;          // [batch], -1: not valid
+  int* const heirs = fork_smem;          // [batch]
   int* const first = heirs + p.batch;    // [batch] the first heir
   int* const start = first + p.batch;    // [rows + 1] pages that the rows before need
+  uint64_t* const known = reinterpret_cast<uint64_t*>(fork_smem + ((2 * p.batch + p.rows + 2) & ~1));  // [rows]
+  auto row_of = [&](int r) { return CACHED ? ForkRow::unpack(known[r]) : fork_row(p, r); };
   __shared__ long long warp_sum[32];
   const int rank = blockIdx.x, tid = rank * kThreads + threadIdx.x;
   const int lane = threadIdx.x & 31, warp = tid >> 5;
@@ -148,14 +155,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   // ---- counts start from the old ones; a warp looks at an old row's pages ----
   if (tid == 0) p.head->copies = p.head->skip = 0;
   for (int b = warp; b < p.batch; b += kAll / 32) {
+    const int* row = p.table + b * p.table_stride;
+    const int head = lane < p.max_pages ? row[lane] : 0;  // before the length is known
     const int len = p.seqlens[b];
     const bool fits = length_fits(p, len);
-    bool page_bad = false;
-    if (fits) {
-      const int pages = (len + part_mask) >> p.page_shift;
-      const int* row = p.table + b * p.table_stride;
-      for (int j = lane; j < pages; j += 32) page_bad |= row[j] < 0 || row[j] >= p.num_pages;
-    }
+    const int pages = fits ? (len + part_mask) >> p.page_shift : 0;
+    bool page_bad = lane < pages && (head < 0 || head >= p.num_pages);
+    for (int j = lane + 32; j < pages; j += 32) page_bad |= row[j] < 0 || row[j] >= p.num_pages;
     page_bad = __any_sync(0xffffffffu, page_bad);
     if (lane == 0) {
       if (!fits || page_bad) paged_error(p.status, fits ? kSitePagedPage : kSitePagedSeq, b);
@@ -169,7 +175,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   // ---- heirs, and the pages that rows need ----
   for (int r = threadIdx.x; r < p.rows; r += kThreads) {
     const ForkRow w = fork_row(p, r);
-    if (w.bad && rank == 0) paged_error(p.status, kSitePagedSeq, r);
+    if constexpr (CACHED) known[r] = w.pack();
+    if (rank == 0) {
+      p.seqlens_out[r] = w.len + w.grow;
+      if (w.bad) paged_error(p.status, kSitePagedSeq, r);
+    }
     if (w.src >= 0) {
       atomicAdd(heirs + w.src, 1);
       atomicMin(first + w.src, r);
@@ -177,13 +187,17 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   auto copies = [&](const ForkRow& w, int r) { return w.src >= 0 && (w.len & part_mask) != 0 && first[w.src] != r; };
+  auto kept_pages = [&](const ForkRow& w, int r) {  // that come from the parent
+    return (w.len >> p.page_shift) + ((w.len & part_mask) != 0 && !copies(w, r) ? 1 : 0);
+  };
   long long needed = 0;
   for (int base = 0; base < p.rows; base += kThreads) {
     const int r = base + threadIdx.x;
     int need = 0;
     if (r < p.rows) {
-      const ForkRow w = fork_row(p, r);
-      need = w.total - w.held + (copies(w, r) ? 1 : 0);
+      const ForkRow w = row_of(r);
+      const int64_t len = w.bad ? 0 : static_cast<int64_t>(w.len) + (p.grow != nullptr ? p.grow[r] : 0);
+      need = static_cast<int>((len + part_mask) >> p.page_shift) - kept_pages(w, r);
     }
     long long total;
     const long long upto = needed + block_scan(need, warp_sum, total);
@@ -206,6 +220,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   // ---- the lowest free pages go to the rows in order ----
   const PageRun run = page_run(p, rank);
   int mine = 0;
+#pragma unroll 4
   for (int64_t i = run.begin; i < run.end; ++i) mine += __ldcg(p.refs_out + i) <= 0;
   long long at;
   const int free_pages = cluster_scan(p, rank, mine, warp_sum, at);
@@ -220,9 +235,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
       else hi = mid - 1;
     }
     if (start[lo + 1] > free_pages) continue;  // too few for the row
-    const ForkRow w = fork_row(p, lo);
+    const ForkRow w = row_of(lo);
     const bool copy = copies(w, lo);
-    const int kept = w.held - (copy ? 1 : 0), j = kept + place - start[lo];
+    const int kept = kept_pages(w, lo), j = kept + place - start[lo];
     p.table_out[lo * p.out_stride + j] = page;
     p.refs_out[page] = 1;
     if (copy && j == kept) {
@@ -237,18 +252,22 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
 
   // ---- a warp writes the rest of a row ----
   for (int r = warp; r < p.rows; r += kAll / 32) {
-    const ForkRow w = fork_row(p, r);
-    const int kept = w.held - (copies(w, r) ? 1 : 0);
-    const bool fails = start[r + 1] > start[r] && start[r + 1] > free_pages;
+    const ForkRow w = row_of(r);
+    const int kept = kept_pages(w, r), total = kept + (start[r + 1] - start[r]);
+    // needs that sum to more than fits are held at the most that does
+    const bool needs = start[r + 1] > start[r] ||
+                       (start[r + 1] == INT_MAX && static_cast<int64_t>(w.len) + (p.grow != nullptr ? p.grow[r] : 0) >
+                                                       static_cast<int64_t>(kept) << p.page_shift);
+    const bool fails = needs && start[r + 1] > free_pages;
     const int* row = p.table + (w.src >= 0 ? w.src : 0) * p.table_stride;
     int* out = p.table_out + r * p.out_stride;
-    if (lane == 0) {
-      p.seqlens_out[r] = fails ? 0 : w.len + w.grow;
-      if (fails && start[r] <= free_pages) paged_error(p.status, kSitePagedFull, r);
+    if (fails && lane == 0) {
+      p.seqlens_out[r] = 0;
+      if (start[r] <= free_pages) paged_error(p.status, kSitePagedFull, r);
     }
     for (int j = lane; j < p.max_pages; j += 32) {
       if (j < kept && !fails) out[j] = row[j];
-      else if (j >= w.total || fails) out[j] = -1;
+      else if (j >= total || fails) out[j] = -1;
       // a row without enough pages gives back what it shares, a first heir the page that is partly filled too
       if (j < kept && fails && (j < w.len >> p.page_shift || first[w.src] == r)) atomicAdd(p.refs_out + row[j], -1);
     }
@@ -423,6 +442,19 @@ void pages_fill(PagesParams& p, uint8_t* ws, int batch, int rows, const fa_kv_ca
   p.page_shift = page_shift(c.page_size);
 }
 
+// Shared memory of the fork's blocks: enough without known rows for the largest tables.
+constexpr size_t kForkSmem = 200 * 1024;
+static_assert(sizeof(int) * (3 * kMaxBatch + 2) <= kForkSmem, "the largest tables");
+
+template <bool CACHED>
+int fork_start(const PagesParams& p, size_t smem, cudaStream_t stream) {
+  static bool ready[64] = {};
+  const int rc = allow_smem(reinterpret_cast<const void*>(kv_fork_kernel<CACHED>), kForkSmem, ready);
+  if (rc != FA_OK) return rc;
+  kv_fork_kernel<CACHED><<<kCluster, kThreads, smem, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 template <int DQK, int DV>
 int copy_start(const CopyParams& p, int sms, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
@@ -514,11 +546,10 @@ int fa_kv_fork(const fa_kv_cache* cache, void* k_bounds, const int* page_refs, i
   p.seqlens_out = seqlens_out;
   p.refs_out = refs_out;
   p.status = host.status;
-  static bool ready[64] = {};
-  rc = allow_smem(reinterpret_cast<const void*>(kv_fork_kernel), sizeof(int) * (3 * kMaxBatch + 1), ready);
+  const size_t least = sizeof(int) * ((2 * static_cast<size_t>(batch) + rows + 2) & ~size_t(1));
+  const size_t cached = least + sizeof(uint64_t) * rows;
+  rc = cached <= kForkSmem ? fork_start<true>(p, cached, stream) : fork_start<false>(p, least, stream);
   if (rc != FA_OK) return rc;
-  kv_fork_kernel<<<kCluster, kThreads, sizeof(int) * (2 * static_cast<size_t>(batch) + rows + 1), stream>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   return copy_launch(p, c, static_cast<uint8_t*>(k_bounds), false, host.sms, stream);
 }
 

@@ -47,15 +47,20 @@ __global__ void __launch_bounds__(kTableThreads) rotary_table_kernel(const __gri
   const int rows = kTableThreads / groups;          // positions of a block's step
   const int g = threadIdx.x % groups, r = threadIdx.x / groups;
   if (r >= rows) return;
-  uint64_t turn[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) turn[k] = p.turn[4 * g + k];
   const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
-  for (int64_t pos = static_cast<int64_t>(blockIdx.x) * rows + r; pos < p.positions; pos += step) {
+  int64_t pos = static_cast<int64_t>(blockIdx.x) * rows + r;
+  uint64_t turns[4], more[4];  // at this position, and for a step
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    turns[k] = static_cast<uint64_t>(pos) * p.turn[4 * g + k];
+    more[k] = static_cast<uint64_t>(step) * p.turn[4 * g + k];
+  }
+  for (; pos < p.positions; pos += step) {
     float c[4], s[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const uint64_t t = static_cast<uint64_t>(pos) * turn[k];
+      const uint64_t t = turns[k];
+      turns[k] += more[k];
       const uint32_t quarter = static_cast<uint32_t>((t + (1ull << 61)) >> 62);
       const uint64_t rest = t - (static_cast<uint64_t>(quarter) << 62);  // signed, of 2^64 a turn
       const float x = fmaf(static_cast<float>(static_cast<int>(rest >> 32)), 0x1p-32f * 6.28318530717958647692f,
@@ -95,13 +100,12 @@ struct RotaryParams {
   uint32_t flip;  // sign bit to change in the sines
 };
 
-// A warp holds kHeads heads at a time in kPasses passes of 32 items of 16 values.
+// A warp holds kHeads heads at a time, 16 values a lane (at d = 192 eight lanes have none).
 template <int D>
 struct RotaryShape {
   static constexpr int kItems = D / 16;
-  static constexpr int kPasses = D == 192 ? 3 : 1;
-  static constexpr int kHeads = 32 * kPasses / kItems;
-  static constexpr int kAhead = D == 192 ? 1 : 4;  // groups of heads whose loads are under way together
+  static constexpr int kHeads = 32 / kItems;
+  static constexpr int kAhead = 4;  // groups of heads whose loads are under way together
   static constexpr int kWarps = 8;
 };
 
@@ -140,69 +144,57 @@ __global__ void __launch_bounds__(32 * RotaryShape<D>::kWarps) rotary_kernel(con
   const int begin = static_cast<int>(static_cast<int64_t>(all) * split / p.splits);
   const int end = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / p.splits);
 
-  int first[Shape::kPasses], second[Shape::kPasses], item[Shape::kPasses], off[Shape::kPasses];
-#pragma unroll
-  for (int k = 0; k < Shape::kPasses; ++k) {
-    item[k] = (32 * k + lane) % Shape::kItems;
-    off[k] = (32 * k + lane) / Shape::kItems;
-    item_columns<D>(item[k], p.rot, first[k], second[k]);
-  }
-  uint4 raw[Shape::kAhead][Shape::kPasses][2];
+  const int item = lane % Shape::kItems, off = lane / Shape::kItems;
+  const bool turned = item * 16 < p.rot, active = off < Shape::kHeads;
+  int first, second;
+  item_columns<D>(item, p.rot, first, second);
+  uint4 raw[Shape::kAhead][2];
+  // the row of this lane's head in group `group`, or NULL
+  auto row_of = [&](int group, auto* const (&base)[2], const int64_t (&stride)[2]) {
+    const int x = group >= p.groups[0];
+    const int head = (x ? group - p.groups[0] : group) * Shape::kHeads + off;
+    return active && group < end && head < p.heads[x] ? base[x] + t * stride[x] + head * D : nullptr;
+  };
   auto load = [&](int group0) {
 #pragma unroll
     for (int i = 0; i < Shape::kAhead; ++i) {
-      const int group = group0 + i;
-      const int x = group >= p.groups[0];
-      const int head0 = (x ? group - p.groups[0] : group) * Shape::kHeads;
-      const __nv_bfloat16* row = p.src[x] + t * p.src_stride[x];
-#pragma unroll
-      for (int k = 0; k < Shape::kPasses; ++k)
-        if (group < end && head0 + off[k] < p.heads[x]) {
-          const __nv_bfloat16* at = row + (head0 + off[k]) * D;
-          raw[i][k][0] = *reinterpret_cast<const uint4*>(at + first[k]);
-          raw[i][k][1] = *reinterpret_cast<const uint4*>(at + second[k]);
-        }
+      const __nv_bfloat16* at = row_of(group0 + i, p.src, p.src_stride);
+      if (at != nullptr) {
+        raw[i][0] = *reinterpret_cast<const uint4*>(at + first);
+        raw[i][1] = *reinterpret_cast<const uint4*>(at + second);
+      }
     }
   };
   load(begin);  // before the position is known
 
   const int pos = rotary_position(p, t);
   if (pos < 0) return;
-  float cs[Shape::kPasses][16];
+  float cs[16];
+  if (turned) {
+    load_cos_sin(cs, p.cos_sin + static_cast<int64_t>(pos) * p.rot, item, p.rot, p.interleaved);
 #pragma unroll
-  for (int k = 0; k < Shape::kPasses; ++k)
-    if (item[k] * 16 < p.rot) {
-      load_cos_sin(cs[k], p.cos_sin + static_cast<int64_t>(pos) * p.rot, item[k], p.rot, p.interleaved);
-#pragma unroll
-      for (int j = 8; j < 16; ++j) cs[k][j] = __uint_as_float(__float_as_uint(cs[k][j]) ^ p.flip);
-    }
+    for (int j = 8; j < 16; ++j) cs[j] = __uint_as_float(__float_as_uint(cs[j]) ^ p.flip);
+  }
 
   for (int group0 = begin; group0 < end; group0 += Shape::kAhead) {
     if (group0 != begin) load(group0);
 #pragma unroll
     for (int i = 0; i < Shape::kAhead; ++i) {
-      const int group = group0 + i;
-      const int x = group >= p.groups[0];
-      const int head0 = (x ? group - p.groups[0] : group) * Shape::kHeads;
-      __nv_bfloat16* row = p.dst[x] + t * p.dst_stride[x];
-#pragma unroll
-      for (int k = 0; k < Shape::kPasses; ++k)
-        if (group < end && head0 + off[k] < p.heads[x]) {
-          uint4 (&v)[2] = raw[i][k];
-          if (item[k] * 16 < p.rot) {
-            float y[16];
-            unpack8(v[0], y);
-            unpack8(v[1], y + 8);
-            turn16(y, cs[k], p.interleaved);
-            v[0] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                              pack_bf16x2(y[6], y[7]));
-            v[1] = make_uint4(pack_bf16x2(y[8], y[9]), pack_bf16x2(y[10], y[11]), pack_bf16x2(y[12], y[13]),
-                              pack_bf16x2(y[14], y[15]));
-          }
-          __nv_bfloat16* at = row + (head0 + off[k]) * D;
-          *reinterpret_cast<uint4*>(at + first[k]) = v[0];
-          *reinterpret_cast<uint4*>(at + second[k]) = v[1];
-        }
+      __nv_bfloat16* at = row_of(group0 + i, p.dst, p.dst_stride);
+      if (at == nullptr) continue;
+      uint4 (&v)[2] = raw[i];
+      if (turned) {
+        float y[16];
+        unpack8(v[0], y);
+        unpack8(v[1], y + 8);
+        turn16(y, cs, p.interleaved);
+        v[0] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                          pack_bf16x2(y[6], y[7]));
+        v[1] = make_uint4(pack_bf16x2(y[8], y[9]), pack_bf16x2(y[10], y[11]), pack_bf16x2(y[12], y[13]),
+                          pack_bf16x2(y[14], y[15]));
+      }
+      *reinterpret_cast<uint4*>(at + first) = v[0];
+      *reinterpret_cast<uint4*>(at + second) = v[1];
     }
   }
 }

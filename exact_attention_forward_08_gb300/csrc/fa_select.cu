@@ -270,12 +270,12 @@ __device__ __forceinline__ int code_place(int row, int chunk) {
   return row * 2 * D + ((chunk ^ ((row & 1) << 2)) << 4);
 }
 
-__device__ __forceinline__ void mma_16x8x16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+__device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                             uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // A block takes 128 pages of a sequence and one key head, 16 a warp, whose bounds it
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kSelectThreads, kScoreBlocks) kv_score_kernel(
     for (int x0 = 0; x0 < tokens; x0 += kTokens) {
       // column g of the second operand: part g & 1 of token x0 + g / 2 (of any content behind the last)
       const uint8_t* q = &sh.q[x0 + (g >> 1)][g & 1][0];
-      float acc[4][4] = {};
+      float acc[4] = {};
 #pragma unroll 1
       for (int st = 0; st < D / 32; ++st) {
         const int chunk = 4 * st + c;
@@ -392,10 +392,13 @@ __global__ void __launch_bounds__(kSelectThreads, kScoreBlocks) kv_score_kernel(
         const uint4 q0 = *reinterpret_cast<const uint4*>(q + 32 * chunk), q1 = *reinterpret_cast<const uint4*>(q + 32 * chunk + 16);
         const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
         const uint32_t wq[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+        float part[4][4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_16x8x16(acc[k], e4m3x2_f16x2(wl[k]), e4m3x2_f16x2(wh[k]), e4m3x2_hi_f16x2(wl[k]), e4m3x2_hi_f16x2(wh[k]),
+          mma_16x8x16(part[k], e4m3x2_f16x2(wl[k]), e4m3x2_f16x2(wh[k]), e4m3x2_hi_f16x2(wl[k]), e4m3x2_hi_f16x2(wh[k]),
                       wq[2 * k], wq[2 * k + 1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] += (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
       }
       const int x = x0 + c;  // this lane's token
       if (x >= tokens) continue;
@@ -403,9 +406,7 @@ __global__ void __launch_bounds__(kSelectThreads, kScoreBlocks) kv_score_kernel(
       for (int half = 0; half < 2; ++half) {
         const int j = j0 + g + 8 * half;
         if (j >= pages) break;
-        const float upper = (acc[0][2 * half] + acc[1][2 * half]) + (acc[2][2 * half] + acc[3][2 * half]);
-        const float lower = (acc[0][2 * half + 1] + acc[1][2 * half + 1]) + (acc[2][2 * half + 1] + acc[3][2 * half + 1]);
-        const float sum = e_g[half] == 255 ? __uint_as_float(0x7fc00000u) : upper + lower;
+        const float sum = e_g[half] == 255 ? __uint_as_float(0x7fc00000u) : acc[2 * half] + acc[2 * half + 1];
         p.keys[((first_token + x) * p.heads + head) * p.max_pages + j] =
             entry_g[half] < 0 ? 0u : score_key(sum, e_g[half] - 127 - sh.q_shift[x]);
       }
@@ -420,10 +421,13 @@ __global__ void __launch_bounds__(kSelectThreads, kScoreBlocks) kv_score_kernel(
 // ---- the choice ----
 
 constexpr int kBinBits = 11, kBins = 1 << kBinBits;
+constexpr int kFewPages = 64;
 
 struct ChooseShared {
   uint32_t stage[kStagePages];  // keys
-  int bins[kBins], bin, rank;
+  int bins[kBins], bin, rank, in_bin, listed;
+  int few[kFewPages];           // pages near the cut, and their scores in 64 bits
+  uint64_t few_score[kFewPages];
   double q[2 * 192];            // q+ and q- in 64 bits
   int sums[2][kSelectWarps];
   uint32_t least[kSelectWarps], most[kSelectWarps], near_low, near_high;
@@ -494,7 +498,8 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
   }
   auto key = [&](int j) { return staged ? sh.stage[j] : __ldcg(keys + j); };
 
-  // ---- T, the k-th largest key: a histogram of the keys from low to high, again of the bin that holds it ----
+  // ---- T, the k-th largest key: a histogram of the keys from low to high, again of the bin that holds it if that
+  // holds many ----
   uint32_t near_low = 0xffffffffu, near_high = 0xffffffffu;
   bool close = false;
   if (k > 0) {
@@ -535,6 +540,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
           if (above < rank && rank <= above + count[i]) {
             sh.bin = kBins - 1 - (tid * kMine + i);
             sh.rank = rank - above;
+            sh.in_bin = count[i];
           }
           above += count[i];
         }
@@ -544,6 +550,25 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
       const uint32_t from = low + (static_cast<uint32_t>(sh.bin) << shift), to = from + ((1u << shift) - 1);
       high = to < from || to > high ? high : to;
       low = from;
+      const int in_bin = sh.in_bin;
+      if (in_bin <= 32 && low < high) {  // few: a warp finds the one that has `rank` - 1 above it
+        if (tid == 0) sh.listed = 0;
+        __syncthreads();
+        for (int j = p.first + tid; j < end; j += kSelectThreads) {
+          const uint32_t v = key(j);
+          if (v >= low && v <= high) sh.few[atomicAdd(&sh.listed, 1)] = static_cast<int>(v);
+        }
+        __syncthreads();
+        const uint32_t v = lane < in_bin ? static_cast<uint32_t>(sh.few[lane]) : 0u;  // every warp for itself
+        int above = 0, with = 0;
+        for (int i = 0; i < in_bin; ++i) {
+          const uint32_t other = __shfl_sync(0xffffffffu, v, i);
+          above += other > v;
+          with += other >= v;
+        }
+        const uint32_t found = __ballot_sync(0xffffffffu, lane < in_bin && above < rank && rank <= with);
+        low = high = __shfl_sync(0xffffffffu, v, __ffs(found) - 1);
+      }
     }
     if (tid == 0) {
       float q_all = 0.f;
@@ -574,8 +599,10 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
   int ties = 0;  // of the pages at cut64, so many are in
   if (close) {
     const __nv_bfloat16* q = p.q + unit * p.ratio * D;
+    if (tid == 0) sh.bin = 0;  // now the number of pages near
     for (int i = tid; i < D; i += kSelectThreads) {
       double pos = 0.0, neg = 0.0;
+#pragma unroll 4
       for (int h = 0; h < p.ratio; ++h) {
         const float v = __bfloat162float(q[h * D + i]);  // a NaN goes into both
         pos += v < 0.f ? 0.0 : static_cast<double>(v), neg += v > 0.f ? 0.0 : static_cast<double>(v);
@@ -584,64 +611,92 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
     }
     __syncthreads();
     int in = 0;
-    uint64_t low64 = ~0ull, high64 = 0;
-    for (int j0 = p.first + warp * 32; j0 < end; j0 += kSelectThreads) {
-      const int j = j0 + lane;
-      const uint32_t v = j < end ? key(j) : 0u;
-      in += j < end && v > near_high;
-      uint32_t todo = __ballot_sync(0xffffffffu, j < end && v >= near_low && v <= near_high);
-      while (todo != 0) {
-        const int at = j0 + __ffs(todo) - 1;
-        todo &= todo - 1;
-        const int page = listed(at);
-        double sum = 0.0;
-        if (page >= 0) {
-          const int64_t ph = static_cast<int64_t>(page) * p.heads + head;
-          const uint8_t* codes = p.bounds + ph * 2 * D;
-          for (int i = lane; i < D / 2; i += 32) {
-            const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(codes) + i);
-            const float2 f0 = f16x2_float2(e4m3x2_f16x2(w)), f1 = f16x2_float2(e4m3x2_hi_f16x2(w));
-            sum += sh.q[4 * i] * f0.x + sh.q[4 * i + 1] * f0.y + sh.q[4 * i + 2] * f1.x + sh.q[4 * i + 3] * f1.y;
-          }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          sum *= scale_double(p.k_scale[ph]);
-        } else {
-          sum = -__longlong_as_double(0x7ff0000000000000ll);
-        }
-        const uint64_t o = order64(sum);
-        low64 = o < low64 ? o : low64, high64 = o > high64 ? o : high64;
-        if (lane == 0) exact[at] = o;
+    for (int j = p.first + tid; j < end; j += kSelectThreads) {
+      const uint32_t v = key(j);
+      in += v > near_high;
+      if (v >= near_low && v <= near_high) {
+        const int place = atomicAdd(&sh.bin, 1);
+        if (place < kFewPages) sh.few[place] = j;
       }
     }
-    in = block_sum(in, sh.sums, turn);  // its barrier: the stores above are there for the block
-    if (lane == 0) sh.least64[warp] = low64, sh.most64[warp] = high64;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kSelectWarps; ++w) {
-      low64 = sh.least64[w] < low64 ? sh.least64[w] : low64;
-      high64 = sh.most64[w] > high64 ? sh.most64[w] : high64;
-    }
+    in = block_sum(in, sh.sums, turn);
     const int need = k - in;  // 1 at least, and no more than are near
-    auto count64 = [&](uint64_t from) {
-      int n = 0;
-      for (int j = p.first + tid; j < end; j += kSelectThreads) {
-        const uint32_t v = key(j);
-        n += v >= near_low && v <= near_high && exact[j] >= from;
+    auto score = [&](int j) {  // by a warp
+      const int page = listed(j);
+      if (page < 0) return order64(-__longlong_as_double(0x7ff0000000000000ll));
+      const int64_t ph = static_cast<int64_t>(page) * p.heads + head;
+      const uint8_t* codes = p.bounds + ph * 2 * D;
+      const int e = p.k_scale[ph];
+      double sum = 0.0;
+#pragma unroll
+      for (int i = lane; i < D / 2; i += 32) {
+        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(codes) + i);
+        const float2 f0 = f16x2_float2(e4m3x2_f16x2(w)), f1 = f16x2_float2(e4m3x2_hi_f16x2(w));
+        sum += (sh.q[4 * i] * f0.x + sh.q[4 * i + 1] * f0.y) + (sh.q[4 * i + 2] * f1.x + sh.q[4 * i + 3] * f1.y);
       }
-      return block_sum(n, sh.sums, turn);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      return order64(sum * scale_double(e));
     };
-    int n = count64(low64);
-    uint64_t lo64 = low64, hi64 = high64;
-    while (n != need && lo64 < hi64) {
-      const uint64_t mid = lo64 + (hi64 - lo64) / 2 + 1;
-      const int m = count64(mid);
-      if (m >= need) lo64 = mid, n = m;
-      else hi64 = mid - 1;
+    const int few = sh.bin;
+    if (few <= kFewPages && staged) {
+      // ---- few: each is compared with the others, and its key becomes the largest or the least ----
+      for (int i = warp; i < few; i += kSelectWarps) {
+        const uint64_t o = score(sh.few[i]);
+        if (lane == 0) sh.few_score[i] = o;
+      }
+      __syncthreads();
+      if (tid < few) {
+        const uint64_t o = sh.few_score[tid];
+        const int j = sh.few[tid];
+        int before = 0;
+        for (int i = 0; i < few; ++i) before += sh.few_score[i] > o || (sh.few_score[i] == o && sh.few[i] < j);
+        sh.stage[j] = before < need ? 0xffffffffu : 0u;
+      }
+      close = false;
+      near_low = max(near_low, 1u);
+      __syncthreads();
+    } else {
+      uint64_t low64 = ~0ull, high64 = 0;
+      for (int j0 = p.first + warp * 32; j0 < end; j0 += kSelectThreads) {
+        const int j = j0 + lane;
+        const uint32_t v = j < end ? key(j) : 0u;
+        uint32_t todo = __ballot_sync(0xffffffffu, j < end && v >= near_low && v <= near_high);
+        while (todo != 0) {
+          const int at = j0 + __ffs(todo) - 1;
+          todo &= todo - 1;
+          const uint64_t o = score(at);
+          low64 = o < low64 ? o : low64, high64 = o > high64 ? o : high64;
+          if (lane == 0) exact[at] = o;
+        }
+      }
+      if (lane == 0) sh.least64[warp] = low64, sh.most64[warp] = high64;
+      __syncthreads();  // the stores above are there for the block
+#pragma unroll
+      for (int w = 0; w < kSelectWarps; ++w) {
+        low64 = sh.least64[w] < low64 ? sh.least64[w] : low64;
+        high64 = sh.most64[w] > high64 ? sh.most64[w] : high64;
+      }
+      auto count64 = [&](uint64_t from) {
+        int n = 0;
+        for (int j = p.first + tid; j < end; j += kSelectThreads) {
+          const uint32_t v = key(j);
+          n += v >= near_low && v <= near_high && exact[j] >= from;
+        }
+        return block_sum(n, sh.sums, turn);
+      };
+      int n = count64(low64);
+      uint64_t lo64 = low64, hi64 = high64;
+      while (n != need && lo64 < hi64) {
+        const uint64_t mid = lo64 + (hi64 - lo64) / 2 + 1;
+        const int m = count64(mid);
+        if (m >= need) lo64 = mid, n = m;
+        else hi64 = mid - 1;
+      }
+      cut64 = lo64;
+      ties = INT_MAX;
+      if (n != need) ties = need - count64(lo64 + 1);  // lo64 is a score of several pages
     }
-    cut64 = lo64;
-    ties = INT_MAX;
-    if (n != need) ties = need - count64(lo64 + 1);  // lo64 is a score of several pages
   }
 
   // ---- the chosen pages in order: a warp counts, then writes, a run of pages ----
@@ -697,10 +752,10 @@ SelectWorkspace select_workspace(int batch, int64_t total, int heads, int max_pa
 }
 
 // Roundings of a score: 2^-24 for each addition to q+ and q-; 2^-22 and less than 2^-28 for their two parts; 2^-23 for
-// each of 2 d / 4 additions to a sum (single precision, rounded in any way) and the last five; 2^-20 for what the key
-// drops; 1 / 256 more of it all for the products of these factors and the rounding of the bound itself.
+// each of 16 additions of a product (single precision, rounded in any way), 2^-24 for each of the d / 32 + 3 after it;
+// 2^-20 for what the key drops; 1 / 256 more of it all for the products of these factors and the bound's own rounding.
 double score_error(int ratio, int d) {
-  return (ratio * 0x1p-24 + 0x1p-22 + 0x1p-28 + (d / 2 + 5) * 0x1p-23 + 0x1p-20) * (1.0 + 0x1p-8);
+  return (ratio * 0x1p-24 + 0x1p-22 + 0x1p-28 + 16 * 0x1p-23 + (d / 32 + 3) * 0x1p-24 + 0x1p-20) * (1.0 + 0x1p-8);
 }
 
 template <int D>
