@@ -112,7 +112,10 @@ def lists_attention(q, cache, lists, lens, scale=None):
 def fork(table, lens, refs, parents, grow, page, num_pages, width):
     """(rows, lengths, counts, copies (from, to, tokens)): lists of Python numbers; rows that find no page become empty."""
     refs = list(refs)
-    heirs = [[r for r, a in enumerate(parents) if a == b] for b in range(len(table))]
+    heirs = [[] for _ in table]
+    for r, a in enumerate(parents):
+        if a >= 0:
+            heirs[a].append(r)
     for b, row in enumerate(table):
         for j in range(-(-lens[b] // page)):
             refs[row[j]] += len(heirs[b]) - 1 if (j + 1) * page <= lens[b] else min(len(heirs[b]), 1) - 1

@@ -199,3 +199,40 @@ def test_two_calls_at_once_with_their_own_workspaces(fa):
             for x, y in zip(got, alone[i][2:]):
                 assert torch.equal(x, y)
 
+
+def test_a_pool_of_more_than_four_gigabytes(fa):
+    """The last pages of a pool whose offsets pass 32 bits: bounds, selection, attention, a fork's copy, a compaction."""
+    heads, page, d, lens = 8, 128, 128, [300, 129]
+    pages = 36000  # 4.7 GB of keys
+    small = ref.Cache(lens, heads, page, d, d, spare=0)
+    n = small.num_pages
+    last = torch.arange(pages - n, pages)
+    k, v = (torch.empty(pages, heads, page, d, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.full((pages, heads), 127, dtype=torch.uint8, device="cuda") for _ in range(2))
+    k[last], v[last] = small.k.view(torch.uint8).cuda(), small.v.view(torch.uint8).cuda()
+    ks[last], vs[last] = small.k_scale.view(torch.uint8).cuda(), small.v_scale.view(torch.uint8).cuda()
+    pool = (*(t.view(torch.float8_e4m3fn) for t in (k, v)), *(t.view(torch.float8_e8m0fnu) for t in (ks, vs)))
+    table = torch.where(small.table >= 0, small.table + (pages - n), small.table).to(torch.int32).cuda()
+    seqlens, refs = int32(lens), int32([0] * (pages - n) + [1] * n)
+    bounds = torch.zeros(pages, heads, 2, d, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    cu = int32([0, 300, 429])
+    fa.kv_bounds(pool[0], bounds, table, seqlens, cu, 429)
+    full = want.all_bounds(small)
+    assert torch.equal(bounds[pages - n:].float().cpu(), full.float())
+    q = torch.randn(2, 16, d, generator=torch.Generator().manual_seed(0)).to(torch.bfloat16)
+    one = int32([0, 1, 2])
+    lists, list_lens = fa.kv_select(q.cuda(), bounds, pool[2], table, seqlens, one, 1, page, 2)
+    ex, ex_lens = want.select(q, full, small.k_scale, small.table, lens, [0, 1, 2], page, 2)
+    assert torch.equal(lists.cpu().long(), torch.where(ex >= 0, ex + pages - n, ex)) and torch.equal(list_lens.cpu().long(), ex_lens)
+    o, lse = fa.attention_forward_lists(q.cuda(), *pool, lists, list_lens)
+    ref.check_attention(o, lse, want.lists_attention(q, small, ex, ex_lens.tolist()), EPS_F16)
+    # a copy from the last page to page 0, then all pages to the front
+    table2, lens2, refs2 = fa.kv_fork(int32([0, 1, 1]), *pool, table, seqlens, refs, k_bounds=bounds)
+    assert table2[2, 1] == 0 and lens2.tolist() == [300, 129, 129]
+    assert torch.equal(k[0, :, :1], k[table2[1, 1].long(), :, :1]) and torch.equal(v[0, :, :1], v[table2[1, 1].long(), :, :1])
+    table3, refs3, page_map, used = fa.kv_compact(*pool, table2, lens2, refs2, k_bounds=bounds)
+    assert int(used) == n + 1 and int(table3.max()) == n
+    moved = torch.where(lists >= 0, page_map[lists.clamp(min=0).long()], lists)
+    again, again_lse = fa.attention_forward_lists(q.cuda(), *pool, moved, list_lens)
+    assert torch.equal(again, o) and torch.equal(again_lse, lse)
+    assert fa.fa_device_status()[0] == 0

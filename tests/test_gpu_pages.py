@@ -37,7 +37,10 @@ class Pool:
         for a, b, pages in share:  # row b begins with row a's first pages, full ones
             order += self.table[b][:pages]
             self.table[b][:pages] = self.table[a][:pages]
-        self.refs = [sum(p in set(row) for row in self.table) for p in range(self.num_pages)]
+        self.refs = [0] * self.num_pages
+        for row in self.table:
+            for p in row:
+                self.refs[p] += 1
         self.lens, self.page, self.heads, self.d = list(lens), page, heads, (d_qk, d_v)
         g = torch.Generator().manual_seed(seed)
         self.data = {n: torch.randint(0, 256, (self.num_pages, heads, page, d), generator=g, dtype=torch.uint8)
@@ -155,6 +158,40 @@ def test_fork_of_many_rows_and_pages(fa):
     assert not check_fork(fa, tight, [b if b % 2 else -1 for b in range(1500)], [64] * 1500)
     tight = Pool([16 * 4] * 1500, 16, 1, 64, 64, spare=0, width=8)
     assert check_fork(fa, tight, [b if b % 2 else -1 for b in range(1500)], [0 if b % 2 else 64 for b in range(1500)])
+
+
+@pytest.mark.parametrize("spare", [3000, 9000, 20000])
+def test_fork_of_the_largest_tables(fa, spare):
+    """As many rows as a call takes, more than a block of the kernel can keep; with too few pages for all of them, and enough:
+    the rows want 15323 new pages, and those without an heir free 10502."""
+    r = random.Random(9)
+    batch = 16384
+    pool = Pool([r.randint(0, 30) for _ in range(batch)], 16, 1, 64, 64, spare=spare, width=5)
+    parents = [r.choice([-1, r.randrange(batch), r.randrange(batch), b]) for b in range(batch)]
+    grow = [r.randint(0, 20) for _ in range(batch)]
+    assert check_fork(fa, pool, parents, grow) == (spare >= 15323 - 10502)
+
+
+def test_fork_wants_more_pages_than_fit_32_bits(fa):
+    """Rows that ask for 2^26 pages each, 40 of them: all fail but those before that fit."""
+    pool = Pool([40, 20], 16, 1, 64, 64, spare=30, width=12)
+    big = 1 << 26
+    table = torch.full((2, big), -7, dtype=torch.int32, device="cuda")
+    table[:, :12] = pool.block_table
+    parents, grow = [0, 1] + [-1] * 40 + [0, 1], [3, 0] + [(big - 8) * 16] * 40 + [0, 5]
+    rows = len(parents)
+    out = torch.empty(rows, big, dtype=torch.int32, device="cuda")
+    got, lens, refs = fa.kv_fork(int32(parents), *pool.cache(), table, pool.seqlens, pool.page_refs, new_tokens=int32(grow),
+                                 k_bounds=pool.bounds(), table_out=out)
+    torch.cuda.synchronize()
+    code, detail = fa.fa_device_status()
+    assert code == fa.FA_ERR_INVALID_ARG and detail[1:] == (515, 2)
+    # rows 0 and 1 keep their pages; the 40 find too few, and so do the last two, which want a copy each
+    assert lens.tolist() == [43, 20] + [0] * 42
+    assert got[0, :3].tolist() == pool.table[0] and got[1, :2].tolist() == pool.table[1]
+    assert (got[2:] == -1).all() and (got[:2, 3:] == -1).all()
+    assert refs.tolist() == pool.refs
+    pool.check_pages([])
 
 
 def test_fork_into_given_tensors(fa):

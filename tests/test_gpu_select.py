@@ -182,6 +182,14 @@ def test_equal_scores_take_the_lowest_pages(fa):
             check(fa, q, bounds, scale, table, [4799], [1], 16, 50, first=3, last=4)
 
 
+def test_equal_scores_among_more_pages_than_are_staged(fa):
+    bounds, scale, table = wide(5000, 1, 64, seed=2)
+    alike = torch.arange(5000) % 40
+    bounds = bounds.view(torch.uint8)[alike].view(torch.float8_e4m3fn)
+    scale = scale.view(torch.uint8)[alike].view(torch.float8_e8m0fnu)
+    check(fa, normal(2, 4, 64), bounds, scale, table, [80000], [2], 16, 333, first=2, last=3)
+
+
 @pytest.mark.parametrize("small", [2.0 ** -12, 2.0 ** -18, 2.0 ** -24, 2.0 ** -30])
 def test_scores_that_fp32_cannot_tell_apart(fa, small):
     """Pages that differ in one channel only, whose query is smaller by 2^12 to 2^30 than the others."""
@@ -202,6 +210,28 @@ def test_scales_and_queries_at_the_ends_of_their_ranges(fa, spread, q_exp):
     bounds, scale, table = wide(400, 2, 64, seed=8, scale=spread)
     q = (normal(2, 4, 64).double() * 2.0 ** q_exp).to(torch.bfloat16)
     check(fa, q, bounds, scale, table, [6400], [2], 16, 37)
+
+
+@pytest.mark.parametrize("q_exp", [-133, -120, -95, -90])
+def test_queries_that_cannot_be_scaled_all_the_way(fa, q_exp):
+    """Largest values down to bf16's smallest numbers, and rows of zeros beside them."""
+    bounds, scale, table = wide(300, 2, 64, seed=9)
+    q = (normal(3, 4, 64).double() * 2.0 ** q_exp).to(torch.bfloat16)
+    q[1] = 0
+    q[2, 0] = 0
+    check(fa, q, bounds, scale, table, [4800], [3], 16, 21)
+
+
+@pytest.mark.parametrize("signs", [1, -1])
+def test_sums_of_equal_signs(fa, signs):
+    """All products of one sign: sums that grow with every term, where products' sums round the most."""
+    g = torch.Generator().manual_seed(1)
+    x = torch.randint(200, 448, (3000, 1, 2, 192), generator=g).float()
+    bounds = (x.sort(2, descending=True)[0] * signs).to(torch.float8_e4m3fn)
+    bounds = bounds if signs > 0 else bounds.view(torch.uint8).flip(2).view(torch.float8_e4m3fn)
+    scale, table = ref.e8m0(torch.zeros(3000, 1)), torch.randperm(3000, generator=g).to(torch.int32)[None]
+    q = normal(4, 8, 192).abs() + 1
+    check(fa, q, bounds, scale, table, [48000], [4], 16, 100)
 
 
 def test_what_is_no_number_is_taken_first(fa):
