@@ -80,6 +80,10 @@ struct PagedJoin {
 };
 
 constexpr int kMinTokens = 64;        // a piece is not cut smaller
+// Tiles that a list's start costs beside its own: its queries, its pages and their scales, one after the other.  64
+// lists of 1 to 64 pages of 64, 32/8 heads of 128: 94 us without, where a piece of many short lists is the last to end,
+// 75.9, 72.7 and 73.7 with 1, 2 and 4.
+constexpr int kListStart = 2;
 constexpr float kPShift = 7.f;        // P is scaled by 2^7: f16 then holds weights down to 2^-31
 constexpr float kRefLag = 8.f;        // the reference follows the maximum when it lags by more (log2 units)
 
@@ -261,9 +265,9 @@ struct PagedLine {
 template <int TILE, int THREADS, int TEAMS, int START, bool LISTS = false>
 __device__ __forceinline__ void paged_line(const PagedParams& p, long long* scan, long long* warp_sum,
                                            PagedCursor* begin_at, int* tiles, PagedLine& line) {
-  static_assert(START == 0 || TEAMS == 1, "tiles are counted for one team");
+  static_assert(START == 0 || TEAMS == 1 || LISTS, "tiles are counted for one team");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (START > 0 && tid == 0) *tiles = 0;
+  if (START > 0 && !LISTS && tid == 0) *tiles = 0;
   PagedSeq mine;
   long long v;                                   // places of this thread's sequence
   auto scan_block = [&](int base) -> long long {  // inclusive scan of THREADS sequences' places into scan[]
@@ -301,7 +305,7 @@ __device__ __forceinline__ void paged_line(const PagedParams& p, long long* scan
   for (int base = 0; base < p.batch; base += THREADS) {
     if (p.batch > THREADS) scan_block(base);
     const long long sum = scan[THREADS - 1];
-    if constexpr (START > 0) {  // each thread for its own sequence
+    if constexpr (START > 0 && !LISTS) {  // each thread for its own sequence
       const long long before = offset + scan[tid] - v, x0 = line.piece(0) * line.per;
       const long long x1 = x0 + line.per < line.total ? x0 + line.per : line.total;
       const long long lo = (x0 > before ? x0 : before) - before, hi = (x1 < before + v ? x1 : before + v) - before;
@@ -333,8 +337,13 @@ __device__ __forceinline__ void paged_line(const PagedParams& p, long long* scan
         c.b = base + lo;
         c.s = paged_seq<TILE, LISTS>(p, c.b);
         const long long in = x - (lo > 0 ? scan[lo - 1] : 0);
-        c.head = static_cast<int>(in / c.s.tiles);
-        c.tile = static_cast<int>(in - static_cast<long long>(c.head) * c.s.tiles);
+        const int unit = c.s.tiles + START;
+        c.head = static_cast<int>(in / unit);
+        c.tile = static_cast<int>(in - static_cast<long long>(c.head) * unit) - START;
+        if constexpr (START > 0) {  // the first tile at this place or behind
+          c.at = x + offset + (c.tile < 0 ? -c.tile : 0);
+          if (c.tile < 0) c.tile = 0;
+        }
         begin_at[tid] = c;
       }
     }
@@ -377,7 +386,9 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   PagedLine line;
-  paged_line<kTile, kThreads, kTeams, 0, LISTS>(p, scan, warp_sum, begin_at, nullptr, line);
+  constexpr int kStart = LISTS ? kListStart : 0;
+  static_assert(!LISTS || kStart > 0, "places of the line count a list's tiles");
+  paged_line<kTile, kThreads, kTeams, kStart, LISTS>(p, scan, warp_sum, begin_at, nullptr, line);
 
   const int team = warp;
   const int g = lane >> 2, c = lane & 3;
@@ -385,6 +396,10 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
   if (count == 0) return;
   const long long piece = line.piece(team), begin = piece * line.per;
   PagedCursor cur = begin_at[team];
+  const long long piece_end = begin + count;
+  if (LISTS && cur.at >= piece_end) return;  // nothing but a unit's start
+  // LISTS: is there a tile in the piece after a cursor's?
+  auto more = [&](const PagedCursor& at) { return at.at + 1 + (at.tile + 1 < at.s.tiles ? 0 : kStart) < piece_end; };
   const uint32_t ring = smem0 + team * kSlots * Shape::kSlotBytes;
 
   // ---- the warp fills its ring: tile after tile, K and V by turns ----
@@ -469,8 +484,9 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
       }
     }
   };
-  auto fill = [&]() {  // the next slot, which has been read
-    if (filled < 2 * count) {
+  bool ahead_more = true;  // the cursor's tile is to be filled in
+  auto fill = [&]() {      // the next slot, which has been read
+    if (LISTS ? ahead_more : filled < 2 * count) {
       const bool is_k = (filled & 1) == 0;
       const int token = ahead.tile * kTile;
       const uint32_t dst = ring + fill_slot * Shape::kSlotBytes;
@@ -484,9 +500,12 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
       if (lane < kTile / 16) slot_scale[team * kSlots + fill_slot][lane] = scale;
       ++filled;
       if (++fill_slot == kSlots) fill_slot = 0;
-      if (!is_k && filled < 2 * count) {  // on to the next tile
+      if constexpr (LISTS) {
+        if (!is_k) ahead_more = more(ahead);
+      }
+      if (!is_k && (LISTS ? ahead_more : filled < 2 * count)) {  // on to the next tile
         const int b = ahead.b, head = ahead.head;
-        paged_next<kTile, 0, LISTS>(p, ahead);
+        paged_next<kTile, kStart, LISTS>(p, ahead);
         if (ahead.head != head) set_head();
         const int next = (ahead.tile * kTile) >> p.page_shift;
         if (!LISTS && ahead.b == b && ahead.head == head + 1 && page0 == 0) take_scales();  // the same pages, the next head
@@ -514,7 +533,9 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
   int min_limit = 0;
   bool started_here = false;
 
-  for (int i = 0; i < count; ++i) {
+  bool list_more = true;
+  for (int i = 0; LISTS ? list_more : i < count; ++i) {
+    if constexpr (LISTS) list_more = more(cur);
     if (i == 0 || cur.tile == 0) {
       // ---- a new (sequence, head): the query rows as B fragments ----
       started_here = cur.tile == 0;
@@ -786,13 +807,13 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
     }
     // ---- the end of the unit or of the piece: write out ----
     const bool unit_end = cur.tile + 1 == cur.s.tiles;
-    if (unit_end || i + 1 == count) {
+    if (unit_end || (LISTS ? !list_more : i + 1 == count)) {
       const bool whole = started_here && unit_end;
       const int64_t part = 2 * piece + (started_here ? 1 : 0);
       if (!whole && started_here && lane == 0) {
         // the rest of the unit lies in the pieces that follow
         PagedJoin j;
-        j.last = static_cast<int>((begin + i + (cur.s.tiles - 1 - cur.tile)) / line.per);
+        j.last = static_cast<int>(((LISTS ? cur.at : begin + i) + (cur.s.tiles - 1 - cur.tile)) / line.per);
         j.cu0 = cur.s.cu0;
         j.head = cur.head;
         j.rows = cur.s.rows;
@@ -839,7 +860,7 @@ __global__ void __launch_bounds__(PagedShape<DQK, DV, NT>::kThreads, 1)
           }
         }
     }
-    if (i + 1 < count) paged_next<kTile, 0, LISTS>(p, cur);
+    if (LISTS ? list_more : i + 1 < count) paged_next<kTile, kStart, LISTS>(p, cur);
   }
 }
 
