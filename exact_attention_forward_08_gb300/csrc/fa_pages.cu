@@ -278,7 +278,6 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     kv_compact_kernel(const __grid_constant__ PagesParams p) {
   __shared__ long long warp_sum[32];
   const int rank = blockIdx.x, tid = rank * kThreads + threadIdx.x;
-  const int lane = threadIdx.x & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- pages in use: how many, and before each page ----
@@ -316,25 +315,25 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     p.page_map[from] = to;
   }
   if (tid == 0) p.head->copies = moves;
-  cluster_sync();
+}
 
-  // ---- the table follows ----
-  for (int b = warp; b < p.batch; b += kAll / 32) {
-    const int len = p.seqlens[b];
-    const bool fits = length_fits(p, len);
-    const int pages = fits ? static_cast<int>((static_cast<int64_t>(len) + (1 << p.page_shift) - 1) >> p.page_shift) : 0;
-    const int* row = p.table + b * p.table_stride;
-    int* out = p.table_out + b * p.out_stride;
-    if (!fits && lane == 0) paged_error(p.status, kSitePagedSeq, b);
-    for (int j = lane; j < p.max_pages; j += 32) {
-      int page = -1;
-      if (j < pages) {
-        page = row[j];
-        page = page >= 0 && page < p.num_pages ? __ldcg(p.page_map + page) : -1;
-        if (page < 0) paged_error(p.status, kSitePagedPage, b);
-      }
-      out[j] = page;
+// The table follows the pages: a warp rewrites a row.
+__device__ __forceinline__ void compact_row(const PagesParams& p, int b) {
+  const int lane = threadIdx.x & 31;
+  const int len = p.seqlens[b];
+  const bool fits = length_fits(p, len);
+  const int pages = fits ? static_cast<int>((static_cast<int64_t>(len) + (1 << p.page_shift) - 1) >> p.page_shift) : 0;
+  const int* row = p.table + b * p.table_stride;
+  int* out = p.table_out + b * p.out_stride;
+  if (!fits && lane == 0) paged_error(p.status, kSitePagedSeq, b);
+  for (int j = lane; j < p.max_pages; j += 32) {
+    int page = -1;
+    if (j < pages) {
+      page = row[j];
+      page = page >= 0 && page < p.num_pages ? p.page_map[page] : -1;
+      if (page < 0) paged_error(p.status, kSitePagedPage, b);
     }
+    out[j] = page;
   }
 }
 
@@ -345,8 +344,9 @@ struct CopyParams {
   uint8_t* scale[2];
   uint8_t* bounds;
   const PagesHead* head;
-  const int *src, *dst, *tokens;  // tokens NULL: whole pages
-  int heads, page, num_pages, d_qk;
+  const int *src, *dst, *tokens;  // tokens: of each copy, unless all of a page
+  int heads, page;
+  PagesParams table;  // whose rows follow (WHOLE)
 };
 
 constexpr int kCopyWarps = 8;   // of a block
@@ -373,13 +373,24 @@ __device__ __forceinline__ void copy_codes(const uint8_t* src, uint8_t* dst, uin
       at += kCopyAhead * step;
     }
 #pragma unroll 1
-    for (; row < tokens; row += kRows, at += step)
-      *reinterpret_cast<uint4*>(dst + at) = *reinterpret_cast<const uint4*>(src + at);
+    for (; row < tokens; row += kRows * 4) {  // the rest, four at a time
+      uint4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[k] = make_uint4(0, 0, 0, 0);
+        if (row + k * kRows < tokens) v[k] = *reinterpret_cast<const uint4*>(src + (at + k * step));
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (row + k * kRows < tokens) *reinterpret_cast<uint4*>(dst + (at + k * step)) = v[k];
+      at += 4 * step;
+    }
   }
 }
 
-// A warp copies one head's keys or values of a page, with their scale (and the bounds of the keys).
-template <int DQK, int DV>
+// A warp copies one head's keys or values of a page, with their scale (and the bounds of the keys): all of a page
+// (WHOLE, compaction, whose table is rewritten here beside the copies) or its first tokens.
+template <int DQK, int DV, bool WHOLE>
 __global__ void __launch_bounds__(32 * kCopyWarps, kCopyBlocks) kv_copy_kernel(const __grid_constant__ CopyParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
@@ -391,7 +402,7 @@ __global__ void __launch_bounds__(32 * kCopyWarps, kCopyBlocks) kv_copy_kernel(c
     const int64_t copy = (u >> 1) / p.heads;
     const int head = static_cast<int>((u >> 1) - copy * p.heads);
     const int from = src_pages[copy], to = p.dst[copy];
-    const int tokens = p.tokens != nullptr ? p.tokens[copy] : p.page;
+    const int tokens = WHOLE ? p.page : p.tokens[copy];
     const uint8_t* src = p.base[x] + from * p.page_stride[x] + head * p.head_stride[x];
     uint8_t* dst = p.base[x] + to * p.page_stride[x] + head * p.head_stride[x];
     const int64_t from_head = static_cast<int64_t>(from) * p.heads + head, to_head = static_cast<int64_t>(to) * p.heads + head;
@@ -402,6 +413,9 @@ __global__ void __launch_bounds__(32 * kCopyWarps, kCopyBlocks) kv_copy_kernel(c
     if (x == 0) copy_codes<DQK>(src, dst, p.token_stride[0], tokens);
     else copy_codes<DV>(src, dst, p.token_stride[1], tokens);
   }
+  if constexpr (WHOLE)
+    for (int b = blockIdx.x * kCopyWarps + (threadIdx.x >> 5); b < p.table.batch; b += static_cast<int>(step))
+      compact_row(p.table, b);
 }
 
 struct PagesWorkspace {
@@ -456,7 +470,7 @@ int fork_start(const PagesParams& p, size_t smem, cudaStream_t stream) {
 }
 
 template <int DQK, int DV>
-int copy_start(const CopyParams& p, int sms, cudaStream_t stream) {
+int copy_start(const CopyParams& p, bool whole, int sms, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kCopyBlocks * sms, 1, 1);
   cfg.blockDim = dim3(32 * kCopyWarps, 1, 1);
@@ -466,7 +480,9 @@ int copy_start(const CopyParams& p, int sms, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_copy_kernel<DQK, DV>, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, whole ? kv_copy_kernel<DQK, DV, true> : kv_copy_kernel<DQK, DV, false>, p) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
 }
 
 int copy_launch(const PagesParams& m, const fa_kv_cache& c, uint8_t* bounds, bool whole, int sms, cudaStream_t stream) {
@@ -484,14 +500,13 @@ int copy_launch(const PagesParams& m, const fa_kv_cache& c, uint8_t* bounds, boo
   p.head = m.head;
   p.src = m.src;
   p.dst = m.dst;
-  p.tokens = whole ? nullptr : m.tokens;
+  p.tokens = m.tokens;
   p.heads = c.heads_kv;
   p.page = c.page_size;
-  p.num_pages = c.num_pages;
-  p.d_qk = c.d_qk;
-  if (c.d_qk == 64) return copy_start<64, 64>(p, sms, stream);
-  if (c.d_qk == 128) return c.d_v == 64 ? copy_start<128, 64>(p, sms, stream) : copy_start<128, 128>(p, sms, stream);
-  return c.d_v == 64 ? copy_start<192, 64>(p, sms, stream) : copy_start<192, 128>(p, sms, stream);
+  p.table = m;
+  if (c.d_qk == 64) return copy_start<64, 64>(p, whole, sms, stream);
+  if (c.d_qk == 128) return c.d_v == 64 ? copy_start<128, 64>(p, whole, sms, stream) : copy_start<128, 128>(p, whole, sms, stream);
+  return c.d_v == 64 ? copy_start<192, 64>(p, whole, sms, stream) : copy_start<192, 128>(p, whole, sms, stream);
 }
 
 }  // namespace

@@ -431,6 +431,7 @@ struct ChooseShared {
   double q[2 * 192];            // q+ and q- in 64 bits
   int sums[2][kSelectWarps];
   uint32_t least[kSelectWarps], most[kSelectWarps], near_low, near_high;
+  bool tied;
   uint64_t least64[kSelectWarps], most64[kSelectWarps];
   int count[kSelectWarps], ties[kSelectWarps], top_e[kSelectWarps];
   float q_size[kSelectWarps];
@@ -501,7 +502,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
   // ---- T, the k-th largest key: a histogram of the keys from low to high, again of the bin that holds it if that
   // holds many ----
   uint32_t near_low = 0xffffffffu, near_high = 0xffffffffu;
-  bool close = false;
+  bool close = false, tied = false;  // tied: the keys near T are equal scores
   if (k > 0) {
     low = __reduce_min_sync(0xffffffffu, low);
     high = __reduce_max_sync(0xffffffffu, high);
@@ -573,8 +574,8 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
     if (tid == 0) {
       float q_all = 0.f;
       for (int w = 0; w < kSelectWarps; ++w) q_all += sh.q_size[w], top_e = max(top_e, sh.top_e[w]);
-      // No score is larger than `size`; computed ones are off by `error` of it at most.  Queries as small as the second
-      // case are not scaled all the way: all pages are near then.
+      // No score is larger than `size`; computed ones are off by `error` of it at most.  Queries below 2^-90 are not
+      // scaled all the way: all pages are near then, but for queries of 0, whose scores are what they are.
       const double size = 448.0 * q_all * scale_double(top_e), margin = 2.0 * size * p.error;
       const double middle = key_score(low), above = middle + margin, under = middle - margin;
       uint32_t last_near = 0xffffffffu, first_near = 0;
@@ -585,10 +586,12 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
         first_near = static_cast<uint32_t>(u >> 32);  // the smallest that is not below
         if (key_order64(first_near) < u) ++first_near;
       }
-      sh.near_low = first_near, sh.near_high = last_near;
+      sh.tied = q_all == 0.f;
+      sh.near_low = sh.tied ? low : first_near, sh.near_high = sh.tied ? low : last_near;
     }
     __syncthreads();
     near_low = sh.near_low, near_high = sh.near_high;
+    tied = sh.tied;
     int n = 0;
     for (int j = p.first + tid; j < end; j += kSelectThreads) n += key(j) >= near_low;
     close = block_sum(n, sh.sums, turn) != k;
@@ -597,7 +600,11 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
   // ---- pages too near to tell get scores in 64 bits ----
   uint64_t cut64 = 0;
   int ties = 0;  // of the pages at cut64, so many are in
-  if (close) {
+  if (close && tied) {
+    int n = 0;
+    for (int j = p.first + tid; j < end; j += kSelectThreads) n += key(j) > near_high;
+    ties = k - block_sum(n, sh.sums, turn);
+  } else if (close) {
     const __nv_bfloat16* q = p.q + unit * p.ratio * D;
     if (tid == 0) sh.bin = 0;  // now the number of pages near
     for (int i = tid; i < D; i += kSelectThreads) {
@@ -706,18 +713,19 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
     if (!close) return v >= near_low ? 2 : 0;
     if (v > near_high) return 2;
     if (v < near_low) return 0;
+    if (tied) return 1;
     const uint64_t o = exact[j];
     return o > cut64 ? 2 : o == cut64 ? (ties == INT_MAX ? 2 : 1) : 0;
   };
   const int per = ((pages + kSelectThreads - 1) / kSelectThreads) * 32;  // pages of a warp
   const int j_begin = warp * per, j_end = j_begin + per < pages ? j_begin + per : pages;
-  int sure = 0, tied = 0;
+  int sure = 0, ties_here = 0;
   for (int j0 = j_begin; j0 < j_end; j0 += 32) {
     const int v = j0 + lane < j_end ? state(j0 + lane) : 0;
     sure += __popc(__ballot_sync(0xffffffffu, v == 2));
-    tied += __popc(__ballot_sync(0xffffffffu, v == 1));
+    ties_here += __popc(__ballot_sync(0xffffffffu, v == 1));
   }
-  if (lane == 0) sh.count[warp] = sure, sh.ties[warp] = tied;
+  if (lane == 0) sh.count[warp] = sure, sh.ties[warp] = ties_here;
   __syncthreads();
   int at = 0, ties_before = 0;
   for (int w = 0; w < warp; ++w) {

@@ -242,6 +242,8 @@ def test_what_is_no_number_is_taken_first(fa):
     q = normal(1, 4, 64)
     got, _ = check(fa, q, bounds, scale, table, [4800], [1], 16, 12)
     assert table[0, 77] in got[0, 0].tolist() and {int(table[0, 40]), int(table[0, 200])} <= set(got[0, 1].tolist())
+    check(fa, torch.zeros_like(q), bounds, scale, table, [4800], [1], 16, 12)
+    check(fa, torch.zeros_like(q), bounds, scale, table, [4800], [1], 16, 4, first=1, last=2)
     for value in (math.inf, -math.inf, math.nan):
         q[0, 1, 7] = value
         check(fa, q, bounds, scale, table, [4800], [1], 16, 12)
