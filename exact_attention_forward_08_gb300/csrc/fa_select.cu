@@ -180,7 +180,7 @@ struct SelectParams {
 };
 
 constexpr int kSelectWarps = 8, kSelectThreads = 32 * kSelectWarps;
-constexpr int kScoreBlocks = 4;    // of an SM
+constexpr int kScoreBlocks = 5;    // of an SM
 constexpr int kChunk = 8;          // tokens whose queries a block holds
 constexpr int kWarpPages = 16;     // pages of a warp
 constexpr int kTilePages = kSelectWarps * kWarpPages;
@@ -298,6 +298,9 @@ __global__ void __launch_bounds__(kSelectThreads, kScoreBlocks) kv_score_kernel(
   const int64_t bh = blockIdx.x / p.tiles;
   const int tile = blockIdx.x - static_cast<int>(bh) * p.tiles;
   const int b = static_cast<int>(bh / p.heads), head = static_cast<int>(bh - static_cast<int64_t>(b) * p.heads);
+  const int j0 = tile * kTilePages + warp * kWarpPages;
+  const int* row = p.table + b * p.table_stride;
+  int entry = lane < kWarpPages && j0 + lane < p.max_pages ? row[j0 + lane] : -1;  // before the length is known
   bool bad;
   const SelectSeq s = select_seq(p, b, bad);
   if (bad && tile == 0 && head == 0 && tid == 0) paged_error(p.status, kSitePagedSeq, b);
@@ -307,15 +310,9 @@ __global__ void __launch_bounds__(kSelectThreads, kScoreBlocks) kv_score_kernel(
   if (pages <= p.top || tile * kTilePages >= pages) return;
 
   // ---- the pages ----
-  const int j0 = tile * kTilePages + warp * kWarpPages;
-  const int* row = p.table + b * p.table_stride;
-  int entry = -1;
-  if (lane < kWarpPages && j0 + lane < pages) {
-    entry = row[j0 + lane];
-    if (entry < 0 || entry >= p.num_pages) {
-      paged_error(p.status, kSitePagedPage, b);
-      entry = -1;
-    }
+  if (entry < 0 || entry >= p.num_pages || j0 + lane >= pages) {
+    if (lane < kWarpPages && j0 + lane < pages) paged_error(p.status, kSitePagedPage, b);
+    entry = -1;
   }
   constexpr int kChunks = 2 * D / 16;
   uint8_t* const codes = &sh.codes[warp][0][0];
@@ -425,7 +422,7 @@ constexpr int kFewPages = 64;
 
 struct ChooseShared {
   uint32_t stage[kStagePages];  // keys
-  int bins[kBins], bin, rank, in_bin, listed;
+  int bins[kBins], bin, rank, in_bin, listed, near;
   int few[kFewPages];           // pages near the cut, and their scores in 64 bits
   uint64_t few_score[kFewPages];
   double q[2 * 192];            // q+ and q- in 64 bits
@@ -471,13 +468,20 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
   const uint32_t* keys = p.keys + unit * p.max_pages;
   uint64_t* exact = p.exact + unit * p.max_pages;
   int turn = 0;
-  // the sum of the sizes of q+ and q-
+  // q+ and q- in 64 bits, for pages whose scores are near, and the sum of their sizes: while scores are computed
   float q_size = 0.f;
   {
-    const __nv_bfloat162* q = reinterpret_cast<const __nv_bfloat162*>(p.q + unit * p.ratio * D);
-    for (int i = tid; i < p.ratio * D / 2; i += kSelectThreads) {
-      const float2 v = __bfloat1622float2(q[i]);
-      q_size += fabsf(v.x) + fabsf(v.y);
+    const __nv_bfloat16* q = p.q + unit * p.ratio * D;
+    for (int i = tid; i < D; i += kSelectThreads) {
+      double pos = 0.0, neg = 0.0;
+#pragma unroll 4
+      for (int h = 0; h < p.ratio; ++h) {
+        const float v = __bfloat162float(q[h * D + i]);  // a NaN goes into both
+        if (!(v < 0.f)) pos += static_cast<double>(v);
+        if (!(v > 0.f)) neg += static_cast<double>(v);
+        q_size += fabsf(v);
+      }
+      sh.q[i] = pos, sh.q[D + i] = neg;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) q_size += __shfl_xor_sync(0xffffffffu, q_size, o);
@@ -503,6 +507,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
   // holds many ----
   uint32_t near_low = 0xffffffffu, near_high = 0xffffffffu;
   bool close = false, tied = false;  // tied: the keys near T are equal scores
+  int above_near = 0;                // pages
   if (k > 0) {
     low = __reduce_min_sync(0xffffffffu, low);
     high = __reduce_max_sync(0xffffffffu, high);
@@ -587,47 +592,31 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
         if (key_order64(first_near) < u) ++first_near;
       }
       sh.tied = q_all == 0.f;
+      sh.near = 0;
       sh.near_low = sh.tied ? low : first_near, sh.near_high = sh.tied ? low : last_near;
     }
     __syncthreads();
     near_low = sh.near_low, near_high = sh.near_high;
     tied = sh.tied;
-    int n = 0;
-    for (int j = p.first + tid; j < end; j += kSelectThreads) n += key(j) >= near_low;
-    close = block_sum(n, sh.sums, turn) != k;
+    for (int j = p.first + tid; j < end; j += kSelectThreads) {
+      const uint32_t v = key(j);
+      above_near += v > near_high;
+      if (v >= near_low && v <= near_high) {
+        const int place = atomicAdd(&sh.near, 1);
+        if (place < kFewPages) sh.few[place] = j;
+      }
+    }
+    above_near = block_sum(above_near, sh.sums, turn);
+    close = above_near + sh.near != k;
   }
+  const int need = k - above_near;  // of the pages near, 1 at least
 
   // ---- pages too near to tell get scores in 64 bits ----
   uint64_t cut64 = 0;
   int ties = 0;  // of the pages at cut64, so many are in
   if (close && tied) {
-    int n = 0;
-    for (int j = p.first + tid; j < end; j += kSelectThreads) n += key(j) > near_high;
-    ties = k - block_sum(n, sh.sums, turn);
+    ties = need;
   } else if (close) {
-    const __nv_bfloat16* q = p.q + unit * p.ratio * D;
-    if (tid == 0) sh.bin = 0;  // now the number of pages near
-    for (int i = tid; i < D; i += kSelectThreads) {
-      double pos = 0.0, neg = 0.0;
-#pragma unroll 4
-      for (int h = 0; h < p.ratio; ++h) {
-        const float v = __bfloat162float(q[h * D + i]);  // a NaN goes into both
-        pos += v < 0.f ? 0.0 : static_cast<double>(v), neg += v > 0.f ? 0.0 : static_cast<double>(v);
-      }
-      sh.q[i] = pos, sh.q[D + i] = neg;
-    }
-    __syncthreads();
-    int in = 0;
-    for (int j = p.first + tid; j < end; j += kSelectThreads) {
-      const uint32_t v = key(j);
-      in += v > near_high;
-      if (v >= near_low && v <= near_high) {
-        const int place = atomicAdd(&sh.bin, 1);
-        if (place < kFewPages) sh.few[place] = j;
-      }
-    }
-    in = block_sum(in, sh.sums, turn);
-    const int need = k - in;  // 1 at least, and no more than are near
     auto score = [&](int j) {  // by a warp
       const int page = listed(j);
       if (page < 0) return order64(-__longlong_as_double(0x7ff0000000000000ll));
@@ -645,7 +634,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       return order64(sum * scale_double(e));
     };
-    const int few = sh.bin;
+    const int few = sh.near;
     if (few <= kFewPages && staged) {
       // ---- few: each is compared with the others, and its key becomes the largest or the least ----
       for (int i = warp; i < few; i += kSelectWarps) {
