@@ -58,26 +58,38 @@ __global__ void __launch_bounds__(kTableThreads) rotary_table_kernel(const __gri
   for (; pos < p.positions; pos += step) {
     float c[4], s[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint64_t t = turns[k];
-      turns[k] += more[k];
-      const uint32_t quarter = static_cast<uint32_t>((t + (1ull << 61)) >> 62);
-      const uint64_t rest = t - (static_cast<uint64_t>(quarter) << 62);  // signed, of 2^64 a turn
-      const float x = fmaf(static_cast<float>(static_cast<int>(rest >> 32)), 0x1p-32f * 6.28318530717958647692f,
-                           static_cast<float>(static_cast<uint32_t>(rest)) * (0x1p-64f * 6.28318530717958647692f));
-      const float x2 = x * x;
-      float sx = fmaf(x2, 1.f / 362880.f, -1.f / 5040.f);
-      sx = fmaf(sx, x2, 1.f / 120.f);
-      sx = fmaf(sx, x2, -1.f / 6.f);
-      sx = fmaf(sx * x2, x, x);
-      float cx = fmaf(x2, -1.f / 3628800.f, 1.f / 40320.f);
-      cx = fmaf(cx, x2, -1.f / 720.f);
-      cx = fmaf(cx, x2, 1.f / 24.f);
-      cx = fmaf(cx, x2, -0.5f);
-      cx = fmaf(cx, x2, 1.f);
-      const float a = quarter & 1 ? sx : cx, b = quarter & 1 ? cx : sx;
-      c[k] = p.magnitude * ((quarter + 1) & 2 ? -a : a);
-      s[k] = p.magnitude * (quarter & 2 ? -b : b);
+    for (int k = 0; k < 4; k += 2) {  // two pairs at a time, in packed arithmetic
+      float x[2];
+      uint32_t shifted[2];  // the angle plus an eighth of a turn: the quarter in its upper two bits
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        shifted[i] = static_cast<uint32_t>(turns[k + i] >> 32) + 0x20000000u;
+        const int rest = static_cast<int>((shifted[i] & 0x3fffffffu) - 0x20000000u);  // of 2^32 a turn
+        x[i] = fmaf(static_cast<float>(rest), 0x1p-32f * 6.28318530717958647692f,
+                    static_cast<float>(static_cast<uint32_t>(turns[k + i])) * (0x1p-64f * 6.28318530717958647692f));
+        turns[k + i] += more[k + i];
+      }
+      auto both = [](float v) { return f2_pack(v, v); };
+      const uint64_t xx = f2_pack(x[0], x[1]), x2 = f2_mul(xx, xx);
+      uint64_t sine = f2_fma(x2, both(1.f / 362880.f), both(-1.f / 5040.f));
+      sine = f2_fma(sine, x2, both(1.f / 120.f));
+      sine = f2_fma(sine, x2, both(-1.f / 6.f));
+      sine = f2_fma(f2_mul(sine, x2), xx, xx);
+      uint64_t cosine = f2_fma(x2, both(-1.f / 3628800.f), both(1.f / 40320.f));
+      cosine = f2_fma(cosine, x2, both(-1.f / 720.f));
+      cosine = f2_fma(cosine, x2, both(1.f / 24.f));
+      cosine = f2_fma(cosine, x2, both(-0.5f));
+      cosine = f2_fma(cosine, x2, both(1.f));
+      float sx[2], cx[2];
+      f2_unpack(f2_mul(sine, both(p.magnitude)), sx[0], sx[1]);
+      f2_unpack(f2_mul(cosine, both(p.magnitude)), cx[0], cx[1]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool odd = (shifted[i] & 0x40000000u) != 0;
+        const uint32_t a = __float_as_uint(odd ? sx[i] : cx[i]), b = __float_as_uint(odd ? cx[i] : sx[i]);
+        c[k + i] = __uint_as_float(a ^ ((shifted[i] + 0x40000000u) & 0x80000000u));
+        s[k + i] = __uint_as_float(b ^ (shifted[i] & 0x80000000u));
+      }
     }
     float* row = p.out + pos * p.rot + 4 * g;
     *reinterpret_cast<float4*>(row) = make_float4(c[0], c[1], c[2], c[3]);
