@@ -1088,10 +1088,27 @@ def _workspace_bytes(name, *sizes):
     return getattr(load_library(), name)(*sizes) or 16
 
 
-def _given_workspace(workspace):
-    if not workspace.is_contiguous():
-        _bad("workspace must be contiguous")
-    return workspace.numel() * workspace.element_size()
+class _Workspace:
+    """A call's workspace: the caller's tensor, or memory of the caching allocator on the call's stream that goes back to it
+    when the call has been issued (later allocations there come after it).  A tensor of its own would cost 6 us a call."""
+    __slots__ = ("ptr", "size", "_free")
+
+    def __init__(self, torch, workspace, stream, name, *sizes):
+        if workspace is None:
+            self.size = _workspace_bytes(name, *sizes)
+            self.ptr = torch._C._cuda_cudaCachingAllocator_raw_alloc(self.size, stream)
+            self._free = torch._C._cuda_cudaCachingAllocator_raw_delete
+        else:
+            if not workspace.is_contiguous():
+                _bad("workspace must be contiguous")
+            self.size, self.ptr, self._free = workspace.numel() * workspace.element_size(), workspace.data_ptr(), None
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *_):
+        if self._free is not None:
+            self._free(self.ptr)
 
 
 def kv_bounds(k_cache, k_bounds, block_table, seqlens_k, cu_seqlens, total: int, stream=None):
@@ -1162,16 +1179,11 @@ def kv_select(q, k_bounds, k_scale, block_table, seqlens_k, cu_seqlens_q, max_se
         list_lens = _empty((total_q,), torch.int32, index, ptr, current)
     else:
         _int32(torch, "list_lens", list_lens, (total_q,))
-    if workspace is None:
-        size = _workspace_bytes("fa_kv_select_workspace_size", batch, total_q, heads, width)
-        workspace = (torch.empty((size,), dtype=torch.uint8, device=index) if ptr == current
-                     else _empty((size,), torch.uint8, index, ptr, current))
-    else:
-        size = _given_workspace(workspace)
-    rc = load_library().fa_kv_select(q.data_ptr(), bounds, k_scale.data_ptr(), block_table.data_ptr(), ts,
-                                     seqlens_k.data_ptr(), cu_seqlens_q.data_ptr(), batch, total_q, max_seqlen_q, heads_q,
-                                     heads, d, pages, page_size, width, 1 if causal else 0, top, keep_first, keep_last,
-                                     lists.data_ptr(), list_lens.data_ptr(), workspace.data_ptr(), size, ptr)
+    with _Workspace(torch, workspace, ptr, "fa_kv_select_workspace_size", batch, total_q, heads, width) as ws:
+        rc = load_library().fa_kv_select(q.data_ptr(), bounds, k_scale.data_ptr(), block_table.data_ptr(), ts,
+                                         seqlens_k.data_ptr(), cu_seqlens_q.data_ptr(), batch, total_q, max_seqlen_q,
+                                         heads_q, heads, d, pages, page_size, width, 1 if causal else 0, top, keep_first,
+                                         keep_last, lists.data_ptr(), list_lens.data_ptr(), ws.ptr, ws.size, ptr)
     if rc != FA_OK:
         raise FaError(rc, "fa_kv_select")
     return lists, list_lens
@@ -1248,15 +1260,10 @@ def attention_forward_lists(q, k_cache, v_cache, k_scale, v_scale, lists, list_l
             lse = _empty((heads_q, total_q), torch.float32, index, ptr, current)
     elif lse.dtype is not torch.float32 or lse.shape != (heads_q, total_q) or not lse.is_contiguous():
         _bad("lse must be a contiguous fp32 tensor [heads_q, total_q]")
-    if workspace is None:
-        size = _workspace_bytes("fa_fwd_lists_workspace_size", heads_q, heads, d_v)
-        workspace = (torch.empty((size,), dtype=torch.uint8, device=index) if ptr == current
-                     else _empty((size,), torch.uint8, index, ptr, current))
-    else:
-        size = _given_workspace(workspace)
-    rc = load_library().fa_fwd_lists(q.data_ptr(), cache, lists.data_ptr(), list_lens.data_ptr(), width, out.data_ptr(),
-                                     lse.data_ptr() if lse is not None else None, total_q, heads_q,
-                                     0.0 if scale is None else scale, workspace.data_ptr(), size, ptr)
+    with _Workspace(torch, workspace, ptr, "fa_fwd_lists_workspace_size", heads_q, heads, d_v) as ws:
+        rc = load_library().fa_fwd_lists(q.data_ptr(), cache, lists.data_ptr(), list_lens.data_ptr(), width, out.data_ptr(),
+                                         lse.data_ptr() if lse is not None else None, total_q, heads_q,
+                                         0.0 if scale is None else scale, ws.ptr, ws.size, ptr)
     if rc != FA_OK:
         raise FaError(rc, "fa_fwd_lists")
     return (out, lse) if return_lse else out
@@ -1340,15 +1347,10 @@ def kv_fork(parents, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k,
     table_out, out_stride = _table_out(torch, table_out, rows, width, index, ptr, current)
     seqlens_out = _int32_out(torch, "seqlens_out", seqlens_out, rows, index, ptr, current)
     refs_out = _int32_out(torch, "refs_out", refs_out, pages, index, ptr, current)
-    if workspace is None:
-        size = _workspace_bytes("fa_kv_pages_workspace_size", batch, rows, pages)
-        workspace = (torch.empty((size,), dtype=torch.uint8, device=index) if ptr == current
-                     else _empty((size,), torch.uint8, index, ptr, current))
-    else:
-        size = _given_workspace(workspace)
-    rc = load_library().fa_kv_fork(cache, bounds, page_refs.data_ptr(), batch, parents.data_ptr(), grow, rows,
-                                   table_out.data_ptr(), out_stride, seqlens_out.data_ptr(), refs_out.data_ptr(),
-                                   workspace.data_ptr(), size, ptr)
+    with _Workspace(torch, workspace, ptr, "fa_kv_pages_workspace_size", batch, rows, pages) as ws:
+        rc = load_library().fa_kv_fork(cache, bounds, page_refs.data_ptr(), batch, parents.data_ptr(), grow, rows,
+                                       table_out.data_ptr(), out_stride, seqlens_out.data_ptr(), refs_out.data_ptr(),
+                                       ws.ptr, ws.size, ptr)
     if rc != FA_OK:
         raise FaError(rc, "fa_kv_fork")
     return table_out, seqlens_out, refs_out
@@ -1381,14 +1383,9 @@ def kv_compact(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, page_
     refs_out = _int32_out(torch, "refs_out", refs_out, pages, index, ptr, current)
     page_map = _int32_out(torch, "page_map", page_map, pages, index, ptr, current)
     used = _int32_out(torch, "used", used, 1, index, ptr, current)
-    if workspace is None:
-        size = _workspace_bytes("fa_kv_pages_workspace_size", batch, 0, pages)
-        workspace = (torch.empty((size,), dtype=torch.uint8, device=index) if ptr == current
-                     else _empty((size,), torch.uint8, index, ptr, current))
-    else:
-        size = _given_workspace(workspace)
-    rc = load_library().fa_kv_compact(cache, bounds, page_refs.data_ptr(), batch, table_out.data_ptr(), out_stride,
-                                      refs_out.data_ptr(), page_map.data_ptr(), used.data_ptr(), workspace.data_ptr(), size, ptr)
+    with _Workspace(torch, workspace, ptr, "fa_kv_pages_workspace_size", batch, 0, pages) as ws:
+        rc = load_library().fa_kv_compact(cache, bounds, page_refs.data_ptr(), batch, table_out.data_ptr(), out_stride,
+                                          refs_out.data_ptr(), page_map.data_ptr(), used.data_ptr(), ws.ptr, ws.size, ptr)
     if rc != FA_OK:
         raise FaError(rc, "fa_kv_compact")
     return table_out, refs_out, page_map, used

@@ -236,3 +236,43 @@ def test_a_pool_of_more_than_four_gigabytes(fa):
     again, again_lse = fa.attention_forward_lists(q.cuda(), *pool, moved, list_lens)
     assert torch.equal(again, o) and torch.equal(again_lse, lse)
     assert fa.fa_device_status()[0] == 0
+
+
+def test_workspaces_go_back(fa):
+    """Calls that allocate their own workspace leave nothing allocated, calls that are refused neither; inside a graph the
+    memory is the graph's."""
+    s = Server(fa)
+    q, cu, lists, list_lens, o, lse = s.step(*STEPS[0], 0)
+    outs = dict(table_out=torch.empty_like(s.table), refs_out=torch.empty_like(s.refs))
+    parents, lens_out, page_map, used = int32(range(6)), torch.empty_like(s.lens), torch.empty_like(s.refs), int32([0])
+
+    def calls(top=4, **kw):
+        fa.kv_select(q, s.bounds, s.ks, s.table, s.lens, cu, 100, s.page, top, keep_first=1, lists=lists, list_lens=list_lens, **kw)
+        fa.attention_forward_lists(q, *s.pool(), lists, list_lens, out=o, lse=lse, **kw)
+        fa.kv_fork(parents, *s.pool(), s.table, s.lens, s.refs, seqlens_out=lens_out, **outs, **kw)
+        fa.kv_compact(*s.pool(), s.table, s.lens, s.refs, page_map=page_map, used=used, **outs, **kw)
+
+    side = torch.cuda.Stream()
+    calls()
+    torch.cuda.synchronize()
+    want_o = o.clone()
+    before = torch.cuda.memory_allocated()
+    for i in range(50):
+        calls(**({"stream": side} if i % 2 else {}))
+        side.synchronize()
+    with pytest.raises(fa.FaError):
+        fa.attention_forward_lists(q, *s.pool(), lists, list_lens, scale=-1.0, out=o, lse=lse)
+    with pytest.raises(fa.FaError):
+        fa.kv_select(q, s.bounds, s.ks, s.table, s.lens, cu, 100, 48, 4, lists=lists, list_lens=list_lens)
+    with pytest.raises(fa.FaError):
+        fa.kv_fork(parents, *s.pool(), s.table, s.lens, s.refs, seqlens_out=s.lens, **outs)
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() <= before
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    keep = torch.empty(1 << 22, dtype=torch.uint8, device="cuda").fill_(255)  # takes what the eager calls gave back
+    o.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want_o) and (keep == 255).all() and fa.fa_device_status()[0] == 0
