@@ -8,11 +8,15 @@
 // quarter turn is split off as an integer, so the sine and cosine are taken of an
 // angle x of at most an eighth of a turn that has all its 24 bits, at any position:
 // by Taylor's series, to x^9 and x^10, whose next terms are below 2^-28 and 2^-33 of
-// the values there.
+// the values there.  Bound by the stores and the arithmetic alike: 131072 positions of
+// 128, 67 MB, 10.9 us (10.0 at the copy rate; 14.7 before two pairs went through packed
+// arithmetic together, 19 with sincospif).
 //
 // Rotation.  A pair (a, b) becomes (a cos - b sin, b cos + a sin) in fp32, each
 // product and sum rounded by itself, then rounded to bf16; the gradient turns
-// back (sin with its sign changed), which is the transposed map, scaled alike.
+// back (sin with its sign changed), which is the transposed map, scaled alike.  Bound
+// by DRAM: 20128 tokens of 16/16 heads of 192, 503 MB, 85 us, 5.9 TB/s (75 at the copy
+// rate); one token of 32/8 heads of 128: 3.0 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -211,7 +215,9 @@ __global__ void __launch_bounds__(32 * RotaryShape<D>::kWarps) rotary_kernel(con
   }
 }
 
-// Warps an SM that a call's tokens are spread over before a warp takes all heads of one.
+// Warps an SM that a call's tokens are spread over before a warp takes all heads of one.  us with 8 / 32 / 128, 32/8
+// heads of 128: 1000 tokens 5.95 / 4.81 / 4.76, 3000 tokens 9.43 / 9.45 / 10.22, 8000 tokens 30.5 / 30.5 / 32.0; up to
+// 256 tokens the same.
 constexpr int kRotaryWarps = 32;
 
 template <int D>

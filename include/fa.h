@@ -635,7 +635,8 @@ int fa_kv_bounds(const fa_kv_cache* cache, void* k_bounds, const int* cu_seqlens
  * list as -1 if it is taken all the same.
  *
  * heads_q * d_qk per token contiguous; table_stride in entries; sizes as in
- * fa_kv_cache.  total_q * heads_kv < 2^31, top <= 2^24.
+ * fa_kv_cache.  total_q * heads_kv and batch * heads_kv * max_pages / 128 < 2^31,
+ * top <= 2^24.
  * workspace: fa_kv_select_workspace_size bytes, 16-byte aligned, no
  * initialisation; calls that may overlap need different ones.  It grows with
  * total_q * heads_kv * max_pages (12 bytes each): pass no wider rows of the table
