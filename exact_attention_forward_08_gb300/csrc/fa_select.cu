@@ -20,7 +20,7 @@
 // choice for each token and key head.  The work is a few MB and a few dozen steps
 // that each wait for the one before, so latency bounds all three.  GPU time of all
 // three, 32/8 heads of 128, pages of 64: one token after 131000, 16.2 us; 24
-// sequences of 100 to 131000 tokens with 3 drafted ones each, 31.5 us (50 MB of
+// sequences of 100 to 131000 tokens with 3 drafted ones each, 31.5 us (45 MB of
 // bounds, 7 us at the copy rate).  The second with scores in FMAs: 64.6 us; with
 // comparisons of scores in fp64, whose unit is slow here: 93; with score and choice
 // in one kernel of clusters, which the longest sequence then holds up: 106.
