@@ -595,9 +595,13 @@ int fa_kv_compact(const fa_kv_cache* cache, void* k_bounds, const int* page_refs
                   size_t workspace_bytes, fa_stream_t stream_) {
   int rc = check_cache(cache);
   if (rc != FA_OK) return rc;
-  const fa_kv_cache& c = *cache;
+  fa_kv_cache c = *cache;
   if (batch < 0 || batch > kMaxBatch || table_out_stride < c.max_pages) return FA_ERR_INVALID_ARG;
-  rc = check_cache_pointers(cache);
+  if (batch == 0) {  // pages that only their counts know: no table is looked at
+    c.block_table = c.seqlens_k = page_refs;
+    table_out = refs_out;
+  }
+  rc = check_cache_pointers(&c);
   if (rc != FA_OK) return rc;
   if (page_refs == nullptr || table_out == nullptr || refs_out == nullptr || page_map == nullptr || used == nullptr ||
       workspace == nullptr || page_map == refs_out || page_map == page_refs)
@@ -610,7 +614,7 @@ int fa_kv_compact(const fa_kv_cache* cache, void* k_bounds, const int* page_refs
   HostDevice host;
   rc = host_device(&host);
   if (rc != FA_OK) return rc;
-  if (!cache_on_device(cache, host.dev) || !host_is_device_ptr(page_refs, host.dev) ||
+  if (!cache_on_device(&c, host.dev) || !host_is_device_ptr(page_refs, host.dev) ||
       (k_bounds != nullptr && !host_is_device_ptr(k_bounds, host.dev)) || !host_is_device_ptr(table_out, host.dev) ||
       !host_is_device_ptr(refs_out, host.dev) || !host_is_device_ptr(page_map, host.dev) ||
       !host_is_device_ptr(used, host.dev) || !host_is_device_ptr(workspace, host.dev))

@@ -90,8 +90,10 @@ __global__ void __launch_bounds__(32 * kBoundsWarps) kv_bounds_kernel(const __gr
   const int lane = threadIdx.x & 31;
   const int64_t most = static_cast<int64_t>(p.max_pages) << p.page_shift;
   int start, n;
-  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < p.batch; i += gridDim.x * blockDim.x)
-    if (!paged_append_range(p.cu[i], p.cu[i + 1], p.seqlens[i], p.total, most, start, n)) paged_error(p.status, kSitePagedSeq, i);
+  const int64_t threads = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < p.batch; i += threads)
+    if (!paged_append_range(p.cu[i], p.cu[i + 1], p.seqlens[i], p.total, most, start, n))
+      paged_error(p.status, kSitePagedSeq, static_cast<int>(i));
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * kBoundsWarps + (threadIdx.x >> 5);
   const int64_t slot = unit / p.heads;
   const int head = static_cast<int>(unit - slot * p.heads);
@@ -190,7 +192,6 @@ constexpr int kScoreBlocks = 5;    // of an SM
 constexpr int kChunk = 8;          // tokens whose queries a block holds
 constexpr int kWarpPages = 16;     // pages of a warp
 constexpr int kTilePages = kSelectWarps * kWarpPages;
-constexpr int kStagePages = 4096;  // keys of a token that are kept in shared memory
 
 struct SelectSeq {
   int c0, n, len;
@@ -247,13 +248,14 @@ __device__ __forceinline__ void copy_wait() {
 }
 
 // Sum over the block; two buffers by turns, one barrier a call.
-__device__ __forceinline__ int block_sum(int v, int (*buffer)[kSelectWarps], int& turn) {
+template <int WARPS>
+__device__ __forceinline__ int block_sum(int v, int (*buffer)[WARPS], int& turn) {
   v = __reduce_add_sync(0xffffffffu, v);
   if ((threadIdx.x & 31) == 0) buffer[turn][threadIdx.x >> 5] = v;
   __syncthreads();
   int sum = 0;
 #pragma unroll
-  for (int w = 0; w < kSelectWarps; ++w) sum += buffer[turn][w];
+  for (int w = 0; w < WARPS; ++w) sum += buffer[turn][w];
   turn ^= 1;
   return sum;
 }
@@ -310,7 +312,7 @@ __global__ void __launch_bounds__(kSelectThreads, kScoreBlocks) kv_score_kernel(
   bool bad;
   const SelectSeq s = select_seq(p, b, bad);
   if (bad && tile == 0 && head == 0 && tid == 0) paged_error(p.status, kSitePagedSeq, b);
-  if (bad || s.n == 0) return;
+  if (bad || static_cast<int64_t>(blockIdx.y) * kChunk >= s.n) return;
   const int round = (1 << p.page_shift) - 1;
   const int pages = (select_seen(p, s, s.n - 1) + round) >> p.page_shift;  // that the last token sees
   if (pages <= p.top || tile * kTilePages >= pages) return;
@@ -338,10 +340,11 @@ __global__ void __launch_bounds__(kSelectThreads, kScoreBlocks) kv_score_kernel(
   const int e_g[2] = {__shfl_sync(0xffffffffu, e, g), __shfl_sync(0xffffffffu, e, g + 8)};
   const int entry_g[2] = {__shfl_sync(0xffffffffu, entry, g), __shfl_sync(0xffffffffu, entry, g + 8)};
 
-  for (int t0 = 0; t0 < s.n; t0 += kChunk) {
-    const int tokens = s.n - t0 < kChunk ? s.n - t0 : kChunk;
-    const int64_t first_token = static_cast<int64_t>(s.c0) + t0;
-    if (t0 > 0) __syncthreads();
+  bool first = true;
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.y) * kChunk; t0 < s.n; t0 += static_cast<int64_t>(gridDim.y) * kChunk) {
+    const int tokens = s.n - t0 < kChunk ? static_cast<int>(s.n - t0) : kChunk;
+    const int64_t first_token = s.c0 + t0;
+    if (!first) __syncthreads();
     if (warp < tokens) {  // ---- q+ and q- ----
       const __nv_bfloat16* q = p.q + ((first_token + warp) * p.heads + head) * p.ratio * D;
       constexpr int kPairs = D / 64;  // pairs of columns of a lane
@@ -379,7 +382,8 @@ __global__ void __launch_bounds__(kSelectThreads, kScoreBlocks) kv_score_kernel(
         }
       if (lane == 0) sh.q_shift[warp] = shift;
     }
-    if (t0 == 0) copy_wait<0>();
+    if (first) copy_wait<0>();
+    first = false;
     __syncthreads();
     if (j0 >= pages) continue;
 #pragma unroll 1
@@ -418,36 +422,46 @@ __global__ void __launch_bounds__(kSelectThreads, kScoreBlocks) kv_score_kernel(
   const int top_e = __reduce_max_sync(0xffffffffu, e == 255 ? 0 : e);
   if (lane == 0) atomicMax(&sh.top_e, top_e);
   __syncthreads();
-  if (tid == 0) p.top_e[bh * p.tiles + tile] = sh.top_e;
+  if (tid == 0) p.top_e[bh * p.tiles + tile] = sh.top_e;  // the same from all blocks of the tile
 }
 
 // ---- the choice ----
 
-constexpr int kBinBits = 11, kBins = 1 << kBinBits;
+// Blocks for tables of up to PAGES pages: their keys are kept in shared memory, WARPS warps look at them, histograms
+// have 2^BITS bins.
+template <int PAGES, int WARPS, int BITS>
+struct ChooseShape {
+  static constexpr int kPages = PAGES, kWarps = WARPS, kThreads = 32 * WARPS, kBinBits = BITS, kBins = 1 << BITS;
+};
+using ChooseSmall = ChooseShape<1024, 4, 9>;
+using ChooseLarge = ChooseShape<4096, 8, 11>;
+
 // Pages near the cut that are compared with one another; more are searched by halving.  All searched: 39.1 us instead of
 // 31.5 for 24 sequences with drafts.
 constexpr int kFewPages = 64;
 
+template <class S>
 struct ChooseShared {
-  uint32_t stage[kStagePages];  // keys
-  int bins[kBins], bin, rank, in_bin, listed, near;
+  uint32_t stage[S::kPages];  // keys
+  int bins[S::kBins], bin, rank, in_bin, listed, near;
   int few[kFewPages];           // pages near the cut, and their scores in 64 bits
   uint64_t few_score[kFewPages];
   double q[2 * 192];            // q+ and q- in 64 bits
-  int sums[2][kSelectWarps];
-  uint32_t least[kSelectWarps], most[kSelectWarps], near_low, near_high;
+  int sums[2][S::kWarps];
+  uint32_t least[S::kWarps], most[S::kWarps], near_low, near_high;
   bool tied;
-  uint64_t least64[kSelectWarps], most64[kSelectWarps];
-  int count[kSelectWarps], ties[kSelectWarps], top_e[kSelectWarps];
-  float q_size[kSelectWarps];
+  uint64_t least64[S::kWarps], most64[S::kWarps];
+  int count[S::kWarps], ties[S::kWarps], top_e[S::kWarps];
+  float q_size[S::kWarps];
 };
 
 // A block takes one token and key head: keys from the score kernel, T from a histogram of 2048 bins, pages near T, the
 // list.  Ten barriers and as many waits for loads: 9 us for 2048 pages, 15 us where four blocks share an SM.  What does
 // not depend on the scores is done while they are computed.
-template <int D>
-__global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_constant__ SelectParams p) {
-  __shared__ ChooseShared sh;
+template <int D, class S>
+__global__ void __launch_bounds__(S::kThreads) kv_choose_kernel(const __grid_constant__ SelectParams p) {
+  constexpr int kThreads = S::kThreads, kWarps = S::kWarps, kBins = S::kBins, kBinBits = S::kBinBits;
+  __shared__ ChooseShared<S> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t unit = blockIdx.x, t = unit / p.heads;
   const int head = static_cast<int>(unit - t * p.heads);
@@ -465,7 +479,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
   int* out = p.lists + unit * p.top;
   if (mine && head == 0 && tid == 0) p.list_lens[t] = pages > p.top ? seen - ((pages - p.top) << p.page_shift) : seen;
   if (pages <= p.top) {  // all of them; a token of no sequence is left as it is
-    for (int i = tid; mine && i < p.top; i += kSelectThreads) {
+    for (int i = tid; mine && i < p.top; i += kThreads) {
       const int page = i < pages ? listed(i) : -1;
       if (i < pages && page < 0) paged_error(p.status, kSitePagedPage, b);
       out[i] = page;
@@ -482,7 +496,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
   float q_size = 0.f;
   {
     const __nv_bfloat16* q = p.q + unit * p.ratio * D;
-    for (int i = tid; i < D; i += kSelectThreads) {
+    for (int i = tid; i < D; i += kThreads) {
       double pos = 0.0, neg = 0.0;
 #pragma unroll 4
       for (int h = 0; h < p.ratio; ++h) {
@@ -500,13 +514,13 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
   int top_e = 0;
   {
     const int* es = p.top_e + (static_cast<int64_t>(b) * p.heads + head) * p.tiles;
-    for (int i = tid; i * kTilePages < pages; i += kSelectThreads) top_e = max(top_e, __ldcg(es + i));
+    for (int i = tid; i * kTilePages < pages; i += kThreads) top_e = max(top_e, __ldcg(es + i));
     top_e = __reduce_max_sync(0xffffffffu, top_e);
     if (lane == 0) sh.top_e[warp] = top_e, sh.q_size[warp] = q_size;
   }
   uint32_t low = 0xffffffffu, high = 0;
-  const bool staged = pages <= kStagePages;
-  for (int j = p.first + tid; j < end; j += kSelectThreads) {
+  const bool staged = pages <= S::kPages;
+  for (int j = p.first + tid; j < end; j += kThreads) {
     const uint32_t v = __ldcg(keys + j);
     if (staged) sh.stage[j] = v;
     low = min(low, v), high = max(high, v);
@@ -524,19 +538,19 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
     if (lane == 0) sh.least[warp] = low, sh.most[warp] = high;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kSelectWarps; ++w) low = min(low, sh.least[w]), high = max(high, sh.most[w]);
+    for (int w = 0; w < kWarps; ++w) low = min(low, sh.least[w]), high = max(high, sh.most[w]);
     int rank = k;
     while (low < high) {
       const int bits = 32 - __clz(high - low), shift = bits > kBinBits ? bits - kBinBits : 0;
-      for (int i = tid; i < kBins; i += kSelectThreads) sh.bins[i] = 0;
+      for (int i = tid; i < kBins; i += kThreads) sh.bins[i] = 0;
       __syncthreads();
-      for (int j = p.first + tid; j < end; j += kSelectThreads) {
+      for (int j = p.first + tid; j < end; j += kThreads) {
         const uint32_t v = key(j);
         if (v >= low && v <= high) atomicAdd(&sh.bins[(v - low) >> shift], 1);
       }
       __syncthreads();
       // a thread's bins, the last thread's are the lowest; those above come from the scan
-      constexpr int kMine = kBins / kSelectThreads;
+      constexpr int kMine = kBins / kThreads;
       int count[kMine], mine_count = 0;
 #pragma unroll
       for (int i = 0; i < kMine; ++i) mine_count += count[i] = sh.bins[kBins - 1 - (tid * kMine + i)];
@@ -570,7 +584,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
       if (in_bin <= 32 && low < high) {  // few: a warp finds the one that has `rank` - 1 above it
         if (tid == 0) sh.listed = 0;
         __syncthreads();
-        for (int j = p.first + tid; j < end; j += kSelectThreads) {
+        for (int j = p.first + tid; j < end; j += kThreads) {
           const uint32_t v = key(j);
           if (v >= low && v <= high) sh.few[atomicAdd(&sh.listed, 1)] = static_cast<int>(v);
         }
@@ -588,7 +602,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
     }
     if (tid == 0) {
       float q_all = 0.f;
-      for (int w = 0; w < kSelectWarps; ++w) q_all += sh.q_size[w], top_e = max(top_e, sh.top_e[w]);
+      for (int w = 0; w < kWarps; ++w) q_all += sh.q_size[w], top_e = max(top_e, sh.top_e[w]);
       // No score is larger than `size`; computed ones are off by `error` of it at most.  Queries below 2^-90 are not
       // scaled all the way: all pages are near then, but for queries of 0, whose scores are what they are.
       const double size = 448.0 * q_all * scale_double(top_e), margin = 2.0 * size * p.error;
@@ -608,7 +622,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
     __syncthreads();
     near_low = sh.near_low, near_high = sh.near_high;
     tied = sh.tied;
-    for (int j = p.first + tid; j < end; j += kSelectThreads) {
+    for (int j = p.first + tid; j < end; j += kThreads) {
       const uint32_t v = key(j);
       above_near += v > near_high;
       if (v >= near_low && v <= near_high) {
@@ -616,7 +630,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
         if (place < kFewPages) sh.few[place] = j;
       }
     }
-    above_near = block_sum(above_near, sh.sums, turn);
+    above_near = block_sum<kWarps>(above_near, sh.sums, turn);
     close = above_near + sh.near != k;
   }
   const int need = k - above_near;  // of the pages near, 1 at least
@@ -647,7 +661,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
     const int few = sh.near;
     if (few <= kFewPages && staged) {
       // ---- few: each is compared with the others, and its key becomes the largest or the least ----
-      for (int i = warp; i < few; i += kSelectWarps) {
+      for (int i = warp; i < few; i += kWarps) {
         const uint64_t o = score(sh.few[i]);
         if (lane == 0) sh.few_score[i] = o;
       }
@@ -664,7 +678,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
       __syncthreads();
     } else {
       uint64_t low64 = ~0ull, high64 = 0;
-      for (int j0 = p.first + warp * 32; j0 < end; j0 += kSelectThreads) {
+      for (int j0 = p.first + warp * 32; j0 < end; j0 += kThreads) {
         const int j = j0 + lane;
         const uint32_t v = j < end ? key(j) : 0u;
         uint32_t todo = __ballot_sync(0xffffffffu, j < end && v >= near_low && v <= near_high);
@@ -679,17 +693,17 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
       if (lane == 0) sh.least64[warp] = low64, sh.most64[warp] = high64;
       __syncthreads();  // the stores above are there for the block
 #pragma unroll
-      for (int w = 0; w < kSelectWarps; ++w) {
+      for (int w = 0; w < kWarps; ++w) {
         low64 = sh.least64[w] < low64 ? sh.least64[w] : low64;
         high64 = sh.most64[w] > high64 ? sh.most64[w] : high64;
       }
       auto count64 = [&](uint64_t from) {
         int n = 0;
-        for (int j = p.first + tid; j < end; j += kSelectThreads) {
+        for (int j = p.first + tid; j < end; j += kThreads) {
           const uint32_t v = key(j);
           n += v >= near_low && v <= near_high && exact[j] >= from;
         }
-        return block_sum(n, sh.sums, turn);
+        return block_sum<kWarps>(n, sh.sums, turn);
       };
       int n = count64(low64);
       uint64_t lo64 = low64, hi64 = high64;
@@ -716,7 +730,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_choose_kernel(const __grid_
     const uint64_t o = exact[j];
     return o > cut64 ? 2 : o == cut64 ? (ties == INT_MAX ? 2 : 1) : 0;
   };
-  const int per = ((pages + kSelectThreads - 1) / kSelectThreads) * 32;  // pages of a warp
+  const int per = ((pages + kThreads - 1) / kThreads) * 32;  // pages of a warp
   const int j_begin = warp * per, j_end = j_begin + per < pages ? j_begin + per : pages;
   int sure = 0, ties_here = 0;
   for (int j0 = j_begin; j0 < j_end; j0 += 32) {
@@ -765,25 +779,39 @@ double score_error(int ratio, int d) {
   return (ratio * 0x1p-24 + 0x1p-22 + 0x1p-28 + 16 * 0x1p-23 + (d / 32 + 3) * 0x1p-24 + 0x1p-20) * (1.0 + 0x1p-8);
 }
 
-template <int D>
-int select_launch(const SelectParams& p, cudaStream_t stream) {
-  const int64_t blocks = static_cast<int64_t>(p.batch) * p.heads * p.tiles;
-  if (blocks > INT_MAX) return FA_ERR_INVALID_ARG;
-  static bool ready[64] = {};
-  const int rc = allow_smem(reinterpret_cast<const void*>(kv_score_kernel<D>), sizeof(ScoreShared<D>), ready);
-  if (rc != FA_OK) return rc;
-  kv_score_kernel<D><<<static_cast<int>(blocks), kSelectThreads, sizeof(ScoreShared<D>), stream>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+template <int D, class S>
+int choose_launch(const SelectParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned int>(p.total * p.heads), 1, 1);
-  cfg.blockDim = dim3(kSelectThreads, 1, 1);
+  cfg.blockDim = dim3(S::kThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_choose_kernel<D>, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kv_choose_kernel<D, S>, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+template <int D>
+int select_launch(const SelectParams& p, int sms, cudaStream_t stream) {
+  const int64_t blocks = static_cast<int64_t>(p.batch) * p.heads * p.tiles;
+  if (blocks > INT_MAX) return FA_ERR_INVALID_ARG;
+  static bool ready[64] = {};
+  const int rc = allow_smem(reinterpret_cast<const void*>(kv_score_kernel<D>), sizeof(ScoreShared<D>), ready);
+  if (rc != FA_OK) return rc;
+  // tokens over blocks as well, where pages alone make few
+  const int64_t chunks = (static_cast<int64_t>(p.max_n) + kChunk - 1) / kChunk, room = 8 * static_cast<int64_t>(sms) / blocks;
+  const int64_t splits = chunks < room ? chunks : room < 1 ? 1 : room;
+  kv_score_kernel<D><<<dim3(static_cast<unsigned int>(blocks), static_cast<unsigned int>(splits)), kSelectThreads,
+                       sizeof(ScoreShared<D>), stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  // Small blocks where more choices are to be made than large ones fit the GPU at once (7 an SM).  us of the call, small
+  // and large: 2048 tokens of 8 key heads over 160 pages 141 and 216, 512 tokens 61 and 81; 24 x 3 tokens over 1024 pages
+  // 25.3 and 24.3, one token 13.3 and 11.3.
+  const bool many = p.total * p.heads > 7 * static_cast<int64_t>(sms);
+  return many && p.max_pages <= ChooseSmall::kPages ? choose_launch<D, ChooseSmall>(p, stream)
+                                                    : choose_launch<D, ChooseLarge>(p, stream);
 }
 
 bool page_size_ok(int n) { return n == 16 || n == 32 || n == 64 || n == 128; }
@@ -911,9 +939,9 @@ int fa_kv_select(const void* q, const void* k_bounds, const uint8_t* k_scale, co
   p.tiles = (max_pages + kTilePages - 1) / kTilePages;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   p.error = score_error(p.ratio, d_qk);
-  if (d_qk == 64) return select_launch<64>(p, stream);
-  if (d_qk == 128) return select_launch<128>(p, stream);
-  return select_launch<192>(p, stream);
+  if (d_qk == 64) return select_launch<64>(p, host.sms, stream);
+  if (d_qk == 128) return select_launch<128>(p, host.sms, stream);
+  return select_launch<192>(p, host.sms, stream);
 }
 
 }  // extern "C"

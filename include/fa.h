@@ -705,7 +705,8 @@ int fa_fwd_lists(const void* q, const fa_kv_cache* cache, const int* lists, cons
  * A row with a length out of range becomes -1 throughout (site 511), so does an
  * entry outside the cache or of a free page (site 512).
  *
- * batch, rows <= 16384 (1 at least for fa_kv_fork).  workspace: at least
+ * batch, rows <= 16384 (1 at least for fa_kv_fork; fa_kv_compact with batch 0 looks
+ * at no table).  workspace: at least
  * fa_kv_pages_workspace_size(batch, rows, num_pages) bytes (rows 0 for
  * fa_kv_compact), 16-byte aligned, no initialisation; calls that may overlap need
  * different ones, and different caches.  Outputs overlap nothing but what is said

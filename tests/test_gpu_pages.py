@@ -278,6 +278,17 @@ def test_compact_without_rows_or_pages_in_use(fa):
     assert moves == []
 
 
+def test_compact_of_pages_in_no_table(fa):
+    pool = Pool([50, 20], 16, spare=9)
+    held = [p for p in range(pool.num_pages) if pool.refs[p] == 0][1::2]
+    for p in held:
+        pool.refs[p] = 1
+        pool.page_refs[p] = 1
+    pool.table, pool.lens = [], []
+    pool.block_table, pool.seqlens = pool.block_table[:0], pool.seqlens[:0]
+    assert check_compact(fa, pool)
+
+
 def test_compact_in_place(fa):
     pool = Pool([50, 20, 130], 16, spare=15, seed=3)
     table, refs = pool.block_table, pool.page_refs

@@ -170,6 +170,15 @@ def test_selection_of_many_sequences(fa):
     assert torch.equal(again, got)
 
 
+@pytest.mark.parametrize("lens,new,dims,page,top", [([3000], [2500], (2, 1, 64), 16, 9), ([900, 40, 700], [700, 40, 1], (4, 2, 128), 32, 5),
+                                                    ([1500] * 12, [97] * 12, (3, 1, 192), 64, 3)])
+def test_selection_for_prompts(fa, lens, new, dims, page, top):
+    """Hundreds and thousands of new tokens: many blocks for the tokens of a tile, small blocks for the choice."""
+    hq, hkv, d = dims
+    cache = ref.Cache(lens, hkv, page, d, 64, seed=page)
+    check(fa, normal(sum(new), hq, d, seed=hq), want.all_bounds(cache), cache.k_scale, cache.table, lens, new, page, top, first=1, pad=1)
+
+
 def test_equal_scores_take_the_lowest_pages(fa):
     """All pages alike, pages alike in groups, and queries that are 0: only the order decides."""
     for groups in (1, 7, 300):
