@@ -19,8 +19,8 @@
 // Three kernels: bounds of the pages with new tokens, scores of all pages, the
 // choice for each token and key head.  The work is a few MB and a few dozen steps
 // that each wait for the one before, so latency bounds all three.  GPU time of all
-// three, 32/8 heads of 128, pages of 64: one token after 131000, 16.2 us; 24
-// sequences of 100 to 131000 tokens with 3 drafted ones each, 31.5 us (45 MB of
+// three, 32/8 heads of 128, pages of 64: one token after 131000, 15.7 us; 24
+// sequences of 100 to 131000 tokens with 3 drafted ones each, 31.4 us (45 MB of
 // bounds, 7 us at the copy rate).  The second with scores in FMAs: 64.6 us; with
 // comparisons of scores in fp64, whose unit is slow here: 93; with score and choice
 // in one kernel of clusters, which the longest sequence then holds up: 106.
@@ -428,13 +428,15 @@ __global__ void __launch_bounds__(kSelectThreads, kScoreBlocks) kv_score_kernel(
 // ---- the choice ----
 
 // Blocks for tables of up to PAGES pages: their keys are kept in shared memory, WARPS warps look at them, histograms
-// have 2^BITS bins.
-template <int PAGES, int WARPS, int BITS>
+// have 2^BITS bins; the table's entries are kept too (ENTRIES), which saves a wait (16.3 and 15.6 us for one token after
+// 131000), or not, where room for more blocks counts (141 and 151 for 2048 tokens over 160 pages).
+template <int PAGES, int WARPS, int BITS, bool ENTRIES>
 struct ChooseShape {
+  static constexpr bool kEntries = ENTRIES;
   static constexpr int kPages = PAGES, kWarps = WARPS, kThreads = 32 * WARPS, kBinBits = BITS, kBins = 1 << BITS;
 };
-using ChooseSmall = ChooseShape<1024, 4, 9>;
-using ChooseLarge = ChooseShape<4096, 8, 11>;
+using ChooseSmall = ChooseShape<1024, 4, 9, false>;
+using ChooseLarge = ChooseShape<4096, 8, 11, true>;
 
 // Pages near the cut that are compared with one another; more are searched by halving.  All searched: 39.1 us instead of
 // 31.5 for 24 sequences with drafts.
@@ -443,6 +445,7 @@ constexpr int kFewPages = 64;
 template <class S>
 struct ChooseShared {
   uint32_t stage[S::kPages];  // keys
+  int entries[S::kEntries ? S::kPages : 1];  // of the table's row
   int bins[S::kBins], bin, rank, in_bin, listed, near;
   int few[kFewPages];           // pages near the cut, and their scores in 64 bits
   uint64_t few_score[kFewPages];
@@ -472,8 +475,9 @@ __global__ void __launch_bounds__(S::kThreads) kv_choose_kernel(const __grid_con
   const int seen = mine ? select_seen(p, s, static_cast<int>(t - s.c0)) : 0;
   const int pages = (seen + (1 << p.page_shift) - 1) >> p.page_shift;
   const int* row = p.table + (mine ? b : 0) * p.table_stride;
+  const bool staged = pages <= S::kPages;
   auto listed = [&](int j) {
-    const int page = row[j];
+    const int page = S::kEntries && pages > p.top && staged ? sh.entries[j] : row[j];
     return page >= 0 && page < p.num_pages ? page : -1;
   };
   int* out = p.lists + unit * p.top;
@@ -492,7 +496,10 @@ __global__ void __launch_bounds__(S::kThreads) kv_choose_kernel(const __grid_con
   const uint32_t* keys = p.keys + unit * p.max_pages;
   uint64_t* exact = p.exact + unit * p.max_pages;
   int turn = 0;
-  // q+ and q- in 64 bits, for pages whose scores are near, and the sum of their sizes: while scores are computed
+  // while scores are computed: the table's entries; q+ and q- in 64 bits, for pages whose scores are near; the sum of
+  // their sizes
+  if constexpr (S::kEntries)
+    for (int j = tid; staged && j < pages; j += kThreads) sh.entries[j] = row[j];
   float q_size = 0.f;
   {
     const __nv_bfloat16* q = p.q + unit * p.ratio * D;
@@ -519,7 +526,6 @@ __global__ void __launch_bounds__(S::kThreads) kv_choose_kernel(const __grid_con
     if (lane == 0) sh.top_e[warp] = top_e, sh.q_size[warp] = q_size;
   }
   uint32_t low = 0xffffffffu, high = 0;
-  const bool staged = pages <= S::kPages;
   for (int j = p.first + tid; j < end; j += kThreads) {
     const uint32_t v = __ldcg(keys + j);
     if (staged) sh.stage[j] = v;
@@ -806,10 +812,10 @@ int select_launch(const SelectParams& p, int sms, cudaStream_t stream) {
   kv_score_kernel<D><<<dim3(static_cast<unsigned int>(blocks), static_cast<unsigned int>(splits)), kSelectThreads,
                        sizeof(ScoreShared<D>), stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  // Small blocks where more choices are to be made than large ones fit the GPU at once (7 an SM).  us of the call, small
+  // Small blocks where more choices are to be made than large ones fit the GPU at once (5 an SM).  us of the call, small
   // and large: 2048 tokens of 8 key heads over 160 pages 141 and 216, 512 tokens 61 and 81; 24 x 3 tokens over 1024 pages
   // 25.3 and 24.3, one token 13.3 and 11.3.
-  const bool many = p.total * p.heads > 7 * static_cast<int64_t>(sms);
+  const bool many = p.total * p.heads > 5 * static_cast<int64_t>(sms);
   return many && p.max_pages <= ChooseSmall::kPages ? choose_launch<D, ChooseSmall>(p, stream)
                                                     : choose_launch<D, ChooseLarge>(p, stream);
 }
