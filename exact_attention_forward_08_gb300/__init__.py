@@ -1088,27 +1088,16 @@ def _workspace_bytes(name, *sizes):
     return getattr(load_library(), name)(*sizes) or 16
 
 
-class _Workspace:
-    """A call's workspace: the caller's tensor, or memory of the caching allocator on the call's stream that goes back to it
-    when the call has been issued (later allocations there come after it).  A tensor of its own would cost 6 us a call."""
-    __slots__ = ("ptr", "size", "_free")
-
-    def __init__(self, torch, workspace, stream, name, *sizes):
-        if workspace is None:
-            self.size = _workspace_bytes(name, *sizes)
-            self.ptr = torch._C._cuda_cudaCachingAllocator_raw_alloc(self.size, stream)
-            self._free = torch._C._cuda_cudaCachingAllocator_raw_delete
-        else:
-            if not workspace.is_contiguous():
-                _bad("workspace must be contiguous")
-            self.size, self.ptr, self._free = workspace.numel() * workspace.element_size(), workspace.data_ptr(), None
-
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *_):
-        if self._free is not None:
-            self._free(self.ptr)
+def _workspace(torch, workspace, stream, name, *sizes):
+    """(pointer, bytes, whether it is to be freed) of a call's workspace: the caller's tensor, or memory of the caching
+    allocator on the call's stream that goes back to it when the call has been issued (what is allocated there later runs
+    after it).  A tensor of its own would cost 6 us a call."""
+    if workspace is None:
+        size = _workspace_bytes(name, *sizes)
+        return torch._C._cuda_cudaCachingAllocator_raw_alloc(size, stream), size, True
+    if not workspace.is_contiguous():
+        _bad("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), False
 
 
 def kv_bounds(k_cache, k_bounds, block_table, seqlens_k, cu_seqlens, total: int, stream=None):
@@ -1179,11 +1168,15 @@ def kv_select(q, k_bounds, k_scale, block_table, seqlens_k, cu_seqlens_q, max_se
         list_lens = _empty((total_q,), torch.int32, index, ptr, current)
     else:
         _int32(torch, "list_lens", list_lens, (total_q,))
-    with _Workspace(torch, workspace, ptr, "fa_kv_select_workspace_size", batch, total_q, heads, width) as ws:
+    ws, size, own = _workspace(torch, workspace, ptr, "fa_kv_select_workspace_size", batch, total_q, heads, width)
+    try:
         rc = load_library().fa_kv_select(q.data_ptr(), bounds, k_scale.data_ptr(), block_table.data_ptr(), ts,
                                          seqlens_k.data_ptr(), cu_seqlens_q.data_ptr(), batch, total_q, max_seqlen_q,
                                          heads_q, heads, d, pages, page_size, width, 1 if causal else 0, top, keep_first,
-                                         keep_last, lists.data_ptr(), list_lens.data_ptr(), ws.ptr, ws.size, ptr)
+                                         keep_last, lists.data_ptr(), list_lens.data_ptr(), ws, size, ptr)
+    finally:
+        if own:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(ws)
     if rc != FA_OK:
         raise FaError(rc, "fa_kv_select")
     return lists, list_lens
@@ -1260,10 +1253,14 @@ def attention_forward_lists(q, k_cache, v_cache, k_scale, v_scale, lists, list_l
             lse = _empty((heads_q, total_q), torch.float32, index, ptr, current)
     elif lse.dtype is not torch.float32 or lse.shape != (heads_q, total_q) or not lse.is_contiguous():
         _bad("lse must be a contiguous fp32 tensor [heads_q, total_q]")
-    with _Workspace(torch, workspace, ptr, "fa_fwd_lists_workspace_size", heads_q, heads, d_v) as ws:
+    ws, size, own = _workspace(torch, workspace, ptr, "fa_fwd_lists_workspace_size", heads_q, heads, d_v)
+    try:
         rc = load_library().fa_fwd_lists(q.data_ptr(), cache, lists.data_ptr(), list_lens.data_ptr(), width, out.data_ptr(),
                                          lse.data_ptr() if lse is not None else None, total_q, heads_q,
-                                         0.0 if scale is None else scale, ws.ptr, ws.size, ptr)
+                                         0.0 if scale is None else scale, ws, size, ptr)
+    finally:
+        if own:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(ws)
     if rc != FA_OK:
         raise FaError(rc, "fa_fwd_lists")
     return (out, lse) if return_lse else out
@@ -1320,7 +1317,8 @@ def kv_fork(parents, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k,
     Full pages are shared, page_refs (int32 [num_pages]) counts their uses; a last page that is not full stays with the
     first heir, others get a copy.  Returns (table_out int32 [rows,max_pages], seqlens_out int32 [rows], refs_out int32
     [num_pages]), allocated when not given; refs_out may be page_refs.  The cache (and ``k_bounds``, if given) changes in
-    new pages only.  Rows out of range and rows that find no free pages become empty, which ``fa_device_status`` reports."""
+    new pages only.  Rows out of range and rows that find no free pages become empty, which ``fa_device_status`` reports.
+    A pool begins with lengths and counts of 0, whatever the table holds."""
     import torch
 
     index = k_cache.get_device()
@@ -1347,10 +1345,14 @@ def kv_fork(parents, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k,
     table_out, out_stride = _table_out(torch, table_out, rows, width, index, ptr, current)
     seqlens_out = _int32_out(torch, "seqlens_out", seqlens_out, rows, index, ptr, current)
     refs_out = _int32_out(torch, "refs_out", refs_out, pages, index, ptr, current)
-    with _Workspace(torch, workspace, ptr, "fa_kv_pages_workspace_size", batch, rows, pages) as ws:
+    ws, size, own = _workspace(torch, workspace, ptr, "fa_kv_pages_workspace_size", batch, rows, pages)
+    try:
         rc = load_library().fa_kv_fork(cache, bounds, page_refs.data_ptr(), batch, parents.data_ptr(), grow, rows,
                                        table_out.data_ptr(), out_stride, seqlens_out.data_ptr(), refs_out.data_ptr(),
-                                       ws.ptr, ws.size, ptr)
+                                       ws, size, ptr)
+    finally:
+        if own:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(ws)
     if rc != FA_OK:
         raise FaError(rc, "fa_kv_fork")
     return table_out, seqlens_out, refs_out
@@ -1383,9 +1385,13 @@ def kv_compact(k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, page_
     refs_out = _int32_out(torch, "refs_out", refs_out, pages, index, ptr, current)
     page_map = _int32_out(torch, "page_map", page_map, pages, index, ptr, current)
     used = _int32_out(torch, "used", used, 1, index, ptr, current)
-    with _Workspace(torch, workspace, ptr, "fa_kv_pages_workspace_size", batch, 0, pages) as ws:
+    ws, size, own = _workspace(torch, workspace, ptr, "fa_kv_pages_workspace_size", batch, 0, pages)
+    try:
         rc = load_library().fa_kv_compact(cache, bounds, page_refs.data_ptr(), batch, table_out.data_ptr(), out_stride,
-                                          refs_out.data_ptr(), page_map.data_ptr(), used.data_ptr(), ws.ptr, ws.size, ptr)
+                                          refs_out.data_ptr(), page_map.data_ptr(), used.data_ptr(), ws, size, ptr)
+    finally:
+        if own:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(ws)
     if rc != FA_OK:
         raise FaError(rc, "fa_kv_compact")
     return table_out, refs_out, page_map, used

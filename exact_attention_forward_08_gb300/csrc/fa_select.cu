@@ -188,7 +188,7 @@ struct SelectParams {
 };
 
 constexpr int kSelectWarps = 8, kSelectThreads = 32 * kSelectWarps;
-constexpr int kScoreBlocks = 5;    // of an SM
+constexpr int kScoreBlocks = 5;    // of an SM (4: the same time)
 constexpr int kChunk = 8;          // tokens whose queries a block holds
 constexpr int kWarpPages = 16;     // pages of a warp
 constexpr int kTilePages = kSelectWarps * kWarpPages;
