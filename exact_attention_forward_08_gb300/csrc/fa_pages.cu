@@ -21,6 +21,7 @@
 
 #include <climits>
 #include <cstring>
+#include <initializer_list>
 
 #include "fa.h"
 #include "fa_host.h"
@@ -256,6 +257,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     const ForkRow w = row_of(lo);
     const bool copy = copies(w, lo);
     const int kept = kept_pages(w, lo), j = kept + place - start[lo];
+    if (j >= p.max_pages) continue;  // only where inputs change while they are read
     p.table_out[lo * p.out_stride + j] = page;
     p.refs_out[page] = 1;
     if (copy && j == kept) {
@@ -557,7 +559,11 @@ int fa_kv_fork(const fa_kv_cache* cache, void* k_bounds, const int* page_refs, i
       refs_out == nullptr || workspace == nullptr)
     return FA_ERR_INVALID_ARG;
   // the old rows are read while the new ones are written
-  if (table_out == c.block_table || seqlens_out == c.seqlens_k) return FA_ERR_INVALID_ARG;
+  for (const int* in : {c.block_table, c.seqlens_k, parents, new_tokens})
+    if (table_out == in || seqlens_out == in || refs_out == in) return FA_ERR_INVALID_ARG;
+  if (table_out == seqlens_out || table_out == refs_out || seqlens_out == refs_out || table_out == page_refs ||
+      seqlens_out == page_refs)
+    return FA_ERR_INVALID_ARG;
   if (!aligned(k_bounds, 16) || !aligned(workspace, 16) || !aligned(page_refs, 4) || !aligned(parents, 4) ||
       !aligned(new_tokens, 4) || !aligned(table_out, 4) || !aligned(seqlens_out, 4) || !aligned(refs_out, 4))
     return FA_ERR_INVALID_ARG;
@@ -604,7 +610,14 @@ int fa_kv_compact(const fa_kv_cache* cache, void* k_bounds, const int* page_refs
   rc = check_cache_pointers(&c);
   if (rc != FA_OK) return rc;
   if (page_refs == nullptr || table_out == nullptr || refs_out == nullptr || page_map == nullptr || used == nullptr ||
-      workspace == nullptr || page_map == refs_out || page_map == page_refs)
+      workspace == nullptr)
+    return FA_ERR_INVALID_ARG;
+  // of the inputs, table_out may be the table and refs_out the counts
+  for (const int* out : {static_cast<const int*>(page_map), static_cast<const int*>(used)})
+    if (out == refs_out || out == page_refs || out == table_out || (batch > 0 && (out == c.block_table || out == c.seqlens_k)))
+      return FA_ERR_INVALID_ARG;
+  if (page_map == used || (batch > 0 && (table_out == refs_out || table_out == page_refs || table_out == c.seqlens_k ||
+                                         refs_out == c.block_table || refs_out == c.seqlens_k)))
     return FA_ERR_INVALID_ARG;
   if (table_out == c.block_table && table_out_stride != c.table_stride && batch > 1) return FA_ERR_INVALID_ARG;
   if (!aligned(k_bounds, 16) || !aligned(workspace, 16) || !aligned(page_refs, 4) || !aligned(table_out, 4) ||

@@ -321,6 +321,8 @@ int fa_rotary(const void* q, const void* k, void* q_out, void* k_out, int64_t q_
     if (src[x] == dst[x] && in[x] != out[x] && total > 1) return FA_ERR_INVALID_ARG;  // in place: the same rows
   }
 
+  if (heads_q > 0 && heads_k > 0 && (q_out == k_out || q_out == k || k_out == q)) return FA_ERR_INVALID_ARG;
+
   HostDevice host;
   const int rc = host_device(&host);
   if (rc != FA_OK) return rc;

@@ -17,7 +17,7 @@ def table(fa, **change):
 
 
 def rotary(fa, **change):
-    a = dict(q=FAKE, k=FAKE, q_out=FAKE, k_out=FAKE, q_stride=512, k_stride=256, q_out_stride=512, k_out_stride=256,
+    a = dict(q=FAKE, k=OTHER, q_out=FAKE, k_out=OTHER, q_stride=512, k_stride=256, q_out_stride=512, k_out_stride=256,
              positions=None, cu=None, batch=0, seqlen=4, total=8, heads_q=4, heads_k=2, d=128, cos_sin=FAKE, max_pos=10,
              rot_dim=64, interleaved=0, backward=0)
     a.update(change)
@@ -46,15 +46,15 @@ def lists(fa, c, **change):
 
 
 def fork(fa, c, **change):
-    a = dict(bounds=FAKE, refs=FAKE, batch=2, parents=FAKE, grow=FAKE, rows=3, table_out=OTHER, out_stride=8, seqlens_out=OTHER,
-             refs_out=FAKE, workspace=FAKE, workspace_bytes=1 << 40)
+    a = dict(bounds=FAKE, refs=OTHER + 48, batch=2, parents=FAKE, grow=FAKE, rows=3, table_out=OTHER, out_stride=8,
+             seqlens_out=OTHER + 16, refs_out=OTHER + 48, workspace=FAKE, workspace_bytes=1 << 40)
     a.update(change)
     return fa.fa_kv_fork(c, *a.values(), None)
 
 
 def compact(fa, c, **change):
-    a = dict(bounds=FAKE, refs=FAKE, batch=2, table_out=FAKE, out_stride=8, refs_out=FAKE, page_map=OTHER, used=FAKE,
-             workspace=FAKE, workspace_bytes=1 << 40)
+    a = dict(bounds=FAKE, refs=OTHER + 48, batch=2, table_out=FAKE, out_stride=8, refs_out=OTHER + 48, page_map=OTHER,
+             used=OTHER + 16, workspace=FAKE, workspace_bytes=1 << 40)
     a.update(change)
     return fa.fa_kv_compact(c, *a.values(), None)
 
@@ -81,7 +81,8 @@ def test_rotary_table_of_no_positions(fa):
     (dict(q=None), 1), (dict(q_out=None), 1), (dict(k=None), 1), (dict(k_out=None), 1), (dict(cos_sin=None), 1),
     (dict(cos_sin=FAKE + 4), 1), (dict(positions=FAKE + 2), 1), (dict(cu=FAKE + 2, batch=1), 1), (dict(q=FAKE + 8), 1),
     (dict(k_out=FAKE + 8), 1), (dict(q_stride=516), 1), (dict(q_stride=504, q_out_stride=504), 1), (dict(k_out_stride=1 << 40), 1),
-    (dict(q_out_stride=520), 1), (dict(heads_q=65537, q_stride=1 << 24, q_out_stride=1 << 24), 1)], ids=str)
+    (dict(q_out_stride=520), 1), (dict(heads_q=65537, q_stride=1 << 24, q_out_stride=1 << 24), 1),
+    (dict(k_out=FAKE), 1), (dict(q_out=OTHER), 1), (dict(q_out=OTHER + 64, k_out=OTHER + 64), 1)], ids=str)
 def test_rotary_refusals(fa, change, code):
     assert rotary(fa, **change) == code
 
@@ -155,7 +156,9 @@ def test_lists_of_no_tokens(fa):
     dict(batch=0), dict(batch=16385), dict(rows=0), dict(rows=16385), dict(out_stride=7), dict(refs=None), dict(refs=FAKE + 2),
     dict(parents=None), dict(parents=FAKE + 2), dict(grow=FAKE + 2), dict(table_out=None), dict(table_out=FAKE),
     dict(table_out=OTHER + 2), dict(seqlens_out=None), dict(seqlens_out=FAKE), dict(seqlens_out=OTHER + 2), dict(refs_out=None),
-    dict(refs_out=FAKE + 2), dict(bounds=FAKE + 8), dict(workspace=None), dict(workspace=FAKE + 8), dict(workspace_bytes=100)],
+    dict(refs_out=FAKE + 2), dict(bounds=FAKE + 8), dict(workspace=None), dict(workspace=FAKE + 8), dict(workspace_bytes=100),
+    dict(refs_out=FAKE), dict(seqlens_out=OTHER), dict(refs_out=OTHER), dict(seqlens_out=OTHER + 48), dict(table_out=OTHER + 48),
+    dict(parents=OTHER + 16), dict(grow=OTHER + 16), dict(grow=OTHER), dict(parents=OTHER + 48)],
     ids=str)
 def test_fork_refusals(fa, change):
     assert fork(fa, cache(fa), **change) == 1
@@ -165,9 +168,20 @@ def test_fork_refusals(fa, change):
     dict(batch=-1), dict(batch=16385), dict(out_stride=7), dict(out_stride=9), dict(refs=None), dict(refs=FAKE + 2),
     dict(table_out=None), dict(table_out=FAKE + 2), dict(refs_out=None), dict(refs_out=FAKE + 2), dict(page_map=None),
     dict(page_map=FAKE), dict(page_map=FAKE + 2), dict(used=None), dict(used=FAKE + 2), dict(bounds=FAKE + 8),
-    dict(workspace=None), dict(workspace=FAKE + 8), dict(workspace_bytes=100)], ids=str)
+    dict(workspace=None), dict(workspace=FAKE + 8), dict(workspace_bytes=100), dict(page_map=OTHER + 48), dict(used=OTHER + 48),
+    dict(used=FAKE), dict(used=OTHER), dict(table_out=OTHER + 48), dict(refs_out=FAKE)], ids=str)
 def test_compact_refusals(fa, change):
-    assert compact(fa, cache(fa), **change) == 1
+    assert compact(fa, cache(fa, seqlens_k=OTHER + 64), **change) == 1
+
+
+@pytest.mark.parametrize("call", [table, rotary, lambda fa: bounds(fa, cache(fa)), select, lambda fa: lists(fa, cache(fa)),
+                                  lambda fa: fork(fa, cache(fa)), lambda fa: compact(fa, cache(fa, seqlens_k=OTHER + 64))])
+def test_what_the_refusals_change_is_otherwise_accepted(fa, call):
+    """The arguments that the cases above start from pass all checks before the device's: without one the call ends there."""
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("made-up pointers are refused here")
+    assert call(fa) == 3
 
 
 def test_calls_without_a_cache(fa):
