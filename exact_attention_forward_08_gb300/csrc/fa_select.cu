@@ -781,6 +781,7 @@ SelectWorkspace select_workspace(int batch, int64_t total, int heads, int max_pa
 // Roundings of a score: 2^-24 for each addition to q+ and q-; 2^-22 and less than 2^-28 for their two parts; 2^-23 for
 // each of 16 additions of a product (single precision, rounded in any way), 2^-24 for each of the d / 32 + 3 after it;
 // 2^-20 for what the key drops; 1 / 256 more of it all for the products of these factors and the bound's own rounding.
+// Scores of normal, of positive and of widely spread queries and codes were off by 12 % of it at most, nearly all the key's.
 double score_error(int ratio, int d) {
   return (ratio * 0x1p-24 + 0x1p-22 + 0x1p-28 + 16 * 0x1p-23 + (d / 32 + 3) * 0x1p-24 + 0x1p-20) * (1.0 + 0x1p-8);
 }
