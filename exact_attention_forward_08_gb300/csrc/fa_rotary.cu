@@ -16,7 +16,7 @@
 // product and sum rounded by itself, then rounded to bf16; the gradient turns
 // back (sin with its sign changed), which is the transposed map, scaled alike.  Bound
 // by DRAM: 20128 tokens of 16/16 heads of 192, 503 MB, 85 us, 5.9 TB/s (75 at the copy
-// rate); one token of 32/8 heads of 128: 3.0 us.
+// rate); one token of 32/8 heads of 128: 2.5 to 2.7 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -121,7 +121,9 @@ template <int D>
 struct RotaryShape {
   static constexpr int kItems = D / 16;
   static constexpr int kHeads = 32 / kItems;
-  static constexpr int kAhead = 4;  // groups of heads whose loads are under way together
+  // groups of heads whose loads are under way together; us with 2 / 3 / 4 / 6: one token of 32/8 heads of 128 2.7 / 2.8 /
+  // 3.1 / 3.4, 8000 tokens 28.1 / 31.6 / 30.5 / 34.4; the 20128 of 16/16 heads of 192 86.3 / 89.3 / 84.6 / 101
+  static constexpr int kAhead = D == 192 ? 4 : 2;
   static constexpr int kWarps = 8;
 };
 
@@ -216,8 +218,8 @@ __global__ void __launch_bounds__(32 * RotaryShape<D>::kWarps) rotary_kernel(con
 }
 
 // Warps an SM that a call's tokens are spread over before a warp takes all heads of one.  us with 8 / 32 / 128, 32/8
-// heads of 128: 1000 tokens 5.95 / 4.81 / 4.76, 3000 tokens 9.43 / 9.45 / 10.22, 8000 tokens 30.5 / 30.5 / 32.0; up to
-// 256 tokens the same.
+// heads of 128, four groups ahead: 1000 tokens 5.95 / 4.81 / 4.76, 3000 tokens 9.43 / 9.45 / 10.22, 8000 tokens 30.5 /
+// 30.5 / 32.0; up to 256 tokens the same.
 constexpr int kRotaryWarps = 32;
 
 template <int D>
