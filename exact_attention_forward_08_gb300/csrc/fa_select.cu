@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(S::kThreads) kv_choose_kernel(const __grid_con
     if (lane == 0) sh.top_e[warp] = top_e, sh.q_size[warp] = q_size;
   }
   uint32_t low = 0xffffffffu, high = 0;
-  for (int j = p.first + tid; j < end; j += kThreads) {
+  for (int j = p.first + tid; k > 0 && j < end; j += kThreads) {
     const uint32_t v = __ldcg(keys + j);
     if (staged) sh.stage[j] = v;
     low = min(low, v), high = max(high, v);
@@ -728,6 +728,7 @@ __global__ void __launch_bounds__(S::kThreads) kv_choose_kernel(const __grid_con
   // ---- the chosen pages in order: a warp counts, then writes, a run of pages ----
   auto state = [&](int j) {  // 2: in, 1: a tie, 0: out
     if (j < p.first || j >= end) return 2;
+    if (k == 0) return 0;  // all places are taken: no keys were staged
     const uint32_t v = key(j);
     if (!close) return v >= near_low ? 2 : 0;
     if (v > near_high) return 2;
