@@ -1315,7 +1315,7 @@ def kv_fork(parents, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k,
     Row r of the result takes over row parents[r] (int32 [rows]; -1: it starts empty) and gets room for new_tokens[r]
     (int32 [rows]) more tokens: beams that fork, requests that end (no row names them) or begin, sequences that grow.
     Full pages are shared, page_refs (int32 [num_pages]) counts their uses; a last page that is not full stays with the
-    first heir, others get a copy.  Returns (table_out int32 [rows,max_pages], seqlens_out int32 [rows], refs_out int32
+    first heir if nothing else uses it (another row or a holder that page_refs counts), other heirs get a copy.  Returns (table_out int32 [rows,max_pages], seqlens_out int32 [rows], refs_out int32
     [num_pages]), allocated when not given; refs_out may be page_refs.  The cache (and ``k_bounds``, if given) changes in
     new pages only.  Rows out of range and rows that find no free pages become empty, which ``fa_device_status`` reports.
     A pool begins with lengths and counts of 0, whatever the table holds."""

@@ -56,7 +56,9 @@ struct PagesParams {
   int* used;
   unsigned int* status;
   PagesHead* head;
-  int* valid;               // [batch] 0: a row whose length or pages are out of range
+  int* valid;               // [batch] 0: a row whose length or pages are out of range; 2: its last page is not full and
+                            // has other uses; 1: any other
+  int* owner;               // [num_pages] of such pages, the first of the new rows that would keep it
   int *src, *dst, *tokens;  // copies
   int batch, rows, num_pages, max_pages, page_shift;
 };
@@ -130,26 +132,30 @@ __device__ __forceinline__ bool length_fits(const PagesParams& p, int len) {
 struct ForkRow {
   int src, len, grow;  // parent (-1: none), its tokens; new tokens (0 if not known)
   bool bad;
+  bool shared;         // the parent's last page is not full and has other uses (false if not known)
   __device__ __forceinline__ uint64_t pack() const {  // without the new tokens
     return static_cast<uint64_t>(src + 1) | static_cast<uint64_t>(len) << 16 | static_cast<uint64_t>(bad) << 63;
   }
   static __device__ __forceinline__ ForkRow unpack(uint64_t x) {
-    return {static_cast<int>(x & 0xffff) - 1, static_cast<int>(x >> 16 & 0x7fffffff), 0, (x >> 63) != 0};
+    return {static_cast<int>(x & 0xffff) - 1, static_cast<int>(x >> 16 & 0x7fffffff), 0, (x >> 63) != 0, false};
   }
 };
 __device__ __forceinline__ ForkRow fork_row(const PagesParams& p, int r) {
-  ForkRow w = {p.parents[r], 0, p.grow != nullptr ? p.grow[r] : 0, false};
+  ForkRow w = {p.parents[r], 0, p.grow != nullptr ? p.grow[r] : 0, false, false};
   w.bad = w.src < -1 || w.src >= p.batch || w.grow < 0;
   if (!w.bad && w.src >= 0) {
     const int valid = __ldcg(p.valid + w.src), len = p.seqlens[w.src];
     w.bad = valid == 0;
+    w.shared = valid == 2;
     w.len = w.bad ? 0 : len;
   }
   w.bad = w.bad || static_cast<int64_t>(w.len) + w.grow > static_cast<int64_t>(p.max_pages) << p.page_shift;
-  return w.bad ? ForkRow{-1, 0, 0, true} : w;
+  return w.bad ? ForkRow{-1, 0, 0, true, false} : w;
 }
 
-// Three barriers of the cluster.  What all rows need of one another (heirs, first
+constexpr int kSharedHeir = 1 << 30;  // among a row's heirs: its last page is not full and has other uses
+
+// Three barriers of the cluster, two more where a last page that is not full has uses beside its row.  What all rows need of one another (heirs, first
 // heirs, the pages needed before each row) every block works out for itself in
 // shared memory, which takes less time than an exchange; pages are shared out.  Rows
 // are kept there once they are known (CACHED), as far as they fit: 12.3 us for 64
@@ -159,7 +165,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     kv_fork_kernel(const __grid_constant__ PagesParams p) {
   extern __shared__ int fork_smem[];
   int* const heirs = fork_smem;          // [batch]
-  int* const first = heirs + p.batch;    // [batch] the first heir
+  int* const first = heirs + p.batch;    // [batch] the heir that keeps a last page that is not full, -1: none does
   int* const start = first + p.batch;    // [rows + 1] pages that the rows before need
   uint64_t* const known = reinterpret_cast<uint64_t*>(fork_smem + ((2 * p.batch + p.rows + 2) & ~1));  // [rows]
   auto row_of = [&](int r) { return CACHED ? ForkRow::unpack(known[r]) : fork_row(p, r); };
@@ -180,16 +186,24 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     bool page_bad = lane < pages && (head < 0 || head >= p.num_pages);
     for (int j = lane + 32; j < pages; j += 32) page_bad |= row[j] < 0 || row[j] >= p.num_pages;
     page_bad = __any_sync(0xffffffffu, page_bad);
-    if (lane == 0) {
-      if (!fits || page_bad) paged_error(p.status, fits ? kSitePagedPage : kSitePagedSeq, b);
-      p.valid[b] = fits && !page_bad ? 1 : 0;
+    if (lane == 0 && (!fits || page_bad)) paged_error(p.status, fits ? kSitePagedPage : kSitePagedSeq, b);
+    int valid = fits && !page_bad ? 1 : 0;
+    if (valid != 0 && (len & part_mask) != 0) {
+      const int last = pages - 1;
+      const int page = last < 32 ? __shfl_sync(0xffffffffu, head, last) : row[last];
+      if (p.refs[page] > 1) {
+        valid = 2;
+        if (lane == 0) p.owner[page] = INT_MAX;
+      }
     }
+    if (lane == 0) p.valid[b] = valid;
   }
   for (int i = tid; i < p.num_pages; i += kAll) p.refs_out[i] = p.refs[i];
   for (int b = threadIdx.x; b < p.batch; b += kThreads) heirs[b] = 0, first[b] = INT_MAX;
   cluster_sync();
 
-  // ---- heirs, and the pages that rows need ----
+  // ---- heirs ----
+  bool shares = false;
   for (int r = threadIdx.x; r < p.rows; r += kThreads) {
     const ForkRow w = fork_row(p, r);
     if constexpr (CACHED) known[r] = w.pack();
@@ -200,9 +214,41 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     if (w.src >= 0) {
       atomicAdd(heirs + w.src, 1);
       atomicMin(first + w.src, r);
+      if (w.shared) atomicOr(heirs + w.src, kSharedHeir), shares = true;
     }
   }
-  __syncthreads();
+  shares = __syncthreads_or(shares) != 0;  // the same in all blocks
+
+  // ---- what the old rows' heirs make of their pages' counts ----
+  for (int b = warp; b < p.batch; b += kAll / 32) {
+    const int n = heirs[b] & ~kSharedHeir;
+    if (heirs[b] == 1) continue;
+    const int valid = __ldcg(p.valid + b);
+    if (valid == 0) continue;
+    const int len = p.seqlens[b], full = len >> p.page_shift;
+    const int* row = p.table + b * p.table_stride;
+    for (int j = lane; n != 1 && j < full; j += 32) atomicAdd(p.refs_out + row[j], n - 1);
+    if ((len & part_mask) != 0 && lane == 0) {
+      if (n == 0 || valid == 2) atomicAdd(p.refs_out + row[full], -1);
+      if (n > 0 && valid == 2) atomicMin(p.owner + row[full], first[b]);
+    }
+  }
+  if (shares) {
+    // ---- a last page that is not full and had other uses: kept by the first heir of all its rows, if no use is left ----
+    cluster_sync();
+    auto last_page = [&](int b) { return p.table[b * p.table_stride + (p.seqlens[b] >> p.page_shift)]; };
+    for (int b = threadIdx.x; b < p.batch; b += kThreads)
+      if ((heirs[b] & kSharedHeir) != 0) {
+        const int page = last_page(b);
+        if (__ldcg(p.refs_out + page) > 0 || __ldcg(p.owner + page) != first[b]) first[b] = -1;
+      }
+    cluster_sync();  // all blocks have read the counts
+    if (rank == 0)
+      for (int b = threadIdx.x; b < p.batch; b += kThreads)
+        if ((heirs[b] & kSharedHeir) != 0 && first[b] >= 0) atomicAdd(p.refs_out + last_page(b), 1);
+  }
+
+  // ---- the pages that rows need ----
   auto copies = [&](const ForkRow& w, int r) { return w.src >= 0 && (w.len & part_mask) != 0 && first[w.src] != r; };
   auto kept_pages = [&](const ForkRow& w, int r) {  // that come from the parent
     return (w.len >> p.page_shift) + ((w.len & part_mask) != 0 && !copies(w, r) ? 1 : 0);
@@ -223,15 +269,6 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) start[0] = 0;
 
-  // ---- what the old rows' heirs make of their pages' counts ----
-  for (int b = warp; b < p.batch; b += kAll / 32) {
-    const int n = heirs[b];
-    if (n == 1 || __ldcg(p.valid + b) == 0) continue;
-    const int len = p.seqlens[b], full = len >> p.page_shift;
-    const int* row = p.table + b * p.table_stride;
-    for (int j = lane; j < full; j += 32) atomicAdd(p.refs_out + row[j], n - 1);
-    if (n == 0 && (len & part_mask) != 0 && lane == 0) atomicAdd(p.refs_out + row[full], -1);
-  }
   cluster_sync();
 
   // ---- the lowest free pages go to the rows in order ----
@@ -288,7 +325,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     for (int j = lane; j < p.max_pages; j += 32) {
       if (j < kept && !fails) out[j] = row[j];
       else if (j >= total || fails) out[j] = -1;
-      // a row without enough pages gives back what it shares, a first heir the page that is partly filled too
+      // a row without enough pages gives back what it shares, and a page that is partly filled if it keeps one
       if (j < kept && fails && (j < w.len >> p.page_shift || first[w.src] == r)) atomicAdd(p.refs_out + row[j], -1);
     }
   }
@@ -443,7 +480,7 @@ __global__ void __launch_bounds__(32 * kCopyWarps, kCopyBlocks) kv_copy_kernel(c
 }
 
 struct PagesWorkspace {
-  size_t head, valid, src, dst, tokens, bytes;
+  size_t head, valid, owner, src, dst, tokens, bytes;
 };
 PagesWorkspace pages_workspace(int batch, int rows, int num_pages) {
   PagesWorkspace w;
@@ -456,6 +493,7 @@ PagesWorkspace pages_workspace(int batch, int rows, int num_pages) {
   const size_t copies = static_cast<size_t>(rows > num_pages ? rows : num_pages);
   w.head = take(sizeof(PagesHead) / sizeof(int));
   w.valid = take(batch);
+  w.owner = take(rows > 0 ? num_pages : 0);
   w.src = take(copies);
   w.dst = take(copies);
   w.tokens = take(rows);
@@ -467,6 +505,7 @@ void pages_fill(PagesParams& p, uint8_t* ws, int batch, int rows, const fa_kv_ca
   const PagesWorkspace w = pages_workspace(batch, rows, c.num_pages);
   p.head = reinterpret_cast<PagesHead*>(ws + w.head);
   p.valid = reinterpret_cast<int*>(ws + w.valid);
+  p.owner = reinterpret_cast<int*>(ws + w.owner);
   p.src = reinterpret_cast<int*>(ws + w.src);
   p.dst = reinterpret_cast<int*>(ws + w.dst);
   p.tokens = reinterpret_cast<int*>(ws + w.tokens);

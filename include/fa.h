@@ -678,9 +678,12 @@ int fa_fwd_lists(const void* q, const fa_kv_cache* cache, const int* lists, cons
  * takes over row parents[r] (-1: it starts empty), then gets room for
  * new_tokens[r] more tokens (NULL: 0).  A parent may have any number of heirs
  * among the rows; one without any is freed.  Full pages are shared by all heirs.
- * A last page that is not full stays with the parent's first heir (the lowest r);
- * each other heir gets a new page with a copy of its tokens, scales and (k_bounds
- * not NULL) bounds, bytes behind them left as they were.  New pages, a row's copy
+ * A last page that is not full, which may receive tokens, belongs to one row
+ * afterwards: if nothing uses it once the old rows that end in it are dropped (as
+ * a full page of another row or by a holder that only its count knows), the first
+ * heir of these rows (the lowest r) keeps it; each other heir, or each heir, gets
+ * a new page with a copy of its tokens, scales and (k_bounds not NULL) bounds,
+ * bytes behind them left as they were.  New pages, a row's copy
  * first, are the lowest free ones after the old rows' uses were dropped, row by
  * row.  So one call forks, reorders, frees and extends.
  *   table_out   [rows, max_pages] int32, row stride table_out_stride, written
