@@ -731,6 +731,16 @@ def _empty(shape, dtype, index, ptr, current):
         return torch.empty(shape, dtype=dtype, device=index)
 
 
+def _zeros(shape, dtype, index, ptr, current):
+    """``_empty`` filled with zeros on the stream `ptr`."""
+    import torch
+
+    if ptr == current:
+        return torch.zeros(shape, dtype=dtype, device=index)
+    with torch.cuda.stream(torch.cuda.ExternalStream(ptr, device=index)):
+        return torch.zeros(shape, dtype=dtype, device=index)
+
+
 # rows (new tokens x query heads a key/value head) up to which a sequence is read straight from the pages
 _PAGED_ROWS = 128
 
@@ -1137,7 +1147,9 @@ def kv_select(q, k_bounds, k_scale, block_table, seqlens_k, cu_seqlens_q, max_se
     ``attention_forward_paged``.  The first ``keep_first`` and the last ``keep_last`` (1 at least) pages that a token sees
     are always taken, the others by the sum over the query heads of the largest score that a key within the bounds can
     have.  Returns (lists int32 [total_q,Hkv,top], list_lens int32 [total_q]) for ``attention_forward_lists``, allocated
-    when not given, as is the workspace (uint8), which grows with total_q * Hkv * the width of block_table."""
+    when not given, as is the workspace (uint8), which grows with total_q * Hkv * the width of block_table.  Rows of tokens
+    of no sequence (a padded batch) have a list_lens of 0 if it is allocated here, and are left as they are if it is given:
+    then it has to hold a length for them, 0 for none."""
     import torch
 
     index = q.get_device()
@@ -1165,7 +1177,9 @@ def kv_select(q, k_bounds, k_scale, block_table, seqlens_k, cu_seqlens_q, max_se
     else:
         _int32(torch, "lists", lists, (total_q, heads, top))
     if list_lens is None:
-        list_lens = _empty((total_q,), torch.int32, index, ptr, current)
+        # attention_forward_lists knows no sequences: rows of none are to be rows without a key (8 us of the host's time,
+        # which callers that keep their own list_lens save)
+        list_lens = _zeros((total_q,), torch.int32, index, ptr, current)
     else:
         _int32(torch, "list_lens", list_lens, (total_q,))
     ws, size, own = _workspace(torch, workspace, ptr, "fa_kv_select_workspace_size", batch, total_q, heads, width)

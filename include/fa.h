@@ -630,8 +630,9 @@ int fa_kv_bounds(const fa_kv_cache* cache, void* k_bounds, const int* cu_seqlens
  *             cache, as in block_table), in the order of the sequence, then -1
  *   list_lens [total_q] int32: tokens that they hold for the token to see, the
  *             last page perhaps in part
- * Rows of tokens of no sequence are left as they are.  A page outside the cache
- * is never followed (site 512); it counts as the last choice, and stands in the
+ * Rows of tokens of no sequence are left as they are: where a batch may be padded,
+ * list_lens holds 0 for them before fa_fwd_lists, which knows no sequences, reads
+ * it.  A page outside the cache is never followed (site 512); it counts as the last choice, and stands in the
  * list as -1 if it is taken all the same.
  *
  * heads_q * d_qk per token contiguous; table_stride in entries; sizes as in

@@ -38,3 +38,53 @@ def test_all_places_forced(fa, pages, new, first, last):  # noqa: F811
         assert status(fa)[0] == 0
         assert torch.equal(lists.cpu(), expect)
         assert torch.equal(list_lens.cpu(), expect_lens)
+
+
+def fill_freed(n, value):
+    """Leaves `value` in the block of n int32 that the allocator hands out next."""
+    blocks = [torch.full((n,), value, dtype=torch.int32, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    del blocks
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_rows_behind_the_last_sequence_see_no_key(fa, side):  # noqa: F811
+    """A padded batch whose list_lens the call allocates: rows of no sequence, and of one that is out of range, have no key
+    for the attention, and no error; a graph finds that anew each time, with fewer sequences and with more."""
+    import paged_ref as ref
+
+    lens, total = [100, 50, 40, 30], 9
+    cache = ref.Cache(lens, 2, 16, 64, 64)
+    k, v, ks, vs, table, seqlens = cache.to_device("cuda")
+    bounds = torch.zeros(cache.num_pages, 2, 2, 64, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    cu_all = int32([0, 100, 150, 190, 220])
+    fa.kv_bounds(k, bounds, table, seqlens, cu_all, 220)
+    q = normal(total, 4, 64).cuda()
+    cu = int32([0, 2, 3, 3, 4])
+    args = (q, bounds, ks, table, seqlens, cu, 2, 16, 3)
+    whole = fa.kv_select(*args, list_lens=torch.zeros(total, dtype=torch.int32, device="cuda"))
+    expect = whole[1].tolist()
+    assert expect[4:] == [0] * 5 and min(expect[:4]) > 0
+    fill_freed(total, 77)
+    stream = torch.cuda.Stream() if side else None
+    torch.cuda.synchronize()
+    lists, list_lens = fa.kv_select(*args, stream=stream)
+    torch.cuda.synchronize()
+    assert list_lens.tolist() == expect
+    o, lse = fa.attention_forward_lists(q, k, v, ks, vs, lists, list_lens)
+    assert status(fa)[0] == 0
+    assert (o[4:] == 0).all() and torch.isinf(lse[:, 4:]).all() and not torch.isinf(lse[:, :4]).any()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lists, list_lens = fa.kv_select(*args)
+        o, lse = fa.attention_forward_lists(q, k, v, ks, vs, lists, list_lens)
+    for rows, offs in ((9, [0, 2, 4, 7, 9]), (1, [0, 0, 0, 1, 1]), (4, [0, 2, 3, 3, 4])):
+        cu.copy_(int32(offs))
+        graph.replay()
+        code, detail = status(fa)
+        if rows == 9:  # three new tokens of one sequence, more than the call allows: that one is left out
+            assert code == fa.FA_ERR_INVALID_ARG and detail[1:] == (511, 2)
+            assert list_lens[4:7].tolist() == [0, 0, 0] and min(list_lens[:4].tolist() + list_lens[7:].tolist()) > 0
+            continue
+        assert code == 0 and list_lens[rows:].tolist() == [0] * (total - rows) and min(list_lens[:rows].tolist()) > 0
+        assert (o[rows:] == 0).all()
