@@ -875,6 +875,9 @@ def attention_forward_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, 
     return (out, lse) if return_lse else out
 
 
+_INT_MAX = 2 ** 31 - 1  # of the C interface's int: ctypes would keep the lower 32 bits of what is larger
+
+
 # ---------------------------------------------------------------------------
 # rotary positions
 # ---------------------------------------------------------------------------
@@ -906,6 +909,8 @@ def rotary_table(positions: int, rot_dim: int, base: float = 10000.0, scaling: s
 
     if scaling not in ROTARY_SCALING:
         _bad(f"scaling must be one of {', '.join(ROTARY_SCALING)}")
+    if not (0 <= positions <= _INT_MAX and 0 <= rot_dim <= _INT_MAX):
+        _bad("positions and rot_dim must not be negative, nor beyond 32 bits")
     if out is not None:
         if out.dtype is not torch.float32 or out.shape != (positions, rot_dim) or not out.is_contiguous() or not out.is_cuda:
             _bad(f"out must be a contiguous fp32 CUDA tensor [{positions}, {rot_dim}]")
@@ -922,8 +927,6 @@ def rotary_table(positions: int, rot_dim: int, base: float = 10000.0, scaling: s
     if stream is not None:
         ptr, current = _call_stream(index, stream)
     if out is None:
-        if positions < 0 or rot_dim < 0:
-            _bad("positions and rot_dim must not be negative")
         out = _empty((positions, rot_dim), torch.float32, index, ptr, current)
     spec = FaRotaryScaling(ROTARY_SCALING[scaling], factor, original, low, high, magnitude)
     rc = fa_rotary_table(out.data_ptr(), positions, rot_dim, base, spec, ptr)
@@ -1126,6 +1129,8 @@ def kv_bounds(k_cache, k_bounds, block_table, seqlens_k, cu_seqlens, total: int,
             return kv_bounds(k_cache, k_bounds, block_table, seqlens_k, cu_seqlens, total, stream)
     pages, heads, page, d = kd
     batch, width, ts = _table_rows(torch, block_table, seqlens_k)
+    if not 0 <= total <= _INT_MAX:
+        _bad("total must not be negative, nor beyond 32 bits")
     _int32(torch, "cu_seqlens", cu_seqlens, (batch + 1,))
     bounds = _bounds(torch, k_bounds, pages, heads, d)
     ptr = torch._C._cuda_getCurrentRawStream(index) if stream is None else _call_stream(index, stream)[0]
@@ -1167,8 +1172,9 @@ def kv_select(q, k_bounds, k_scale, block_table, seqlens_k, cu_seqlens_q, max_se
     bounds = _bounds(torch, k_bounds, pages, heads, d)
     batch, width, ts = _table_rows(torch, block_table, seqlens_k)
     _int32(torch, "cu_seqlens_q", cu_seqlens_q, (batch + 1,))
-    if top < 0:
-        _bad("top must not be negative")
+    if max(max_seqlen_q, page_size, top, keep_first, keep_last) > _INT_MAX or \
+            min(max_seqlen_q, page_size, top, keep_first, keep_last) < 0:
+        _bad("max_seqlen_q, page_size, top, keep_first and keep_last must not be negative, nor beyond 32 bits")
     ptr = current = torch._C._cuda_getCurrentRawStream(index)
     if stream is not None:
         ptr, current = _call_stream(index, stream)

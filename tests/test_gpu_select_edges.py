@@ -88,3 +88,31 @@ def test_rows_behind_the_last_sequence_see_no_key(fa, side):  # noqa: F811
             continue
         assert code == 0 and list_lens[rows:].tolist() == [0] * (total - rows) and min(list_lens[:rows].tolist()) > 0
         assert (o[rows:] == 0).all()
+
+
+BEYOND = [2 ** 32, 2 ** 31, -2 ** 32, 2 ** 64]
+
+
+def test_numbers_beyond_32_bits_are_refused(fa):  # noqa: F811
+    """What the C interface's integers cannot hold is an error, and not its lower 32 bits."""
+    import paged_ref as ref
+
+    cache = ref.Cache([100, 50], 2, 16, 64, 64)
+    k, _, ks, _, table, lens = cache.to_device("cuda")
+    bounds = torch.zeros(cache.num_pages, 2, 2, 64, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    cu = int32([0, 1, 2])
+    out = torch.full((2, 2, 4), -2, dtype=torch.int32, device="cuda")
+    good = dict(q=normal(2, 4, 64).cuda(), k_bounds=bounds, k_scale=ks, block_table=table, seqlens_k=lens, cu_seqlens_q=cu,
+                max_seqlen_q=1, page_size=16, top=4, keep_first=0, keep_last=1, lists=out)
+    for name in ("max_seqlen_q", "page_size", "top", "keep_first", "keep_last"):
+        for more in BEYOND:
+            with pytest.raises(fa.FaError):
+                fa.kv_select(**{**good, name: good[name] + more})
+    for more in BEYOND:
+        with pytest.raises(fa.FaError):
+            fa.kv_bounds(k, bounds, table, lens, cu, 2 + more)
+        with pytest.raises(fa.FaError):
+            fa.rotary_table(8 + more, 64)
+        with pytest.raises(fa.FaError):
+            fa.rotary_table(0, 64 + more)
+    assert status(fa)[0] == 0 and (out == -2).all()
