@@ -554,8 +554,11 @@ int fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse, c
  *                       r = original f_i / (2 pi) turns within the trained length
  *                       and w = (r - low) / (high - low), kept in [0, 1]
  *                       (0 <= low < high, original > 0)
- * Angles are exact to 2^-64 turns a position, so values are off by a few units
- * of the last place at any position.  magnitude is in [2^-64, 2^64].  One launch.
+ * Frequencies are computed in double: off by at most (2 ln base + 8) 2^-53 of
+ * themselves (base as it is scaled), by parts by (ln base + 10) (1 + high / (high -
+ * low)) 2^-53 of the unscaled f_i, and by 2^-65 turns.  The angle's reduction is
+ * exact, so a value is off by p times that, by 7 * 2^-24 of itself and by 2^-51, in
+ * terms of the magnitude, which is in [2^-64, 2^64].  One launch.
  */
 enum fa_rotary_kind { FA_ROTARY_PLAIN = 0, FA_ROTARY_LINEAR = 1, FA_ROTARY_BASE = 2, FA_ROTARY_BY_PARTS = 3 };
 
