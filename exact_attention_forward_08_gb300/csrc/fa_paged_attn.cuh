@@ -33,7 +33,7 @@
 // LISTS, fa_fwd_lists: the same over lists of pages, one for each token and key
 // head, a token's rows at a time.  A list stands in the table's place, its length in
 // the sequence's, and nothing else is masked; more than 16 query heads a key head go
-// in groups that read the pages again (out of L2).  64 lists of 1 to 64 pages of 64,
+// in equal groups that read the pages again (out of L2); a prime ratio makes a group a head.  64 lists of 1 to 64 pages of 64,
 // 32/8 heads of 128: 73.0 us with the merge, 443 MB, 6.1 TB/s; one of 32 pages 11.2.
 #pragma once
 #include <cuda_runtime.h>

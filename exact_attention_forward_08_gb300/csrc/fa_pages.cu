@@ -12,8 +12,10 @@
 // scans in order of rows and of pages.
 //
 // Bound by latency, but for large copies.  GPU time: 64 beams over one another's
-// rows of 624 to 2554 tokens, 854 pages, 19 partly filled ones copied, 12.9 us; 256
-// requests in 14613 pages, a tenth of which changes, 13.1 us; compaction of 1042 pages
+// rows of 624 to 2554 tokens, 854 pages, 19 partly filled ones copied, 12.5 us; 256
+// requests in 14613 pages, a tenth of which changes, 13.1 us; 64 rows of 2000 tokens
+// 10.5 us, 12.3 if a holder beside the table has each row's last page, and 39.1 and
+// 40.8 with rows of 131000 tokens, whose tables the eight blocks write; compaction of 1042 pages
 // among 1147 of 16 tokens 8.3 us, of 1910 among 3821 of 64 tokens, 257 MB read and
 // written, 50.0 us: 8 for the steps, 38 for the copies, 6.8 TB/s.  In a pool of a
 // million pages 68 and 52 us.

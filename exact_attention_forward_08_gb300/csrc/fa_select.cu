@@ -458,9 +458,11 @@ struct ChooseShared {
   float q_size[S::kWarps];
 };
 
-// A block takes one token and key head: keys from the score kernel, T from a histogram of 2048 bins, pages near T, the
-// list.  Ten barriers and as many waits for loads: 9 us for 2048 pages, 15 us where four blocks share an SM.  What does
-// not depend on the scores is done while they are computed.
+// A block takes one token and key head: keys from the score kernel, T from a histogram of 2048 bins (512 in the small
+// blocks), pages near T, the list.  Ten barriers and as many waits for loads: 9 us for 2048 pages, 15 us where four
+// blocks share an SM.  What does not depend on the scores is done while they are computed.  Of more pages than are
+// staged every pass reads the keys from global memory, and pages near T, two as well as many, are searched by halving:
+// the call for one token over 8188 pages takes 50.8 us, over 4094 18.1; for 24 sequences of 3 tokens 173 and 62.
 template <int D, class S>
 __global__ void __launch_bounds__(S::kThreads) kv_choose_kernel(const __grid_constant__ SelectParams p) {
   constexpr int kThreads = S::kThreads, kWarps = S::kWarps, kBins = S::kBins, kBinBits = S::kBinBits;
